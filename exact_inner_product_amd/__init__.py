@@ -29,6 +29,8 @@ EXPORTS = (
     "mips_topk_ranges",
     "mips_topk_masks_workspace_size", "mips_topk_masks",
     "mips_merge_topk", "mips_merge_interests", "mips_type_bitmap", "mips_set_timing_events", "mips_status_string", "mips_last_hip_error",
+    "mips_embedding_lookup", "mips_embedding_grad_workspace_size", "mips_embedding_grad",
+    "mips_clip_workspace_size", "mips_clip_grad_norm",
 )
 MERGE_MAX_LISTS = 64
 MAX_MASKS = 4  # result sets of one mips_topk_masks pass
@@ -85,6 +87,17 @@ def lib() -> C.CDLL:
         L.mips_status_string.argtypes = [C.c_int]
         L.mips_status_string.restype = C.c_char_p
         L.mips_last_hip_error.argtypes = []
+        f32 = C.c_float
+        L.mips_embedding_lookup.argtypes = [p, i32, i64, i32, i64, p, i32, i64, f32, p, p]
+        L.mips_embedding_grad_workspace_size.argtypes = [i64, i64, i32]
+        L.mips_embedding_grad_workspace_size.restype = sz
+        L.mips_embedding_grad.argtypes = [p, i32, i64, i32, i64, p, i32, i64, f32, i32, p, i32, i64, p,
+                                          sz, p]
+        L.mips_clip_workspace_size.argtypes = [i32]
+        L.mips_clip_workspace_size.restype = sz
+        L.mips_clip_grad_norm.argtypes = [p, p, p, p, i32, f32, p, p, sz, p]
+        for f in (L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
+            f.restype = C.c_int
         for f in (L.mips_l2_normalize, L.mips_prepare_corpus, L.mips_topk, L.mips_topk_noalloc,
                   L.mips_topk_ranges,
                   L.mips_topk_masks,
@@ -466,3 +479,6 @@ def recall_vs_exact(approx_ids, queries: torch.Tensor, corpus: Corpus, k: int,
 def set_timing_events(before, after) -> None:
     """Record hipEvents around the main score kernel of later topk calls (None, None stops)."""
     lib().mips_set_timing_events(before, after)
+
+
+from .training import (clip_grad_norm, embedding_grad, embedding_lookup)  # noqa: E402

@@ -1,0 +1,666 @@
+// embedding.hip -- embedding lookup with scaling and its gradient by sorted tokens (gfx950).
+//
+// Lookup:   out[t] = scale * table[id_t], a zero row where id_t is outside [0, rows).
+// Gradient: out[v] = scale * sum over the tokens t with id_t = v of grad[t].
+//
+// Both move rows and compute next to nothing, so both are bound by memory traffic (and, for
+// few tokens, by launches). The gradient's sum is a segmented sum over the tokens sorted by
+// id: no atomics on floats, so that the same call gives the same bits, and a hot id's
+// thousands of tokens are split over many groups of lanes.
+#include "common.h"
+#include "host.h"
+
+namespace mips {
+
+// ------------------------------------------------------------- 16-byte vectors of rows
+// A unit is up to 16 bytes of one row: 4 floats, 8 bf16, or (rows that are not 16-byte
+// multiples or not aligned) a single element.
+template <int DT, bool VEC>
+struct Unit {
+  static constexpr int N = VEC ? (DT == MIPS_F32 ? 4 : 8) : 1;
+  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[N]) {
+    if constexpr (DT == MIPS_F32) {
+      if constexpr (VEC) {
+        const float4 x = *(const float4*)((const float*)p + i);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        v[0] = ((const float*)p)[i];
+      }
+    } else {
+      if constexpr (VEC) {
+        const u32x4_t x = *(const u32x4_t*)((const uint16_t*)p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = __uint_as_float(x[j] << 16);
+          v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+        }
+      } else {
+        v[0] = bf16_to_f32(((const uint16_t*)p)[i]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[N]) {
+    if constexpr (DT == MIPS_F32) {
+      if constexpr (VEC)
+        *(float4*)((float*)p + i) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        ((float*)p)[i] = v[0];
+    } else {
+      // the one rounding to bf16, to nearest even (the compiler's conversion keeps NaN)
+      if constexpr (VEC) {
+        bf16x8_t o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
+        *(bf16x8_t*)((uint16_t*)p + i) = o;
+      } else {
+        ((__bf16*)p)[i] = (__bf16)v[0];
+      }
+    }
+  }
+};
+
+template <typename IdT>
+__device__ __forceinline__ int64_t id_at(const void* ids, int64_t t) {
+  return (int64_t)((const IdT*)ids)[t];
+}
+
+// ------------------------------------------------------------------------------ lookup
+constexpr int kLookupRows = 4;  // rows in flight per group of lanes
+
+struct LookupArgs {
+  const void* table;
+  int64_t rows, row_stride;
+  const void* ids;
+  int64_t t;
+  float scale;
+  void* out;
+  int d, nunit, tpr_log;  // units per row; log2 of the lanes that share a row
+};
+
+// 2^tpr_log lanes share a row and take its units in turn; each group moves kLookupRows
+// rows, all of their loads issued before the first store, which keeps several row fetches in
+// flight per lane (random rows of a large table miss every cache).
+template <int DT, bool VEC, typename IdT>
+__global__ __launch_bounds__(256) void lookup_kernel(LookupArgs A) {
+  using U = Unit<DT, VEC>;
+  const int tpr = 1 << A.tpr_log;
+  const int sub = threadIdx.x & (tpr - 1);
+  const int groups = 256 >> A.tpr_log;
+  const int64_t t0 = (int64_t)blockIdx.x * groups * kLookupRows + (threadIdx.x >> A.tpr_log);
+  int64_t row[kLookupRows];
+#pragma unroll
+  for (int u = 0; u < kLookupRows; ++u) {
+    const int64_t t = t0 + u * groups;
+    row[u] = t < A.t ? id_at<IdT>(A.ids, t) : -1;
+    if (row[u] < 0 || row[u] >= A.rows) row[u] = -1;
+  }
+  for (int j = sub; j < A.nunit; j += tpr) {
+    float v[kLookupRows][U::N];
+#pragma unroll
+    for (int u = 0; u < kLookupRows; ++u) {
+#pragma unroll
+      for (int e = 0; e < U::N; ++e) v[u][e] = 0.0f;
+      if (row[u] >= 0) U::load(A.table, row[u] * A.row_stride + (int64_t)j * U::N, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kLookupRows; ++u) {
+      const int64_t t = t0 + u * groups;
+      if (t >= A.t) continue;
+      if (row[u] >= 0) {
+#pragma unroll
+        for (int e = 0; e < U::N; ++e) v[u][e] *= A.scale;
+      }
+      U::store(A.out, t * A.d + (int64_t)j * U::N, v[u]);
+    }
+  }
+}
+
+static int log2_lanes(int nunit) {  // lanes that share a row: the least power of two >= nunit, at most 64
+  int l = 0;
+  while ((1 << l) < nunit && l < 6) ++l;
+  return l;
+}
+
+template <int DT, bool VEC>
+static int launch_lookup(LookupArgs A, int id_bits, hipStream_t s) {
+  A.nunit = A.d / Unit<DT, VEC>::N;
+  A.tpr_log = log2_lanes(A.nunit);
+  const int64_t per = (256 >> A.tpr_log) * kLookupRows;
+  const int E = elem_bytes(DT), I = id_bits / 8;
+  const int64_t total = A.t;
+  for (int64_t t0 = 0; t0 < total; t0 += per * kMaxGridBlocks) {
+    LookupArgs P = A;
+    P.t = total - t0 < per * kMaxGridBlocks ? total - t0 : per * kMaxGridBlocks;
+    P.ids = (const uint8_t*)A.ids + t0 * I;
+    P.out = (uint8_t*)A.out + t0 * A.d * E;
+    const dim3 grid((unsigned)((P.t + per - 1) / per));
+    if (id_bits == 32)
+      hipLaunchKernelGGL((lookup_kernel<DT, VEC, int32_t>), grid, dim3(256), 0, s, P);
+    else
+      hipLaunchKernelGGL((lookup_kernel<DT, VEC, int64_t>), grid, dim3(256), 0, s, P);
+    if (const int rc = check_launch()) return rc;
+  }
+  return MIPS_OK;
+}
+
+// ------------------------------------------------------------------ sorting the tokens
+// The (id, token) pairs sorted by id, equal ids in token order: the order of the segmented
+// sum, and so its rounding, follows from the ids alone. Ids outside [0, rows) take the key
+// `rows` and sort behind every row.
+//
+// Few tokens (t <= kRankMax): one kernel; a token's place is the number of tokens that
+// precede it, counted by comparing it with every other (t^2 comparisons spread over the
+// chip). Otherwise a least-significant-digit radix sort of 8-bit digits over at most
+// kSortBlocks contiguous ranges of tokens, two kernels a digit: the ranges' digit counts,
+// then every range scans all counts for its own offsets and scatters. Inside a range a wave
+// takes 64 keys at a time and ranks equal digits by ballots, which keeps the sort stable.
+constexpr int kRankMax = 8192;
+constexpr int kRankTokens = 16;  // tokens ranked per workgroup
+constexpr int kSortBlocks = 256;
+constexpr int kSortTile = 2048;  // tokens of a range, at least
+constexpr int kSortThreads = 256;
+
+__device__ __forceinline__ uint32_t key_of(int64_t id, int64_t rows) {
+  return (id < 0 || id >= rows) ? (uint32_t)rows : (uint32_t)id;
+}
+
+// Writes zeros to the dense gradient: workgroup w of nw clears its share of `bytes` (a
+// multiple of the element size) at p. Run by the first kernel of the gradient in workgroups
+// of its own, beside the sort.
+struct ZeroArgs {
+  void* p;
+  int64_t rows, stride_b;  // rows and bytes between them
+  int64_t row_b;           // bytes of a row
+  int nblocks;             // workgroups that clear (0: accumulate into what is there)
+};
+
+__device__ __forceinline__ void zero_rows(const ZeroArgs& Z, int w) {
+  const u32x4_t z = {0u, 0u, 0u, 0u};
+  if (Z.stride_b == Z.row_b && ((uintptr_t)Z.p & 15) == 0) {
+    const int64_t total = Z.rows * Z.row_b, n16 = total / 16;
+    u32x4_t* p = (u32x4_t*)Z.p;
+    for (int64_t i = (int64_t)w * 256 + threadIdx.x; i < n16; i += (int64_t)Z.nblocks * 256) p[i] = z;
+    if (w == 0 && threadIdx.x < (total & 15) / 2)
+      ((uint16_t*)Z.p)[n16 * 8 + threadIdx.x] = 0;
+  } else {
+    for (int64_t r = w; r < Z.rows; r += Z.nblocks) {
+      uint16_t* p = (uint16_t*)((uint8_t*)Z.p + r * Z.stride_b);
+      for (int64_t j = threadIdx.x; j < Z.row_b / 2; j += 256) p[j] = 0;
+    }
+  }
+}
+
+struct RankArgs {
+  const void* ids;
+  int64_t t, rows;
+  uint32_t* keys;  // sorted
+  uint32_t* toks;
+  int nrank;       // workgroups that rank; the others clear the output
+  ZeroArgs Z;
+};
+
+template <typename IdT>
+__global__ __launch_bounds__(256) void rank_sort_kernel(RankArgs A) {
+  if ((int)blockIdx.x >= A.nrank) {
+    zero_rows(A.Z, (int)blockIdx.x - A.nrank);
+    return;
+  }
+  __shared__ uint32_t mine[kRankTokens];
+  __shared__ uint32_t cnt[4][kRankTokens];
+  const int t = (int)A.t, t0 = blockIdx.x * kRankTokens;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x < kRankTokens)
+    mine[threadIdx.x] = t0 + (int)threadIdx.x < t ? key_of(id_at<IdT>(A.ids, t0 + threadIdx.x), A.rows) : 0u;
+  __syncthreads();
+  uint32_t k[kRankTokens], c[kRankTokens];
+#pragma unroll
+  for (int i = 0; i < kRankTokens; ++i) {
+    k[i] = mine[i];
+    c[i] = 0u;
+  }
+  // token j precedes token i if its key is smaller, or equal with j < i. Tokens before this
+  // workgroup's precede at equal keys, tokens after it do not: one comparison with k + 1 or
+  // k; only the workgroup's own tokens need the test of j.
+  for (int j = threadIdx.x; j < t; j += 256) {
+    const uint32_t kj = key_of(id_at<IdT>(A.ids, j), A.rows);
+    const uint32_t adj = j < t0 ? 1u : 0u;
+    const int in = j - t0;
+#pragma unroll
+    for (int i = 0; i < kRankTokens; ++i) {
+      const uint32_t lim = k[i] + ((in >= 0 && in < i) ? 1u : adj);
+      c[i] += kj < lim ? 1u : 0u;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRankTokens; ++i) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) c[i] += __shfl_xor(c[i], o, kWave);
+    if (lane == 0) cnt[wave][i] = c[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kRankTokens && t0 + (int)threadIdx.x < t) {
+    const int i = threadIdx.x;
+    const uint32_t r = cnt[0][i] + cnt[1][i] + cnt[2][i] + cnt[3][i];
+    A.keys[r] = mine[i];
+    A.toks[r] = (uint32_t)(t0 + i);
+  }
+}
+
+struct SortArgs {
+  const void* ids;          // first pass: the ids; NULL afterwards
+  int64_t t, rows;
+  int64_t per;              // tokens per range
+  int nb;                   // ranges
+  int shift;
+  const uint32_t *keys_in, *toks_in;
+  uint32_t *keys_out, *toks_out;
+  uint32_t* counts;         // [nb][256]
+  ZeroArgs Z;
+};
+
+template <typename IdT>
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& A, int64_t i) {
+  return A.ids ? key_of(id_at<IdT>(A.ids, i), A.rows) : A.keys_in[i];
+}
+
+template <typename IdT>
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs A) {
+  if ((int)blockIdx.x >= A.nb) {
+    zero_rows(A.Z, (int)blockIdx.x - A.nb);
+    return;
+  }
+  __shared__ uint32_t hist[256];
+  hist[threadIdx.x] = 0u;
+  __syncthreads();
+  const int64_t i0 = blockIdx.x * A.per, i1 = min(A.t, i0 + A.per);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
+    atomicAdd(&hist[(sort_key<IdT>(A, i) >> A.shift) & 255u], 1u);
+  __syncthreads();
+  A.counts[blockIdx.x * 256 + threadIdx.x] = hist[threadIdx.x];
+}
+
+template <typename IdT>
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs A) {
+  __shared__ uint32_t base[256];      // next place of each digit of this range
+  __shared__ uint32_t wcnt[4][256];   // a step's counts per wave and digit
+  __shared__ uint32_t wsum[4];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  // digit t: tokens of the ranges before this one, and of all ranges
+  uint32_t before = 0u, all = 0u;
+#pragma unroll 8
+  for (int b = 0; b < A.nb; ++b) {
+    const uint32_t c = A.counts[b * 256 + t];
+    all += c;
+    before += b < (int)blockIdx.x ? c : 0u;
+  }
+  uint32_t incl = all;  // prefix over the digits
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint32_t u = __shfl_up(incl, o, kWave);
+    if (lane >= o) incl += u;
+  }
+  if (lane == kWave - 1) wsum[wave] = incl;
+  __syncthreads();
+  uint32_t off = incl - all;
+  for (int w = 0; w < wave; ++w) off += wsum[w];
+  base[t] = off + before;
+  __syncthreads();
+
+  const int64_t i0 = blockIdx.x * A.per, i1 = min(A.t, i0 + A.per);
+  for (int64_t s0 = i0; s0 < i1; s0 += kSortThreads) {  // uniform: every thread takes each step
+#pragma unroll
+    for (int w = 0; w < 4; ++w) wcnt[w][t] = 0u;
+    __syncthreads();
+    const int64_t i = s0 + t;
+    const bool on = i < i1;
+    const uint32_t key = on ? sort_key<IdT>(A, i) : 0u;
+    const uint32_t tok = !on ? 0u : (A.ids ? (uint32_t)i : A.toks_in[i]);
+    const uint32_t dig = (key >> A.shift) & 255u;
+    // lanes of the wave with the same digit
+    uint64_t same = __ballot(on);
+#pragma unroll
+    for (int bit = 0; bit < 8; ++bit) {
+      const uint64_t m = __ballot((dig >> bit) & 1u);
+      same &= ((dig >> bit) & 1u) ? m : ~m;
+    }
+    const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
+    if (on && rank == 0u) wcnt[wave][dig] = (uint32_t)__popcll(same);
+    __syncthreads();
+    if (on) {
+      uint32_t p = base[dig] + rank;
+      for (int w = 0; w < wave; ++w) p += wcnt[w][dig];
+      A.keys_out[p] = key;
+      A.toks_out[p] = tok;
+    }
+    __syncthreads();
+    base[t] += wcnt[0][t] + wcnt[1][t] + wcnt[2][t] + wcnt[3][t];
+  }
+}
+
+// --------------------------------------------------------------------- segmented sum
+// A group of 2^tpr_log lanes sums `chunk` consecutive sorted tokens. A segment (one id's
+// tokens) that lies inside a chunk is written to its row at once. A segment that crosses
+// chunks leaves one f32 partial row per chunk: slot 2c for the chunk's first segment where it
+// began before the chunk, slot 2c + 1 for its last where it goes on behind it. join_kernel
+// adds those rows.
+struct SegArgs {
+  const void* grad;
+  int64_t grad_stride;
+  const uint32_t *keys, *toks;
+  int64_t t, rows;
+  int d, nunit, tpr_log, chunk;
+  float scale;
+  int accumulate;
+  void* out;
+  int64_t out_stride;
+  float* part;  // [2 * nchunk][d]
+  int64_t nchunk;
+};
+
+constexpr int kSegBatch = 4;  // row fetches in flight per lane
+
+template <int DT, int OUT, bool VEC>
+__device__ __forceinline__ void write_row(const SegArgs& A, uint32_t key, int64_t j,
+                                          float (&a)[Unit<DT, VEC>::N]) {
+  constexpr int N = Unit<DT, VEC>::N;
+  const int64_t at = (int64_t)key * A.out_stride + j;
+#pragma unroll
+  for (int e = 0; e < N; ++e) a[e] *= A.scale;
+  if constexpr (OUT == DT) {
+    if (A.accumulate) {
+      float o[N];
+      Unit<DT, VEC>::load(A.out, at, o);
+#pragma unroll
+      for (int e = 0; e < N; ++e) a[e] += o[e];
+    }
+    Unit<DT, VEC>::store(A.out, at, a);
+  } else {  // bf16 gradients into an f32 table: 8 elements, two 16-byte stores
+    float* p = (float*)A.out + at;
+#pragma unroll
+    for (int e = 0; e < N; ++e) p[e] = A.accumulate ? p[e] + a[e] : a[e];
+  }
+}
+
+template <int DT, int OUT, bool VEC>
+__global__ __launch_bounds__(256) void segment_kernel(SegArgs A) {
+  using U = Unit<DT, VEC>;
+  constexpr int N = U::N;
+  const int tpr = 1 << A.tpr_log;
+  const int sub = threadIdx.x & (tpr - 1);
+  const int64_t c = (int64_t)blockIdx.x * (256 >> A.tpr_log) + (threadIdx.x >> A.tpr_log);
+  if (c >= A.nchunk) return;
+  const int64_t i0 = c * A.chunk, i1 = min(A.t, i0 + A.chunk);
+  const uint32_t none = (uint32_t)A.rows;
+  const uint32_t prev = i0 > 0 ? A.keys[i0 - 1] : 0xFFFFFFFFu;  // keys are at most 2^31
+  const uint32_t next = i1 < A.t ? A.keys[i1] : 0xFFFFFFFFu;
+  for (int u = sub; u < A.nunit; u += tpr) {
+    const int64_t j = (int64_t)u * N;
+    float a[N] = {};
+    uint32_t cur = A.keys[i0];
+    bool began = cur != prev;  // the current segment began in this chunk
+    auto close = [&](bool ends) __attribute__((always_inline)) {
+      if (cur != none) {
+        if (began && ends) {
+          write_row<DT, OUT, VEC>(A, cur, j, a);
+        } else {
+          float* p = A.part + (2 * c + (began ? 1 : 0)) * A.d + j;
+#pragma unroll
+          for (int e = 0; e < N; ++e) p[e] = a[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) a[e] = 0.0f;
+    };
+    for (int64_t i = i0; i < i1; i += kSegBatch) {
+      uint32_t k[kSegBatch];
+      float v[kSegBatch][N];
+#pragma unroll
+      for (int b = 0; b < kSegBatch; ++b) {
+        const int64_t ib = i + b < i1 ? i + b : i1 - 1;
+        k[b] = A.keys[ib];
+        U::load(A.grad, (int64_t)A.toks[ib] * A.grad_stride + j, v[b]);
+      }
+#pragma unroll
+      for (int b = 0; b < kSegBatch; ++b) {
+        if (i + b >= i1) break;
+        if (k[b] != cur) {
+          close(true);
+          cur = k[b];
+          began = true;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) a[e] += v[b][e];
+      }
+    }
+    // the last segment; one that both entered and leaves the chunk takes the chunk's slot 2c
+    if (cur != next) close(true);
+    else close(false);
+  }
+}
+
+// One workgroup per chunk whose last segment began in it and goes on: adds that segment's
+// partial rows, 2^tpr_log lanes a row, the groups taking chunks in turn, then the groups'
+// sums in LDS in a fixed order.
+template <int DT, int OUT, bool VEC>
+__global__ __launch_bounds__(256) void join_kernel(SegArgs A) {
+  constexpr int N = Unit<DT, VEC>::N;
+  __shared__ float red[256 * N];
+  const int64_t c = blockIdx.x;
+  const int64_t last = (c + 1) * A.chunk - 1;  // this chunk's last token (a later chunk exists)
+  if (last + 1 >= A.t) return;
+  const uint32_t key = A.keys[last];
+  const int64_t first = c * A.chunk;
+  if (key == (uint32_t)A.rows || A.keys[last + 1] != key) return;
+  if (A.keys[first] == key && first > 0 && A.keys[first - 1] == key) return;  // began earlier
+  // end of the segment: the first token with a larger key
+  int64_t lo = last + 1, hi = A.t;
+  while (lo < hi) {
+    const int64_t m = (lo + hi) >> 1;
+    if (A.keys[m] > key) hi = m;
+    else lo = m + 1;
+  }
+  const int64_t c1 = (lo - 1) / A.chunk;  // chunk of the segment's last token
+  const int tpr = 1 << A.tpr_log;
+  const int sub = threadIdx.x & (tpr - 1), g = threadIdx.x >> A.tpr_log, ng = 256 >> A.tpr_log;
+  for (int u0 = 0; u0 < A.nunit; u0 += tpr) {
+    const int u = u0 + sub;
+    float a[N] = {};
+    if (u < A.nunit) {
+      const int64_t j = (int64_t)u * N;
+#pragma unroll 4
+      for (int64_t q = c + g; q <= c1; q += ng) {
+        const float* p = A.part + (2 * q + (q == c ? 1 : 0)) * A.d + j;
+#pragma unroll
+        for (int e = 0; e < N; ++e) a[e] += p[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) red[threadIdx.x * N + e] = a[e];
+    __syncthreads();
+    for (int h = ng >> 1; h >= 1; h >>= 1) {
+      if (g < h) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          red[threadIdx.x * N + e] += red[(threadIdx.x + h * tpr) * N + e];
+      }
+      __syncthreads();
+    }
+    if (g == 0 && u < A.nunit) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) a[e] = red[threadIdx.x * N + e];
+      write_row<DT, OUT, VEC>(A, key, (int64_t)u * N, a);
+    }
+    __syncthreads();
+  }
+}
+
+// Sorted tokens per group: enough groups to fill the chip (about 16 waves a compute unit) before
+// a group takes more than 8 tokens, at most 64.
+static int seg_chunk(int64_t t, int tpr_log) {
+  const int64_t groups = (int64_t)4096 * 64 >> tpr_log;
+  int c = 8;
+  while (c < 64 && t / c > groups) c *= 2;
+  return c;
+}
+
+template <int DT, int OUT, bool VEC>
+static int launch_segments(SegArgs A, hipStream_t s) {
+  A.nunit = A.d / Unit<DT, VEC>::N;
+  A.tpr_log = log2_lanes(A.nunit);
+  A.chunk = seg_chunk(A.t, A.tpr_log);
+  A.nchunk = (A.t + A.chunk - 1) / A.chunk;
+  const int groups = 256 >> A.tpr_log;
+  hipLaunchKernelGGL((segment_kernel<DT, OUT, VEC>), dim3((unsigned)((A.nchunk + groups - 1) / groups)),
+                     dim3(256), 0, s, A);
+  if (const int rc = check_launch()) return rc;
+  if (A.nchunk > 1) {
+    hipLaunchKernelGGL((join_kernel<DT, OUT, VEC>), dim3((unsigned)(A.nchunk - 1)), dim3(256), 0, s, A);
+    return check_launch();
+  }
+  return MIPS_OK;
+}
+
+struct GradPlan {
+  int64_t per;
+  int nb, passes;
+  size_t keys[2], toks[2], counts, part, bytes;
+};
+
+static GradPlan grad_plan(int64_t t, int64_t rows, int d) {
+  GradPlan P{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t p = at;
+    at += (n + 255) / 256 * 256;
+    return p;
+  };
+  int bits = 1;  // keys 0 .. rows
+  while ((int64_t(1) << bits) <= rows) ++bits;
+  const bool rank = t <= kRankMax;
+  P.passes = rank ? 0 : (bits + 7) / 8;
+  P.nb = (int)((t + kSortTile - 1) / kSortTile < kSortBlocks ? (t + kSortTile - 1) / kSortTile : kSortBlocks);
+  if (P.nb < 1) P.nb = 1;
+  P.per = (t + P.nb - 1) / P.nb;
+  P.keys[0] = take((size_t)t * 4);
+  P.toks[0] = take((size_t)t * 4);
+  if (!rank) {
+    P.keys[1] = take((size_t)t * 4);
+    P.toks[1] = take((size_t)t * 4);
+    P.counts = take((size_t)P.nb * 256 * 4);
+  }
+  // partial rows: two per chunk (rows in 16-byte units share the fewest lanes, and so have
+  // the smallest chunks)
+  const int chunk = seg_chunk(t, log2_lanes(d / 8));
+  P.part = take((size_t)((t + chunk - 1) / chunk) * 2 * (size_t)d * 4);
+  P.bytes = at;
+  return P;
+}
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 64;
+
+static bool dtype_ok(int dt) { return dt == MIPS_F32 || dt == MIPS_BF16; }
+
+}  // namespace mips
+
+extern "C" {
+
+int mips_embedding_lookup(const void* table, int32_t dtype, int64_t rows, int32_t d,
+                          int64_t row_stride, const void* ids, int32_t id_bits, int64_t t,
+                          float scale, void* out, void* stream) {
+  using namespace mips;
+  if (t < 0 || rows < 1 || d < 1 || row_stride < d) return MIPS_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (id_bits != 32 && id_bits != 64) || d > MIPS_EMBEDDING_D_MAX)
+    return MIPS_ERR_UNSUPPORTED;
+  if (t == 0) return MIPS_OK;
+  const int E = elem_bytes(dtype);
+  if (!table || !ids || !out || !aligned(table, E) || !aligned(out, E) || !aligned(ids, id_bits / 8))
+    return MIPS_ERR_INVALID_ARG;
+  LookupArgs A{table, rows, row_stride, ids, t, scale, out, d, 0, 0};
+  hipStream_t s = (hipStream_t)stream;
+  const bool vec = aligned(table, 16) && aligned(out, 16) && (row_stride * E) % 16 == 0 && (d * E) % 16 == 0;
+  if (dtype == MIPS_F32) return vec ? launch_lookup<MIPS_F32, true>(A, id_bits, s) : launch_lookup<MIPS_F32, false>(A, id_bits, s);
+  return vec ? launch_lookup<MIPS_BF16, true>(A, id_bits, s) : launch_lookup<MIPS_BF16, false>(A, id_bits, s);
+}
+
+size_t mips_embedding_grad_workspace_size(int64_t t, int64_t rows, int32_t d) {
+  if (t < 0 || t > MIPS_TOKENS_MAX || rows < 1 || rows > mips::kMaxRows || d < 1 || d > MIPS_EMBEDDING_D_MAX)
+    return 0;
+  return t == 0 ? 256 : mips::grad_plan(t, rows, d).bytes;
+}
+
+int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t d,
+                        int64_t grad_stride, const void* ids, int32_t id_bits, int64_t rows,
+                        float scale, int32_t accumulate, void* out, int32_t out_dtype,
+                        int64_t out_stride, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  using namespace mips;
+  if (t < 0 || rows < 1 || d < 1 || grad_stride < d || out_stride < d) return MIPS_ERR_INVALID_ARG;
+  if (!dtype_ok(grad_dtype) || (out_dtype != grad_dtype && out_dtype != MIPS_F32) ||
+      (id_bits != 32 && id_bits != 64) || d > MIPS_EMBEDDING_D_MAX || t > MIPS_TOKENS_MAX ||
+      rows > kMaxRows)
+    return MIPS_ERR_UNSUPPORTED;
+  const int E = elem_bytes(grad_dtype), O = elem_bytes(out_dtype);
+  if (!out || !aligned(out, O)) return MIPS_ERR_INVALID_ARG;
+  if (t > 0 && (!grad || !ids || !aligned(grad, E) || !aligned(ids, id_bits / 8) || !workspace ||
+                !aligned(workspace, 256)))
+    return MIPS_ERR_INVALID_ARG;
+  hipStream_t s = (hipStream_t)stream;
+  GradPlan P{};
+  if (t > 0) {
+    P = grad_plan(t, rows, d);
+    if (workspace_bytes < P.bytes) return MIPS_ERR_WORKSPACE;
+  }
+  // workgroups that clear the output: 64 KiB each at least, at most 8 a compute unit
+  ZeroArgs Z{out, rows, out_stride * O, (int64_t)d * O, 0};
+  if (!accumulate) {
+    const int64_t want = (rows * d * O + 65535) / 65536;
+    Z.nblocks = (int)(want < 2048 ? want : 2048);
+  }
+  uint8_t* ws = (uint8_t*)workspace;
+  int src = 0;
+  if (t == 0) {  // nothing but the zeros
+    if (Z.nblocks > 0) {
+      RankArgs R{};
+      R.Z = Z;
+      hipLaunchKernelGGL(rank_sort_kernel<int32_t>, dim3(Z.nblocks), dim3(256), 0, s, R);
+      return check_launch();
+    }
+    return MIPS_OK;
+  }
+  if (P.passes == 0) {
+    RankArgs R{ids, t, rows, (uint32_t*)(ws + P.keys[0]), (uint32_t*)(ws + P.toks[0]),
+               (int)((t + kRankTokens - 1) / kRankTokens), Z};
+    const dim3 grid(R.nrank + Z.nblocks);
+    if (id_bits == 32) hipLaunchKernelGGL(rank_sort_kernel<int32_t>, grid, dim3(256), 0, s, R);
+    else hipLaunchKernelGGL(rank_sort_kernel<int64_t>, grid, dim3(256), 0, s, R);
+    if (const int rc = check_launch()) return rc;
+  } else {
+    for (int p = 0; p < P.passes; ++p) {
+      const int in = (p + 1) & 1, to = p & 1;  // pass 0 reads the ids and writes buffer 0
+      SortArgs S{p == 0 ? ids : nullptr, t, rows, P.per, P.nb, 8 * p,
+                 (const uint32_t*)(ws + P.keys[in]), (const uint32_t*)(ws + P.toks[in]),
+                 (uint32_t*)(ws + P.keys[to]), (uint32_t*)(ws + P.toks[to]),
+                 (uint32_t*)(ws + P.counts), Z};
+      if (p > 0) S.Z.nblocks = 0;
+      const dim3 gc(P.nb + S.Z.nblocks), gs(P.nb);
+      if (id_bits == 32) hipLaunchKernelGGL(sort_count_kernel<int32_t>, gc, dim3(kSortThreads), 0, s, S);
+      else hipLaunchKernelGGL(sort_count_kernel<int64_t>, gc, dim3(kSortThreads), 0, s, S);
+      if (const int rc = check_launch()) return rc;
+      if (id_bits == 32) hipLaunchKernelGGL(sort_scatter_kernel<int32_t>, gs, dim3(kSortThreads), 0, s, S);
+      else hipLaunchKernelGGL(sort_scatter_kernel<int64_t>, gs, dim3(kSortThreads), 0, s, S);
+      if (const int rc = check_launch()) return rc;
+      src = to;
+    }
+  }
+  SegArgs G{grad, grad_stride, (const uint32_t*)(ws + P.keys[src]), (const uint32_t*)(ws + P.toks[src]),
+            t, rows, d, 0, 0, 0, scale, accumulate, out, out_stride, (float*)(ws + P.part), 0};
+  const bool vec = aligned(grad, 16) && aligned(out, 16) && (grad_stride * E) % 16 == 0 &&
+                   (out_stride * O) % 16 == 0 && (d * E) % 16 == 0;
+  if (grad_dtype == MIPS_F32)
+    return vec ? launch_segments<MIPS_F32, MIPS_F32, true>(G, s) : launch_segments<MIPS_F32, MIPS_F32, false>(G, s);
+  if (out_dtype == MIPS_BF16)
+    return vec ? launch_segments<MIPS_BF16, MIPS_BF16, true>(G, s) : launch_segments<MIPS_BF16, MIPS_BF16, false>(G, s);
+  return vec ? launch_segments<MIPS_BF16, MIPS_F32, true>(G, s) : launch_segments<MIPS_BF16, MIPS_F32, false>(G, s);
+}
+
+}  // extern "C"

@@ -15,6 +15,7 @@
  * workspace sizes; mips_topk_noalloc (mips_topk with library-held scratch);
  * mips_merge_topk and mips_merge_interests (merges of sorted result lists);
  * mips_type_bitmap (per-type exclusion bitmaps); status strings and a timing hook.
+ * For training: mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm.
  *
  * Conventions shared by every entry point:
  *  - All buffers are caller-owned (except the static scratch array of
@@ -337,6 +338,76 @@ MIPS_API int mips_merge_topk(const float *in_scores, const int32_t *in_ids, cons
 MIPS_API int mips_merge_interests(const float *in_scores, const int32_t *in_ids, int32_t b, int32_t m,
                                   int32_t k_in, int32_t k_out, float *out_scores, int32_t *out_ids,
                                   void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Training: the steps around the search that make and use the vectors. The conventions
+ * above hold, with these of their own: matrices are row-major with a row stride in
+ * elements; NaN and infinities are allowed and propagate as in the formulas.
+ */
+
+/* Largest width of an embedding row, and most tokens of one mips_embedding_grad call. */
+#define MIPS_EMBEDDING_D_MAX 16384
+#define MIPS_TOKENS_MAX 1073741824
+
+/*
+ * mips_embedding_lookup -- out[i] = scale * table[ids[i]], computed in binary32 and rounded
+ * once to the table's type; a row of zeros for an id outside [0, rows) (padding).
+ *   table       device, [rows, d] of dtype MIPS_F32 or MIPS_BF16, row_stride >= d.
+ *   rows        >= 1.  d 1 .. MIPS_EMBEDDING_D_MAX.
+ *   ids         device, int32 or int64 [t] (id_bits 32 or 64); t >= 0 (0 enqueues nothing).
+ *   out         device, [t, d] contiguous, of dtype; may not overlap the table.
+ * Rows that are 16-byte multiples at 16-byte aligned addresses (table, out and row_stride)
+ * move in 16-byte units, others one element at a time.
+ * Errors: INVALID_ARG (NULL, t < 0, rows < 1, d < 1, row_stride < d, a pointer not aligned
+ * to its element), UNSUPPORTED (dtype, id_bits, d), HIP.
+ */
+MIPS_API int mips_embedding_lookup(const void *table, int32_t dtype, int64_t rows, int32_t d,
+                                   int64_t row_stride, const void *ids, int32_t id_bits, int64_t t,
+                                   float scale, void *out, void *stream);
+
+/*
+ * mips_embedding_grad -- the gradient of mips_embedding_lookup for the table:
+ * out[v] = scale * sum of grad[i] over the tokens i with ids[i] = v, zero rows for ids that
+ * no token has. The tokens are sorted by id (stably) and summed in binary32 in that order:
+ * the same call gives the same bits. Ids outside [0, rows) take no part.
+ *   grad        device, [t, d] of grad_dtype MIPS_F32 or MIPS_BF16, grad_stride >= d.
+ *   ids         device, int32 or int64 [t]; t 0 .. MIPS_TOKENS_MAX.
+ *   rows        1 .. 2^31 - 64.
+ *   accumulate  nonzero: the sums are added to out (rows without a token stay as they are);
+ *               zero: out is written whole.
+ *   out         device, [rows, d] of grad_dtype, or MIPS_F32 with bf16 gradients;
+ *               out_stride >= d; may not overlap grad.
+ *   workspace   device, 256-byte aligned, mips_embedding_grad_workspace_size bytes (0 is
+ *               returned for unsupported sizes). Calls that share one must be ordered.
+ * Errors: INVALID_ARG (NULL, sizes or strides below their minima, misaligned pointers),
+ * UNSUPPORTED (dtypes, id_bits, d, t or rows above the limits), WORKSPACE, HIP.
+ */
+MIPS_API size_t mips_embedding_grad_workspace_size(int64_t t, int64_t rows, int32_t d);
+MIPS_API int mips_embedding_grad(const void *grad, int32_t grad_dtype, int64_t t, int32_t d,
+                                 int64_t grad_stride, const void *ids, int32_t id_bits,
+                                 int64_t rows, float scale, int32_t accumulate, void *out,
+                                 int32_t out_dtype, int64_t out_stride, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * mips_clip_grad_norm -- the 2-norm over all elements of several tensors, and the tensors
+ * scaled by min(1, max_norm / (norm + 1e-6)). Squares are summed in binary64, the scaling is
+ * one binary32 product rounded to the tensor's type. A NaN among the elements makes the norm
+ * and every output NaN; an infinite one makes the factor 0.
+ *   tensors, outs, counts, dtypes   host arrays of ntensors >= 1 entries: device pointers,
+ *               element counts (0 .. 2^38) and MIPS_F32 or MIPS_BF16. outs[i] may equal
+ *               tensors[i] (scaled in place; not written when the factor is 1) and may not
+ *               otherwise overlap any tensor. 16-byte aligned pairs move in 16-byte units.
+ *   max_norm    >= 0; infinity only takes the norm (and copies).
+ *   out_norm    device float [1].
+ *   workspace   device, 256-byte aligned, mips_clip_workspace_size(ntensors) bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED (a dtype), WORKSPACE, HIP.
+ */
+MIPS_API size_t mips_clip_workspace_size(int32_t ntensors);
+MIPS_API int mips_clip_grad_norm(const void *const *tensors, void *const *outs,
+                                 const int64_t *counts, const int32_t *dtypes, int32_t ntensors,
+                                 float max_norm, float *out_norm, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 /*
  * mips_set_timing_events -- profiling hook (host, per calling thread). When both are
