@@ -31,6 +31,7 @@ EXPORTS = (
     "mips_merge_topk", "mips_merge_interests", "mips_type_bitmap", "mips_set_timing_events", "mips_status_string", "mips_last_hip_error",
     "mips_embedding_lookup", "mips_embedding_grad_workspace_size", "mips_embedding_grad",
     "mips_clip_workspace_size", "mips_clip_grad_norm",
+    "mips_logprobs_workspace_size", "mips_logprobs",
 )
 MERGE_MAX_LISTS = 64
 MAX_MASKS = 4  # result sets of one mips_topk_masks pass
@@ -96,7 +97,11 @@ def lib() -> C.CDLL:
         L.mips_clip_workspace_size.argtypes = [i32]
         L.mips_clip_workspace_size.restype = sz
         L.mips_clip_grad_norm.argtypes = [p, p, p, p, i32, f32, p, p, sz, p]
-        for f in (L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
+        L.mips_logprobs_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+        L.mips_logprobs_workspace_size.restype = sz
+        L.mips_logprobs.argtypes = [p, i64, i32, p, i32, i64, i64, i32, i32, p, p, i64, f32, p, i32, i32,
+                                    i32, p, p, p, p, p, p, sz, p]
+        for f in (L.mips_logprobs, L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
             f.restype = C.c_int
         for f in (L.mips_l2_normalize, L.mips_prepare_corpus, L.mips_topk, L.mips_topk_noalloc,
                   L.mips_topk_ranges,
@@ -481,4 +486,5 @@ def set_timing_events(before, after) -> None:
     lib().mips_set_timing_events(before, after)
 
 
-from .training import (clip_grad_norm, embedding_grad, embedding_lookup)  # noqa: E402
+from .training import (ALTERNATIVES_MAX, ItemLogprobs, clip_grad_norm, embedding_grad,  # noqa: E402
+                       embedding_lookup, item_logprobs)

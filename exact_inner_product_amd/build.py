@@ -19,13 +19,16 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmips.so")
 SOURCES = ["api.hip", "normalize.hip", "topk.hip", "merge.hip", "noalloc.hip",
-           "embedding.hip", "gradnorm.hip"]
+           "embedding.hip", "gradnorm.hip", "logprobs.hip"]
 
 # (dtype macro, width) pairs of the score pass; must match corpus_d_supported in host.h
 SCORE_UNITS = ([("MIPS_F32", d) for d in (16, 32, 64, 128)] +
                [("MIPS_BF16", d) for d in (16, 32, 64, 128, 256)] +
                [("MIPS_FP8_E4M3", d) for d in (64, 128, 256)] +
                [("MIPS_INT8", d) for d in (32, 64, 128, 256)])
+# (operand type, width) pairs of the softmax passes; must match width_of in logprobs.hip
+SOFTMAX_UNITS = ([("MIPS_F32", d) for d in (16, 32, 64, 128)] +
+                 [("MIPS_BF16", d) for d in (16, 32, 64, 128, 256)])
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -55,9 +58,10 @@ def build(verbose: bool = False) -> str:
     os.makedirs(OBJ_DIR)
     units = [(os.path.join(CSRC, s), [], os.path.join(OBJ_DIR, s.replace(".hip", ".o")))
              for s in SOURCES]
-    for ct, d in SCORE_UNITS:
-        obj = os.path.join(OBJ_DIR, f"score_{ct.split('_', 1)[1].lower()}_d{d}.o")
-        units.append((os.path.join(CSRC, "score_inst.hip"), [f"-DMIPS_CT={ct}", f"-DMIPS_D={d}"], obj))
+    for src, pairs in (("score", SCORE_UNITS), ("softmax", SOFTMAX_UNITS)):
+        for ct, d in pairs:
+            obj = os.path.join(OBJ_DIR, f"{src}_{ct.split('_', 1)[1].lower()}_d{d}.o")
+            units.append((os.path.join(CSRC, f"{src}_inst.hip"), [f"-DMIPS_CT={ct}", f"-DMIPS_D={d}"], obj))
 
     def compile_one(unit):
         src, defs, obj = unit

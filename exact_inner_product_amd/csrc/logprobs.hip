@@ -1,0 +1,474 @@
+// logprobs.hip -- log probabilities of given items under a softmax over an item table, with
+// the log-sum-exp, the entropy and the most likely alternatives (gfx950): the entry point and
+// the passes behind the statistics pass of softmax.h.
+//
+// Alternatives. The statistics pass leaves each tile's largest logit per query. The k best items
+// lie in the k best tiles, ordered by (largest logit descending, tile ascending): for an item
+// outside them, each of those k tiles holds an item with a larger logit, or with an equal one
+// and a lower id. The same holds for groups of tiles. So the finish pass picks the k best
+// groups, among their tiles the k best, scores those tiles' rows again with the same matrix
+// instructions (bitwise the same scores) and picks the k best rows: exact, with ties by the
+// lowest id, at the cost of k tiles of rows a query instead of a second pass over the table.
+#include "host.h"
+#include "select.h"
+#include "softmax_api.h"
+
+namespace mips {
+
+constexpr int kGroupThreads = 256;
+constexpr int64_t kTopDirect = 2048;   // tiles that the finish pass reads without groups
+constexpr int64_t kTopGroups = 16384;  // groups that it reads, at most
+constexpr size_t kBmaxBytes = size_t(1) << 30;  // tile maxima of one batch of queries, at most
+
+// The largest value of each group of `per` tiles, for 32 queries at a time: one thread per
+// (query column, group), reading 128-byte rows of the maxima.
+__global__ __launch_bounds__(kGroupThreads) void group_max_kernel(const float* __restrict__ bmax, int64_t ntiles,
+                                                                  int per, int64_t ngroups, int64_t gblocks,
+                                                                  float* __restrict__ gmax) {
+  const int64_t f = blockIdx.x / gblocks;
+  const int64_t g = (blockIdx.x % gblocks) * (kGroupThreads / kFrag) + (threadIdx.x >> 5);
+  if (g >= ngroups) return;
+  const int64_t t0 = g * per, t1 = min(ntiles, t0 + per);
+  const float* p = bmax + f * ntiles * kFrag + (threadIdx.x & 31);
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int64_t t = t0; t < t1; ++t) m = fmaxf(m, p[t * kFrag]);
+  gmax[(f * ngroups + g) * kFrag + (threadIdx.x & 31)] = m;
+}
+
+struct FinishArgs {
+  Table items, queries;
+  bool packed_f32;           // items hold dims 8c + 2t + h (a packed f32 corpus)
+  int b;
+  const float* bias;
+  const uint32_t* exclude;
+  int64_t exclude_words;
+  float scale;
+  int nslices;
+  const float4* part;
+  const void* ids;           // [b, g]
+  int id_bits, g, k;
+  const float *bmax, *gmax;  // gmax NULL: no groups
+  int64_t ntiles, ngroups;
+  int per, rm;
+  float *logprobs, *lse, *entropy, *alt_logprobs;
+  int32_t* alt_ids;
+};
+
+// One 16-byte slot of a row (chunk c, half h).
+template <bool ROWS>
+__device__ __forceinline__ u32x4_t item_slot(const Table& T, int64_t row, int c, int h) {
+  if constexpr (ROWS) {
+    const int off = 32 * c + 16 * h;
+    if (off >= T.row_b) return u32x4_t{0u, 0u, 0u, 0u};
+    return *(const u32x4_t*)(T.p + row * T.stride_b + off);
+  } else {
+    return *(const u32x4_t*)(T.p + (row >> 5) * (32 * (int64_t)T.row_b) + (int64_t)c * kChunkBytes +
+                             ((row & 31) + 32 * h) * 16);
+  }
+}
+
+// Scores of one query (in `q`, MFMA operands of every column) with 32 rows, lane (l, h)
+// giving row l: the accumulation of the statistics pass, chunk by chunk, so bitwise its
+// scores. Returns row (lane & 31)'s score in every lane.
+template <int CT, bool ROWS>
+__device__ __forceinline__ float score_row(const FinishArgs& A, const u32x4_t* q, int64_t row, float* scr) {
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int nch = (A.items.row_b + 31) / 32;
+  f32x16_t acc = {};
+  for (int c = 0; c < nch; ++c) {
+    const u32x4_t a = item_slot<ROWS>(A.items, row, c, h), b = q[2 * c + h];
+    if constexpr (CT == MIPS_BF16) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                    __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[t]), __uint_as_float(b[t]), acc, 0, 0, 0);
+    }
+  }
+  // every column holds the query's scores: lanes 0 and 32 give the rows of their half
+  if ((lane & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) scr[acc_row(i, lane)] = acc[i];
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  const float s = scr[lane & 31];
+  __builtin_amdgcn_wave_barrier();
+  return s;
+}
+
+__device__ __forceinline__ float logit(const FinishArgs& A, float s, int64_t row) {
+  const float l = __fmul_rn(s, A.scale);
+  return A.bias ? __fadd_rn(l, A.bias[row]) : l;
+}
+
+__device__ __forceinline__ bool excluded(const FinishArgs& A, int q, int64_t row) {
+  if (!A.exclude) return false;
+  return (A.exclude[(int64_t)q * A.exclude_words + (row >> 5)] >> (row & 31)) & 1u;
+}
+
+// One workgroup per query: joins the slices' statistics, scores the given ids, and picks the
+// alternatives.
+template <int CT, bool ROWS>
+__global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];  // keys of the rescored rows
+  __shared__ u32x4_t q[64];        // the query: slot 2c + h
+  __shared__ float4 red[4];
+  __shared__ float scr[4][kFrag];
+  __shared__ uint64_t best[MIPS_ALTERNATIVES_MAX];
+  __shared__ int64_t list[MIPS_ALTERNATIVES_MAX];
+  __shared__ SelScratch S;
+  __shared__ uint32_t nvalid;
+  const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
+
+  const int nch = (A.items.row_b + 31) / 32;
+  for (int i = t; i < 2 * nch; i += kSelThreads) {
+    const int c = i >> 1, h = i & 1;
+    const uint8_t* row = A.queries.p + (int64_t)b * A.queries.stride_b;
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (A.packed_f32) {
+      const uint32_t* r = (const uint32_t*)row + 8 * c + h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = r[2 * e];
+    } else if (32 * c + 16 * h < A.queries.row_b) {
+      v = *(const u32x4_t*)(row + 32 * c + 16 * h);
+    }
+    q[i] = v;
+  }
+
+  // statistics
+  float m = kMasked, z = 0.0f, x = 0.0f;
+  for (int s = t; s < A.nslices; s += kSelThreads) {
+    const float4 p = A.part[(int64_t)s * A.b + b];
+    if (p.x > kEmpty || p.y != p.y) {
+      const float mn = p.x > m ? p.x : m;
+      const float g0 = __builtin_amdgcn_exp2f(m - mn), g1 = __builtin_amdgcn_exp2f(p.x - mn);
+      x = (g0 > 0.0f ? g0 * (x + (m - mn) * z) : 0.0f) + g1 * (p.z + (p.x - mn) * p.y);
+      z = g0 * z + g1 * p.y;
+      m = mn;
+    }
+  }
+  auto join = [&](float m2, float z2, float x2) __attribute__((always_inline)) {
+    const float mn = m2 > m ? m2 : m;
+    const float g0 = __builtin_amdgcn_exp2f(m - mn), g1 = __builtin_amdgcn_exp2f(m2 - mn);
+    // an empty side has no sums; its reference is no number to multiply with
+    x = (m > kEmpty ? g0 * (x + (m - mn) * z) : 0.0f) + (m2 > kEmpty ? g1 * (x2 + (m2 - mn) * z2) : 0.0f);
+    z = (m > kEmpty ? g0 * z : z) + (m2 > kEmpty ? g1 * z2 : z2);
+    m = mn;
+  };
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const float m2 = __shfl_xor(m, o, kWave), z2 = __shfl_xor(z, o, kWave), x2 = __shfl_xor(x, o, kWave);
+    join(m2, z2, x2);
+  }
+  if (lane == 0) red[wave] = make_float4(m, z, x, 0.0f);
+  __syncthreads();
+  m = red[0].x, z = red[0].y, x = red[0].z;
+  for (int w = 1; w < 4; ++w) join(red[w].x, red[w].y, red[w].z);
+  const bool empty = m <= kEmpty && z == 0.0f;
+  const float lse = empty ? -INFINITY : m * kLn2 + logf(z);
+  if (t == 0) {
+    A.lse[b] = lse;
+    if (A.entropy) {
+      const float h = kLn2 * (log2f(z) - x / z);
+      A.entropy[b] = empty ? 0.0f : (h < 0.0f ? 0.0f : h);
+    }
+  }
+
+  // given ids, 32 a wave at a time
+  for (int g0 = wave * kFrag; g0 < A.g; g0 += 4 * kFrag) {
+    const int gi = g0 + (lane & 31);
+    const int64_t at = (int64_t)b * A.g + (gi < A.g ? gi : A.g - 1);
+    const int64_t id = A.id_bits == 32 ? (int64_t)((const int32_t*)A.ids)[at] : ((const int64_t*)A.ids)[at];
+    const bool pad = id < 0 || id >= A.items.n;
+    const int64_t row = pad ? 0 : id;
+    const float s = score_row<CT, ROWS>(A, q, row, scr[wave]);
+    if (lane < kFrag && gi < A.g)
+      A.logprobs[at] = pad ? 0.0f : (excluded(A, b, row) ? -INFINITY : logit(A, s, row) - lse);
+  }
+  if (A.k == 0) return;
+
+  // The r best of n keys, sorted, in best[]; keys of 0 are no candidates. Returns r.
+  auto pick = [&](auto get, int64_t n) __attribute__((always_inline)) {
+    __syncthreads();
+    if (t == 0) nvalid = 0u;
+    __syncthreads();
+    uint32_t mine = 0u;
+    for (int64_t i = t; i < n; i += kSelThreads) mine += get(i) != 0ull;
+    atomicAdd(&nvalid, mine);
+    __syncthreads();
+    const int r = (int)min<int64_t>(nvalid, A.k);
+    if (r > 0) {
+      Sel64 sel{1ull, ~0ull};  // all candidates
+      if ((int64_t)nvalid > r) sel = select_top(get, n, r, S);
+      if (t == 0) S.hist[0] = 0u;
+      __syncthreads();
+      for (int64_t i = t; i < n; i += kSelThreads) {
+        const uint64_t key = get(i);
+        if ((key & sel.mask) >= sel.prefix) {
+          const uint32_t slot = atomicAdd(&S.hist[0], 1u);
+          if (slot < (uint32_t)r) best[slot] = key;
+        }
+      }
+      __syncthreads();
+      bitonic_sort_desc_p<MIPS_ALTERNATIVES_MAX>(best, r);
+    }
+    return r;
+  };
+  auto tile_key = [&](float v, int64_t i) __attribute__((always_inline)) {
+    return v == -INFINITY ? 0ull : composite(score_key(v), (uint32_t)i);
+  };
+  const int64_t f = b / kFrag;
+  const int col = b % kFrag;
+  int r;
+  if (A.gmax) {
+    const float* gm = A.gmax + f * A.ngroups * kFrag + col;
+    r = pick([&](int64_t i) { return tile_key(gm[i * kFrag], i); }, A.ngroups);
+    if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.per;
+    __syncthreads();
+    const float* bm = A.bmax + f * A.ntiles * kFrag + col;
+    r = pick(
+        [&](int64_t i) {
+          const int64_t tile = list[i / A.per] + i % A.per;
+          return tile < A.ntiles ? tile_key(bm[tile * kFrag], tile) : 0ull;
+        },
+        (int64_t)r * A.per);
+  } else {
+    const float* bm = A.bmax + f * A.ntiles * kFrag + col;
+    r = pick([&](int64_t i) { return tile_key(bm[i * kFrag], i); }, A.ntiles);
+  }
+  if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.rm;  // first 32-row block of the tile
+  __syncthreads();
+  uint64_t* keys = (uint64_t*)dyn;
+  const int nb = r * A.rm;
+  for (int i = wave; i < nb; i += 4) {
+    const int64_t row = (list[i / A.rm] + i % A.rm) * kFrag + (lane & 31);
+    const bool live = row < A.items.n;
+    const int64_t rl = live ? row : A.items.n - 1;
+    const float s = score_row<CT, ROWS>(A, q, rl, scr[wave]);
+    if (lane < kFrag)
+      keys[i * kFrag + lane] =
+          live && !excluded(A, b, rl) ? composite(score_key(logit(A, s, rl)), (uint32_t)rl) : 0ull;
+  }
+  r = pick([&](int64_t i) { return keys[i]; }, (int64_t)nb * kFrag);
+  for (int i = t; i < A.k; i += kSelThreads) {
+    const int64_t at = (int64_t)b * A.k + i;
+    A.alt_ids[at] = i < r ? (int32_t)composite_id(best[i]) : -1;
+    A.alt_logprobs[at] = i < r ? key_score((uint32_t)(best[i] >> 32)) - lse : -INFINITY;
+  }
+}
+
+// ------------------------------------------------------------------------- the host side
+static int width_of(int dtype, int row_b) {  // the kernels' width for rows of row_b bytes
+  const int d = row_b / elem_bytes(dtype);
+  for (int w = 16; w <= (dtype == MIPS_F32 ? 128 : 256); w *= 2)
+    if (d <= w) return w;
+  return 0;
+}
+
+struct StatsPlan {
+  int width, nqf, nqblk, nslices, qbatch;
+  int64_t ntiles, ngroups;
+  int per;
+  size_t part, bmax, gmax, bytes;
+};
+
+// Query fragments a workgroup holds: the fewest that cover the batch, at most 8 (or what fits
+// the LDS): each item tile in registers is then used against as many queries as possible.
+static StatsPlan stats_plan(int b, int64_t n, int d, int dtype, int k) {
+  StatsPlan P{};
+  P.width = width_of(dtype, d * elem_bytes(dtype));
+  const int cap = stats_fits(dtype, P.width, 8) ? 8 : 4;
+  const int frag = (b + kFrag - 1) / kFrag;
+  P.nqf = 1;
+  while (P.nqf < cap && P.nqf < frag) P.nqf *= 2;
+  const int rm = stats_rm(dtype, P.width);
+  P.ntiles = (n + kFrag * rm - 1) / (kFrag * rm);
+  P.ngroups = 0;
+  P.per = 0;
+  P.qbatch = b;
+  if (k > 0) {
+    // queries of one batch: their tile maxima stay within kBmaxBytes
+    const int64_t q = (int64_t)(kBmaxBytes / (size_t)(P.ntiles * 4)) / kFrag * kFrag;
+    if (q < b) P.qbatch = (int)(q < kFrag ? kFrag : q);
+    if (P.ntiles > kTopDirect) {
+      P.per = 32;
+      while ((P.ntiles + P.per - 1) / P.per > kTopGroups) P.per *= 2;
+      P.ngroups = (P.ntiles + P.per - 1) / P.per;
+    }
+  }
+  P.nqblk = (P.qbatch + kFrag * P.nqf - 1) / (kFrag * P.nqf);
+  // one workgroup a compute unit, in slices of at least one tile a wave, a multiple of 8 (XCDs)
+  // where there are that many
+  int64_t s = device_cu_count() / P.nqblk;
+  const int64_t most = (P.ntiles + kStatsWaves - 1) / kStatsWaves;
+  if (s > most) s = most;
+  if (s >= 8) s = s / 8 * 8;
+  P.nslices = (int)(s < 1 ? 1 : s);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  const size_t q32 = (size_t)((P.qbatch + kFrag - 1) / kFrag) * kFrag;
+  P.part = take((size_t)P.nslices * P.qbatch * sizeof(float4));
+  if (k > 0) {
+    P.bmax = take(q32 * P.ntiles * 4);
+    if (P.ngroups) P.gmax = take(q32 * P.ngroups * 4);
+  }
+  P.bytes = at;
+  return P;
+}
+
+static int stats_dispatch(int dtype, int width, int nqf, bool rows, const StatsArgs& A, int grid, hipStream_t s) {
+  if (dtype == MIPS_F32) {
+    switch (width) {
+      case 16: return launch_stats<MIPS_F32, 16>(nqf, rows, A, grid, s);
+      case 32: return launch_stats<MIPS_F32, 32>(nqf, rows, A, grid, s);
+      case 64: return launch_stats<MIPS_F32, 64>(nqf, rows, A, grid, s);
+      case 128: return launch_stats<MIPS_F32, 128>(nqf, rows, A, grid, s);
+    }
+  } else {
+    switch (width) {
+      case 16: return launch_stats<MIPS_BF16, 16>(nqf, rows, A, grid, s);
+      case 32: return launch_stats<MIPS_BF16, 32>(nqf, rows, A, grid, s);
+      case 64: return launch_stats<MIPS_BF16, 64>(nqf, rows, A, grid, s);
+      case 128: return launch_stats<MIPS_BF16, 128>(nqf, rows, A, grid, s);
+      case 256: return launch_stats<MIPS_BF16, 256>(nqf, rows, A, grid, s);
+    }
+  }
+  return MIPS_ERR_UNSUPPORTED;
+}
+
+template <int CT, bool ROWS>
+static int launch_finish(const FinishArgs& A, int b, hipStream_t s) {
+  static const hipError_t attr =
+      hipFuncSetAttribute((const void*)finish_kernel<CT, ROWS>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                          MIPS_ALTERNATIVES_MAX * 2 * kFrag * 8);
+  (void)attr;
+  hipLaunchKernelGGL((finish_kernel<CT, ROWS>), dim3(b), dim3(kSelThreads), (size_t)A.k * A.rm * kFrag * 8, s, A);
+  return check_launch();
+}
+
+// Sizes that both entry points share; MIPS_OK or a status.
+static int check_sizes(int b, int64_t n, int d, int dtype, int layout) {
+  if (b < 1 || n < 1 || d < 1) return MIPS_ERR_INVALID_ARG;
+  if (dtype != MIPS_F32 && dtype != MIPS_BF16) return MIPS_ERR_UNSUPPORTED;
+  if (layout != MIPS_ROWS && layout != MIPS_PACKED) return MIPS_ERR_INVALID_ARG;
+  if (n > (int64_t(1) << 31) - 64 || b > MIPS_B_MAX) return MIPS_ERR_UNSUPPORTED;
+  const int row_b = d * elem_bytes(dtype);
+  if (width_of(dtype, row_b) == 0 || row_b % 16 != 0) return MIPS_ERR_UNSUPPORTED;
+  if (layout == MIPS_PACKED && !corpus_d_supported(dtype, d)) return MIPS_ERR_UNSUPPORTED;
+  return MIPS_OK;
+}
+
+// A row-major operand: 16-byte aligned rows at most 2^25 bytes apart.
+static bool rows_ok(const void* p, int64_t stride, int d, int dtype) {
+  const int64_t sb = stride * elem_bytes(dtype);
+  return aligned(p, 16) && stride >= d && sb % 16 == 0 && sb <= (int64_t(1) << 25);
+}
+
+}  // namespace mips
+
+extern "C" {
+
+size_t mips_logprobs_workspace_size(int32_t b, int64_t n, int32_t d, int32_t dtype, int32_t k) {
+  using namespace mips;
+  if (k < 0 || k > MIPS_ALTERNATIVES_MAX || check_sizes(b, n, d, dtype, MIPS_ROWS) != MIPS_OK) return 0;
+  return stats_plan(b, n, d, dtype, k).bytes;
+}
+
+int mips_logprobs(const void* queries, int64_t query_stride, int32_t b, const void* items,
+                  int32_t layout, int64_t item_stride, int64_t n, int32_t d, int32_t dtype,
+                  const float* bias, const uint32_t* exclude, int64_t exclude_row_words,
+                  float scale, const void* ids, int32_t id_bits, int32_t g, int32_t k,
+                  float* out_logprobs, float* out_lse, float* out_entropy, int32_t* out_alt_ids,
+                  float* out_alt_logprobs, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace mips;
+  if (const int rc = check_sizes(b, n, d, dtype, layout)) return rc;
+  if (g < 0 || k < 0 || !(scale >= MIPS_SCALE_MIN && scale <= MIPS_SCALE_MAX)) return MIPS_ERR_INVALID_ARG;
+  if (k > MIPS_ALTERNATIVES_MAX || (g > 0 && id_bits != 32 && id_bits != 64)) return MIPS_ERR_UNSUPPORTED;
+  const int64_t words = (n + 31) / 32;
+  if (!queries || !items || !out_lse || !workspace || (g > 0 && (!ids || !out_logprobs)) ||
+      (k > 0 && (!out_alt_ids || !out_alt_logprobs)))
+    return MIPS_ERR_INVALID_ARG;
+  if (!rows_ok(queries, query_stride, d, dtype) || !aligned(items, 16) ||
+      (layout == MIPS_ROWS && !rows_ok(items, item_stride, d, dtype)))
+    return MIPS_ERR_INVALID_ARG;
+  if (exclude_row_words < 0 || (exclude_row_words > 0 && (!exclude || exclude_row_words < words)))
+    return MIPS_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || (bias && !aligned(bias, 4)) || (exclude && !aligned(exclude, 4)) ||
+      !aligned(out_lse, 4) || (out_entropy && !aligned(out_entropy, 4)) ||
+      (g > 0 && (!aligned(ids, id_bits / 8) || !aligned(out_logprobs, 4))) ||
+      (k > 0 && (!aligned(out_alt_ids, 4) || !aligned(out_alt_logprobs, 4))))
+    return MIPS_ERR_INVALID_ARG;
+  const StatsPlan P = stats_plan(b, n, d, dtype, k);
+  if (workspace_bytes < P.bytes) return MIPS_ERR_WORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  uint8_t* ws = (uint8_t*)workspace;
+  const int E = elem_bytes(dtype), row_b = d * E;
+  const bool rows = layout == MIPS_ROWS;
+  for (int q0 = 0; q0 < b; q0 += P.qbatch) {
+    const int nb = b - q0 < P.qbatch ? b - q0 : P.qbatch;
+    StatsArgs A{};
+    A.items = Table{(const uint8_t*)items, rows ? item_stride * E : 0, n, row_b};
+    A.queries = Table{(const uint8_t*)queries + q0 * query_stride * E, query_stride * E, nb, row_b};
+    A.b = nb;
+    A.bias = bias;
+    A.exclude = exclude ? exclude + q0 * exclude_row_words : nullptr;
+    A.exclude_words = exclude_row_words;
+    A.scale = scale;
+    A.scx = bias ? kLog2e : scale * kLog2e;
+    A.vmask = kMasked / A.scx;
+    A.nqblk = (nb + kFrag * P.nqf - 1) / (kFrag * P.nqf);
+    A.nslices = P.nslices;
+    A.ntiles = P.ntiles;
+    A.part = (float4*)(ws + P.part);
+    A.bmax = k > 0 ? (float*)(ws + P.bmax) : nullptr;
+    if (const int rc = stats_dispatch(dtype, P.width, P.nqf, rows, A, A.nqblk * P.nslices, s)) return rc;
+    if (P.ngroups) {
+      const int64_t gblocks = (P.ngroups + 7) / 8;
+      const int64_t nf = (nb + kFrag - 1) / kFrag;
+      hipLaunchKernelGGL(group_max_kernel, dim3((unsigned)(gblocks * nf)), dim3(kGroupThreads), 0, s, A.bmax, P.ntiles,
+                         P.per, P.ngroups, gblocks, (float*)(ws + P.gmax));
+      if (const int rc = check_launch()) return rc;
+    }
+    FinishArgs F{};
+    F.items = A.items;
+    F.queries = A.queries;
+    F.packed_f32 = !rows && dtype == MIPS_F32;
+    F.b = nb;
+    F.bias = bias;
+    F.exclude = A.exclude;
+    F.exclude_words = exclude_row_words;
+    F.scale = scale;
+    F.nslices = P.nslices;
+    F.part = A.part;
+    F.ids = g > 0 ? (const uint8_t*)ids + (int64_t)q0 * g * (id_bits / 8) : nullptr;
+    F.id_bits = id_bits;
+    F.g = g;
+    F.k = k;
+    F.bmax = A.bmax;
+    F.gmax = P.ngroups ? (float*)(ws + P.gmax) : nullptr;
+    F.ntiles = P.ntiles;
+    F.ngroups = P.ngroups;
+    F.per = P.per;
+    F.rm = stats_rm(dtype, P.width);
+    F.logprobs = g > 0 ? out_logprobs + (int64_t)q0 * g : nullptr;
+    F.lse = out_lse + q0;
+    F.entropy = out_entropy ? out_entropy + q0 : nullptr;
+    F.alt_ids = k > 0 ? out_alt_ids + (int64_t)q0 * k : nullptr;
+    F.alt_logprobs = k > 0 ? out_alt_logprobs + (int64_t)q0 * k : nullptr;
+    int rc;
+    if (dtype == MIPS_F32) rc = rows ? launch_finish<MIPS_F32, true>(F, nb, s) : launch_finish<MIPS_F32, false>(F, nb, s);
+    else rc = rows ? launch_finish<MIPS_BF16, true>(F, nb, s) : launch_finish<MIPS_BF16, false>(F, nb, s);
+    if (rc) return rc;
+  }
+  return MIPS_OK;
+}
+
+}  // extern "C"

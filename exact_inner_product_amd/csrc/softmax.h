@@ -1,0 +1,320 @@
+// softmax.h -- the fused score and softmax-statistics pass for gfx950; included only by
+// softmax_inst.hip.
+#pragma once
+
+#include <utility>
+
+#include "host.h"
+#include "softmax_api.h"
+
+namespace mips {
+
+template <int N, typename F>
+__device__ __forceinline__ void unroll_for(F&& f) {
+  if constexpr (N > 0) {
+    unroll_for<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+}
+
+// One 16-byte chunk of both operands: a 32x32x16 bf16 product, or four 32x32x2 f32 ones.
+template <int CT>
+__device__ __forceinline__ void mfma_chunk(f32x16_t& acc, u32x4_t a, u32x4_t b) {
+  if constexpr (CT == MIPS_BF16) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                  __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[t]), __uint_as_float(b[t]), acc, 0, 0, 0);
+  }
+}
+
+// Sets the bits of the 16 rows that accumulator registers 0..15 of this lane hold: bit i is
+// row 8 (i >> 2) + 4 (lane >> 5) + (i & 3) of the block's word.
+__device__ __forceinline__ uint32_t lane_bits(uint32_t w, int lane) {
+  const uint32_t wl = w >> (4 * (lane >> 5));
+  return (wl & 0xFu) | ((wl >> 4) & 0xF0u) | ((wl >> 8) & 0xF00u) | ((wl >> 12) & 0xF000u);
+}
+
+// Per query: the running reference m, the sum of e_j = 2^(y_j - m) and the sum of
+// e_j (y_j - m), y = l * log2(e), over the items of a slice.
+//
+// One workgroup = 8 waves (two per SIMD) = one slice of the items x one block of 32 NQF
+// queries. The query block sits in LDS as MFMA operands; each wave streams its own tiles of RM
+// 32-row item blocks from memory into registers, NS - 1 stages ahead, and multiplies each tile
+// with every query fragment. An accumulator register holds one item's score for the lane's
+// own query column (lane & 31), so the statistics of a column are per lane, with no
+// exchange between lanes until the end of the slice. They live in LDS between tiles (three
+// values per fragment and lane), which lets the fragment loop stay a loop: kept in registers,
+// they would have to be unrolled over fragments, ring stages and both epilogues, far past
+// the instruction cache.
+//
+// What bounds it: with few queries the items' bytes; with many the epilogue. Per score it takes
+// half a maximum, a fused multiply-add for the exponent, one exp2 (a quarter-rate instruction),
+// an addition and a fused multiply-add: about 30 cycles a wave of 64 scores, against 16 for
+// the matrix products of a bf16 row of 128.
+template <int CT, int D, int NQF, bool ROWS>
+__global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void stats_kernel(
+    StatsArgs A) {
+  constexpr int E = elem_bytes(CT);
+  constexpr int NCH = chunks_per_block(CT, D);
+  constexpr int RM = stats_rm(CT, D);
+  constexpr int NS = stats_ns(CT, D);
+  constexpr int64_t BLK = block_bytes(CT, D);
+  constexpr int QB = kFrag * NQF;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // Workgroup -> (slice, query block): consecutive workgroups go to different XCDs, and the
+  // query blocks of one slice share an XCD (and its L2).
+  int slice, qblk;
+  {
+    const int w = blockIdx.x;
+    if (A.nslices % 8 == 0) {
+      const int xcd = w & 7, idx = w >> 3;
+      slice = (idx / A.nqblk) * 8 + xcd;
+      qblk = idx % A.nqblk;
+    } else {
+      slice = w / A.nqblk;
+      qblk = w % A.nqblk;
+    }
+  }
+  const int qbase = qblk * QB;
+  const int nq = min(QB, A.b - qbase);           // live columns
+  const int nfr = (nq + kFrag - 1) / kFrag;      // live fragments
+
+  // Query tile: slot s of chunk c of fragment f holds query 32f + (s & 31), bytes
+  // 32c + 16 (s >> 5) .. of its row; for a packed f32 corpus, dims 8c + 2t + (s >> 5).
+  {
+    u32x4_t* dst = (u32x4_t*)lds;
+    for (int i = threadIdx.x; i < nfr * NCH * 64; i += kStatsThreads) {
+      const int s = i & 63, c = (i >> 6) % NCH, f = (i >> 6) / NCH;
+      const int q = f * kFrag + (s & 31);
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (q < nq) {
+        const uint8_t* row = A.queries.p + (int64_t)(qbase + q) * A.queries.stride_b;
+        if constexpr (CT == MIPS_F32 && !ROWS) {
+          const uint32_t* r = (const uint32_t*)row + 8 * c + (s >> 5);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = r[2 * t];
+        } else {
+          const int off = 32 * c + 16 * (s >> 5);
+          if (off < A.queries.row_b) v = *(const u32x4_t*)(row + off);
+        }
+      }
+      dst[i] = v;
+    }
+  }
+  float* st = (float*)(lds + (size_t)QB * D * E) + (size_t)wave * NQF * 3 * kWave + lane;
+  for (int f = 0; f < NQF; ++f) {
+    st[(3 * f + 0) * kWave] = kMasked;
+    st[(3 * f + 1) * kWave] = 0.0f;
+    st[(3 * f + 2) * kWave] = 0.0f;
+  }
+  __syncthreads();
+
+  const int64_t t_begin = (int64_t)slice * A.ntiles / A.nslices;
+  const int64_t t_end = (int64_t)(slice + 1) * A.ntiles / A.nslices;
+  const int64_t nblocks = (A.items.n + kFrag - 1) / kFrag;
+
+  // A stage's loads are unconditional (blocks past the end read the last block again and are
+  // masked out), so that the compiler's wait counts stay exact. Lane r < RM also loads the
+  // exclusion word of block r.
+  auto load_stage = [&](u32x4_t (&a)[RM][NCH], uint32_t& xraw, int64_t tile) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < RM; ++r) {
+      const int64_t fr = min<int64_t>(tile * RM + r, nblocks - 1);
+      if constexpr (ROWS) {
+        const int64_t rows = min<int64_t>(kFrag, A.items.n - fr * kFrag);
+        const __amdgpu_buffer_rsrc_t rs =
+            rows_rsrc(A.items.p + fr * kFrag * A.items.stride_b, (int)((rows - 1) * A.items.stride_b) + A.items.row_b);
+        const int base = (lane & 31) * (int)A.items.stride_b + 16 * (lane >> 5);
+        const int left = A.items.row_b - 16 * (lane >> 5);  // chunks at or past the row's end read zeros
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          a[r][c] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 32 * c < left ? base + 32 * c : 0x7FFFFFF0, 0, 0));
+      } else {
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(A.items.p + fr * BLK, (int)BLK);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          a[r][c] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, c * kChunkBytes, 0));
+      }
+    }
+    const int64_t fr = min<int64_t>(tile * RM + (lane < RM ? lane : RM - 1), nblocks - 1);
+    const uint32_t* wp = (A.exclude && A.exclude_words == 0) ? A.exclude + fr : (const uint32_t*)A.items.p;
+    xraw = *wp;
+  };
+
+  auto compute_stage = [&](const u32x4_t (&a)[RM][NCH], uint32_t xraw, int64_t tile) __attribute__((always_inline)) {
+    // words of the tile's blocks, rows past n set; uniform
+    uint32_t word[RM], any = 0u;
+#pragma unroll
+    for (int r = 0; r < RM; ++r) {
+      const int64_t left = A.items.n - (tile * RM + r) * kFrag;
+      uint32_t w = (A.exclude && A.exclude_words == 0) ? (uint32_t)__builtin_amdgcn_readlane((int)xraw, r) : 0u;
+      if (left < kFrag) w |= left <= 0 ? ~0u : ~0u << left;
+      word[r] = w;
+      any |= w;
+    }
+    const bool plain = any == 0u && A.bias == nullptr && A.exclude_words == 0;  // uniform
+    for (int f = 0; f < nfr; ++f) {
+      uint32_t wq[RM];
+      if (A.exclude_words != 0) {  // this column's own words
+        const int q = min(qbase + f * kFrag + (lane & 31), A.b - 1);
+#pragma unroll
+        for (int r = 0; r < RM; ++r)
+          wq[r] = A.exclude[(int64_t)q * A.exclude_words + min<int64_t>(tile * RM + r, nblocks - 1)];
+      }
+      f32x16_t acc[RM];
+#pragma unroll
+      for (int r = 0; r < RM; ++r) acc[r] = f32x16_t{};
+      const u32x4_t* bsrc = (const u32x4_t*)(lds + (size_t)f * BLK) + lane;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const u32x4_t b = bsrc[c * 64];
+#pragma unroll
+        for (int r = 0; r < RM; ++r) mfma_chunk<CT>(acc[r], a[r][c], b);
+      }
+      float m = st[(3 * f + 0) * kWave], z = st[(3 * f + 1) * kWave], x = st[(3 * f + 2) * kWave];
+      if (!plain) {
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+          const uint32_t bits = lane_bits(word[r] | (A.exclude_words != 0 ? wq[r] : 0u), lane);
+          if (A.bias) {
+            // rows 8q + 4 (lane >> 5) + (0..3) for q = 0..3 (rows past n read 0 and are masked)
+            const int64_t blk = min<int64_t>(tile * RM + r, nblocks - 1);
+            const __amdgpu_buffer_rsrc_t rs =
+                rows_rsrc(A.bias + blk * kFrag, (int)min<int64_t>(kFrag, A.items.n - blk * kFrag) * 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const u32x4_t v = __builtin_bit_cast(
+                  u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (lane >> 5) * 16 + q * 32, 0, 0));
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[r][4 * q + e] = __fadd_rn(__fmul_rn(acc[r][4 * q + e], A.scale), __uint_as_float(v[e]));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[r][i] = ((bits >> i) & 1u) ? A.vmask : acc[r][i];
+        }
+      }
+      float vm = acc[0][0];
+#pragma unroll
+      for (int r = 0; r < RM; ++r)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) vm = fmaxf(vm, acc[r][i]);
+      if (A.bmax) {
+        const float v2 = fmaxf(vm, __shfl_xor(vm, 32, kWave));
+        const float l = v2 * A.scx <= kEmpty ? -INFINITY : (A.bias ? v2 : v2 * A.scale);
+        if (lane < kFrag) A.bmax[((int64_t)(qbase / kFrag + f) * A.ntiles + tile) * kFrag + lane] = l;
+      }
+      const float mn = vm * A.scx;
+      if (__ballot(mn > m + kSlack) != 0ull) {
+        if (mn > m) {
+          const float g = __builtin_amdgcn_exp2f(m - mn);
+          // (a sum over masked values alone is dropped here, whatever it holds)
+          x = g > 0.0f ? g * (x - (mn - m) * z) : 0.0f;
+          z = g > 0.0f ? g * z : 0.0f;
+          m = mn;
+        }
+      }
+      float z0 = 0.0f, z1 = 0.0f, x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+      for (int r = 0; r < RM; ++r) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float ta = fmaf(acc[r][i], A.scx, -m), tb = fmaf(acc[r][i + 1], A.scx, -m);
+          const float ea = __builtin_amdgcn_exp2f(ta), eb = __builtin_amdgcn_exp2f(tb);
+          z0 += ea;
+          z1 += eb;
+          x0 = fmaf(ea, ta, x0);
+          x1 = fmaf(eb, tb, x1);
+        }
+      }
+      st[(3 * f + 0) * kWave] = m;
+      st[(3 * f + 1) * kWave] = z + (z0 + z1);
+      st[(3 * f + 2) * kWave] = x + (x0 + x1);
+    }
+  };
+
+  u32x4_t a[NS][RM][NCH];
+  uint32_t xw[NS];
+  int64_t t = t_begin + wave;
+  if (t < t_end) {
+    unroll_for<NS - 1>([&](auto uc) __attribute__((always_inline)) {
+      constexpr int u = decltype(uc)::value;
+      load_stage(a[u], xw[u], t + u * kStatsWaves);
+    });
+    auto step = [&](auto uc) __attribute__((always_inline)) {
+      constexpr int u = decltype(uc)::value;
+      constexpr int ld = (u + NS - 1) % NS;
+      load_stage(a[ld], xw[ld], t + (u + NS - 1) * kStatsWaves);
+      compute_stage(a[u], xw[u], t + u * kStatsWaves);
+      return t + (u + 1) * kStatsWaves >= t_end;
+    };
+    if constexpr (NS == 3) {
+      while (!(step(std::integral_constant<int, 0>{}) || step(std::integral_constant<int, 1>{}) ||
+               step(std::integral_constant<int, 2>{})))
+        t += NS * kStatsWaves;
+    } else {
+      while (!(step(std::integral_constant<int, 0>{}) || step(std::integral_constant<int, 1>{})))
+        t += NS * kStatsWaves;
+    }
+  }
+  __syncthreads();
+
+  // The column's statistics over the 8 waves and the two halves of each.
+  const float* all = (const float*)(lds + (size_t)QB * D * E);
+  for (int q = threadIdx.x; q < nq; q += kStatsThreads) {
+    const int f = q / kFrag, l = q % kFrag;
+    auto at = [&](int w, int k) { return all[((w >> 1) * NQF * 3 + 3 * f + k) * kWave + l + 32 * (w & 1)]; };
+    float m = kMasked;
+    for (int w = 0; w < 2 * kStatsWaves; ++w) m = fmaxf(m, at(w, 0));
+    float z = 0.0f, x = 0.0f;
+    for (int w = 0; w < 2 * kStatsWaves; ++w) {
+      const float mw = at(w, 0), zw = at(w, 1), g = __builtin_amdgcn_exp2f(mw - m);
+      if (mw > kEmpty) {
+        z = fmaf(g, zw, z);
+        x = fmaf(g, at(w, 2) + (mw - m) * zw, x);
+      } else if (zw != zw) {
+        z = zw;  // only NaN was seen
+      }
+    }
+    A.part[(int64_t)slice * A.b + qbase + q] = make_float4(m, z, x, 0.0f);
+  }
+}
+
+template <int CT, int D, int NQF, bool ROWS>
+static int launch_stats_one(const StatsArgs& A, int grid, hipStream_t s) {
+  constexpr int lds = stats_lds(CT, D, NQF);
+  static const hipError_t attr = hipFuncSetAttribute((const void*)stats_kernel<CT, D, NQF, ROWS>,
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  (void)attr;
+  hipLaunchKernelGGL((stats_kernel<CT, D, NQF, ROWS>), dim3(grid), dim3(kStatsThreads), lds, s, A);
+  return check_launch();
+}
+
+template <int CT, int D>
+int launch_stats(int nqf, bool rows, const StatsArgs& A, int grid, hipStream_t s) {
+  switch (nqf) {
+    case 1: return rows ? launch_stats_one<CT, D, 1, true>(A, grid, s) : launch_stats_one<CT, D, 1, false>(A, grid, s);
+    case 2: return rows ? launch_stats_one<CT, D, 2, true>(A, grid, s) : launch_stats_one<CT, D, 2, false>(A, grid, s);
+    case 4: return rows ? launch_stats_one<CT, D, 4, true>(A, grid, s) : launch_stats_one<CT, D, 4, false>(A, grid, s);
+    case 8:
+      if constexpr (stats_fits(CT, D, 8))
+        return rows ? launch_stats_one<CT, D, 8, true>(A, grid, s) : launch_stats_one<CT, D, 8, false>(A, grid, s);
+      break;
+  }
+  return MIPS_ERR_UNSUPPORTED;
+}
+
+}  // namespace mips

@@ -1,0 +1,80 @@
+// softmax_api.h -- softmax over an item table: shared constants, operand loads and argument
+// blocks of its kernels, and the launchers that each per-(type, width) translation unit
+// instantiates.
+//
+// With s_bj = q_b . c_j accumulated in binary32, a logit is
+//   l_bj = fl(fl(s_bj * scale) + bias_j)          (no bias: fl(s_bj * scale))
+// and every kernel works with p_bj = exp(l_bj - lse_b), lse_b = log sum_j exp(l_bj) over the
+// eligible items j.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+
+namespace mips {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Masked logits are a large negative finite value (in log2 units), so that the running sums
+// need no special case: exp2 of it is 0 and 0 times it is 0. A maximum at or below kEmpty means
+// that no eligible item has been seen; what was summed until then is dropped.
+constexpr float kMasked = -1e30f;
+constexpr float kEmpty = -0.9e30f;
+
+// The exponents' reference is not the exact running maximum: it follows when a value exceeds it
+// by kSlack (log2 units), so that the rescaling branch is taken a few times per slice instead
+// of every few tiles. Sums of 2^31 terms of 2^16 stay far inside binary32.
+constexpr float kSlack = 16.0f;
+
+// An item table (or a batch of queries): rows of row_b bytes every stride_b bytes (ROWS; both
+// multiples of 16, 16-byte aligned), or the fragment-tiled layout of a packed corpus.
+struct Table {
+  const uint8_t* p;
+  int64_t stride_b;
+  int64_t n;
+  int row_b;
+};
+
+struct StatsArgs {
+  Table items, queries;
+  int b;
+  const float* bias;         // [n] or NULL
+  const uint32_t* exclude;   // bitmap or NULL
+  int64_t exclude_words;     // words per query; 0: one bitmap for the batch
+  float scale;
+  float scx;                 // log2 units per unit of a score (no bias) or of a logit
+  float vmask;               // a masked score or logit: kMasked / scx
+  int nqblk, nslices;
+  int64_t ntiles;
+  float4* part;              // [nslices][b]: reference, sum, sum of e * exponent
+  float* bmax;               // [ceil(b/32)][ntiles][32] largest logit of each tile, or NULL
+};
+
+// 32-row blocks per tile of the pass: 8 KiB of items a wave and stage, at most 2 (more
+// accumulators than that spill).
+__host__ __device__ constexpr int stats_rm(int ct, int d) {
+  const int r = 8192 / (int)block_bytes(ct, d);
+  return r < 1 ? 1 : (r > 2 ? 2 : r);
+}
+// Stages in the register ring (one in use, the others in flight).
+__host__ __device__ constexpr int stats_ns(int ct, int d) {
+  return stats_rm(ct, d) * block_bytes(ct, d) > 8192 ? 2 : 3;
+}
+constexpr int kStatsThreads = 512;
+constexpr int kStatsWaves = 8;
+// LDS of a workgroup of 32 * nqf queries: the query tile and three values per wave, query
+// fragment and lane.
+__host__ __device__ constexpr int stats_lds(int ct, int d, int nqf) {
+  return kFrag * nqf * d * elem_bytes(ct) + kStatsWaves * nqf * 3 * kWave * 4;
+}
+__host__ __device__ constexpr bool stats_fits(int ct, int d, int nqf) {
+  return stats_lds(ct, d, nqf) <= 160 * 1024;
+}
+
+template <int CT, int D>
+int launch_stats(int nqf, bool rows, const StatsArgs& A, int grid, hipStream_t s);
+
+}  // namespace mips

@@ -1,16 +1,18 @@
-"""Python binding of libmips' training operators: embedding lookup and its gradient, and
-gradient-norm clipping. Argument marshalling only, as in the package's other entry points: the
+"""Python binding of libmips' training and evaluation operators: log probabilities over an item
+table, embedding lookup and its gradient, and gradient-norm clipping. Argument marshalling only, as in the package's other entry points: the
 work is in the HIP kernels behind include/mips.h.
 """
 from __future__ import annotations
 
 import ctypes as C
+import dataclasses
 import math
-from typing import List, Optional, Sequence, Tuple
+from typing import List, Optional, Sequence, Tuple, Union
 
 import torch
 
-from . import BF16, F32, MipsError, _check, _ptr, _stream, empty_workspace, lib
+from . import (BF16, F32, Corpus, MipsError, _check, _ptr, _stream, check_version,
+               empty_workspace, lib)
 
 
 def _code(t: torch.Tensor, what: str) -> int:
@@ -49,6 +51,125 @@ def _rows_arg(x: torch.Tensor) -> torch.Tensor:
 
 def _row_stride(x: torch.Tensor) -> int:
     return max(int(x.stride(0)), int(x.shape[1])) if x.shape[0] > 1 else int(x.shape[1])
+
+
+# ---------------------------------------------------------------- log probabilities
+ALTERNATIVES_MAX = 64
+ROWS, PACKED = 0, 1
+
+
+@dataclasses.dataclass
+class ItemLogprobs:
+    """What item_logprobs returns; tensors that were not asked for are None."""
+    logprobs: Optional[torch.Tensor]      # float32 [b, g]
+    logsumexp: torch.Tensor               # float32 [b]
+    entropy: Optional[torch.Tensor]       # float32 [b]
+    alt_ids: Optional[torch.Tensor]       # int32 [b, k]
+    alt_logprobs: Optional[torch.Tensor]  # float32 [b, k]
+
+
+def _operand(x: torch.Tensor, d: int) -> torch.Tensor:
+    """x as [rows, d] with 16-byte aligned rows; d is x's width rounded up to 16 bytes. Rows that
+    are so already are used in place, others are copied once (padded with zeros)."""
+    e = x.element_size()
+    if x.shape[1] == d and x.data_ptr() % 16 == 0 and (x.stride(1) == 1 or d == 1):
+        if x.shape[0] == 1 or (x.stride(0) >= d and x.stride(0) * e % 16 == 0 and x.stride(0) * e <= 1 << 25):
+            return x
+    y = torch.zeros((x.shape[0], d), dtype=x.dtype, device=x.device)
+    y[:, :x.shape[1]] = x
+    return y
+
+
+def _exclude_words(exclude: Optional[torch.Tensor], n: int, b: int) -> Tuple[Optional[torch.Tensor], int]:
+    """(contiguous bitmap or None, words per query), as topk's exclude."""
+    if exclude is None:
+        return None, 0
+    words = (n + 31) // 32
+    if exclude.dtype not in (torch.int32, torch.uint32):
+        raise TypeError("exclude must be int32 or uint32")
+    if exclude.dim() == 1 and exclude.numel() >= words:
+        return exclude.contiguous(), 0
+    if exclude.dim() == 2 and exclude.shape[0] == b and exclude.shape[1] >= words:
+        return exclude.contiguous(), int(exclude.shape[1])
+    raise ValueError(f"exclude must be [>= {words}] or [{b}, >= {words}], got {tuple(exclude.shape)}")
+
+
+def _softmax_args(queries, items, ids, bias, exclude, model_version=None):
+    """Checked and laid out operands of the softmax entry points: (queries, items pointer,
+    layout, item stride, n, d, dtype code, ids, id bits, bias, exclude, exclude words)."""
+    if queries.dim() != 2 or queries.shape[0] < 1:
+        raise ValueError(f"queries must be [b >= 1, d], got {tuple(queries.shape)}")
+    b, width = queries.shape
+    if isinstance(items, Corpus):
+        check_version(items, model_version)
+        if items.dtype not in ("f32", "bf16"):
+            raise TypeError(f"log probabilities need an f32 or bf16 index, got {items.dtype}")
+        n, code, layout, stride, held = items.n, items.code, PACKED, 0, items.packed
+        if items.d != width:
+            raise ValueError(f"queries have width {width}, the index {items.d}")
+        _code(queries, "queries")
+        queries = queries.to(torch.float32 if code == F32 else torch.bfloat16)  # as topk rounds them
+        d = width
+    else:
+        if items.dim() != 2 or items.shape[0] < 1 or items.shape[1] != width:
+            raise ValueError(f"items must be [n >= 1, {width}], got {tuple(items.shape)}")
+        if items.dtype != queries.dtype:
+            raise TypeError(f"queries are {queries.dtype}, items {items.dtype}")
+        n, code, layout = items.shape[0], _code(items, "items"), ROWS
+        per = 16 // items.element_size()
+        d = (width + per - 1) // per * per
+        held = _operand(items, d)
+        stride = _row_stride(held)
+    _on_gpu(queries.device, items=held, ids=ids, bias=bias, exclude=exclude)
+    queries = _operand(queries, d)
+    bits = 32
+    if ids is not None:
+        if ids.dim() != 2 or ids.shape[0] != b:
+            raise ValueError(f"ids must be [{b}, g], got {tuple(ids.shape)}")
+        ids, bits = _ids_arg(ids)
+    if bias is not None:
+        if bias.dtype != torch.float32 or tuple(bias.shape) != (n,):
+            raise ValueError(f"bias must be float32 [{n}], got {bias.dtype} {tuple(bias.shape)}")
+        bias = bias.contiguous()
+    exclude, words = _exclude_words(exclude, n, b)
+    return queries, held, layout, stride, n, d, code, ids, bits, bias, exclude, words
+
+
+def item_logprobs(queries: torch.Tensor, items: Union[torch.Tensor, Corpus], ids: Optional[torch.Tensor] = None, *,
+                  scale: float = 1.0, bias: Optional[torch.Tensor] = None,
+                  exclude: Optional[torch.Tensor] = None, entropy: bool = True, alternatives: int = 0,
+                  workspace: Optional[torch.Tensor] = None, model_version: Optional[str] = None) -> ItemLogprobs:
+    """Log probabilities under the softmax of scale * queries @ items.T + bias over all items,
+    without the score matrix: of the given ids, with the log-sum-exp, the entropy and the
+    `alternatives` most likely items (ties by the lowest id).
+
+    queries: float32 or bfloat16 [b, d]; items: [n, d] of the same type (any strides; rows that
+    are not 16-byte aligned are copied first), d up to 128 (float32) or 256 (bfloat16), or an
+    f32 or bf16 Corpus. ids: int32/int64 [b, g]; an id outside [0, n) is padding (0).
+    scale: 1 / temperature, positive. bias: float32 [n], e.g. -log q of a sampled softmax.
+    exclude: bitmap as topk's; excluded items have probability 0.
+    """
+    q, held, layout, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(
+        queries, items, ids, bias, exclude, model_version)
+    b, dev = q.shape[0], q.device
+    g = 0 if ids is None else ids.shape[1]
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = ItemLogprobs(
+        logprobs=None if ids is None else torch.empty((b, g), **f32), logsumexp=torch.empty((b,), **f32),
+        entropy=torch.empty((b,), **f32) if entropy else None,
+        alt_ids=torch.empty((b, alternatives), dtype=torch.int32, device=dev) if alternatives > 0 else None,
+        alt_logprobs=torch.empty((b, alternatives), **f32) if alternatives > 0 else None)
+    if workspace is None:
+        nbytes = lib().mips_logprobs_workspace_size(b, n, d, code, alternatives)
+        if nbytes == 0:
+            raise MipsError(2, "mips_logprobs_workspace_size")
+        workspace = empty_workspace(nbytes, dev)
+    _check(lib().mips_logprobs(_ptr(q), _row_stride(q), b, _ptr(held), layout, stride, n, d, code, _ptr(bias),
+                               _ptr(exclude), words, float(scale), _ptr(ids), bits, g, alternatives,
+                               _ptr(out.logprobs), _ptr(out.logsumexp), _ptr(out.entropy), _ptr(out.alt_ids),
+                               _ptr(out.alt_logprobs), _ptr(workspace), workspace.numel(), _stream(dev)),
+           "mips_logprobs")
+    return out
 
 
 # ------------------------------------------------------------------------ embedding

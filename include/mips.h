@@ -15,7 +15,7 @@
  * workspace sizes; mips_topk_noalloc (mips_topk with library-held scratch);
  * mips_merge_topk and mips_merge_interests (merges of sorted result lists);
  * mips_type_bitmap (per-type exclusion bitmaps); status strings and a timing hook.
- * For training: mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm.
+ * For training and evaluation: mips_logprobs; mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm.
  *
  * Conventions shared by every entry point:
  *  - All buffers are caller-owned (except the static scratch array of
@@ -408,6 +408,60 @@ MIPS_API int mips_clip_grad_norm(const void *const *tensors, void *const *outs,
                                  const int64_t *counts, const int32_t *dtypes, int32_t ntensors,
                                  float max_norm, float *out_norm, void *workspace,
                                  size_t workspace_bytes, void *stream);
+
+/*
+ * mips_logprobs -- log probabilities under the softmax of a batch of queries over an item
+ * table: with s_bj = queries[b] . items[j] accumulated in binary32,
+ *   l_bj = fl(fl(s_bj * scale) + bias[j])    (fl(s_bj * scale) without a bias),
+ *   lse_b = log sum over the eligible items j of exp(l_bj),
+ *   out_logprobs[b][i] = l_bj - lse_b for j = ids[b][i],
+ *   out_entropy[b] = - sum_j p_bj log p_bj,  p_bj = exp(l_bj - lse_b),
+ *   alternatives: the k eligible items of the largest l_bj, ties by the lowest id.
+ * The scores are never written to memory. scale is 1 / temperature; the bias is, for
+ * instance, - log q of a sampled softmax ("Two-Tower Retrieval at Industrial Scale", the logQ
+ * correction).
+ *   queries      device, [b, d] row-major of dtype, query_stride elements apart.
+ *   b            1 .. MIPS_B_MAX.
+ *   items        device; layout MIPS_ROWS: [n, d] row-major of dtype, item_stride elements
+ *                apart; MIPS_PACKED: packed by mips_prepare_corpus (dtype, n, d; item_stride
+ *                is not used).
+ *   n            1 .. 2^31 - 64.
+ *   d            a multiple of 16 bytes, up to 128 (MIPS_F32) or 256 (MIPS_BF16); for
+ *                MIPS_PACKED as mips_prepare_corpus. Rows are 16-byte aligned (base and
+ *                stride) and at most 2^25 bytes apart.
+ *   dtype        MIPS_F32 or MIPS_BF16, of queries and items.
+ *   bias         device float [n] or NULL.
+ *   exclude, exclude_row_words   as mips_topk: ids whose bit is set have probability 0,
+ *                whatever their rows hold (NaN and infinities included).
+ *   scale        MIPS_SCALE_MIN .. MIPS_SCALE_MAX.
+ *   ids          device, int32 or int64 (id_bits) [b, g], g >= 0. An id outside [0, n) is
+ *                padding: log probability 0. An excluded one has -INFINITY.
+ *   k            0 .. MIPS_ALTERNATIVES_MAX.
+ *   out_logprobs device float [b, g]; out_lse device float [b]; out_entropy device float [b]
+ *                or NULL; out_alt_ids device int32 [b, k] and out_alt_logprobs device float
+ *                [b, k]: largest first, missing ones (-1, -INFINITY).
+ *                A query without an eligible item has lse -INFINITY and entropy 0.
+ *   workspace    device, 256-byte aligned, mips_logprobs_workspace_size bytes (it depends on
+ *                the device's compute units; 0 for unsupported sizes). Calls that share one
+ *                must be ordered.
+ * Errors: INVALID_ARG (NULL, sizes, scale, strides, alignment, exclude_row_words as
+ * mips_topk), UNSUPPORTED (dtype, d, n, b or k above their limits, id_bits), WORKSPACE, HIP.
+ */
+#define MIPS_ROWS 0
+#define MIPS_PACKED 1
+#define MIPS_ALTERNATIVES_MAX 64
+#define MIPS_SCALE_MIN 1e-6f
+#define MIPS_SCALE_MAX 1e6f
+MIPS_API size_t mips_logprobs_workspace_size(int32_t b, int64_t n, int32_t d, int32_t dtype,
+                                             int32_t k);
+MIPS_API int mips_logprobs(const void *queries, int64_t query_stride, int32_t b, const void *items,
+                           int32_t layout, int64_t item_stride, int64_t n, int32_t d,
+                           int32_t dtype, const float *bias, const uint32_t *exclude,
+                           int64_t exclude_row_words, float scale, const void *ids,
+                           int32_t id_bits, int32_t g, int32_t k, float *out_logprobs,
+                           float *out_lse, float *out_entropy, int32_t *out_alt_ids,
+                           float *out_alt_logprobs, void *workspace, size_t workspace_bytes,
+                           void *stream);
 
 /*
  * mips_set_timing_events -- profiling hook (host, per calling thread). When both are
