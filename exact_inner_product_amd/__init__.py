@@ -32,6 +32,7 @@ EXPORTS = (
     "mips_embedding_lookup", "mips_embedding_grad_workspace_size", "mips_embedding_grad",
     "mips_clip_workspace_size", "mips_clip_grad_norm",
     "mips_logprobs_workspace_size", "mips_logprobs",
+    "mips_logprobs_backward_workspace_size", "mips_logprobs_backward",
 )
 MERGE_MAX_LISTS = 64
 MAX_MASKS = 4  # result sets of one mips_topk_masks pass
@@ -101,7 +102,11 @@ def lib() -> C.CDLL:
         L.mips_logprobs_workspace_size.restype = sz
         L.mips_logprobs.argtypes = [p, i64, i32, p, i32, i64, i64, i32, i32, p, p, i64, f32, p, i32, i32,
                                     i32, p, p, p, p, p, p, sz, p]
-        for f in (L.mips_logprobs, L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
+        L.mips_logprobs_backward_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+        L.mips_logprobs_backward_workspace_size.restype = sz
+        L.mips_logprobs_backward.argtypes = [p, i64, i32, p, i64, i64, i32, i32, p, p, i64, f32, p, i32, i32,
+                                             p, p, p, p, p, p, p, p, sz, p]
+        for f in (L.mips_logprobs, L.mips_logprobs_backward, L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
             f.restype = C.c_int
         for f in (L.mips_l2_normalize, L.mips_prepare_corpus, L.mips_topk, L.mips_topk_noalloc,
                   L.mips_topk_ranges,
@@ -486,5 +491,5 @@ def set_timing_events(before, after) -> None:
     lib().mips_set_timing_events(before, after)
 
 
-from .training import (ALTERNATIVES_MAX, ItemLogprobs, clip_grad_norm, embedding_grad,  # noqa: E402
-                       embedding_lookup, item_logprobs)
+from .training import (ALTERNATIVES_MAX, TARGETS_MAX, ItemLogprobs, clip_grad_norm, embedding_grad,  # noqa: E402
+                       embedding_lookup, item_logprobs, item_logprobs_backward)

@@ -78,3 +78,48 @@ template <int CT, int D>
 int launch_stats(int nqf, bool rows, const StatsArgs& A, int grid, hipStream_t s);
 
 }  // namespace mips
+
+// ---------------------------------------------------------------------- the backward pass
+namespace mips {
+
+// Per query: what the weights of its scores need (log2 units: lse * log2 e), and its targets.
+// Padded queries (up to a multiple of kGradTile) have lse2 = 1e30, so that p = 0.
+struct QueryTerms {
+  const float* lse2;
+  const float* coef;   // -(sum of the targets' gradients + gradient of the entropy * entropy)
+  const float* hent;   // -gradient of the entropy * ln 2
+  const int32_t* tgt;  // [b][g]; -1: no target
+  const float* gval;   // [b][g]
+  int g;
+};
+
+struct GradArgs {
+  Table own, str;            // the rows whose gradient is computed, and the rows summed over
+  QueryTerms q;
+  const float* bias;
+  const uint32_t* exclude;
+  int64_t exclude_words;
+  float scale, scx;
+  int use_hent;
+  int nown, nsplit;          // own tiles and splits of the streamed rows
+  int64_t ntiles;            // tiles of streamed rows
+  void* out;                 // [own.n, d] of the operands' type; nsplit == 1
+  float* part;               // [nsplit][own.n][d], otherwise
+  float* bias_part;          // items' pass: [nsplit][own.n] gradient of the bias, or NULL
+};
+
+constexpr int kGradTile = 64;  // streamed rows per tile
+
+__host__ __device__ constexpr int grad_waves(int ct, int d) { return d * elem_bytes(ct) > 256 ? 4 : 8; }
+__host__ __device__ constexpr int grad_own(int ct, int d) { return 32 * grad_waves(ct, d); }
+// LDS of a workgroup: two tiles of streamed rows (at least 128 bytes a row) and, for each, four
+// values a row and the rows' g targets (items' pass) or bias (queries' pass).
+__host__ __device__ constexpr int grad_row_bytes(int ct, int d) { return d * elem_bytes(ct) < 128 ? 128 : d * elem_bytes(ct); }
+__host__ __device__ constexpr int grad_lds(int ct, int d, int g) {
+  return 2 * kGradTile * (grad_row_bytes(ct, d) + 16 + 4 * g);
+}
+
+template <int CT, int D>
+int launch_grad(bool items, bool extra, const GradArgs& A, hipStream_t s);
+
+}  // namespace mips

@@ -55,6 +55,7 @@ def _row_stride(x: torch.Tensor) -> int:
 
 # ---------------------------------------------------------------- log probabilities
 ALTERNATIVES_MAX = 64
+TARGETS_MAX = 64  # given ids a query, of item_logprobs_backward
 ROWS, PACKED = 0, 1
 
 
@@ -170,6 +171,57 @@ def item_logprobs(queries: torch.Tensor, items: Union[torch.Tensor, Corpus], ids
                                _ptr(out.alt_logprobs), _ptr(workspace), workspace.numel(), _stream(dev)),
            "mips_logprobs")
     return out
+
+
+def item_logprobs_backward(grad_logprobs: Optional[torch.Tensor], queries: torch.Tensor, items: torch.Tensor,
+                           ids: Optional[torch.Tensor], forward: ItemLogprobs, *, scale: float = 1.0,
+                           bias: Optional[torch.Tensor] = None, exclude: Optional[torch.Tensor] = None,
+                           grad_entropy: Optional[torch.Tensor] = None, need_queries: bool = True,
+                           need_items: bool = True, need_bias: bool = False,
+                           workspace: Optional[torch.Tensor] = None
+                           ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """The gradient of item_logprobs over a row table: (grad_queries [b, d], grad_items [n, d],
+    grad_bias float32 [n]), the first two of the operands' type; None where not needed.
+
+    grad_logprobs: float32 [b, g], the gradient of each log probability (a loss that is the
+    mean of -log p of one target has -1/b); grad_entropy: float32 [b] or None. `forward` is the
+    result of item_logprobs on the same arguments (its logsumexp, and its entropy with
+    grad_entropy). Up to TARGETS_MAX ids a query.
+    """
+    q, held, _, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(queries, items, ids, bias, exclude)
+    if isinstance(items, Corpus):
+        raise TypeError("the gradient needs a table of rows, not a packed index")
+    b, dev, width = q.shape[0], q.device, queries.shape[1]
+    g = 0 if ids is None else ids.shape[1]
+    lse, ent = forward.logsumexp, forward.entropy
+    if grad_entropy is not None and ent is None:
+        raise ValueError("grad_entropy needs the forward pass' entropy")
+    if (ids is None) != (grad_logprobs is None):
+        raise ValueError("grad_logprobs and ids go together")
+    for name, t, shape in (("grad_logprobs", grad_logprobs, (b, g)), ("grad_entropy", grad_entropy, (b,)),
+                           ("logsumexp", lse, (b,))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be float32 {list(shape)}, got {t.dtype} {tuple(t.shape)}")
+    _on_gpu(dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, logsumexp=lse)
+    grad_logprobs = None if grad_logprobs is None else grad_logprobs.contiguous()
+    grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
+    dq = torch.empty((b, d), dtype=q.dtype, device=dev) if need_queries else None
+    di = torch.empty((n, d), dtype=q.dtype, device=dev) if need_items else None
+    db = torch.empty((n,), dtype=torch.float32, device=dev) if need_bias else None
+    if workspace is None:
+        nbytes = lib().mips_logprobs_backward_workspace_size(b, n, d, code, g)
+        if nbytes == 0:
+            raise MipsError(2, "mips_logprobs_backward_workspace_size")
+        workspace = empty_workspace(nbytes, dev)
+    _check(lib().mips_logprobs_backward(_ptr(q), _row_stride(q), b, _ptr(held), stride, n, d, code, _ptr(bias),
+                                        _ptr(exclude), words, float(scale), _ptr(ids), bits, g, _ptr(lse),
+                                        _ptr(ent), _ptr(grad_logprobs), _ptr(grad_entropy), _ptr(dq), _ptr(di),
+                                        _ptr(db), _ptr(workspace), workspace.numel(), _stream(dev)),
+           "mips_logprobs_backward")
+    if d != width:  # rows were padded to 16 bytes
+        dq = None if dq is None else dq[:, :width].contiguous()
+        di = None if di is None else di[:, :width].contiguous()
+    return dq, di, db
 
 
 # ------------------------------------------------------------------------ embedding

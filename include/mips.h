@@ -15,7 +15,8 @@
  * workspace sizes; mips_topk_noalloc (mips_topk with library-held scratch);
  * mips_merge_topk and mips_merge_interests (merges of sorted result lists);
  * mips_type_bitmap (per-type exclusion bitmaps); status strings and a timing hook.
- * For training and evaluation: mips_logprobs; mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm.
+ * For training and evaluation: mips_logprobs and its gradient
+ * mips_logprobs_backward; mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm.
  *
  * Conventions shared by every entry point:
  *  - All buffers are caller-owned (except the static scratch array of
@@ -462,6 +463,42 @@ MIPS_API int mips_logprobs(const void *queries, int64_t query_stride, int32_t b,
                            float *out_lse, float *out_entropy, int32_t *out_alt_ids,
                            float *out_alt_logprobs, void *workspace, size_t workspace_bytes,
                            void *stream);
+
+/*
+ * mips_logprobs_backward -- the gradient of mips_logprobs (MIPS_ROWS) for queries, items and
+ * bias, given those of the log probabilities (G, [b, g]) and, optionally, of the entropies (H', [b]):
+ *   w_bj = sum_i G_bi [ids_bi = j] - p_bj (sum_i G_bi + H'_b (log p_bj + entropy_b)),
+ *   grad_queries[b] = scale sum_j w_bj items[j],  grad_items[j] = scale sum_b w_bj queries[b],
+ *   grad_bias[j] = sum_b w_bj,
+ * over the eligible items; padding and excluded targets have no gradient. The scores are computed
+ * again, once for each of the two sums, and never written. Sums are in binary32 in a fixed
+ * order (the same call gives the same bits); with MIPS_BF16 the weights w are rounded to bf16
+ * before they multiply the rows, and the gradients to bf16 at the end.
+ *   queries .. g   as the forward call's; g at most MIPS_TARGETS_MAX, n at most 2^30. An item that the shared
+ *               bitmap excludes may hold anything; with one bitmap per query, the rows must be
+ *               finite (a row may be excluded for some queries and not for others).
+ *   lse, entropy   device float [b], the forward call's (entropy only with grad_entropy).
+ *   grad_logprobs  device float [b, g]; grad_entropy device float [b] or NULL.
+ *   grad_queries   device, [b, d] contiguous of dtype, or NULL: not wanted; grad_items device,
+ *               [n, d] contiguous of dtype, or NULL; grad_bias device float [n] or NULL. One of
+ *               them at least. Gradients are written whole (not accumulated), 16-byte aligned.
+ *   workspace   device, 256-byte aligned, mips_logprobs_backward_workspace_size bytes (0 for
+ *               unsupported sizes). Calls that share one must be ordered.
+ * Errors: as mips_logprobs; INVALID_ARG without any output, or grad_entropy without entropy;
+ * UNSUPPORTED for g > MIPS_TARGETS_MAX or n > 2^30.
+ */
+#define MIPS_TARGETS_MAX 64
+MIPS_API size_t mips_logprobs_backward_workspace_size(int32_t b, int64_t n, int32_t d,
+                                                      int32_t dtype, int32_t g);
+MIPS_API int mips_logprobs_backward(const void *queries, int64_t query_stride, int32_t b,
+                                    const void *items, int64_t item_stride, int64_t n, int32_t d,
+                                    int32_t dtype, const float *bias, const uint32_t *exclude,
+                                    int64_t exclude_row_words, float scale, const void *ids,
+                                    int32_t id_bits, int32_t g, const float *lse,
+                                    const float *entropy, const float *grad_logprobs,
+                                    const float *grad_entropy, void *grad_queries,
+                                    void *grad_items, float *grad_bias, void *workspace,
+                                    size_t workspace_bytes, void *stream);
 
 /*
  * mips_set_timing_events -- profiling hook (host, per calling thread). When both are
