@@ -68,25 +68,40 @@ __device__ __forceinline__ u32x4_t item_slot(const Table& T, int64_t row, int c,
   }
 }
 
-// Scores of one query (in `q`, MFMA operands of every column) with 32 rows, lane (l, h)
-// giving row l: the accumulation of the statistics pass, chunk by chunk, so bitwise its
-// scores. Returns row (lane & 31)'s score in every lane.
+// acc += the products of chunks [c0, c0 + 8) of 32 item rows (lane (l, h): row l) and 32
+// query columns, `col(c)` giving the lane's query slot of chunk c: all item loads issued first.
+template <int CT, bool ROWS, typename Q>
+__device__ __forceinline__ void score_chunks(const Table& items, int64_t row, int c0, int nch, Q col, f32x16_t& acc) {
+  const int h = (threadIdx.x & 63) >> 5;
+  u32x4_t a[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    a[u] = c0 + u < nch ? item_slot<ROWS>(items, row, c0 + u, h) : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    if (c0 + u >= nch) break;
+    const u32x4_t b = col(c0 + u);
+    if constexpr (CT == MIPS_BF16) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[u]),
+                                                    __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[u][t]), __uint_as_float(b[t]), acc, 0, 0, 0);
+    }
+  }
+}
+
+// Scores of one query (slots in LDS, for every column) with 32 rows, lane (l, h) giving row l:
+// the accumulation of the statistics pass, chunk by chunk, so bitwise its scores. Returns row
+// (lane & 31)'s score in every lane.
 template <int CT, bool ROWS>
 __device__ __forceinline__ float score_row(const FinishArgs& A, const u32x4_t* q, int64_t row, float* scr) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int nch = (A.items.row_b + 31) / 32;
   f32x16_t acc = {};
-  for (int c = 0; c < nch; ++c) {
-    const u32x4_t a = item_slot<ROWS>(A.items, row, c, h), b = q[2 * c + h];
-    if constexpr (CT == MIPS_BF16) {
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                    __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[t]), __uint_as_float(b[t]), acc, 0, 0, 0);
-    }
-  }
+  for (int c0 = 0; c0 < nch; c0 += 8)
+    score_chunks<CT, ROWS>(A.items, row, c0, nch, [&](int c) { return q[2 * c + h]; }, acc);
   // every column holds the query's scores: lanes 0 and 32 give the rows of their half
   if ((lane & 31) == 0) {
 #pragma unroll
@@ -110,111 +125,180 @@ __device__ __forceinline__ bool excluded(const FinishArgs& A, int q, int64_t row
   return (A.exclude[(int64_t)q * A.exclude_words + (row >> 5)] >> (row & 31)) & 1u;
 }
 
-// One workgroup per query: joins the slices' statistics, scores the given ids, and picks the
-// alternatives.
+// Slot (chunk c, half h) of a query's row, in the order of the item rows' slots.
+__device__ __forceinline__ u32x4_t query_slot(const FinishArgs& A, int64_t b, int c, int h) {
+  const uint8_t* row = A.queries.p + b * A.queries.stride_b;
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (A.packed_f32) {
+    const uint32_t* r = (const uint32_t*)row + 8 * c + h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r[2 * e];
+  } else if (32 * c + 16 * h < A.queries.row_b) {
+    v = *(const u32x4_t*)(row + 32 * c + 16 * h);
+  }
+  return v;
+}
+
+// Statistics of a query over some items; join() adds those of others.
+struct Stats {
+  float m = kMasked, z = 0.0f, x = 0.0f;
+  __device__ __forceinline__ void join(float m2, float z2, float x2) {
+    const float mn = m2 > m ? m2 : m;
+    const float g0 = __builtin_amdgcn_exp2f(m - mn), g1 = __builtin_amdgcn_exp2f(m2 - mn);
+    // an empty side has no sums (or only NaN); its reference is no number to multiply with
+    x = (m > kEmpty ? g0 * (x + (m - mn) * z) : 0.0f) + (m2 > kEmpty ? g1 * (x2 + (m2 - mn) * z2) : 0.0f);
+    z = (m > kEmpty ? g0 * z : z) + (m2 > kEmpty ? g1 * z2 : z2);
+    m = mn;
+  }
+  __device__ __forceinline__ void join_lanes(int from, int to) {  // over lanes at distances from, 2 from .. to
+#pragma unroll
+    for (int o = from; o <= to; o <<= 1) {
+      const float m2 = __shfl_xor(m, o, kWave), z2 = __shfl_xor(z, o, kWave), x2 = __shfl_xor(x, o, kWave);
+      join(m2, z2, x2);
+    }
+  }
+  __device__ __forceinline__ bool empty() const { return m <= kEmpty && z == 0.0f; }
+  __device__ __forceinline__ float lse() const { return empty() ? -INFINITY : m * kLn2 + logf(z); }
+  __device__ __forceinline__ float entropy() const {
+    const float h = kLn2 * (log2f(z) - x / z);
+    return empty() ? 0.0f : (h < 0.0f ? 0.0f : h);
+  }
+};
+
+__device__ __forceinline__ void read_ids(const FinishArgs& A, int64_t at, bool& pad, int64_t& row) {
+  const int64_t id = A.id_bits == 32 ? (int64_t)((const int32_t*)A.ids)[at] : ((const int64_t*)A.ids)[at];
+  pad = id < 0 || id >= A.items.n;
+  row = pad ? 0 : id;
+}
+
+// Without alternatives: one workgroup per 32 queries. Eight threads a query join the slices'
+// statistics; then each wave scores 32 (query, id) pairs at a time, pair i's item as row i and
+// its query as column i of one matrix product, whose diagonal holds the scores.
+template <int CT, bool ROWS>
+__global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
+  __shared__ float s_lse[kFrag];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+  const int b0 = blockIdx.x * kFrag, nb = min(kFrag, A.b - b0);
+  {
+    const int q = t >> 3, sub = t & 7;
+    Stats S;
+    if (q < nb)
+#pragma unroll 4
+      for (int s = sub; s < A.nslices; s += 8) {
+        const float4 p = A.part[(int64_t)s * A.b + b0 + q];
+        S.join(p.x, p.y, p.z);
+      }
+    S.join_lanes(1, 4);
+    if (sub == 0 && q < nb) {
+      const float lse = S.lse();
+      A.lse[b0 + q] = lse;
+      s_lse[q] = lse;
+      if (A.entropy) A.entropy[b0 + q] = S.entropy();
+    }
+  }
+  __syncthreads();
+  const int nch = (A.items.row_b + 31) / 32;
+  for (int p0 = wave * kFrag; p0 < nb * A.g; p0 += 4 * kFrag) {
+    const int p = min(p0 + (lane & 31), nb * A.g - 1);  // this lane's pair
+    const int64_t at = (int64_t)b0 * A.g + p;
+    bool pad;
+    int64_t row;
+    read_ids(A, at, pad, row);
+    const int bl = p / A.g;
+    f32x16_t acc = {};
+    for (int c0 = 0; c0 < nch; c0 += 8)
+      score_chunks<CT, ROWS>(A.items, row, c0, nch, [&](int c) { return query_slot(A, b0 + bl, c, h); }, acc);
+    float s = 0.0f;  // the diagonal: held by the lane of the pair's column whose half has its row
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s = acc_row(i, lane) == (lane & 31) ? acc[i] : s;
+    if (((lane >> 2) & 1) == h && p0 + (lane & 31) < nb * A.g)
+      A.logprobs[at] = pad ? 0.0f : (excluded(A, b0 + bl, row) ? -INFINITY : logit(A, s, row) - s_lse[bl]);
+  }
+}
+
+// With alternatives: one workgroup per query joins the slices' statistics, scores the given ids
+// and picks the alternatives.
+constexpr int kPickCap = 256;  // candidates of a pick that are sorted at once
+
 template <int CT, bool ROWS>
 __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];  // keys of the rescored rows
   __shared__ u32x4_t q[64];        // the query: slot 2c + h
   __shared__ float4 red[4];
   __shared__ float scr[4][kFrag];
-  __shared__ uint64_t best[MIPS_ALTERNATIVES_MAX];
+  __shared__ uint64_t best[kPickCap];
   __shared__ int64_t list[MIPS_ALTERNATIVES_MAX];
   __shared__ SelScratch S;
-  __shared__ uint32_t nvalid;
+  __shared__ uint32_t cnt;
   const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
 
   const int nch = (A.items.row_b + 31) / 32;
-  for (int i = t; i < 2 * nch; i += kSelThreads) {
-    const int c = i >> 1, h = i & 1;
-    const uint8_t* row = A.queries.p + (int64_t)b * A.queries.stride_b;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (A.packed_f32) {
-      const uint32_t* r = (const uint32_t*)row + 8 * c + h;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = r[2 * e];
-    } else if (32 * c + 16 * h < A.queries.row_b) {
-      v = *(const u32x4_t*)(row + 32 * c + 16 * h);
-    }
-    q[i] = v;
-  }
-
-  // statistics
-  float m = kMasked, z = 0.0f, x = 0.0f;
+  for (int i = t; i < 2 * nch; i += kSelThreads) q[i] = query_slot(A, b, i >> 1, i & 1);
+  Stats st;
   for (int s = t; s < A.nslices; s += kSelThreads) {
     const float4 p = A.part[(int64_t)s * A.b + b];
-    if (p.x > kEmpty || p.y != p.y) {
-      const float mn = p.x > m ? p.x : m;
-      const float g0 = __builtin_amdgcn_exp2f(m - mn), g1 = __builtin_amdgcn_exp2f(p.x - mn);
-      x = (g0 > 0.0f ? g0 * (x + (m - mn) * z) : 0.0f) + g1 * (p.z + (p.x - mn) * p.y);
-      z = g0 * z + g1 * p.y;
-      m = mn;
-    }
+    st.join(p.x, p.y, p.z);
   }
-  auto join = [&](float m2, float z2, float x2) __attribute__((always_inline)) {
-    const float mn = m2 > m ? m2 : m;
-    const float g0 = __builtin_amdgcn_exp2f(m - mn), g1 = __builtin_amdgcn_exp2f(m2 - mn);
-    // an empty side has no sums; its reference is no number to multiply with
-    x = (m > kEmpty ? g0 * (x + (m - mn) * z) : 0.0f) + (m2 > kEmpty ? g1 * (x2 + (m2 - mn) * z2) : 0.0f);
-    z = (m > kEmpty ? g0 * z : z) + (m2 > kEmpty ? g1 * z2 : z2);
-    m = mn;
-  };
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const float m2 = __shfl_xor(m, o, kWave), z2 = __shfl_xor(z, o, kWave), x2 = __shfl_xor(x, o, kWave);
-    join(m2, z2, x2);
-  }
-  if (lane == 0) red[wave] = make_float4(m, z, x, 0.0f);
+  st.join_lanes(1, 32);
+  if (lane == 0) red[wave] = make_float4(st.m, st.z, st.x, 0.0f);
   __syncthreads();
-  m = red[0].x, z = red[0].y, x = red[0].z;
-  for (int w = 1; w < 4; ++w) join(red[w].x, red[w].y, red[w].z);
-  const bool empty = m <= kEmpty && z == 0.0f;
-  const float lse = empty ? -INFINITY : m * kLn2 + logf(z);
+  st.m = red[0].x, st.z = red[0].y, st.x = red[0].z;
+  for (int w = 1; w < 4; ++w) st.join(red[w].x, red[w].y, red[w].z);
+  const float lse = st.lse();
   if (t == 0) {
     A.lse[b] = lse;
-    if (A.entropy) {
-      const float h = kLn2 * (log2f(z) - x / z);
-      A.entropy[b] = empty ? 0.0f : (h < 0.0f ? 0.0f : h);
-    }
+    if (A.entropy) A.entropy[b] = st.entropy();
   }
 
-  // given ids, 32 a wave at a time
-  for (int g0 = wave * kFrag; g0 < A.g; g0 += 4 * kFrag) {
+  // given ids, 32 a wave at a time (the last wave first: the picks begin with the first)
+  for (int g0 = (3 - wave) * kFrag; g0 < A.g; g0 += 4 * kFrag) {
     const int gi = g0 + (lane & 31);
     const int64_t at = (int64_t)b * A.g + (gi < A.g ? gi : A.g - 1);
-    const int64_t id = A.id_bits == 32 ? (int64_t)((const int32_t*)A.ids)[at] : ((const int64_t*)A.ids)[at];
-    const bool pad = id < 0 || id >= A.items.n;
-    const int64_t row = pad ? 0 : id;
+    bool pad;
+    int64_t row;
+    read_ids(A, at, pad, row);
     const float s = score_row<CT, ROWS>(A, q, row, scr[wave]);
     if (lane < kFrag && gi < A.g)
       A.logprobs[at] = pad ? 0.0f : (excluded(A, b, row) ? -INFINITY : logit(A, s, row) - lse);
   }
-  if (A.k == 0) return;
 
-  // The r best of n keys, sorted, in best[]; keys of 0 are no candidates. Returns r.
+  // The min(k, candidates) best of n distinct keys, sorted, in best[]; keys of 0 are no
+  // candidates. Returns their number. Each thread takes the largest of its keys; the k-th
+  // largest of these 256 is a bound that k keys reach, and few others do when the best keys
+  // are spread over the threads. Those are sorted together. Where more than kPickCap reach it,
+  // the radix select finds the k best first.
   auto pick = [&](auto get, int64_t n) __attribute__((always_inline)) {
+    uint64_t mine = 0ull;
+#pragma unroll 8
+    for (int64_t i = t; i < n; i += kSelThreads) {
+      const uint64_t key = get(i);
+      mine = key > mine ? key : mine;
+    }
+    __syncthreads();  // (best[] of the pick before has been read)
+    best[t] = mine;
+    if (t == 0) cnt = 0u;
     __syncthreads();
-    if (t == 0) nvalid = 0u;
+    bitonic_sort_desc_p<kSelThreads>(best, kSelThreads);
+    uint64_t bound = best[A.k - 1];
+    bound = bound == 0ull ? 1ull : bound;
     __syncthreads();
-    uint32_t mine = 0u;
-    for (int64_t i = t; i < n; i += kSelThreads) mine += get(i) != 0ull;
-    atomicAdd(&nvalid, mine);
-    __syncthreads();
-    const int r = (int)min<int64_t>(nvalid, A.k);
-    if (r > 0) {
-      Sel64 sel{1ull, ~0ull};  // all candidates
-      if ((int64_t)nvalid > r) sel = select_top(get, n, r, S);
-      if (t == 0) S.hist[0] = 0u;
-      __syncthreads();
-      for (int64_t i = t; i < n; i += kSelThreads) {
-        const uint64_t key = get(i);
-        if ((key & sel.mask) >= sel.prefix) {
-          const uint32_t slot = atomicAdd(&S.hist[0], 1u);
-          if (slot < (uint32_t)r) best[slot] = key;
-        }
+#pragma unroll 8
+    for (int64_t i = t; i < n; i += kSelThreads) {
+      const uint64_t key = get(i);
+      if (key >= bound) {
+        const uint32_t slot = atomicAdd(&cnt, 1u);
+        if (slot < (uint32_t)kPickCap) best[slot] = key;
       }
-      __syncthreads();
-      bitonic_sort_desc_p<MIPS_ALTERNATIVES_MAX>(best, r);
+    }
+    __syncthreads();
+    const uint32_t found = cnt;
+    const int r = (int)min<uint32_t>(found, (uint32_t)A.k);
+    if (found > (uint32_t)kPickCap) {
+      const Sel64 sel = select_top(get, n, r, S);
+      gather_sort(get, n, r, sel, best, &cnt);
+    } else {
+      if (found <= 64u) bitonic_sort_desc_p<64>(best, (int)found);
+      else bitonic_sort_desc_p<kPickCap>(best, (int)found);
     }
     return r;
   };
@@ -253,6 +337,7 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
       keys[i * kFrag + lane] =
           live && !excluded(A, b, rl) ? composite(score_key(logit(A, s, rl)), (uint32_t)rl) : 0ull;
   }
+  __syncthreads();
   r = pick([&](int64_t i) { return keys[i]; }, (int64_t)nb * kFrag);
   for (int i = t; i < A.k; i += kSelThreads) {
     const int64_t at = (int64_t)b * A.k + i;
@@ -276,15 +361,14 @@ struct StatsPlan {
   size_t part, bmax, gmax, bytes;
 };
 
-// Query fragments a workgroup holds: the fewest that cover the batch, at most 8 (or what fits
-// the LDS): each item tile in registers is then used against as many queries as possible.
+// Query fragments a workgroup holds and slices of the items: the pair with the least estimated
+// time, rounds of workgroups (one a compute unit) times the time of one: its query tile, then
+// the tiles of a wave, each against every fragment, at no less than the time its bytes take at
+// the memory's rate. In microseconds, as measured at the widths 64 to 128: a fragment's fill
+// 0.3, a tile and fragment 0.45 (f32: twice the products' time), start and end 4.
 static StatsPlan stats_plan(int b, int64_t n, int d, int dtype, int k) {
   StatsPlan P{};
   P.width = width_of(dtype, d * elem_bytes(dtype));
-  const int cap = stats_fits(dtype, P.width, 8) ? 8 : 4;
-  const int frag = (b + kFrag - 1) / kFrag;
-  P.nqf = 1;
-  while (P.nqf < cap && P.nqf < frag) P.nqf *= 2;
   const int rm = stats_rm(dtype, P.width);
   P.ntiles = (n + kFrag * rm - 1) / (kFrag * rm);
   P.ngroups = 0;
@@ -295,19 +379,38 @@ static StatsPlan stats_plan(int b, int64_t n, int d, int dtype, int k) {
     const int64_t q = (int64_t)(kBmaxBytes / (size_t)(P.ntiles * 4)) / kFrag * kFrag;
     if (q < b) P.qbatch = (int)(q < kFrag ? kFrag : q);
     if (P.ntiles > kTopDirect) {
+      // groups of about sqrt(tiles / k): as many group maxima to read as tiles of k groups
       P.per = 32;
-      while ((P.ntiles + P.per - 1) / P.per > kTopGroups) P.per *= 2;
+      while ((int64_t)P.per * P.per * k < P.ntiles || (P.ntiles + P.per - 1) / P.per > kTopGroups) P.per *= 2;
       P.ngroups = (P.ntiles + P.per - 1) / P.per;
     }
   }
-  P.nqblk = (P.qbatch + kFrag * P.nqf - 1) / (kFrag * P.nqf);
-  // one workgroup a compute unit, in slices of at least one tile a wave, a multiple of 8 (XCDs)
-  // where there are that many
-  int64_t s = device_cu_count() / P.nqblk;
-  const int64_t most = (P.ntiles + kStatsWaves - 1) / kStatsWaves;
-  if (s > most) s = most;
-  if (s >= 8) s = s / 8 * 8;
-  P.nslices = (int)(s < 1 ? 1 : s);
+  const int cus = device_cu_count();
+  const double tile_us = dtype == MIPS_F32 ? 0.45 * rm * (0.5 + P.width / 32.0) : 0.45 * rm * (0.5 + P.width / 256.0);
+  const double tile_bytes = (double)rm * block_bytes(dtype, P.width);
+  double best = 1e30;
+  for (int nqf = 1; nqf <= 8; nqf *= 2) {
+    if (!stats_fits(dtype, P.width, nqf)) break;
+    const int nqblk = (P.qbatch + kFrag * nqf - 1) / (kFrag * nqf);
+    const int frags = nqblk == 1 ? (P.qbatch + kFrag - 1) / kFrag : nqf;
+    // slices of at least one tile a wave; a multiple of 8 (XCDs) where there are that many
+    int64_t s = cus / nqblk;
+    const int64_t most = (P.ntiles + kStatsWaves - 1) / kStatsWaves;
+    if (s > most) s = most;
+    if (s >= 8) s = s / 8 * 8;
+    if (s < 1) s = 1;
+    const int64_t per = (P.ntiles + s * kStatsWaves - 1) / (s * kStatsWaves);
+    const int64_t rounds = (nqblk * s + cus - 1) / cus;
+    const double mem = (double)kStatsWaves * tile_bytes / (5.0e6 / cus);  // us: a round of tiles of one unit
+    const double t = (double)rounds * (4.0 + 0.3 * frags + (double)per * (frags * tile_us > mem ? frags * tile_us : mem));
+    if (t < best) {
+      best = t;
+      P.nqf = nqf;
+      P.nqblk = nqblk;
+      P.nslices = (int)s;
+    }
+    if (nqblk == 1) break;
+  }
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t p = at;
@@ -350,7 +453,10 @@ static int launch_finish(const FinishArgs& A, int b, hipStream_t s) {
       hipFuncSetAttribute((const void*)finish_kernel<CT, ROWS>, hipFuncAttributeMaxDynamicSharedMemorySize,
                           MIPS_ALTERNATIVES_MAX * 2 * kFrag * 8);
   (void)attr;
-  hipLaunchKernelGGL((finish_kernel<CT, ROWS>), dim3(b), dim3(kSelThreads), (size_t)A.k * A.rm * kFrag * 8, s, A);
+  if (A.k == 0)
+    hipLaunchKernelGGL((pairs_kernel<CT, ROWS>), dim3((b + kFrag - 1) / kFrag), dim3(256), 0, s, A);
+  else
+    hipLaunchKernelGGL((finish_kernel<CT, ROWS>), dim3(b), dim3(kSelThreads), (size_t)A.k * A.rm * kFrag * 8, s, A);
   return check_launch();
 }
 
