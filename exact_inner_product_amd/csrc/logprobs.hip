@@ -68,15 +68,19 @@ __device__ __forceinline__ u32x4_t item_slot(const Table& T, int64_t row, int c,
   }
 }
 
-// acc += the products of chunks [c0, c0 + 8) of 32 item rows (lane (l, h): row l) and 32
-// query columns, `col(c)` giving the lane's query slot of chunk c: all item loads issued first.
-template <int CT, bool ROWS, typename Q>
-__device__ __forceinline__ void score_chunks(const Table& items, int64_t row, int c0, int nch, Q col, f32x16_t& acc) {
+// Chunks [c0, c0 + 8) of 32 item rows, lane (l, h) loading its half of row l.
+template <bool ROWS>
+__device__ __forceinline__ void load_chunks(const Table& items, int64_t row, int c0, int nch, u32x4_t (&a)[8]) {
   const int h = (threadIdx.x & 63) >> 5;
-  u32x4_t a[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u)
     a[u] = c0 + u < nch ? item_slot<ROWS>(items, row, c0 + u, h) : u32x4_t{0u, 0u, 0u, 0u};
+}
+
+// acc += the products of those chunks with 32 query columns, `col(c)` giving the lane's query
+// slot of chunk c.
+template <int CT, typename Q>
+__device__ __forceinline__ void score_chunks(const u32x4_t (&a)[8], int c0, int nch, Q col, f32x16_t& acc) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     if (c0 + u >= nch) break;
@@ -92,16 +96,20 @@ __device__ __forceinline__ void score_chunks(const Table& items, int64_t row, in
   }
 }
 
-// Scores of one query (slots in LDS, for every column) with 32 rows, lane (l, h) giving row l:
-// the accumulation of the statistics pass, chunk by chunk, so bitwise its scores. Returns row
-// (lane & 31)'s score in every lane.
+// Scores of one query (slots in LDS, for every column) with 32 rows, lane (l, h) giving row l
+// and its first 8 chunks: the accumulation of the statistics pass, chunk by chunk, so bitwise
+// its scores. Returns row (lane & 31)'s score in every lane.
 template <int CT, bool ROWS>
-__device__ __forceinline__ float score_row(const FinishArgs& A, const u32x4_t* q, int64_t row, float* scr) {
+__device__ __forceinline__ float score_row(const FinishArgs& A, const u32x4_t* q, int64_t row, float* scr,
+                                           u32x4_t (&a)[8]) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int nch = (A.items.row_b + 31) / 32;
   f32x16_t acc = {};
-  for (int c0 = 0; c0 < nch; c0 += 8)
-    score_chunks<CT, ROWS>(A.items, row, c0, nch, [&](int c) { return q[2 * c + h]; }, acc);
+  score_chunks<CT>(a, 0, nch, [&](int c) { return q[2 * c + h]; }, acc);
+  for (int c0 = 8; c0 < nch; c0 += 8) {
+    load_chunks<ROWS>(A.items, row, c0, nch, a);
+    score_chunks<CT>(a, c0, nch, [&](int c) { return q[2 * c + h]; }, acc);
+  }
   // every column holds the query's scores: lanes 0 and 32 give the rows of their half
   if ((lane & 31) == 0) {
 #pragma unroll
@@ -206,8 +214,11 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
     read_ids(A, at, pad, row);
     const int bl = p / A.g;
     f32x16_t acc = {};
-    for (int c0 = 0; c0 < nch; c0 += 8)
-      score_chunks<CT, ROWS>(A.items, row, c0, nch, [&](int c) { return query_slot(A, b0 + bl, c, h); }, acc);
+    for (int c0 = 0; c0 < nch; c0 += 8) {
+      u32x4_t a[8];
+      load_chunks<ROWS>(A.items, row, c0, nch, a);
+      score_chunks<CT>(a, c0, nch, [&](int c) { return query_slot(A, b0 + bl, c, h); }, acc);
+    }
     float s = 0.0f;  // the diagonal: held by the lane of the pair's column whose half has its row
 #pragma unroll
     for (int i = 0; i < 16; ++i) s = acc_row(i, lane) == (lane & 31) ? acc[i] : s;
@@ -218,7 +229,7 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
 
 // With alternatives: one workgroup per query joins the slices' statistics, scores the given ids
 // and picks the alternatives.
-constexpr int kPickCap = 256;  // candidates of a pick that are sorted at once
+constexpr int kPickCap = 256;  // candidates of a pick that are ranked by counting
 
 template <int CT, bool ROWS>
 __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
@@ -226,7 +237,9 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   __shared__ u32x4_t q[64];        // the query: slot 2c + h
   __shared__ float4 red[4];
   __shared__ float scr[4][kFrag];
-  __shared__ uint64_t best[kPickCap];
+  __shared__ uint64_t found[kPickCap];
+  __shared__ __attribute__((aligned(16))) uint32_t maxima[kSelThreads];
+  __shared__ uint64_t best[MIPS_ALTERNATIVES_MAX];
   __shared__ int64_t list[MIPS_ALTERNATIVES_MAX];
   __shared__ SelScratch S;
   __shared__ uint32_t cnt;
@@ -257,16 +270,19 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
     bool pad;
     int64_t row;
     read_ids(A, at, pad, row);
-    const float s = score_row<CT, ROWS>(A, q, row, scr[wave]);
+    u32x4_t a[8];
+    load_chunks<ROWS>(A.items, row, 0, nch, a);
+    const float s = score_row<CT, ROWS>(A, q, row, scr[wave], a);
     if (lane < kFrag && gi < A.g)
       A.logprobs[at] = pad ? 0.0f : (excluded(A, b, row) ? -INFINITY : logit(A, s, row) - lse);
   }
 
   // The min(k, candidates) best of n distinct keys, sorted, in best[]; keys of 0 are no
   // candidates. Returns their number. Each thread takes the largest of its keys; the k-th
-  // largest of these 256 is a bound that k keys reach, and few others do when the best keys
-  // are spread over the threads. Those are sorted together. Where more than kPickCap reach it,
-  // the radix select finds the k best first.
+  // largest score among these 256 is a bound that k keys reach, and few others do when the best
+  // keys are spread over the threads. Every wave finds it by itself, bit by bit, from all 256
+  // maxima (4 a lane). The keys that reach it are ranked by counting the larger ones. Where
+  // more than kPickCap reach it, the radix select finds the k best.
   auto pick = [&](auto get, int64_t n) __attribute__((always_inline)) {
     uint64_t mine = 0ull;
 #pragma unroll 8
@@ -274,32 +290,43 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
       const uint64_t key = get(i);
       mine = key > mine ? key : mine;
     }
-    __syncthreads();  // (best[] of the pick before has been read)
-    best[t] = mine;
+    maxima[t] = (uint32_t)(mine >> 32);
     if (t == 0) cnt = 0u;
     __syncthreads();
-    bitonic_sort_desc_p<kSelThreads>(best, kSelThreads);
-    uint64_t bound = best[A.k - 1];
-    bound = bound == 0ull ? 1ull : bound;
-    __syncthreads();
+    const uint4 m4 = *(const uint4*)(maxima + 4 * lane);
+    uint32_t bound = 0u;
+#pragma unroll
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t c = bound | (1u << bit);
+      const int above = __popcll(__ballot(m4.x >= c)) + __popcll(__ballot(m4.y >= c)) +
+                        __popcll(__ballot(m4.z >= c)) + __popcll(__ballot(m4.w >= c));
+      bound = above >= A.k ? c : bound;
+    }
+    const uint64_t least = bound == 0u ? 1ull : (uint64_t)bound << 32;
 #pragma unroll 8
     for (int64_t i = t; i < n; i += kSelThreads) {
       const uint64_t key = get(i);
-      if (key >= bound) {
+      if (key >= least) {
         const uint32_t slot = atomicAdd(&cnt, 1u);
-        if (slot < (uint32_t)kPickCap) best[slot] = key;
+        if (slot < (uint32_t)kPickCap) found[slot] = key;
       }
     }
     __syncthreads();
-    const uint32_t found = cnt;
-    const int r = (int)min<uint32_t>(found, (uint32_t)A.k);
-    if (found > (uint32_t)kPickCap) {
+    const int c = (int)cnt;
+    const int r = min(c, A.k);
+    if (c > kPickCap) {
       const Sel64 sel = select_top(get, n, r, S);
       gather_sort(get, n, r, sel, best, &cnt);
-    } else {
-      if (found <= 64u) bitonic_sort_desc_p<64>(best, (int)found);
-      else bitonic_sort_desc_p<kPickCap>(best, (int)found);
+      return r;
     }
+    if (t < c) {
+      const uint64_t key = found[t];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < c; ++j) rank += found[j] > key ? 1 : 0;
+      if (rank < r) best[rank] = key;
+    }
+    __syncthreads();
     return r;
   };
   auto tile_key = [&](float v, int64_t i) __attribute__((always_inline)) {
@@ -328,11 +355,24 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   __syncthreads();
   uint64_t* keys = (uint64_t*)dyn;
   const int nb = r * A.rm;
+  // each wave's next block is on its way while this one is scored
+  auto row_of = [&](int i) __attribute__((always_inline)) {
+    return (list[i / A.rm] + i % A.rm) * kFrag + (lane & 31);
+  };
+  u32x4_t ahead[8];
+  auto fetch = [&](int i) __attribute__((always_inline)) {
+    load_chunks<ROWS>(A.items, min<int64_t>(row_of(i), A.items.n - 1), 0, nch, ahead);
+  };
+  if (wave < nb) fetch(wave);
   for (int i = wave; i < nb; i += 4) {
-    const int64_t row = (list[i / A.rm] + i % A.rm) * kFrag + (lane & 31);
+    const int64_t row = row_of(i);
     const bool live = row < A.items.n;
     const int64_t rl = live ? row : A.items.n - 1;
-    const float s = score_row<CT, ROWS>(A, q, rl, scr[wave]);
+    u32x4_t now[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) now[u] = ahead[u];
+    if (i + 4 < nb) fetch(i + 4);
+    const float s = score_row<CT, ROWS>(A, q, rl, scr[wave], now);
     if (lane < kFrag)
       keys[i * kFrag + lane] =
           live && !excluded(A, b, rl) ? composite(score_key(logit(A, s, rl)), (uint32_t)rl) : 0ull;
