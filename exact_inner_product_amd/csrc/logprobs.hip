@@ -571,6 +571,7 @@ int mips_logprobs(const void* queries, int64_t query_stride, int32_t b, const vo
     A.scx = bias ? kLog2e : scale * kLog2e;
     A.vmask = kMasked / A.scx;
     A.nqblk = (nb + kFrag * P.nqf - 1) / (kFrag * P.nqf);
+    A.ent = out_entropy != nullptr;
     A.nslices = P.nslices;
     A.ntiles = P.ntiles;
     A.part = (float4*)(ws + P.part);

@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t lane_bits(uint32_t w, int lane) {
 // half a maximum, a fused multiply-add for the exponent, one exp2 (a quarter-rate instruction),
 // an addition and a fused multiply-add: about 30 cycles a wave of 64 scores, against 16 for
 // the matrix products of a bf16 row of 128.
-template <int CT, int D, int NQF, bool ROWS>
+template <int CT, int D, int NQF, bool ROWS, bool ENT>
 __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void stats_kernel(
     StatsArgs A) {
   constexpr int E = elem_bytes(CT);
@@ -154,6 +154,18 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
     xraw = *wp;
   };
 
+  // Operand chunks of the products to come, kLook ahead; a chunk is replaced as soon as its
+  // products have been issued.
+  constexpr int kLook = NCH < 8 ? NCH : (NCH == 8 ? 8 : 4);
+  u32x4_t bq[kLook];
+  // Behind chunk c of fragment f: its chunk c + kLook, or those of the fragment that follows.
+  auto refill = [&](int c, int f, int follow) __attribute__((always_inline)) {
+    const int cc = c + kLook;
+    bq[c % kLook] = ((const u32x4_t*)(lds + (size_t)(cc < NCH ? f : follow) * BLK) + lane)[(cc % NCH) * 64];
+  };
+#pragma unroll
+  for (int c = 0; c < kLook; ++c) bq[c] = ((const u32x4_t*)lds + lane)[c * 64];
+
   auto compute_stage = [&](const u32x4_t (&a)[RM][NCH], uint32_t xraw, int64_t tile) __attribute__((always_inline)) {
     // words of the tile's blocks, rows past n set; uniform
     uint32_t word[RM], any = 0u;
@@ -165,60 +177,64 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       word[r] = w;
       any |= w;
     }
-    const bool plain = any == 0u && A.bias == nullptr && A.exclude_words == 0;  // uniform
-    for (int f = 0; f < nfr; ++f) {
-      uint32_t wq[RM];
+    // One fragment: `cur` holds its scores, `nxt` receives those of the next one, whose products
+    // run while this one's exponentials are taken.
+    auto fragment = [&](f32x16_t (&cur)[RM], f32x16_t (&nxt)[RM], int f) __attribute__((always_inline)) {
+      if (A.bias) {
+        // rows 8q + 4 (lane >> 5) + (0..3) for q = 0..3 (rows past n read 0 and are masked)
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+          const int64_t blk = min<int64_t>(tile * RM + r, nblocks - 1);
+          const __amdgpu_buffer_rsrc_t rs =
+              rows_rsrc(A.bias + blk * kFrag, (int)min<int64_t>(kFrag, A.items.n - blk * kFrag) * 4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const u32x4_t v = __builtin_bit_cast(
+                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (lane >> 5) * 16 + q * 32, 0, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              cur[r][4 * q + e] = __fadd_rn(__fmul_rn(cur[r][4 * q + e], A.scale), __uint_as_float(v[e]));
+          }
+        }
+      }
+      if (any != 0u) {
+        // Register i holds row 8 (i >> 2) + (i & 3) in lanes 0-31 and that row + 4 in lanes
+        // 32-63: a wave-uniform lane mask, built on the scalar unit, applied by one select.
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int b0 = 8 * (i >> 2) + (i & 3);
+            const uint64_t lanes = (((word[r] >> b0) & 1u) ? 0x00000000FFFFFFFFull : 0ull) |
+                                   (((word[r] >> (b0 + 4)) & 1u) ? 0xFFFFFFFF00000000ull : 0ull);
+            cur[r][i] = __builtin_amdgcn_inverse_ballot_w64(lanes) ? A.vmask : cur[r][i];
+          }
+        }
+      }
       if (A.exclude_words != 0) {  // this column's own words
         const int q = min(qbase + f * kFrag + (lane & 31), A.b - 1);
 #pragma unroll
-        for (int r = 0; r < RM; ++r)
-          wq[r] = A.exclude[(int64_t)q * A.exclude_words + min<int64_t>(tile * RM + r, nblocks - 1)];
-      }
-      f32x16_t acc[RM];
-#pragma unroll
-      for (int r = 0; r < RM; ++r) acc[r] = f32x16_t{};
-      const u32x4_t* bsrc = (const u32x4_t*)(lds + (size_t)f * BLK) + lane;
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const u32x4_t b = bsrc[c * 64];
-#pragma unroll
-        for (int r = 0; r < RM; ++r) mfma_chunk<CT>(acc[r], a[r][c], b);
-      }
-      float m = st[(3 * f + 0) * kWave], z = st[(3 * f + 1) * kWave], x = st[(3 * f + 2) * kWave];
-      if (!plain) {
-#pragma unroll
         for (int r = 0; r < RM; ++r) {
-          const uint32_t bits = lane_bits(word[r] | (A.exclude_words != 0 ? wq[r] : 0u), lane);
-          if (A.bias) {
-            // rows 8q + 4 (lane >> 5) + (0..3) for q = 0..3 (rows past n read 0 and are masked)
-            const int64_t blk = min<int64_t>(tile * RM + r, nblocks - 1);
-            const __amdgpu_buffer_rsrc_t rs =
-                rows_rsrc(A.bias + blk * kFrag, (int)min<int64_t>(kFrag, A.items.n - blk * kFrag) * 4);
+          const uint32_t bits =
+              lane_bits(A.exclude[(int64_t)q * A.exclude_words + min<int64_t>(tile * RM + r, nblocks - 1)], lane);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const u32x4_t v = __builtin_bit_cast(
-                  u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (lane >> 5) * 16 + q * 32, 0, 0));
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[r][4 * q + e] = __fadd_rn(__fmul_rn(acc[r][4 * q + e], A.scale), __uint_as_float(v[e]));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[r][i] = ((bits >> i) & 1u) ? A.vmask : acc[r][i];
+          for (int i = 0; i < 16; ++i) cur[r][i] = ((bits >> i) & 1u) ? A.vmask : cur[r][i];
         }
       }
-      float vm = acc[0][0];
+      float m = st[(3 * f + 0) * kWave], z = st[(3 * f + 1) * kWave], x = st[(3 * f + 2) * kWave];
+      float vm = cur[0][0];
 #pragma unroll
       for (int r = 0; r < RM; ++r)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) vm = fmaxf(vm, acc[r][i]);
+        for (int i = 0; i < 16; ++i) vm = fmaxf(vm, cur[r][i]);
       if (A.bmax) {
-        const float v2 = fmaxf(vm, __shfl_xor(vm, 32, kWave));
+        const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(vm), __float_as_uint(vm), false, false);
+        const float v2 = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));  // both halves' rows
         const float l = v2 * A.scx <= kEmpty ? -INFINITY : (A.bias ? v2 : v2 * A.scale);
         if (lane < kFrag) A.bmax[((int64_t)(qbase / kFrag + f) * A.ntiles + tile) * kFrag + lane] = l;
       }
       const float mn = vm * A.scx;
-      if (__ballot(mn > m + kSlack) != 0ull) {
+      if (__builtin_expect(__ballot(mn > m + kSlack) != 0ull, 0)) {
         if (mn > m) {
           const float g = __builtin_amdgcn_exp2f(m - mn);
           // (a sum over masked values alone is dropped here, whatever it holds)
@@ -227,22 +243,54 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
           m = mn;
         }
       }
+      // Each chunk's products for the next fragment (after the last one: of the first again, unused,
+      // which cost nothing beside the exponentials; a branch would part the two), then its share of this one's exponentials. The
+      // barriers keep the compiler from parting the two again.
       float z0 = 0.0f, z1 = 0.0f, x0 = 0.0f, x1 = 0.0f;
+      const int g = f + 1 < nfr ? f + 1 : 0, follow = f + 2 < nfr ? f + 2 : 0;
 #pragma unroll
-      for (int r = 0; r < RM; ++r) {
+      for (int c = 0; c < NCH; ++c) {
+        if constexpr (NQF > 1) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float ta = fmaf(acc[r][i], A.scx, -m), tb = fmaf(acc[r][i + 1], A.scx, -m);
-          const float ea = __builtin_amdgcn_exp2f(ta), eb = __builtin_amdgcn_exp2f(tb);
-          z0 += ea;
-          z1 += eb;
-          x0 = fmaf(ea, ta, x0);
-          x1 = fmaf(eb, tb, x1);
+          for (int r = 0; r < RM; ++r) {
+            if (c == 0) nxt[r] = f32x16_t{};
+            mfma_chunk<CT>(nxt[r], a[r][c], bq[c % kLook]);
+          }
+          refill(c, g, follow);
         }
+#pragma unroll
+        for (int k = c * 16 * RM / NCH; k < (c + 1) * 16 * RM / NCH; ++k) {
+          const float t = fmaf(cur[k >> 4][k & 15], A.scx, -m), e = __builtin_amdgcn_exp2f(t);
+          if (k & 1) {
+            z1 += e;
+            if constexpr (ENT) x1 = fmaf(e, t, x1);
+          } else {
+            z0 += e;
+            if constexpr (ENT) x0 = fmaf(e, t, x0);
+          }
+        }
+        if constexpr (NQF > 1) __builtin_amdgcn_sched_barrier(0);
       }
       st[(3 * f + 0) * kWave] = m;
       st[(3 * f + 1) * kWave] = z + (z0 + z1);
-      st[(3 * f + 2) * kWave] = x + (x0 + x1);
+      if constexpr (ENT) st[(3 * f + 2) * kWave] = x + (x0 + x1);
+    };
+    f32x16_t acc0[RM], acc1[RM];
+#pragma unroll
+    for (int r = 0; r < RM; ++r) acc0[r] = f32x16_t{};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+      for (int r = 0; r < RM; ++r) mfma_chunk<CT>(acc0[r], a[r][c], bq[c % kLook]);
+      refill(c, 0, nfr > 1 ? 1 : 0);
+    }
+    if constexpr (NQF > 1) {
+      for (int f = 0; f < nfr; f += 2) {
+        fragment(acc0, acc1, f);
+        if (f + 1 < nfr) fragment(acc1, acc0, f + 1);
+      }
+    } else {
+      fragment(acc0, acc1, 0);
     }
   };
 
@@ -293,14 +341,20 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
   }
 }
 
-template <int CT, int D, int NQF, bool ROWS>
-static int launch_stats_one(const StatsArgs& A, int grid, hipStream_t s) {
+template <int CT, int D, int NQF, bool ROWS, bool ENT>
+static int launch_stats_two(const StatsArgs& A, int grid, hipStream_t s) {
   constexpr int lds = stats_lds(CT, D, NQF);
-  static const hipError_t attr = hipFuncSetAttribute((const void*)stats_kernel<CT, D, NQF, ROWS>,
+  static const hipError_t attr = hipFuncSetAttribute((const void*)stats_kernel<CT, D, NQF, ROWS, ENT>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   (void)attr;
-  hipLaunchKernelGGL((stats_kernel<CT, D, NQF, ROWS>), dim3(grid), dim3(kStatsThreads), lds, s, A);
+  hipLaunchKernelGGL((stats_kernel<CT, D, NQF, ROWS, ENT>), dim3(grid), dim3(kStatsThreads), lds, s, A);
   return check_launch();
+}
+
+template <int CT, int D, int NQF, bool ROWS>
+static int launch_stats_one(const StatsArgs& A, int grid, hipStream_t s) {
+  return A.ent ? launch_stats_two<CT, D, NQF, ROWS, true>(A, grid, s)
+               : launch_stats_two<CT, D, NQF, ROWS, false>(A, grid, s);
 }
 
 template <int CT, int D>

@@ -49,6 +49,7 @@ struct StatsArgs {
   float vmask;               // a masked score or logit: kMasked / scx
   int nqblk, nslices;
   int64_t ntiles;
+  int ent;                   // whether the entropy's sums are wanted
   float4* part;              // [nslices][b]: reference, sum, sum of e * exponent
   float* bmax;               // [ceil(b/32)][ntiles][32] largest logit of each tile, or NULL
 };
