@@ -12,7 +12,9 @@ struct TermsArgs {
   int64_t n;
   const uint32_t* exclude;
   int64_t exclude_words;
-  float *lse2, *coef, *hent, *gval;
+  int extra;             // see QueryTerms
+  float *add, *coef, *hent, *sign, *gval;
+  uint32_t* neg;
   int32_t* tgt;
 };
 
@@ -36,19 +38,23 @@ __global__ __launch_bounds__(256) void terms_kernel(TermsArgs A) {
     A.gval[at] = v;
     sum += v;
   }
-  float lse2 = 1e30f, coef = 0.0f, hent = 0.0f;
+  float add = kMasked, coef = 0.0f, hent = 0.0f;
   if (b < A.b && A.lse[b] != -INFINITY) {
-    lse2 = A.lse[b] * kLog2e;
     coef = -sum;
     if (A.grad_entropy) {
       const float h = A.grad_entropy[b];
       coef = -fmaf(h, A.entropy[b], sum);
       hent = -h * kLn2;
     }
+    add = -A.lse[b] * kLog2e;
+    if (!A.extra) add = coef == 0.0f ? kMasked : add + log2f(fabsf(coef));
   }
-  A.lse2[b] = lse2;
+  A.add[b] = add;
   A.coef[b] = coef;
   A.hent[b] = hent;
+  A.sign[b] = coef < 0.0f ? -1.0f : 1.0f;
+  const uint64_t neg = __ballot(coef < 0.0f);  // (bpad is a multiple of 64: whole waves get here)
+  if ((threadIdx.x & 31) == 0) A.neg[b >> 5] = (uint32_t)(neg >> (threadIdx.x & 32));
 }
 
 struct JoinArgs {
@@ -57,6 +63,7 @@ struct JoinArgs {
   int64_t rows;
   int d;
   float scale;
+  const float* sign;  // a factor per row, or NULL
   void* out;          // [rows, d]
   const int32_t* tgt; // queries' pass: the targets' rows are added here, unrounded
   const float* gval;
@@ -86,6 +93,10 @@ __global__ __launch_bounds__(256) void join_rows_kernel(JoinArgs A) {
   for (int s = 0; s < A.nsplit; ++s) {
     const float4 p = *(const float4*)(A.part + ((int64_t)s * A.rows + row) * A.d + c);
     v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+  }
+  if (A.sign) {
+    const float k = A.sign[row];
+    v.x *= k, v.y *= k, v.z *= k, v.w *= k;
   }
   for (int g = 0; g < A.g; ++g) {
     const int32_t t = A.tgt[row * A.g + g];
@@ -154,7 +165,7 @@ static SplitPlan split_plan(int dtype, int width, int d, int64_t own, int64_t st
 struct BackwardPlan {
   int width, bpad;
   SplitPlan q, i;
-  size_t lse2, coef, hent, gval, tgt, part, bias_part, bytes;
+  size_t add, coef, hent, sign, neg, gval, tgt, part, bias_part, bytes;
 };
 
 static BackwardPlan backward_plan(int b, int64_t n, int d, int dtype, int g) {
@@ -169,9 +180,11 @@ static BackwardPlan backward_plan(int b, int64_t n, int d, int dtype, int g) {
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  P.lse2 = take((size_t)P.bpad * 4);
+  P.add = take((size_t)P.bpad * 4);
   P.coef = take((size_t)P.bpad * 4);
   P.hent = take((size_t)P.bpad * 4);
+  P.sign = take((size_t)P.bpad * 4);
+  P.neg = take((size_t)P.bpad / 8);
   P.gval = take((size_t)P.bpad * g * 4);
   P.tgt = take((size_t)P.bpad * g * 4);
   // the two passes run one after the other and share the partial sums' room
@@ -259,23 +272,24 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
   uint8_t* ws = (uint8_t*)workspace;
   const int E = elem_bytes(dtype);
 
+  const bool extra = grad_entropy || grad_bias || exclude_row_words > 0;
   TermsArgs T{lse, entropy, grad_logprobs, grad_entropy, ids, id_bits, b, P.bpad, g, n, exclude, exclude_row_words,
-              (float*)(ws + P.lse2), (float*)(ws + P.coef), (float*)(ws + P.hent), (float*)(ws + P.gval),
-              (int32_t*)(ws + P.tgt)};
+              extra, (float*)(ws + P.add), (float*)(ws + P.coef), (float*)(ws + P.hent), (float*)(ws + P.sign),
+              (float*)(ws + P.gval), (uint32_t*)(ws + P.neg), (int32_t*)(ws + P.tgt)};
   hipLaunchKernelGGL(terms_kernel, dim3((P.bpad + 255) / 256), dim3(256), 0, s, T);
   if (const int rc = check_launch()) return rc;
 
   const Table tq{(const uint8_t*)queries, query_stride * E, b, d * E};
   const Table ti{(const uint8_t*)items, item_stride * E, n, d * E};
   GradArgs A{};
-  A.q = QueryTerms{T.lse2, T.coef, T.hent, T.tgt, T.gval, g};
+  A.q = QueryTerms{T.add, T.coef, T.hent, T.neg, T.tgt, T.gval, g};
   A.bias = bias;
   A.exclude = exclude;
   A.exclude_words = exclude_row_words;
   A.scale = scale;
-  A.scx = bias ? kLog2e : scale * kLog2e;
+  A.scx = scale * kLog2e;
+  A.inv_scx = 1.0f / A.scx;
   A.use_hent = grad_entropy != nullptr;
-  const bool extra = bias || exclude || grad_entropy || grad_bias;
 
   if (grad_items || grad_bias) {
     A.own = ti;
@@ -288,7 +302,7 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
     A.bias_part = grad_bias ? (float*)(ws + P.bias_part) : nullptr;
     if (const int rc = grad_dispatch(dtype, P.width, true, extra, A, s)) return rc;
     if (grad_items && P.i.nsplit > 1) {
-      const JoinArgs J{A.part, P.i.nsplit, n, d, scale, grad_items, nullptr, nullptr, 0, ti};
+      const JoinArgs J{A.part, P.i.nsplit, n, d, scale, nullptr, grad_items, nullptr, nullptr, 0, ti};
       if (const int rc = launch_join(J, dtype, s)) return rc;
     }
     if (grad_bias) {
@@ -307,7 +321,7 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
     A.part = (float*)(ws + P.part);
     A.bias_part = nullptr;
     if (const int rc = grad_dispatch(dtype, P.width, false, extra, A, s)) return rc;
-    const JoinArgs J{A.part, P.q.nsplit, b, d, scale, grad_queries, T.tgt, T.gval, g, ti};
+    const JoinArgs J{A.part, P.q.nsplit, b, d, scale, extra ? nullptr : T.sign, grad_queries, T.tgt, T.gval, g, ti};
     if (const int rc = launch_join(J, dtype, s)) return rc;
   }
   return MIPS_OK;

@@ -83,14 +83,21 @@ int launch_stats(int nqf, bool rows, const StatsArgs& A, int grid, hipStream_t s
 // ---------------------------------------------------------------------- the backward pass
 namespace mips {
 
-// Per query: what the weights of its scores need (log2 units: lse * log2 e), and its targets.
-// Padded queries (up to a multiple of kGradTile) have lse2 = 1e30, so that p = 0.
+// What a score's weight needs besides the score, s in its own units and everything else in
+// log2 units:  w = 2^(s scx + add_b + add_j), with the signs applied where they are uniform.
+//  plain: add_b = log2 |coef_b| - lse_b log2 e, so that w = p |coef_b|, coef_b = - sum_i g_bi;
+//  extra (entropy gradient, bitmaps per query, bias gradient): add_b = - lse_b log2 e and
+//         w = p (coef_b + hent_b log2 p), coef_b with the entropy's share, hent_b = - h_b ln 2.
+// add_j = bias_j log2 e. The streamed rows' addend is divided by scx and enters the scores'
+// products as one more 16-byte chunk, against a chunk of ones. Queries are padded to a multiple
+// of kGradTile with addends of kMasked.
 struct QueryTerms {
-  const float* lse2;
-  const float* coef;   // -(sum of the targets' gradients + gradient of the entropy * entropy)
-  const float* hent;   // -gradient of the entropy * ln 2
-  const int32_t* tgt;  // [b][g]; -1: no target
-  const float* gval;   // [b][g]
+  const float* add;      // add_b
+  const float* coef;
+  const float* hent;
+  const uint32_t* neg;   // bit b & 31 of word b >> 5: coef_b < 0 (plain)
+  const int32_t* tgt;    // [b][g]; -1: no target
+  const float* gval;     // [b][g]
   int g;
 };
 
@@ -100,7 +107,7 @@ struct GradArgs {
   const float* bias;
   const uint32_t* exclude;
   int64_t exclude_words;
-  float scale, scx;
+  float scale, scx, inv_scx;
   int use_hent;
   int nown, nsplit;          // own tiles and splits of the streamed rows
   int64_t ntiles;            // tiles of streamed rows
@@ -110,14 +117,15 @@ struct GradArgs {
 };
 
 constexpr int kGradTile = 64;  // streamed rows per tile
+constexpr int kGradBufs = 3;   // tiles in LDS: this one, the next, and the one being written
 
 __host__ __device__ constexpr int grad_waves(int ct, int d) { return d * elem_bytes(ct) > 256 ? 4 : 8; }
 __host__ __device__ constexpr int grad_own(int ct, int d) { return 32 * grad_waves(ct, d); }
-// LDS of a workgroup: two tiles of streamed rows (at least 128 bytes a row) and, for each, four
-// values a row and the rows' g targets (items' pass) or bias (queries' pass).
+// LDS of a workgroup, per tile: the rows (at least 128 bytes each), their addends as a 16-byte
+// chunk, two more values a row and g targets.
 __host__ __device__ constexpr int grad_row_bytes(int ct, int d) { return d * elem_bytes(ct) < 128 ? 128 : d * elem_bytes(ct); }
 __host__ __device__ constexpr int grad_lds(int ct, int d, int g) {
-  return 2 * kGradTile * (grad_row_bytes(ct, d) + 16 + 4 * g);
+  return kGradBufs * kGradTile * (grad_row_bytes(ct, d) + 16 + 8 + 4 * g);
 }
 
 template <int CT, int D>

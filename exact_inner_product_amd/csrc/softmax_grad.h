@@ -28,8 +28,11 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 // One workgroup = grad_waves waves of 32 own rows each, one split of the streamed rows. A wave
 // holds its rows as MFMA operands in registers, and the 32 x D sums. Per 32 streamed rows:
 //  1. scores, transposed: the streamed rows as the first operand, the own rows as the second,
-//     so that a lane holds 16 scores of its own row (column lane & 31);
-//  2. weights, in place;
+//     so that a lane holds 16 scores of its own row (column lane & 31). The streamed rows'
+//     addends come in as one more chunk, split into three bf16 parts (24 bits): read from LDS
+//     per row instead, they would take four 16-byte reads a lane, as much as half of all
+//     operand reads, and the pass was bound by LDS with them;
+//  2. weights, in place: a fused multiply-add, an exp2 and half a conversion a score;
 //  3. sums += weights x streamed rows. The accumulator layout of step 1 is an operand layout of
 //     step 3 with the streamed rows in another order, so the weights stay in their lanes; the
 //     other operand takes the streamed rows in the same order, transposed by the LDS read
@@ -37,9 +40,11 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 // In bf16 the weights are rounded to bf16 for step 3, to nearest: an independent relative error
 // of at most 2^-8 each, under sums that are rounded to bf16 themselves. Sums are in binary32.
 //
-// Tiles of 64 streamed rows are double-buffered: the next tile's rows are loaded to registers
-// before this tile's products and stored to the other buffer after them, with one barrier a
-// tile.
+// Step 1 of the next 32 rows is interleaved with step 2 of these, chunk by chunk, so that the
+// matrix pipe works under the exponentials. Tiles of 64 streamed rows go through three LDS
+// buffers: the tile after the next is on its way from memory, the next is written at the start
+// of a tile, and one barrier in the middle of the tile makes it readable before its first
+// scores are due at the end.
 template <int CT, int D, bool ITEMS, bool EXTRA>
 __global__ __launch_bounds__(64 * grad_waves(CT, D))
 __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4))) void grad_kernel(GradArgs A) {
@@ -50,20 +55,19 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
   constexpr int SL = RB / 16;                   // slots of a row in LDS
   constexpr int NLD = kGradTile * SL / NT;      // slots each thread moves per tile
   constexpr int DT = (D + 31) / 32;             // 32-column tiles of the sums
-  constexpr int JB = kGradTile / 32;
+  constexpr int kLook = NCH < 4 ? NCH : 4;      // operand chunks read ahead
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  // [2] tiles | [2][64] lse2 or bias | [2][64] coef | [2][64] hent | [2][64] words | [2][64][g] targets
-  float* va = (float*)(lds + 2 * kGradTile * RB);
-  float* vb = va + 2 * kGradTile;
-  float* vc = vb + 2 * kGradTile;
-  int32_t* vt = (int32_t*)(vc + 2 * kGradTile + 2 * kGradTile);
+  // per buffer: rows | addend chunks | coef | hent | targets
+  uint8_t* vadd = lds + kGradBufs * kGradTile * RB;
+  float* vcoef = (float*)(vadd + kGradBufs * kGradTile * 16);
+  float* vhent = vcoef + kGradBufs * kGradTile;
+  int32_t* vtgt = (int32_t*)(vhent + kGradBufs * kGradTile);
 
   const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // Workgroup -> (split, own tile): the own tiles of one split share an XCD, and its L2 the
-  // streamed rows, where there are enough splits; else the other way round it makes no
-  // difference.
+  // Workgroup -> (split, own tile): consecutive workgroups go to different XCDs; the own tiles
+  // of one split share an XCD, and its L2 the streamed rows, where the splits allow it.
   int split, tile_own;
   {
     const int w = blockIdx.x;
@@ -88,19 +92,24 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
     x[c] = u32x4_t{0u, 0u, 0u, 0u};
     if (live && off < A.own.row_b) x[c] = *(const u32x4_t*)(A.own.p + own_c * A.own.stride_b + off);
   }
+  // the addend chunk's partner: ones for its three parts (f32: for its one), in the first half
+  const u32x4_t ones = h != 0 ? u32x4_t{0u, 0u, 0u, 0u}
+                              : (CT == MIPS_BF16 ? u32x4_t{0x3F803F80u, 0x00003F80u, 0u, 0u}
+                                                 : u32x4_t{0x3F800000u, 0u, 0u, 0u});
   f32x16_t sum[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) sum[d] = f32x16_t{};
   float dbias = 0.0f;
 
   // the lane's own terms
-  float my_lse2 = 1e30f, my_coef = 0.0f, my_hent = 0.0f, my_bias = 0.0f;
+  const float masked_add = kMasked * A.inv_scx;
+  float my_add = 0.0f, my_coef = 0.0f, my_hent = 0.0f;
   if constexpr (!ITEMS) {
-    my_lse2 = A.q.lse2[own_c];
-    my_coef = live ? A.q.coef[own_c] : 0.0f;
+    my_add = live ? A.q.add[own_c] : kMasked;
+    if (EXTRA) my_coef = live ? A.q.coef[own_c] : 0.0f;
     if (EXTRA) my_hent = live ? A.q.hent[own_c] : 0.0f;
-  } else if (EXTRA) {
-    if (A.bias) my_bias = A.bias[own_c];
+  } else {
+    if (A.bias) my_add = A.bias[own_c] * kLog2e;
   }
 
   const int64_t t_begin = (int64_t)split * A.ntiles / A.nsplit, t_end = (int64_t)(split + 1) * A.ntiles / A.nsplit;
@@ -109,7 +118,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
   u32x4_t ld[NLD];
   float la = 0.0f, lb = 0.0f, lc = 0.0f;
   int32_t lt = -1;
-  uint32_t lw[NLD];
+  uint32_t lw[NLD], law = 0u;
   const bool shared_mask = A.exclude != nullptr && A.exclude_words == 0;
   auto stage_load = [&](int64_t tile) __attribute__((always_inline)) {
 #pragma unroll
@@ -118,16 +127,17 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
       const int64_t r = tile * kGradTile + j;
       ld[i] = u32x4_t{0u, 0u, 0u, 0u};
       if (r < A.str.n && 16 * s < A.str.row_b) ld[i] = *(const u32x4_t*)(A.str.p + r * A.str.stride_b + 16 * s);
-      if (!ITEMS && EXTRA && shared_mask) lw[i] = r < A.str.n ? A.exclude[r >> 5] : 0u;
+      if (!ITEMS && shared_mask) lw[i] = r < A.str.n ? A.exclude[r >> 5] : 0u;
     }
     if (threadIdx.x < kGradTile) {
       const int64_t r = tile * kGradTile + threadIdx.x;
       if constexpr (ITEMS) {  // padded arrays: every row of a tile has its terms
-        la = A.q.lse2[r];
-        lb = A.q.coef[r];
+        la = A.q.add[r] * A.inv_scx;
+        if (EXTRA) lb = A.q.coef[r];
         if (EXTRA) lc = A.q.hent[r];
-      } else if (EXTRA) {
-        la = A.bias && r < A.str.n ? A.bias[r] : 0.0f;
+      } else {
+        la = r >= A.str.n ? masked_add : (A.bias ? A.bias[r] * kLog2e * A.inv_scx : 0.0f);
+        law = shared_mask && r < A.str.n ? A.exclude[r >> 5] >> (r & 31) : 0u;
       }
     }
     if constexpr (ITEMS) {
@@ -140,18 +150,27 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
       const int e = i * NT + threadIdx.x, j = e / SL, s = e % SL;
       u32x4_t v = ld[i];
       // an excluded item's row may hold anything: it takes no part in the sums
-      if (!ITEMS && EXTRA && shared_mask && ((lw[i] >> (j & 31)) & 1u)) v = u32x4_t{0u, 0u, 0u, 0u};
+      if (!ITEMS && shared_mask && ((lw[i] >> (j & 31)) & 1u)) v = u32x4_t{0u, 0u, 0u, 0u};
       *(u32x4_t*)(lds + (size_t)buf * kGradTile * RB + j * RB + ((s ^ (swz(j) & (SL - 1))) << 4)) = v;
     }
     if (threadIdx.x < kGradTile) {
-      if (ITEMS || EXTRA) va[buf * kGradTile + threadIdx.x] = la;
-      if (ITEMS) vb[buf * kGradTile + threadIdx.x] = lb;
-      if (ITEMS && EXTRA) vc[buf * kGradTile + threadIdx.x] = lc;
+      const float a = (!ITEMS && (law & 1u)) ? masked_add : la;
+      u32x4_t v = {__float_as_uint(a), 0u, 0u, 0u};
+      if constexpr (CT == MIPS_BF16) {
+        const __bf16 p0 = (__bf16)a, p1 = (__bf16)(a - (float)p0), p2 = (__bf16)(a - (float)p0 - (float)p1);
+        v = u32x4_t{(uint32_t)__builtin_bit_cast(uint16_t, p0) | ((uint32_t)__builtin_bit_cast(uint16_t, p1) << 16),
+                    (uint32_t)__builtin_bit_cast(uint16_t, p2), 0u, 0u};
+      }
+      *(u32x4_t*)(vadd + (buf * kGradTile + threadIdx.x) * 16) = v;
+      if (ITEMS && EXTRA) {
+        vcoef[buf * kGradTile + threadIdx.x] = lb;
+        vhent[buf * kGradTile + threadIdx.x] = lc;
+      }
     }
     if constexpr (ITEMS) {
-      if ((int)threadIdx.x < kGradTile * A.q.g) vt[buf * kGradTile * A.q.g + threadIdx.x] = lt;
+      if ((int)threadIdx.x < kGradTile * A.q.g) vtgt[buf * kGradTile * A.q.g + threadIdx.x] = lt;
       for (int i = NT + threadIdx.x; i < kGradTile * A.q.g; i += NT)
-        vt[buf * kGradTile * A.q.g + i] = A.q.tgt[tile * kGradTile * A.q.g + i];
+        vtgt[buf * kGradTile * A.q.g + i] = A.q.tgt[tile * kGradTile * A.q.g + i];
     }
   };
 
@@ -165,33 +184,41 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
   for (int o = 0; o < 2; ++o)
     tbase[o] = (4 * h + (tl >> 2)) * RB + (((4 * o + 2 * tg + ((tl & 3) >> 1)) ^ (((tl >> 2) << 1) | h)) << 4) + 8 * (tl & 1);
 
-  auto compute = [&](int64_t tile, int buf) __attribute__((always_inline)) {
-    const uint8_t* y = lds + (size_t)buf * kGradTile * RB;
-#pragma unroll 1
-    for (int jb = 0; jb < JB; ++jb) {
-      // masks: bit i of `bits` <=> register i's pair takes no part
-      uint32_t bits = 0u;
-      bool masked = false;  // uniform
-      if constexpr (!ITEMS) {
-        const int64_t left = A.str.n - (tile * kGradTile + jb * 32);
-        uint32_t w = 0u;
-        if (left < 32) w = left <= 0 ? ~0u : ~0u << left;
-        if (EXTRA && A.exclude && left > 0) {
-          const int64_t blk = tile * JB + jb;
-          if (A.exclude_words == 0) {
-            w |= (uint32_t)__builtin_amdgcn_readfirstlane((int)A.exclude[blk]);
-            masked = w != 0u;
-          } else {
-            w |= A.exclude[own_c * A.exclude_words + blk];
-            masked = true;
-          }
-        } else {
-          masked = w != 0u;
-        }
-        if (masked) bits = lane_bits(w, lane);
-      } else if (EXTRA) {
-        if (A.exclude && A.exclude_words != 0) {  // each query's own word of this wave's block of items
-          masked = true;
+  // Operand chunks of a block's scores: chunk NCH is the addends'.
+  u32x4_t yq[kLook];
+  auto read_chunk = [&](int buf, int jb, int c) __attribute__((always_inline)) {
+    if (c == NCH) return *(const u32x4_t*)(vadd + (buf * kGradTile + jb * 32 + col) * 16);
+    return *(const u32x4_t*)(lds + (size_t)buf * kGradTile * RB + jb * 32 * RB + sbase[c & 3] + (c >> 2) * 128);
+  };
+  auto read_first = [&](int buf, int jb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < kLook; ++c) yq[c] = read_chunk(buf, jb, c);
+  };
+  // Chunk c's products for block jb, and the read of chunk c + kLook.
+  auto score_chunk = [&](f32x16_t& s, int buf, int jb, int c) __attribute__((always_inline)) {
+    if (c == 0) s = f32x16_t{};
+    if (c < NCH) {
+      mfma_chunk<CT>(s, yq[c % kLook], x[c < NCH ? c : 0]);
+    } else if constexpr (CT == MIPS_BF16) {
+      mfma_chunk<CT>(s, yq[c % kLook], ones);
+    } else {
+      s = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(yq[c % kLook][0]), __uint_as_float(ones[0]), s, 0, 0, 0);
+    }
+    if (c + kLook <= NCH) yq[c % kLook] = read_chunk(buf, jb, c + kLook);
+  };
+
+  // Steps 2 and 3 of block jb of tile `tile` (buffer buf), whose scores are in `s`, with step 1
+  // of block nj of buffer nbuf into `nxt` between; then `between`, the first chunk reads of the
+  // block after that, and the sums.
+  auto block = [&](f32x16_t& s, f32x16_t& nxt, int64_t tile, int buf, int jb, int nbuf, int nj,
+                   auto between) __attribute__((always_inline)) {
+    uint32_t bits = 0u;  // bit i: register i's pair takes no part
+    if constexpr (EXTRA) {
+      if (A.exclude && A.exclude_words != 0) {
+        if constexpr (!ITEMS) {  // this query's own word of the block of items
+          if (tile * kGradTile + jb * 32 < A.str.n)
+            bits = lane_bits(A.exclude[own_c * A.exclude_words + tile * (kGradTile / 32) + jb], lane);
+        } else {                 // each query's own word of this wave's block of items
           const int64_t blk = min(own0, A.own.n - 1) >> 5;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -200,113 +227,129 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
           }
         }
       }
-
-      f32x16_t s = {};
+    }
+    float w[16];
+    float ck[16], hk[16];
+    if constexpr (EXTRA && ITEMS) {
 #pragma unroll
-      for (int c = 0; c < NCH; ++c)
-        mfma_chunk<CT>(s, *(const u32x4_t*)(y + jb * 32 * RB + sbase[c & 3] + (c >> 2) * 128), x[c]);
-
-      // weights
-      float w[16];
+      for (int q = 0; q < 4; ++q) {  // registers 4q .. 4q + 3: rows 8q + 4h ..
+        const float4 a = *(const float4*)(vcoef + buf * kGradTile + jb * 32 + 8 * q + 4 * h);
+        const float4 b = *(const float4*)(vhent + buf * kGradTile + jb * 32 + 8 * q + 4 * h);
+        ck[4 * q] = a.x, ck[4 * q + 1] = a.y, ck[4 * q + 2] = a.z, ck[4 * q + 3] = a.w;
+        hk[4 * q] = b.x, hk[4 * q + 1] = b.y, hk[4 * q + 2] = b.z, hk[4 * q + 3] = b.w;
+      }
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = buf * kGradTile + jb * 32 + 8 * q + 4 * h;  // registers 4q .. 4q + 3
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a, c = a;
-        if (ITEMS || (EXTRA && A.bias)) a = *(const float4*)(va + at);
-        if (ITEMS) b = *(const float4*)(vb + at);
-        if (ITEMS && EXTRA) c = *(const float4*)(vc + at);
+    for (int c = 0; c <= NCH; ++c) {
+      score_chunk(nxt, nbuf, nj, c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * q + e;
-          const float ae = e == 0 ? a.x : (e == 1 ? a.y : (e == 2 ? a.z : a.w));
-          const float be = e == 0 ? b.x : (e == 1 ? b.y : (e == 2 ? b.z : b.w));
-          const float ce = e == 0 ? c.x : (e == 1 ? c.y : (e == 2 ? c.z : c.w));
-          const float lse2 = ITEMS ? ae : my_lse2;
-          float v = s[i];
-          if (EXTRA && A.bias) v = __fadd_rn(__fmul_rn(v, A.scale), ITEMS ? my_bias : ae);
-          const float t = fmaf(v, A.scx, -lse2);
-          const float p = __builtin_amdgcn_exp2f(t);
-          float k = ITEMS ? be : my_coef;
-          if (EXTRA && A.use_hent) k += (p > 0.0f ? t : 0.0f) * (ITEMS ? ce : my_hent);
-          w[i] = p * k;
+      for (int i = c * 16 / (NCH + 1); i < (c + 1) * 16 / (NCH + 1); ++i) {
+        const float t = fmaf(s[i], A.scx, my_add);
+        w[i] = __builtin_amdgcn_exp2f(t);
+        if constexpr (EXTRA) {
+          float k = ITEMS ? ck[i] : my_coef;
+          if (A.use_hent) k = fmaf(t, ITEMS ? hk[i] : my_hent, k);
+          w[i] = ((bits >> i) & 1u) ? 0.0f : w[i] * k;
         }
       }
-      if (masked) {
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (ITEMS) {
+      if constexpr (!EXTRA) {
+        // the queries whose coefficient is negative (none, or all, in most losses)
+        const uint32_t neg = A.q.neg[tile * (kGradTile / 32) + jb];
+        if (neg != 0u) {
+          const uint32_t nb = lane_bits(neg, lane);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = ((bits >> i) & 1u) ? 0.0f : w[i];
-      }
-      if constexpr (ITEMS) {
-        // targets among this wave's items: rare, so one ballot a target column
-        for (int g = 0; g < A.q.g; ++g) {
-          const int32_t tgt = vt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
-          if (__ballot(tgt >= own0 && tgt < own0 + 32) != 0ull) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int j = jb * 32 + acc_row(i, lane);
-              if (vt[(buf * kGradTile + j) * A.q.g + g] == (int32_t)own)
-                w[i] += A.q.gval[(tile * kGradTile + j) * A.q.g + g];
-            }
-          }
-        }
-        if (EXTRA && A.bias_part) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dbias += w[i];
+          for (int i = 0; i < 16; ++i) w[i] = ((nb >> i) & 1u) ? -w[i] : w[i];
         }
       }
-
-      // sums += w^T Y
-      if constexpr (CT == MIPS_BF16) {
+      // targets among this wave's items: rare, so one ballot a target column, and the pairs it
+      // finds one by one: row j of the block is register 4 (j >> 3) + (j & 3) of half (j >> 2) & 1
+      for (int g = 0; g < A.q.g; ++g) {
+        const int32_t tgt = vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
+        uint32_t hits = (uint32_t)__ballot(tgt >= own0 && tgt < own0 + 32);
+        while (hits != 0u) {
+          const int j = __builtin_ctz(hits);
+          hits &= hits - 1u;
+          const int to = __builtin_amdgcn_readlane(tgt, j) - (int)own0 + 32 * ((j >> 2) & 1);
+          const float v = lane == to ? A.q.gval[(tile * kGradTile + jb * 32 + j) * A.q.g + g] : 0.0f;
+          const int at = 4 * (j >> 3) + (j & 3);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          bf16x8_t wa;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) wa[e] = (__bf16)w[8 * kb + e];
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
-            const uint8_t* p = y + (jb * 32 + 16 * kb) * RB + tbase[d & 1] + (d >> 1) * 128;
-            const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-            const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * RB));
-            const bf16x8_t yb = __builtin_bit_cast(
-                bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, yb, sum[d], 0, 0, 0);
-          }
+          for (int i = 0; i < 16; ++i) w[i] += i == at ? v : 0.0f;
         }
-      } else {
+      }
+      if (EXTRA && A.bias_part) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = jb * 32 + 8 * (i >> 2) + (i & 3);  // + 4h: swz of row j + 4h is swz(j) ^ h
-          const uint8_t* row = y + (j + 4 * h) * RB;
+        for (int i = 0; i < 16; ++i) dbias += w[i];
+      }
+    }
+    between();
+    // sums += w^T Y
+    const uint8_t* y = lds + (size_t)buf * kGradTile * RB + jb * 32 * RB;
+    if constexpr (CT == MIPS_BF16) {
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const int slot = (8 * d + (col >> 2)) ^ (swz(j) ^ h);
-            sum[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(w[i], *(const float*)(row + (slot << 4) + 4 * (col & 3)),
-                                                          sum[d], 0, 0, 0);
-          }
+      for (int kb = 0; kb < 2; ++kb) {
+        bf16x8_t wa;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wa[e] = (__bf16)w[8 * kb + e];
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+          const uint8_t* p = y + 16 * kb * RB + tbase[d & 1] + (d >> 1) * 128;
+          const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+          const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * RB));
+          const bf16x8_t yb = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, yb, sum[d], 0, 0, 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = 8 * (i >> 2) + (i & 3);  // + 4h: swz of row j + 4h is swz(j) ^ h
+        const uint8_t* row = y + (j + 4 * h) * RB;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const int slot = (8 * d + (col >> 2)) ^ (swz(j) ^ h);
+          sum[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(w[i], *(const float*)(row + (slot << 4) + 4 * (col & 3)),
+                                                        sum[d], 0, 0, 0);
         }
       }
     }
   };
 
+  static_assert(kGradTile == 64 && kGradBufs == 3, "the loop below takes two blocks a tile, three buffers");
   if (t_begin < t_end) {
+    f32x16_t s0, s1;
     stage_load(t_begin);
     stage_store(t_begin, 0);
+    if (t_begin + 1 < t_end) stage_load(t_begin + 1);
     __syncthreads();
+    read_first(0, 0);
+#pragma unroll
+    for (int c = 0; c <= NCH; ++c) score_chunk(s0, 0, 0, c);
+    read_first(0, 1);
     int buf = 0;
     for (int64_t t = t_begin; t < t_end; ++t) {
-      const bool more = t + 1 < t_end;
-      if (more) stage_load(t + 1);
-      compute(t, buf);
-      if (more) stage_store(t + 1, buf ^ 1);
-      __syncthreads();
-      buf ^= 1;
+      const int nbuf = buf == 2 ? 0 : buf + 1;
+      // (written last two tiles ago and read until one tile ago: everybody has passed the
+      // barrier of the last tile since)
+      if (t + 1 < t_end) stage_store(t + 1, nbuf);
+      if (t + 2 < t_end) stage_load(t + 2);
+      block(s0, s1, t, buf, 0, buf, 1, [&]() __attribute__((always_inline)) {
+        __syncthreads();  // the next tile is readable
+        read_first(nbuf, 0);
+      });
+      // (after the last tile: scores of what the buffer holds, unused)
+      block(s1, s0, t, buf, 1, nbuf, 0, [&]() __attribute__((always_inline)) { read_first(nbuf, 1); });
+      buf = nbuf;
     }
   }
 
   // rows acc_row(i, lane) of the wave's tile, column 32 d + col
   const int d_live = A.own.row_b / E;
   uint32_t dead = 0u;  // excluded items have no gradient
-  if (ITEMS && EXTRA && shared_mask && own0 < A.own.n) dead = A.exclude[own0 >> 5];
+  if (ITEMS && shared_mask && own0 < A.own.n) dead = A.exclude[own0 >> 5];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int r = acc_row(i, lane);
