@@ -260,7 +260,9 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
         }
 #pragma unroll
         for (int k = c * 16 * RM / NCH; k < (c + 1) * 16 * RM / NCH; ++k) {
-          const float t = fmaf(cur[k >> 4][k & 15], A.scx, -m), e = __builtin_amdgcn_exp2f(t);
+          const float t = fmaf(cur[k >> 4][k & 15], A.scx, -m);
+          float e = __builtin_amdgcn_exp2f(t);
+          if constexpr (NQF > 1) asm volatile("" : "+v"(e));  // computed here, under these products
           if (k & 1) {
             z1 += e;
             if constexpr (ENT) x1 = fmaf(e, t, x1);

@@ -251,6 +251,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
           if (A.use_hent) k = fmaf(t, ITEMS ? hk[i] : my_hent, k);
           w[i] = ((bits >> i) & 1u) ? 0.0f : w[i] * k;
         }
+        asm volatile("" : "+v"(w[i]));  // computed here, under these products
       }
       __builtin_amdgcn_sched_barrier(0);
     }
