@@ -122,10 +122,10 @@ constexpr int kGradBufs = 3;   // tiles in LDS: this one, the next, and the one 
 __host__ __device__ constexpr int grad_waves(int ct, int d) { return d * elem_bytes(ct) > 256 ? 4 : 8; }
 __host__ __device__ constexpr int grad_own(int ct, int d) { return 32 * grad_waves(ct, d); }
 // LDS of a workgroup, per tile: the rows (at least 128 bytes each), their addends as a 16-byte
-// chunk, two more values a row and g targets.
+// chunk, two more values a row and g targets; and 64 bytes of signs.
 __host__ __device__ constexpr int grad_row_bytes(int ct, int d) { return d * elem_bytes(ct) < 128 ? 128 : d * elem_bytes(ct); }
 __host__ __device__ constexpr int grad_lds(int ct, int d, int g) {
-  return kGradBufs * kGradTile * (grad_row_bytes(ct, d) + 16 + 8 + 4 * g);
+  return kGradBufs * kGradTile * (grad_row_bytes(ct, d) + 16 + 8 + 4 * g) + 64;
 }
 
 template <int CT, int D>

@@ -57,11 +57,12 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
   constexpr int DT = (D + 31) / 32;             // 32-column tiles of the sums
   constexpr int kLook = NCH < 4 ? NCH : 4;      // operand chunks read ahead
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  // per buffer: rows | addend chunks | coef | hent | targets
+  // per buffer: rows | addend chunks | coef | hent | signs | targets
   uint8_t* vadd = lds + kGradBufs * kGradTile * RB;
   float* vcoef = (float*)(vadd + kGradBufs * kGradTile * 16);
   float* vhent = vcoef + kGradBufs * kGradTile;
-  int32_t* vtgt = (int32_t*)(vhent + kGradBufs * kGradTile);
+  uint32_t* vneg = (uint32_t*)(vhent + kGradBufs * kGradTile);  // [3][2], 16 words kept
+  int32_t* vtgt = (int32_t*)(vneg + 16);
 
   const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -118,7 +119,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
   u32x4_t ld[NLD];
   float la = 0.0f, lb = 0.0f, lc = 0.0f;
   int32_t lt = -1;
-  uint32_t lw[NLD], law = 0u;
+  uint32_t lw[NLD], law = 0u, ln = 0u;
   const bool shared_mask = A.exclude != nullptr && A.exclude_words == 0;
   auto stage_load = [&](int64_t tile) __attribute__((always_inline)) {
 #pragma unroll
@@ -142,6 +143,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
     }
     if constexpr (ITEMS) {
       if ((int)threadIdx.x < kGradTile * A.q.g) lt = A.q.tgt[tile * kGradTile * A.q.g + threadIdx.x];
+      if (!EXTRA && threadIdx.x < kGradTile / 32) ln = A.q.neg[tile * (kGradTile / 32) + threadIdx.x];
     }
   };
   auto stage_store = [&](int64_t tile, int buf) __attribute__((always_inline)) {
@@ -168,6 +170,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
       }
     }
     if constexpr (ITEMS) {
+      if (!EXTRA && threadIdx.x < kGradTile / 32) vneg[buf * (kGradTile / 32) + threadIdx.x] = ln;
       if ((int)threadIdx.x < kGradTile * A.q.g) vtgt[buf * kGradTile * A.q.g + threadIdx.x] = lt;
       for (int i = NT + threadIdx.x; i < kGradTile * A.q.g; i += NT)
         vtgt[buf * kGradTile * A.q.g + i] = A.q.tgt[tile * kGradTile * A.q.g + i];
@@ -228,6 +231,13 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
         }
       }
     }
+    // the block's first targets and signs, read ahead of the products
+    int32_t tgt0 = -1;
+    uint32_t negw = 0u;
+    if constexpr (ITEMS) {
+      if (A.q.g > 0) tgt0 = vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g];
+      if (!EXTRA) negw = vneg[buf * (kGradTile / 32) + jb];
+    }
     float w[16];
     float ck[16], hk[16];
     if constexpr (EXTRA && ITEMS) {
@@ -258,7 +268,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
     if constexpr (ITEMS) {
       if constexpr (!EXTRA) {
         // the queries whose coefficient is negative (none, or all, in most losses)
-        const uint32_t neg = A.q.neg[tile * (kGradTile / 32) + jb];
+        const uint32_t neg = (uint32_t)__builtin_amdgcn_readfirstlane((int)negw);
         if (neg != 0u) {
           const uint32_t nb = lane_bits(neg, lane);
 #pragma unroll
@@ -268,7 +278,7 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
       // targets among this wave's items: rare, so one ballot a target column, and the pairs it
       // finds one by one: row j of the block is register 4 (j >> 3) + (j & 3) of half (j >> 2) & 1
       for (int g = 0; g < A.q.g; ++g) {
-        const int32_t tgt = vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
+        const int32_t tgt = g == 0 ? tgt0 : vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
         uint32_t hits = (uint32_t)__ballot(tgt >= own0 && tgt < own0 + 32);
         while (hits != 0u) {
           const int j = __builtin_ctz(hits);
