@@ -135,8 +135,7 @@ struct SplitPlan {
   int64_t ntiles;
 };
 
-// Splits of the streamed rows: the number that minimises rounds of workgroups (one a compute
-// unit) times tiles of a split, plus the traffic of the partial sums it takes. Rates as measured
+// Splits of the streamed rows: the number that minimises rounds of workgroups times tiles of a split, plus the traffic of the partial sums it takes. Rates as measured
 // for one workgroup's products (bf16 4e12, f32 0.3e12 flop/s) and for the partial rows' write
 // and read (4e12 bytes/s): they only weigh the two against each other.
 static SplitPlan split_plan(int dtype, int width, int d, int64_t own, int64_t streamed, bool direct) {
@@ -146,7 +145,7 @@ static SplitPlan split_plan(int dtype, int width, int d, int64_t own, int64_t st
   P.ntiles = (streamed + kGradTile - 1) / kGradTile;
   const double tile_s = 4.0 * kGradTile * per * width / (dtype == MIPS_BF16 ? 4e12 : 0.3e12);
   const double part_s = 8.0 * (double)own * d / 4e12;
-  const int cus = device_cu_count();
+  const int cus = device_cu_count() * grad_per_unit(dtype, width);
   double best = 1e30;
   P.nsplit = 1;
   // (with four rounds or more the last one's idle units cost little: no split)

@@ -47,7 +47,7 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 // scores are due at the end.
 template <int CT, int D, bool ITEMS, bool EXTRA>
 __global__ __launch_bounds__(64 * grad_waves(CT, D))
-__attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4))) void grad_kernel(GradArgs A) {
+__attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad_kernel(GradArgs A) {
   constexpr int E = elem_bytes(CT);
   constexpr int NCH = chunks_per_block(CT, D);  // 32-byte steps of a row
   constexpr int NT = 64 * grad_waves(CT, D);
@@ -265,6 +265,22 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    // the streamed rows as the sums' operand: lane (column, h) holds rows 4h + (0..3) and
+    // 8 + 4h + (0..3) of half kb; the first half's are read ahead of what comes between
+    const uint8_t* y = lds + (size_t)buf * kGradTile * RB + jb * 32 * RB;
+    auto read_columns = [&](int kb, int d) __attribute__((always_inline)) {
+      typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+      const uint8_t* p = y + 16 * kb * RB + tbase[d & 1] + (d >> 1) * 128;
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * RB));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    constexpr int kAhead = CT == MIPS_BF16 ? (DT < 4 ? DT : 4) : 1;
+    bf16x8_t ahead[kAhead];
+    if constexpr (CT == MIPS_BF16) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) ahead[d] = read_columns(0, d);
+    }
     if constexpr (ITEMS) {
       if constexpr (!EXTRA) {
         // the queries whose coefficient is negative (none, or all, in most losses)
@@ -297,7 +313,6 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
     }
     between();
     // sums += w^T Y
-    const uint8_t* y = lds + (size_t)buf * kGradTile * RB + jb * 32 * RB;
     if constexpr (CT == MIPS_BF16) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
@@ -305,14 +320,9 @@ __attribute__((amdgpu_waves_per_eu(grad_waves(CT, D) / 4, grad_waves(CT, D) / 4)
 #pragma unroll
         for (int e = 0; e < 8; ++e) wa[e] = (__bf16)w[8 * kb + e];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
-          const uint8_t* p = y + 16 * kb * RB + tbase[d & 1] + (d >> 1) * 128;
-          const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-          const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * RB));
-          const bf16x8_t yb = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-          sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, yb, sum[d], 0, 0, 0);
-        }
+        for (int d = 0; d < DT; ++d)
+          sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              wa, kb == 0 && d < kAhead ? ahead[d < kAhead ? d : 0] : read_columns(kb, d), sum[d], 0, 0, 0);
       }
     } else {
 #pragma unroll
