@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t lane_bits(uint32_t w, int lane) {
 // half a maximum, a fused multiply-add for the exponent, one exp2 (a quarter-rate instruction),
 // an addition and a fused multiply-add: about 30 cycles a wave of 64 scores, against 16 for
 // the matrix products of a bf16 row of 128.
-template <int CT, int D, int NQF, bool ROWS, bool ENT>
+template <int CT, int D, int NQF, bool ROWS, int MODE>
 __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void stats_kernel(
     StatsArgs A) {
   constexpr int E = elem_bytes(CT);
@@ -67,6 +67,7 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
   constexpr int NS = stats_ns(CT, D);
   constexpr int64_t BLK = block_bytes(CT, D);
   constexpr int QB = kFrag * NQF;
+  constexpr bool ENT = MODE != STATS_LSE, BM = MODE == STATS_ALT;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int lane = threadIdx.x & 63;
@@ -177,25 +178,35 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       word[r] = w;
       any |= w;
     }
+    // the tile's biases: rows 8q + 4 (lane >> 5) + (0..3) for q = 0..3 (rows past n read 0 and
+    // are masked); kept for all fragments where the registers allow it
+    constexpr bool kKeepBias = RM == 1 && NCH <= 8;
+    float bv[RM][16];
+    auto load_bias = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < RM; ++r) {
+        const int64_t blk = min<int64_t>(tile * RM + r, nblocks - 1);
+        const __amdgpu_buffer_rsrc_t rs =
+            rows_rsrc(A.bias + blk * kFrag, (int)min<int64_t>(kFrag, A.items.n - blk * kFrag) * 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const u32x4_t v = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (lane >> 5) * 16 + q * 32, 0, 0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bv[r][4 * q + e] = __uint_as_float(v[e]);
+        }
+      }
+    };
+    if (kKeepBias && A.bias) load_bias();
     // One fragment: `cur` holds its scores, `nxt` receives those of the next one, whose products
     // run while this one's exponentials are taken.
     auto fragment = [&](f32x16_t (&cur)[RM], f32x16_t (&nxt)[RM], int f) __attribute__((always_inline)) {
       if (A.bias) {
-        // rows 8q + 4 (lane >> 5) + (0..3) for q = 0..3 (rows past n read 0 and are masked)
+        if (!kKeepBias) load_bias();
 #pragma unroll
-        for (int r = 0; r < RM; ++r) {
-          const int64_t blk = min<int64_t>(tile * RM + r, nblocks - 1);
-          const __amdgpu_buffer_rsrc_t rs =
-              rows_rsrc(A.bias + blk * kFrag, (int)min<int64_t>(kFrag, A.items.n - blk * kFrag) * 4);
+        for (int r = 0; r < RM; ++r)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const u32x4_t v = __builtin_bit_cast(
-                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (lane >> 5) * 16 + q * 32, 0, 0));
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              cur[r][4 * q + e] = __fadd_rn(__fmul_rn(cur[r][4 * q + e], A.scale), __uint_as_float(v[e]));
-          }
-        }
+          for (int i = 0; i < 16; ++i) cur[r][i] = __fadd_rn(__fmul_rn(cur[r][i], A.scale), bv[r][i]);
       }
       if (any != 0u) {
         // Register i holds row 8 (i >> 2) + (i & 3) in lanes 0-31 and that row + 4 in lanes
@@ -227,11 +238,15 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       for (int r = 0; r < RM; ++r)
 #pragma unroll
         for (int i = 0; i < 16; ++i) vm = fmaxf(vm, cur[r][i]);
-      if (A.bmax) {
+      if constexpr (BM) {
         const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(vm), __float_as_uint(vm), false, false);
         const float v2 = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));  // both halves' rows
         const float l = v2 * A.scx <= kEmpty ? -INFINITY : (A.bias ? v2 : v2 * A.scale);
-        if (lane < kFrag) A.bmax[((int64_t)(qbase / kFrag + f) * A.ntiles + tile) * kFrag + lane] = l;
+        // unconditional, the upper lanes out of the buffer's range: a store that may or may not
+        // be issued makes the compiler's wait counts for the item loads behind it inexact
+        const __amdgpu_buffer_rsrc_t rs =
+            rows_rsrc(A.bmax + ((int64_t)(qbase / kFrag + f) * A.ntiles + tile) * kFrag, kFrag * 4);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), rs, lane * 4, 0, 0);
       }
       const float mn = vm * A.scx;
       if (__builtin_expect(__ballot(mn > m + kSlack) != 0ull, 0)) {
@@ -343,20 +358,21 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
   }
 }
 
-template <int CT, int D, int NQF, bool ROWS, bool ENT>
+template <int CT, int D, int NQF, bool ROWS, int MODE>
 static int launch_stats_two(const StatsArgs& A, int grid, hipStream_t s) {
   constexpr int lds = stats_lds(CT, D, NQF);
-  static const hipError_t attr = hipFuncSetAttribute((const void*)stats_kernel<CT, D, NQF, ROWS, ENT>,
+  static const hipError_t attr = hipFuncSetAttribute((const void*)stats_kernel<CT, D, NQF, ROWS, MODE>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   (void)attr;
-  hipLaunchKernelGGL((stats_kernel<CT, D, NQF, ROWS, ENT>), dim3(grid), dim3(kStatsThreads), lds, s, A);
+  hipLaunchKernelGGL((stats_kernel<CT, D, NQF, ROWS, MODE>), dim3(grid), dim3(kStatsThreads), lds, s, A);
   return check_launch();
 }
 
 template <int CT, int D, int NQF, bool ROWS>
 static int launch_stats_one(const StatsArgs& A, int grid, hipStream_t s) {
-  return A.ent ? launch_stats_two<CT, D, NQF, ROWS, true>(A, grid, s)
-               : launch_stats_two<CT, D, NQF, ROWS, false>(A, grid, s);
+  if (A.bmax) return launch_stats_two<CT, D, NQF, ROWS, STATS_ALT>(A, grid, s);
+  return A.ent ? launch_stats_two<CT, D, NQF, ROWS, STATS_ENT>(A, grid, s)
+               : launch_stats_two<CT, D, NQF, ROWS, STATS_LSE>(A, grid, s);
 }
 
 template <int CT, int D>

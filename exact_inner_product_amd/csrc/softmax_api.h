@@ -38,6 +38,9 @@ struct Table {
   int row_b;
 };
 
+// What the statistics pass computes: the sum, the entropy's sum too, or both and tile maxima.
+enum { STATS_LSE = 0, STATS_ENT = 1, STATS_ALT = 2 };
+
 struct StatsArgs {
   Table items, queries;
   int b;
