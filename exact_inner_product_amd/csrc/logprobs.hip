@@ -2,34 +2,34 @@
 // the log-sum-exp, the entropy and the most likely alternatives (gfx950): the entry point and
 // the passes behind the statistics pass of softmax.h.
 //
-// Alternatives. The statistics pass leaves each tile's largest logit per query. The k best items
-// lie in the k best tiles, ordered by (largest logit descending, tile ascending): for an item
-// outside them, each of those k tiles holds an item with a larger logit, or with an equal one
-// and a lower id. The same holds for groups of tiles. So the finish pass picks the k best
-// groups, among their tiles the k best, scores those tiles' rows again with the same matrix
+// Alternatives. The statistics pass leaves the largest logit of each run of tiles per query. The
+// k best items lie in the k best runs, ordered by (largest logit descending, run ascending): for
+// an item outside them, each of those k runs holds an item with a larger logit, or with an equal
+// one and a lower id. The same holds for groups of runs. So the finish pass picks the k best
+// groups, among their runs the k best, scores those runs' rows again with the same matrix
 // instructions (bitwise the same scores) and picks the k best rows: exact, with ties by the
-// lowest id, at the cost of k tiles of rows a query instead of a second pass over the table.
+// lowest id, at the cost of k runs of rows a query instead of a second pass over the table.
 #include "host.h"
-#include "select.h"
 #include "softmax_api.h"
 
 namespace mips {
 
 constexpr int kGroupThreads = 256;
-constexpr int64_t kTopDirect = 2048;   // tiles that the finish pass reads without groups
+constexpr int64_t kTopDirect = 2048;   // runs that the finish pass reads without groups
 constexpr int64_t kTopGroups = 16384;  // groups that it reads, at most
-constexpr size_t kBmaxBytes = size_t(1) << 30;  // tile maxima of one batch of queries, at most
+constexpr int64_t kKeyBytes = 32 * 1024;  // keys of the rescored rows, at most
+constexpr size_t kBmaxBytes = size_t(1) << 30;  // run maxima of one batch of queries, at most
 
-// The largest value of each group of `per` tiles, for 32 queries at a time: one thread per
+// The largest value of each group of `per` runs, for 32 queries at a time: one thread per
 // (query column, group), reading 128-byte rows of the maxima.
-__global__ __launch_bounds__(kGroupThreads) void group_max_kernel(const float* __restrict__ bmax, int64_t ntiles,
+__global__ __launch_bounds__(kGroupThreads) void group_max_kernel(const float* __restrict__ bmax, int64_t nruns,
                                                                   int per, int64_t ngroups, int64_t gblocks,
                                                                   float* __restrict__ gmax) {
   const int64_t f = blockIdx.x / gblocks;
   const int64_t g = (blockIdx.x % gblocks) * (kGroupThreads / kFrag) + (threadIdx.x >> 5);
   if (g >= ngroups) return;
-  const int64_t t0 = g * per, t1 = min(ntiles, t0 + per);
-  const float* p = bmax + f * ntiles * kFrag + (threadIdx.x & 31);
+  const int64_t t0 = g * per, t1 = min(nruns, t0 + per);
+  const float* p = bmax + f * nruns * kFrag + (threadIdx.x & 31);
   float m = -INFINITY;
 #pragma unroll 8
   for (int64_t t = t0; t < t1; ++t) m = fmaxf(m, p[t * kFrag]);
@@ -49,8 +49,8 @@ struct FinishArgs {
   const void* ids;           // [b, g]
   int id_bits, g, k;
   const float *bmax, *gmax;  // gmax NULL: no groups
-  int64_t ntiles, ngroups;
-  int per, rm;
+  int64_t nruns, ngroups;
+  int per, rm;               // runs of a group, 32-row blocks of a run
   float *logprobs, *lse, *entropy, *alt_logprobs;
   int32_t* alt_ids;
 };
@@ -229,26 +229,27 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
 
 // With alternatives: one workgroup per query joins the slices' statistics, scores the given ids
 // and picks the alternatives.
+constexpr int kFinThreads = 512;
+constexpr int kFinWaves = kFinThreads / kWave;
 constexpr int kPickCap = 256;  // candidates of a pick that are ranked by counting
 
 template <int CT, bool ROWS>
-__global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
+__global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];  // keys of the rescored rows
   __shared__ u32x4_t q[64];        // the query: slot 2c + h
-  __shared__ float4 red[4];
-  __shared__ float scr[4][kFrag];
+  __shared__ float4 red[kFinWaves];
+  __shared__ float scr[kFinWaves][kFrag];
   __shared__ uint64_t found[kPickCap];
-  __shared__ __attribute__((aligned(16))) uint32_t maxima[kSelThreads];
+  __shared__ __attribute__((aligned(16))) uint32_t maxima[kFinThreads];
   __shared__ uint64_t best[MIPS_ALTERNATIVES_MAX];
   __shared__ int64_t list[MIPS_ALTERNATIVES_MAX];
-  __shared__ SelScratch S;
   __shared__ uint32_t cnt;
   const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
 
   const int nch = (A.items.row_b + 31) / 32;
-  for (int i = t; i < 2 * nch; i += kSelThreads) q[i] = query_slot(A, b, i >> 1, i & 1);
+  for (int i = t; i < 2 * nch; i += kFinThreads) q[i] = query_slot(A, b, i >> 1, i & 1);
   Stats st;
-  for (int s = t; s < A.nslices; s += kSelThreads) {
+  for (int s = t; s < A.nslices; s += kFinThreads) {
     const float4 p = A.part[(int64_t)s * A.b + b];
     st.join(p.x, p.y, p.z);
   }
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   if (lane == 0) red[wave] = make_float4(st.m, st.z, st.x, 0.0f);
   __syncthreads();
   st.m = red[0].x, st.z = red[0].y, st.x = red[0].z;
-  for (int w = 1; w < 4; ++w) st.join(red[w].x, red[w].y, red[w].z);
+  for (int w = 1; w < kFinWaves; ++w) st.join(red[w].x, red[w].y, red[w].z);
   const float lse = st.lse();
   if (t == 0) {
     A.lse[b] = lse;
@@ -264,7 +265,7 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   }
 
   // given ids, 32 a wave at a time (the last wave first: the picks begin with the first)
-  for (int g0 = (3 - wave) * kFrag; g0 < A.g; g0 += 4 * kFrag) {
+  for (int g0 = (kFinWaves - 1 - wave) * kFrag; g0 < A.g; g0 += kFinWaves * kFrag) {
     const int gi = g0 + (lane & 31);
     const int64_t at = (int64_t)b * A.g + (gi < A.g ? gi : A.g - 1);
     bool pad;
@@ -279,21 +280,26 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
 
   // The min(k, candidates) best of n distinct keys, sorted, in best[]; keys of 0 are no
   // candidates. Returns their number. Each thread takes the largest of its keys; the k-th
-  // largest score among these 256 is a bound that k keys reach, and few others do when the best
-  // keys are spread over the threads. Every wave finds it by itself, bit by bit, from all 256
-  // maxima (4 a lane). The keys that reach it are ranked by counting the larger ones. Where
-  // more than kPickCap reach it, the radix select finds the k best.
+  // largest score among those of 256 pairs of threads is a bound that k keys reach, and few
+  // others do when the best keys are spread over the threads. Every wave finds it by itself, bit
+  // by bit, from all 256 (4 a lane). The keys that reach it are ranked by counting the larger
+  // ones. Where more than kPickCap reach it, the bound is found among all keys, bit by bit over
+  // their 64 bits.
   auto pick = [&](auto get, int64_t n) __attribute__((always_inline)) {
     uint64_t mine = 0ull;
-#pragma unroll 8
-    for (int64_t i = t; i < n; i += kSelThreads) {
+#pragma unroll 4
+    for (int64_t i = t; i < n; i += kFinThreads) {
       const uint64_t key = get(i);
       mine = key > mine ? key : mine;
     }
     maxima[t] = (uint32_t)(mine >> 32);
     if (t == 0) cnt = 0u;
     __syncthreads();
-    const uint4 m4 = *(const uint4*)(maxima + 4 * lane);
+    uint4 m4 = *(const uint4*)(maxima + 4 * lane);
+    {
+      const uint4 o = *(const uint4*)(maxima + 256 + 4 * lane);
+      m4 = make_uint4(max(m4.x, o.x), max(m4.y, o.y), max(m4.z, o.z), max(m4.w, o.w));
+    }
     uint32_t bound = 0u;
 #pragma unroll
     for (int bit = 31; bit >= 0; --bit) {
@@ -302,23 +308,40 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
                         __popcll(__ballot(m4.z >= c)) + __popcll(__ballot(m4.w >= c));
       bound = above >= A.k ? c : bound;
     }
-    const uint64_t least = bound == 0u ? 1ull : (uint64_t)bound << 32;
-#pragma unroll 8
-    for (int64_t i = t; i < n; i += kSelThreads) {
-      const uint64_t key = get(i);
-      if (key >= least) {
-        const uint32_t slot = atomicAdd(&cnt, 1u);
-        if (slot < (uint32_t)kPickCap) found[slot] = key;
+    uint64_t least = bound == 0u ? 1ull : (uint64_t)bound << 32;
+    auto collect = [&]() __attribute__((always_inline)) {
+#pragma unroll 4
+      for (int64_t i = t; i < n; i += kFinThreads) {
+        const uint64_t key = get(i);
+        if (key >= least) {
+          const uint32_t slot = atomicAdd(&cnt, 1u);
+          if (slot < (uint32_t)kPickCap) found[slot] = key;
+        }
       }
+      __syncthreads();
+    };
+    collect();
+    if (cnt > (uint32_t)kPickCap) {
+      uint64_t bound64 = 0ull;
+      for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t c = bound64 | (1ull << bit);
+        uint32_t above = 0u;
+        for (int64_t i = t; i < n; i += kFinThreads) above += get(i) >= c ? 1u : 0u;
+        __syncthreads();
+        if (t == 0) cnt = 0u;
+        __syncthreads();
+        atomicAdd(&cnt, above);
+        __syncthreads();
+        bound64 = cnt >= (uint32_t)A.k ? c : bound64;
+      }
+      least = bound64;  // (more than kPickCap >= k candidates: it is one of them)
+      __syncthreads();
+      if (t == 0) cnt = 0u;
+      __syncthreads();
+      collect();
     }
-    __syncthreads();
     const int c = (int)cnt;
     const int r = min(c, A.k);
-    if (c > kPickCap) {
-      const Sel64 sel = select_top(get, n, r, S);
-      gather_sort(get, n, r, sel, best, &cnt);
-      return r;
-    }
     if (t < c) {
       const uint64_t key = found[t];
       int rank = 0;
@@ -329,7 +352,7 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
     __syncthreads();
     return r;
   };
-  auto tile_key = [&](float v, int64_t i) __attribute__((always_inline)) {
+  auto run_key = [&](float v, int64_t i) __attribute__((always_inline)) {
     return v == -INFINITY ? 0ull : composite(score_key(v), (uint32_t)i);
   };
   const int64_t f = b / kFrag;
@@ -337,21 +360,21 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   int r;
   if (A.gmax) {
     const float* gm = A.gmax + f * A.ngroups * kFrag + col;
-    r = pick([&](int64_t i) { return tile_key(gm[i * kFrag], i); }, A.ngroups);
+    r = pick([&](int64_t i) { return run_key(gm[i * kFrag], i); }, A.ngroups);
     if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.per;
     __syncthreads();
-    const float* bm = A.bmax + f * A.ntiles * kFrag + col;
+    const float* bm = A.bmax + f * A.nruns * kFrag + col;
     r = pick(
         [&](int64_t i) {
-          const int64_t tile = list[i / A.per] + i % A.per;
-          return tile < A.ntiles ? tile_key(bm[tile * kFrag], tile) : 0ull;
+          const int64_t u = list[i / A.per] + i % A.per;
+          return u < A.nruns ? run_key(bm[u * kFrag], u) : 0ull;
         },
         (int64_t)r * A.per);
   } else {
-    const float* bm = A.bmax + f * A.ntiles * kFrag + col;
-    r = pick([&](int64_t i) { return tile_key(bm[i * kFrag], i); }, A.ntiles);
+    const float* bm = A.bmax + f * A.nruns * kFrag + col;
+    r = pick([&](int64_t i) { return run_key(bm[i * kFrag], i); }, A.nruns);
   }
-  if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.rm;  // first 32-row block of the tile
+  if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.rm;  // first 32-row block of the run
   __syncthreads();
   uint64_t* keys = (uint64_t*)dyn;
   const int nb = r * A.rm;
@@ -364,14 +387,14 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
     load_chunks<ROWS>(A.items, min<int64_t>(row_of(i), A.items.n - 1), 0, nch, ahead);
   };
   if (wave < nb) fetch(wave);
-  for (int i = wave; i < nb; i += 4) {
+  for (int i = wave; i < nb; i += kFinWaves) {
     const int64_t row = row_of(i);
     const bool live = row < A.items.n;
     const int64_t rl = live ? row : A.items.n - 1;
     u32x4_t now[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) now[u] = ahead[u];
-    if (i + 4 < nb) fetch(i + 4);
+    if (i + kFinWaves < nb) fetch(i + kFinWaves);
     const float s = score_row<CT, ROWS>(A, q, rl, scr[wave], now);
     if (lane < kFrag)
       keys[i * kFrag + lane] =
@@ -379,7 +402,7 @@ __global__ __launch_bounds__(kSelThreads) void finish_kernel(FinishArgs A) {
   }
   __syncthreads();
   r = pick([&](int64_t i) { return keys[i]; }, (int64_t)nb * kFrag);
-  for (int i = t; i < A.k; i += kSelThreads) {
+  for (int i = t; i < A.k; i += kFinThreads) {
     const int64_t at = (int64_t)b * A.k + i;
     A.alt_ids[at] = i < r ? (int32_t)composite_id(best[i]) : -1;
     A.alt_logprobs[at] = i < r ? key_score((uint32_t)(best[i] >> 32)) - lse : -INFINITY;
@@ -396,8 +419,8 @@ static int width_of(int dtype, int row_b) {  // the kernels' width for rows of r
 
 struct StatsPlan {
   int width, nqf, nqblk, nslices, qbatch;
-  int64_t ntiles, ngroups;
-  int per;
+  int64_t ntiles, nruns, ngroups;
+  int per, run_log;
   size_t part, bmax, gmax, bytes;
 };
 
@@ -411,21 +434,30 @@ static StatsPlan stats_plan(int b, int64_t n, int d, int dtype, int k) {
   P.width = width_of(dtype, d * elem_bytes(dtype));
   const int rm = stats_rm(dtype, P.width);
   P.ntiles = (n + kFrag * rm - 1) / (kFrag * rm);
+  const int cus = device_cu_count();
   P.ngroups = 0;
   P.per = 0;
+  P.run_log = 0;
   P.qbatch = b;
   if (k > 0) {
-    // queries of one batch: their tile maxima stay within kBmaxBytes
-    const int64_t q = (int64_t)(kBmaxBytes / (size_t)(P.ntiles * 4)) / kFrag * kFrag;
+    // Runs of up to 4 tiles, as long as a wave has 16 runs and the k runs' keys fit 32 KiB: a
+    // store of maxima per tile took 100 of 549 us at 50 x 10M x 128.
+    while (P.run_log < 2 && (P.ntiles >> (P.run_log + 1)) >= (int64_t)cus * kStatsWaves * 16 &&
+           ((int64_t)k * rm << (P.run_log + 1)) * kFrag * 8 <= kKeyBytes)
+      ++P.run_log;
+  }
+  P.nruns = (P.ntiles + (1 << P.run_log) - 1) >> P.run_log;
+  if (k > 0) {
+    // queries of one batch: their run maxima stay within kBmaxBytes
+    const int64_t q = (int64_t)(kBmaxBytes / (size_t)(P.nruns * 4)) / kFrag * kFrag;
     if (q < b) P.qbatch = (int)(q < kFrag ? kFrag : q);
-    if (P.ntiles > kTopDirect) {
-      // groups of about sqrt(tiles / k): as many group maxima to read as tiles of k groups
+    if (P.nruns > kTopDirect) {
+      // groups of about sqrt(runs / k): as many group maxima to read as runs of k groups
       P.per = 32;
-      while ((int64_t)P.per * P.per * k < P.ntiles || (P.ntiles + P.per - 1) / P.per > kTopGroups) P.per *= 2;
-      P.ngroups = (P.ntiles + P.per - 1) / P.per;
+      while ((int64_t)P.per * P.per * k < P.nruns || (P.nruns + P.per - 1) / P.per > kTopGroups) P.per *= 2;
+      P.ngroups = (P.nruns + P.per - 1) / P.per;
     }
   }
-  const int cus = device_cu_count();
   const double tile_us = dtype == MIPS_F32 ? 0.45 * rm * (0.5 + P.width / 32.0) : 0.45 * rm * (0.5 + P.width / 256.0);
   const double tile_bytes = (double)rm * block_bytes(dtype, P.width);
   double best = 1e30;
@@ -433,9 +465,9 @@ static StatsPlan stats_plan(int b, int64_t n, int d, int dtype, int k) {
     if (!stats_fits(dtype, P.width, nqf)) break;
     const int nqblk = (P.qbatch + kFrag * nqf - 1) / (kFrag * nqf);
     const int frags = nqblk == 1 ? (P.qbatch + kFrag - 1) / kFrag : nqf;
-    // slices of at least one tile a wave; a multiple of 8 (XCDs) where there are that many
+    // slices of at least one run a wave; a multiple of 8 (XCDs) where there are that many
     int64_t s = cus / nqblk;
-    const int64_t most = (P.ntiles + kStatsWaves - 1) / kStatsWaves;
+    const int64_t most = (P.nruns + kStatsWaves - 1) / kStatsWaves;
     if (s > most) s = most;
     if (s >= 8) s = s / 8 * 8;
     if (s < 1) s = 1;
@@ -460,7 +492,7 @@ static StatsPlan stats_plan(int b, int64_t n, int d, int dtype, int k) {
   const size_t q32 = (size_t)((P.qbatch + kFrag - 1) / kFrag) * kFrag;
   P.part = take((size_t)P.nslices * P.qbatch * sizeof(float4));
   if (k > 0) {
-    P.bmax = take(q32 * P.ntiles * 4);
+    P.bmax = take(q32 * P.nruns * 4);
     if (P.ngroups) P.gmax = take(q32 * P.ngroups * 4);
   }
   P.bytes = at;
@@ -491,12 +523,12 @@ template <int CT, bool ROWS>
 static int launch_finish(const FinishArgs& A, int b, hipStream_t s) {
   static const hipError_t attr =
       hipFuncSetAttribute((const void*)finish_kernel<CT, ROWS>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                          MIPS_ALTERNATIVES_MAX * 2 * kFrag * 8);
+                          kKeyBytes);
   (void)attr;
   if (A.k == 0)
     hipLaunchKernelGGL((pairs_kernel<CT, ROWS>), dim3((b + kFrag - 1) / kFrag), dim3(256), 0, s, A);
   else
-    hipLaunchKernelGGL((finish_kernel<CT, ROWS>), dim3(b), dim3(kSelThreads), (size_t)A.k * A.rm * kFrag * 8, s, A);
+    hipLaunchKernelGGL((finish_kernel<CT, ROWS>), dim3(b), dim3(kFinThreads), (size_t)A.k * A.rm * kFrag * 8, s, A);
   return check_launch();
 }
 
@@ -573,14 +605,15 @@ int mips_logprobs(const void* queries, int64_t query_stride, int32_t b, const vo
     A.nqblk = (nb + kFrag * P.nqf - 1) / (kFrag * P.nqf);
     A.ent = out_entropy != nullptr;
     A.nslices = P.nslices;
-    A.ntiles = P.ntiles;
+    A.nruns = P.nruns;
+    A.run_log = P.run_log;
     A.part = (float4*)(ws + P.part);
     A.bmax = k > 0 ? (float*)(ws + P.bmax) : nullptr;
     if (const int rc = stats_dispatch(dtype, P.width, P.nqf, rows, A, A.nqblk * P.nslices, s)) return rc;
     if (P.ngroups) {
       const int64_t gblocks = (P.ngroups + 7) / 8;
       const int64_t nf = (nb + kFrag - 1) / kFrag;
-      hipLaunchKernelGGL(group_max_kernel, dim3((unsigned)(gblocks * nf)), dim3(kGroupThreads), 0, s, A.bmax, P.ntiles,
+      hipLaunchKernelGGL(group_max_kernel, dim3((unsigned)(gblocks * nf)), dim3(kGroupThreads), 0, s, A.bmax, P.nruns,
                          P.per, P.ngroups, gblocks, (float*)(ws + P.gmax));
       if (const int rc = check_launch()) return rc;
     }
@@ -601,10 +634,10 @@ int mips_logprobs(const void* queries, int64_t query_stride, int32_t b, const vo
     F.k = k;
     F.bmax = A.bmax;
     F.gmax = P.ngroups ? (float*)(ws + P.gmax) : nullptr;
-    F.ntiles = P.ntiles;
+    F.nruns = P.nruns;
     F.ngroups = P.ngroups;
     F.per = P.per;
-    F.rm = stats_rm(dtype, P.width);
+    F.rm = stats_rm(dtype, P.width) << P.run_log;
     F.logprobs = g > 0 ? out_logprobs + (int64_t)q0 * g : nullptr;
     F.lse = out_lse + q0;
     F.entropy = out_entropy ? out_entropy + q0 : nullptr;

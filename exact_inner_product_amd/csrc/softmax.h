@@ -113,16 +113,23 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       dst[i] = v;
     }
   }
-  float* st = (float*)(lds + (size_t)QB * D * E) + (size_t)wave * NQF * 3 * kWave + lane;
+  constexpr int SV = stats_values(MODE);
+  float* st = (float*)(lds + (size_t)QB * D * E) + (size_t)wave * NQF * SV * kWave + lane;
   for (int f = 0; f < NQF; ++f) {
-    st[(3 * f + 0) * kWave] = kMasked;
-    st[(3 * f + 1) * kWave] = 0.0f;
-    st[(3 * f + 2) * kWave] = 0.0f;
+    st[(SV * f + 0) * kWave] = kMasked;
+    st[(SV * f + 1) * kWave] = 0.0f;
+    st[(SV * f + 2) * kWave] = 0.0f;
   }
   __syncthreads();
 
-  const int64_t t_begin = (int64_t)slice * A.ntiles / A.nslices;
-  const int64_t t_end = (int64_t)(slice + 1) * A.ntiles / A.nslices;
+  // Tiles go in runs of 2^run_log consecutive ones, a wave's runs kStatsWaves apart: the run
+  // is the unit of the maxima. Tile i of this wave, of `count`:
+  const int run = 1 << A.run_log;
+  const int64_t r_begin = (int64_t)slice * A.nruns / A.nslices, r_end = (int64_t)(slice + 1) * A.nruns / A.nslices;
+  const int64_t count = (r_end - r_begin - wave + kStatsWaves - 1) / kStatsWaves * run;
+  auto tile_of = [&](int64_t i) __attribute__((always_inline)) {
+    return ((r_begin + wave + (i >> A.run_log) * kStatsWaves) << A.run_log) + (i & (run - 1));
+  };
   const int64_t nblocks = (A.items.n + kFrag - 1) / kFrag;
 
   // A stage's loads are unconditional (blocks past the end read the last block again and are
@@ -167,7 +174,8 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
   for (int c = 0; c < kLook; ++c) bq[c] = ((const u32x4_t*)lds + lane)[c * 64];
 
-  auto compute_stage = [&](const u32x4_t (&a)[RM][NCH], uint32_t xraw, int64_t tile) __attribute__((always_inline)) {
+  auto compute_stage = [&](const u32x4_t (&a)[RM][NCH], uint32_t xraw, int64_t i_tile) __attribute__((always_inline)) {
+    const int64_t tile = tile_of(i_tile);
     // words of the tile's blocks, rows past n set; uniform
     uint32_t word[RM], any = 0u;
 #pragma unroll
@@ -232,7 +240,7 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
           for (int i = 0; i < 16; ++i) cur[r][i] = ((bits >> i) & 1u) ? A.vmask : cur[r][i];
         }
       }
-      float m = st[(3 * f + 0) * kWave], z = st[(3 * f + 1) * kWave], x = st[(3 * f + 2) * kWave];
+      float m = st[(SV * f + 0) * kWave], z = st[(SV * f + 1) * kWave], x = st[(SV * f + 2) * kWave];
       float vm = cur[0][0];
 #pragma unroll
       for (int r = 0; r < RM; ++r)
@@ -241,12 +249,17 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       if constexpr (BM) {
         const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(vm), __float_as_uint(vm), false, false);
         const float v2 = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));  // both halves' rows
-        const float l = v2 * A.scx <= kEmpty ? -INFINITY : (A.bias ? v2 : v2 * A.scale);
-        // unconditional, the upper lanes out of the buffer's range: a store that may or may not
-        // be issued makes the compiler's wait counts for the item loads behind it inexact
-        const __amdgpu_buffer_rsrc_t rs =
-            rows_rsrc(A.bmax + ((int64_t)(qbase / kFrag + f) * A.ntiles + tile) * kFrag, kFrag * 4);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), rs, lane * 4, 0, 0);
+        // the run's maximum so far, stored behind its last tile
+        const int in_run = (int)(i_tile & (run - 1));
+        const float v3 = in_run == 0 ? v2 : fmaxf(v2, st[(SV * f + 3) * kWave]);
+        st[(SV * f + 3) * kWave] = v3;
+        const float l = v3 * A.scx <= kEmpty ? -INFINITY : (A.bias ? v3 : v3 * A.scale);
+        // the store is unconditional, out of the buffer's range where nothing is to be stored (the
+        // upper lanes, the earlier tiles): one that may or may not be issued makes the compiler's
+        // wait counts for the item loads behind it inexact
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(
+            A.bmax + ((int64_t)(qbase / kFrag + f) * A.nruns + (tile >> A.run_log)) * kFrag, kFrag * 4);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), rs, in_run == run - 1 ? lane * 4 : 1024, 0, 0);
       }
       const float mn = vm * A.scx;
       if (__builtin_expect(__ballot(mn > m + kSlack) != 0ull, 0)) {
@@ -288,9 +301,9 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
         }
         if constexpr (NQF > 1) __builtin_amdgcn_sched_barrier(0);
       }
-      st[(3 * f + 0) * kWave] = m;
-      st[(3 * f + 1) * kWave] = z + (z0 + z1);
-      if constexpr (ENT) st[(3 * f + 2) * kWave] = x + (x0 + x1);
+      st[(SV * f + 0) * kWave] = m;
+      st[(SV * f + 1) * kWave] = z + (z0 + z1);
+      if constexpr (ENT) st[(SV * f + 2) * kWave] = x + (x0 + x1);
     };
     f32x16_t acc0[RM], acc1[RM];
 #pragma unroll
@@ -313,26 +326,26 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
 
   u32x4_t a[NS][RM][NCH];
   uint32_t xw[NS];
-  int64_t t = t_begin + wave;
-  if (t < t_end) {
+  int64_t i = 0;
+  if (count > 0) {
     unroll_for<NS - 1>([&](auto uc) __attribute__((always_inline)) {
       constexpr int u = decltype(uc)::value;
-      load_stage(a[u], xw[u], t + u * kStatsWaves);
+      load_stage(a[u], xw[u], tile_of(i + u));
     });
     auto step = [&](auto uc) __attribute__((always_inline)) {
       constexpr int u = decltype(uc)::value;
       constexpr int ld = (u + NS - 1) % NS;
-      load_stage(a[ld], xw[ld], t + (u + NS - 1) * kStatsWaves);
-      compute_stage(a[u], xw[u], t + u * kStatsWaves);
-      return t + (u + 1) * kStatsWaves >= t_end;
+      load_stage(a[ld], xw[ld], tile_of(i + u + NS - 1));
+      compute_stage(a[u], xw[u], i + u);
+      return i + u + 1 >= count;
     };
     if constexpr (NS == 3) {
       while (!(step(std::integral_constant<int, 0>{}) || step(std::integral_constant<int, 1>{}) ||
                step(std::integral_constant<int, 2>{})))
-        t += NS * kStatsWaves;
+        i += NS;
     } else {
       while (!(step(std::integral_constant<int, 0>{}) || step(std::integral_constant<int, 1>{})))
-        t += NS * kStatsWaves;
+        i += NS;
     }
   }
   __syncthreads();
@@ -341,7 +354,7 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
   const float* all = (const float*)(lds + (size_t)QB * D * E);
   for (int q = threadIdx.x; q < nq; q += kStatsThreads) {
     const int f = q / kFrag, l = q % kFrag;
-    auto at = [&](int w, int k) { return all[((w >> 1) * NQF * 3 + 3 * f + k) * kWave + l + 32 * (w & 1)]; };
+    auto at = [&](int w, int k) { return all[((w >> 1) * NQF * SV + SV * f + k) * kWave + l + 32 * (w & 1)]; };
     float m = kMasked;
     for (int w = 0; w < 2 * kStatsWaves; ++w) m = fmaxf(m, at(w, 0));
     float z = 0.0f, x = 0.0f;
@@ -360,7 +373,7 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
 
 template <int CT, int D, int NQF, bool ROWS, int MODE>
 static int launch_stats_two(const StatsArgs& A, int grid, hipStream_t s) {
-  constexpr int lds = stats_lds(CT, D, NQF);
+  constexpr int lds = stats_lds(CT, D, NQF, MODE);
   static const hipError_t attr = hipFuncSetAttribute((const void*)stats_kernel<CT, D, NQF, ROWS, MODE>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   (void)attr;

@@ -51,10 +51,11 @@ struct StatsArgs {
   float scx;                 // log2 units per unit of a score (no bias) or of a logit
   float vmask;               // a masked score or logit: kMasked / scx
   int nqblk, nslices;
-  int64_t ntiles;
+  int64_t nruns;             // runs of 2^run_log tiles
+  int run_log;
   int ent;                   // whether the entropy's sums are wanted
   float4* part;              // [nslices][b]: reference, sum, sum of e * exponent
-  float* bmax;               // [ceil(b/32)][ntiles][32] largest logit of each tile, or NULL
+  float* bmax;               // [ceil(b/32)][nruns][32] largest logit of each run, or NULL
 };
 
 // 32-row blocks per tile of the pass: 8 KiB of items a wave and stage, at most 2 (more
@@ -69,10 +70,12 @@ __host__ __device__ constexpr int stats_ns(int ct, int d) {
 }
 constexpr int kStatsThreads = 512;
 constexpr int kStatsWaves = 8;
-// LDS of a workgroup of 32 * nqf queries: the query tile and three values per wave, query
-// fragment and lane.
-__host__ __device__ constexpr int stats_lds(int ct, int d, int nqf) {
-  return kFrag * nqf * d * elem_bytes(ct) + kStatsWaves * nqf * 3 * kWave * 4;
+// Values kept per wave, query fragment and lane: reference, sum, the entropy's sum, and the run's
+// maximum where it is wanted.
+__host__ __device__ constexpr int stats_values(int mode) { return mode == STATS_ALT ? 4 : 3; }
+// LDS of a workgroup of 32 * nqf queries: the query tile and those values.
+__host__ __device__ constexpr int stats_lds(int ct, int d, int nqf, int mode = STATS_ALT) {
+  return kFrag * nqf * d * elem_bytes(ct) + kStatsWaves * nqf * stats_values(mode) * kWave * 4;
 }
 __host__ __device__ constexpr bool stats_fits(int ct, int d, int nqf) {
   return stats_lds(ct, d, nqf) <= 160 * 1024;

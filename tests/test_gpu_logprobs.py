@@ -213,6 +213,26 @@ def test_packed_corpus_equals_its_rows(dtype, d):
         mips.item_logprobs(q, corpus, ids, model_version="b")
 
 
+def test_alternatives_whose_runs_fall_to_few_threads():
+    """The best items 512 tiles apart, so that the threads that look through the tiles' maxima
+    find them all in the same places: more candidates than are ranked at once."""
+    dev = _dev()
+    for n, d in ((65000, 128), (1_300_000, 16)):
+        items = torch.full((n, d), 2.0 ** -8)
+        items[:, 0] = 0.0
+        k = 64
+        where = torch.arange(0, n, 32)
+        # rising over tiles t = 0, 512, 1024 .. more than over their neighbours
+        items[where, 0] = ((where // 32 % 512 < 2).float() * 0.5).clamp(min=0)
+        items[where, 1] = (where // 32 % 251).float() / 256
+        q = torch.zeros(2, d)
+        q[:, 0] = 1.0
+        q[:, 1] = 0.25
+        items, q = items.bfloat16(), q.bfloat16()
+        r = mips.item_logprobs(q.to(dev), items.to(dev), scale=3.0, alternatives=k)
+        check(r, logits64(q, items, 3.0), None, k)
+
+
 def test_alternatives_are_the_searchs_results():
     dev = _dev()
     rng = np.random.default_rng(8)
