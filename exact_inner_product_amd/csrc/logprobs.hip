@@ -231,6 +231,8 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
 // and picks the alternatives.
 constexpr int kFinThreads = 512;
 constexpr int kFinWaves = kFinThreads / kWave;
+constexpr int kIdsKept = 128;  // given ids that are read ahead
+constexpr int kKept = 4;       // keys that a thread keeps in registers
 constexpr int kPickCap = 256;  // candidates of a pick that are ranked by counting
 
 template <int CT, bool ROWS>
@@ -243,41 +245,20 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
   __shared__ __attribute__((aligned(16))) uint32_t maxima[kFinThreads];
   __shared__ uint64_t best[MIPS_ALTERNATIVES_MAX];
   __shared__ int64_t list[MIPS_ALTERNATIVES_MAX];
+  __shared__ int32_t s_ids[kIdsKept];
   __shared__ uint32_t cnt;
   const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
 
-  const int nch = (A.items.row_b + 31) / 32;
-  for (int i = t; i < 2 * nch; i += kFinThreads) q[i] = query_slot(A, b, i >> 1, i & 1);
-  Stats st;
-  for (int s = t; s < A.nslices; s += kFinThreads) {
-    const float4 p = A.part[(int64_t)s * A.b + b];
-    st.join(p.x, p.y, p.z);
-  }
-  st.join_lanes(1, 32);
-  if (lane == 0) red[wave] = make_float4(st.m, st.z, st.x, 0.0f);
-  __syncthreads();
-  st.m = red[0].x, st.z = red[0].y, st.x = red[0].z;
-  for (int w = 1; w < kFinWaves; ++w) st.join(red[w].x, red[w].y, red[w].z);
-  const float lse = st.lse();
-  if (t == 0) {
-    A.lse[b] = lse;
-    if (A.entropy) A.entropy[b] = st.entropy();
-  }
-
-  // given ids, 32 a wave at a time (the last wave first: the picks begin with the first)
-  for (int g0 = (kFinWaves - 1 - wave) * kFrag; g0 < A.g; g0 += kFinWaves * kFrag) {
-    const int gi = g0 + (lane & 31);
-    const int64_t at = (int64_t)b * A.g + (gi < A.g ? gi : A.g - 1);
-    bool pad;
-    int64_t row;
-    read_ids(A, at, pad, row);
-    u32x4_t a[8];
-    load_chunks<ROWS>(A.items, row, 0, nch, a);
-    const float s = score_row<CT, ROWS>(A, q, row, scr[wave], a);
-    if (lane < kFrag && gi < A.g)
-      A.logprobs[at] = pad ? 0.0f : (excluded(A, b, row) ? -INFINITY : logit(A, s, row) - lse);
-  }
-
+  // everything that the first steps read is asked for at once
+  auto run_key = [&](float v, int64_t i) __attribute__((always_inline)) {
+    return v == -INFINITY ? 0ull : composite(score_key(v), (uint32_t)i);
+  };
+  const int64_t f = b / kFrag;
+  const int col = b % kFrag;
+  const float* bm = A.bmax + f * A.nruns * kFrag + col;
+  const float* top = A.gmax ? A.gmax + f * A.ngroups * kFrag + col : bm;  // the first pick's values
+  const int64_t ntop = A.gmax ? A.ngroups : A.nruns;
+  auto top_key = [&](int64_t i) __attribute__((always_inline)) { return run_key(top[i * kFrag], i); };
   // The min(k, candidates) best of n distinct keys, sorted, in best[]; keys of 0 are no
   // candidates. Returns their number. Each thread takes the largest of its keys; the k-th
   // largest score among those of 256 pairs of threads is a bound that k keys reach, and few
@@ -285,10 +266,20 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
   // by bit, from all 256 (4 a lane). The keys that reach it are ranked by counting the larger
   // ones. Where more than kPickCap reach it, the bound is found among all keys, bit by bit over
   // their 64 bits.
-  auto pick = [&](auto get, int64_t n) __attribute__((always_inline)) {
+  // A thread's first kKept keys stay in registers, loaded by keep().
+  auto keep = [&](auto get, int64_t n, uint64_t (&kept)[kKept]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kKept; ++u) {
+      const int64_t i = t + u * kFinThreads;
+      kept[u] = i < n ? get(i) : 0ull;
+    }
+  };
+  auto pick = [&](auto get, int64_t n, const uint64_t (&kept)[kKept]) __attribute__((always_inline)) {
     uint64_t mine = 0ull;
+#pragma unroll
+    for (int u = 0; u < kKept; ++u) mine = kept[u] > mine ? kept[u] : mine;
 #pragma unroll 4
-    for (int64_t i = t; i < n; i += kFinThreads) {
+    for (int64_t i = t + kKept * kFinThreads; i < n; i += kFinThreads) {
       const uint64_t key = get(i);
       mine = key > mine ? key : mine;
     }
@@ -310,14 +301,16 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     }
     uint64_t least = bound == 0u ? 1ull : (uint64_t)bound << 32;
     auto collect = [&]() __attribute__((always_inline)) {
-#pragma unroll 4
-      for (int64_t i = t; i < n; i += kFinThreads) {
-        const uint64_t key = get(i);
+      auto take = [&](uint64_t key) __attribute__((always_inline)) {
         if (key >= least) {
           const uint32_t slot = atomicAdd(&cnt, 1u);
           if (slot < (uint32_t)kPickCap) found[slot] = key;
         }
-      }
+      };
+#pragma unroll
+      for (int u = 0; u < kKept; ++u) take(kept[u]);
+#pragma unroll 4
+      for (int64_t i = t + kKept * kFinThreads; i < n; i += kFinThreads) take(get(i));
       __syncthreads();
     };
     collect();
@@ -352,56 +345,91 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     __syncthreads();
     return r;
   };
-  auto run_key = [&](float v, int64_t i) __attribute__((always_inline)) {
-    return v == -INFINITY ? 0ull : composite(score_key(v), (uint32_t)i);
-  };
-  const int64_t f = b / kFrag;
-  const int col = b % kFrag;
-  int r;
+  uint64_t kept[kKept];
+  keep(top_key, ntop, kept);
+  const int nch = (A.items.row_b + 31) / 32;
+  const int ng = (A.g + kFrag - 1) / kFrag;  // blocks of given ids
+  for (int i = t; i < min(A.g, kIdsKept); i += kFinThreads) {
+    bool pad;
+    int64_t row;
+    read_ids(A, (int64_t)b * A.g + i, pad, row);
+    s_ids[i] = pad ? -1 : (int32_t)row;
+  }
+  for (int i = t; i < 2 * nch; i += kFinThreads) q[i] = query_slot(A, b, i >> 1, i & 1);
+  Stats st;
+  for (int s = t; s < A.nslices; s += kFinThreads) {
+    const float4 p = A.part[(int64_t)s * A.b + b];
+    st.join(p.x, p.y, p.z);
+  }
+  st.join_lanes(1, 32);
+  if (lane == 0) red[wave] = make_float4(st.m, st.z, st.x, 0.0f);
+  __syncthreads();
+  st.m = red[0].x, st.z = red[0].y, st.x = red[0].z;
+  for (int w = 1; w < kFinWaves; ++w) st.join(red[w].x, red[w].y, red[w].z);
+  const float lse = st.lse();
+  if (t == 0) {
+    A.lse[b] = lse;
+    if (A.entropy) A.entropy[b] = st.entropy();
+  }
+
+  int r = pick(top_key, ntop, kept);
   if (A.gmax) {
-    const float* gm = A.gmax + f * A.ngroups * kFrag + col;
-    r = pick([&](int64_t i) { return run_key(gm[i * kFrag], i); }, A.ngroups);
     if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.per;
     __syncthreads();
-    const float* bm = A.bmax + f * A.nruns * kFrag + col;
-    r = pick(
-        [&](int64_t i) {
-          const int64_t u = list[i / A.per] + i % A.per;
-          return u < A.nruns ? run_key(bm[u * kFrag], u) : 0ull;
-        },
-        (int64_t)r * A.per);
-  } else {
-    const float* bm = A.bmax + f * A.nruns * kFrag + col;
-    r = pick([&](int64_t i) { return run_key(bm[i * kFrag], i); }, A.nruns);
+    auto key = [&](int64_t i) __attribute__((always_inline)) {
+      const int64_t u = list[i / A.per] + i % A.per;
+      return u < A.nruns ? run_key(bm[u * kFrag], u) : 0ull;
+    };
+    const int64_t n = (int64_t)r * A.per;
+    keep(key, n, kept);
+    r = pick(key, n, kept);
   }
   if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.rm;  // first 32-row block of the run
   __syncthreads();
+  // The rows of the runs and the given ids, 32 a wave at a time; each wave's next block is on
+  // its way while this one is scored.
   uint64_t* keys = (uint64_t*)dyn;
   const int nb = r * A.rm;
-  // each wave's next block is on its way while this one is scored
-  auto row_of = [&](int i) __attribute__((always_inline)) {
-    return (list[i / A.rm] + i % A.rm) * kFrag + (lane & 31);
+  auto row_of = [&](int i) __attribute__((always_inline)) -> int64_t {  // -1: padding
+    if (i < nb) return (list[i / A.rm] + i % A.rm) * kFrag + (lane & 31);
+    const int g = (i - nb) * kFrag + (lane & 31);
+    if (g >= A.g) return -1;
+    if (g < kIdsKept) return s_ids[g];
+    bool pad;
+    int64_t row;
+    read_ids(A, (int64_t)b * A.g + g, pad, row);
+    return pad ? -1 : row;
   };
   u32x4_t ahead[8];
+  int64_t next = -1;
   auto fetch = [&](int i) __attribute__((always_inline)) {
-    load_chunks<ROWS>(A.items, min<int64_t>(row_of(i), A.items.n - 1), 0, nch, ahead);
+    next = row_of(i);
+    load_chunks<ROWS>(A.items, max<int64_t>(0, min<int64_t>(next, A.items.n - 1)), 0, nch, ahead);
   };
-  if (wave < nb) fetch(wave);
-  for (int i = wave; i < nb; i += kFinWaves) {
-    const int64_t row = row_of(i);
-    const bool live = row < A.items.n;
-    const int64_t rl = live ? row : A.items.n - 1;
+  if (wave < nb + ng) fetch(wave);
+  for (int i = wave; i < nb + ng; i += kFinWaves) {
+    const int64_t row = next;
+    const bool live = row >= 0 && row < A.items.n;
+    const int64_t rl = live ? row : 0;
     u32x4_t now[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) now[u] = ahead[u];
-    if (i + kFinWaves < nb) fetch(i + kFinWaves);
+    if (i + kFinWaves < nb + ng) fetch(i + kFinWaves);
     const float s = score_row<CT, ROWS>(A, q, rl, scr[wave], now);
-    if (lane < kFrag)
-      keys[i * kFrag + lane] =
-          live && !excluded(A, b, rl) ? composite(score_key(logit(A, s, rl)), (uint32_t)rl) : 0ull;
+    const bool out = live && excluded(A, b, rl);
+    const float l = logit(A, s, rl);
+    if (lane >= kFrag) continue;
+    if (i < nb) {
+      keys[i * kFrag + lane] = live && !out ? composite(score_key(l), (uint32_t)rl) : 0ull;
+    } else {
+      const int g = (i - nb) * kFrag + lane;
+      if (g < A.g) A.logprobs[(int64_t)b * A.g + g] = !live ? 0.0f : (out ? -INFINITY : l - lse);
+    }
   }
   __syncthreads();
-  r = pick([&](int64_t i) { return keys[i]; }, (int64_t)nb * kFrag);
+  auto row_key = [&](int64_t i) __attribute__((always_inline)) { return keys[i]; };
+  keep(row_key, (int64_t)nb * kFrag, kept);
+  r = pick(row_key, (int64_t)nb * kFrag, kept);
   for (int i = t; i < A.k; i += kFinThreads) {
     const int64_t at = (int64_t)b * A.k + i;
     A.alt_ids[at] = i < r ? (int32_t)composite_id(best[i]) : -1;
