@@ -158,9 +158,8 @@ struct Stats {
     z = (m > kEmpty ? g0 * z : z) + (m2 > kEmpty ? g1 * z2 : z2);
     m = mn;
   }
-  __device__ __forceinline__ void join_lanes(int from, int to) {  // over lanes at distances from, 2 from .. to
-#pragma unroll
-    for (int o = from; o <= to; o <<= 1) {
+  __device__ __forceinline__ void join_lanes(int n) {  // over the first n (rounded up to 2^i) lanes
+    for (int o = 1; o < n; o <<= 1) {
       const float m2 = __shfl_xor(m, o, kWave), z2 = __shfl_xor(z, o, kWave), x2 = __shfl_xor(x, o, kWave);
       join(m2, z2, x2);
     }
@@ -196,7 +195,7 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
         const float4 p = A.part[(int64_t)s * A.b + b0 + q];
         S.join(p.x, p.y, p.z);
       }
-    S.join_lanes(1, 4);
+    S.join_lanes(8);
     if (sub == 0 && q < nb) {
       const float lse = S.lse();
       A.lse[b0 + q] = lse;
@@ -261,9 +260,9 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
   auto top_key = [&](int64_t i) __attribute__((always_inline)) { return run_key(top[i * kFrag], i); };
   // The min(k, candidates) best of n distinct keys, sorted, in best[]; keys of 0 are no
   // candidates. Returns their number. Each thread takes the largest of its keys; the k-th
-  // largest score among those of 256 pairs of threads is a bound that k keys reach, and few
-  // others do when the best keys are spread over the threads. Every wave finds it by itself, bit
-  // by bit, from all 256 (4 a lane). The keys that reach it are ranked by counting the larger
+  // largest score among those of 64 groups of threads (k > 32: 256 pairs) is a bound that k keys
+  // reach, and few others do when the best keys are spread over the threads. Every wave finds it
+  // by itself, bit by bit, from all of them. The keys that reach it are ranked by counting the larger
   // ones. Where more than kPickCap reach it, the bound is found among all keys, bit by bit over
   // their 64 bits.
   // A thread's first kKept keys stay in registers, loaded by keep().
@@ -292,12 +291,21 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
       m4 = make_uint4(max(m4.x, o.x), max(m4.y, o.y), max(m4.z, o.z), max(m4.w, o.w));
     }
     uint32_t bound = 0u;
+    if (A.k <= 32) {  // 64 groups of threads bound few more candidates than 256, and are quicker
+      const uint32_t m1 = max(max(m4.x, m4.y), max(m4.z, m4.w));
 #pragma unroll
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t c = bound | (1u << bit);
-      const int above = __popcll(__ballot(m4.x >= c)) + __popcll(__ballot(m4.y >= c)) +
-                        __popcll(__ballot(m4.z >= c)) + __popcll(__ballot(m4.w >= c));
-      bound = above >= A.k ? c : bound;
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = bound | (1u << bit);
+        bound = __popcll(__ballot(m1 >= c)) >= A.k ? c : bound;
+      }
+    } else {
+#pragma unroll 1
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = bound | (1u << bit);
+        const int above = __popcll(__ballot(m4.x >= c)) + __popcll(__ballot(m4.y >= c)) +
+                          __popcll(__ballot(m4.z >= c)) + __popcll(__ballot(m4.w >= c));
+        bound = above >= A.k ? c : bound;
+      }
     }
     uint64_t least = bound == 0u ? 1ull : (uint64_t)bound << 32;
     auto collect = [&]() __attribute__((always_inline)) {
@@ -335,10 +343,21 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     }
     const int c = (int)cnt;
     const int r = min(c, A.k);
-    if (t < c) {
+    if (c <= kWave) {
+      if (wave == 0) {
+        const uint64_t key = lane < c ? found[lane] : 0ull;
+        int rank = 0;
+        for (int j = 0; j < c; ++j) {
+          const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), j) << 32) |
+                                 (uint32_t)__builtin_amdgcn_readlane((int)key, j);
+          rank += other > key ? 1 : 0;
+        }
+        if (lane < c && rank < r) best[rank] = key;
+      }
+    } else if (t < c) {
       const uint64_t key = found[t];
       int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < c; ++j) rank += found[j] > key ? 1 : 0;
       if (rank < r) best[rank] = key;
     }
@@ -361,11 +380,11 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     const float4 p = A.part[(int64_t)s * A.b + b];
     st.join(p.x, p.y, p.z);
   }
-  st.join_lanes(1, 32);
+  st.join_lanes(min(kWave, A.nslices));
   if (lane == 0) red[wave] = make_float4(st.m, st.z, st.x, 0.0f);
   __syncthreads();
   st.m = red[0].x, st.z = red[0].y, st.x = red[0].z;
-  for (int w = 1; w < kFinWaves; ++w) st.join(red[w].x, red[w].y, red[w].z);
+  for (int w = 1; w < min(kFinWaves, (A.nslices + kWave - 1) / kWave); ++w) st.join(red[w].x, red[w].y, red[w].z);
   const float lse = st.lse();
   if (t == 0) {
     A.lse[b] = lse;
