@@ -50,82 +50,56 @@ struct FinishArgs {
   int id_bits, g, k;
   const float *bmax, *gmax;  // gmax NULL: no groups
   int64_t nruns, ngroups;
-  int per, rm;               // runs of a group, 32-row blocks of a run
+  int per_log, rm_log;       // runs of a group, 32-row blocks of a run: powers of two
   float *logprobs, *lse, *entropy, *alt_logprobs;
   int32_t* alt_ids;
 };
 
-// One 16-byte slot of a row (chunk c, half h).
-template <bool ROWS>
-__device__ __forceinline__ u32x4_t item_slot(const Table& T, int64_t row, int c, int h) {
+// Chunks 0 .. NCH - 1 of 32 item rows, lane (l, h) loading its half h of each chunk of row l.
+template <bool ROWS, int NCH>
+__device__ __forceinline__ void load_chunks(const Table& items, int64_t row, u32x4_t (&a)[NCH]) {
+  const int h = (threadIdx.x & 63) >> 5;
   if constexpr (ROWS) {
-    const int off = 32 * c + 16 * h;
-    if (off >= T.row_b) return u32x4_t{0u, 0u, 0u, 0u};
-    return *(const u32x4_t*)(T.p + row * T.stride_b + off);
+    const uint8_t* p = items.p + row * items.stride_b + 16 * h;
+    const int left = items.row_b - 16 * h;  // chunks at or past the row's end are zero
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) a[c] = 32 * c < left ? *(const u32x4_t*)(p + 32 * c) : u32x4_t{0u, 0u, 0u, 0u};
   } else {
-    return *(const u32x4_t*)(T.p + (row >> 5) * (32 * (int64_t)T.row_b) + (int64_t)c * kChunkBytes +
-                             ((row & 31) + 32 * h) * 16);
+    const uint8_t* p = items.p + (row >> 5) * (NCH * (int64_t)kChunkBytes) + ((row & 31) + 32 * h) * 16;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) a[c] = *(const u32x4_t*)(p + c * kChunkBytes);
   }
 }
 
-// Chunks [c0, c0 + 8) of 32 item rows, lane (l, h) loading its half of row l.
-template <bool ROWS>
-__device__ __forceinline__ void load_chunks(const Table& items, int64_t row, int c0, int nch, u32x4_t (&a)[8]) {
-  const int h = (threadIdx.x & 63) >> 5;
+// The scores of 32 item rows with 32 query columns, of which the diagonal is taken: lane (l, h)
+// gives its halves of row l and of column l's query, and gets the score of row l with it if
+// diagonal() holds, else nothing. The accumulation of the statistics pass, chunk by chunk, so
+// bitwise its scores.
+__device__ __forceinline__ bool diagonal() { return (((threadIdx.x >> 2) & 1) ^ ((threadIdx.x >> 5) & 1)) == 0; }
+template <int CT, int NCH>
+__device__ __forceinline__ float score_rows(const u32x4_t (&a)[NCH], const u32x4_t (&q)[NCH]) {
+  const int lane = threadIdx.x & 63;
+  f32x16_t acc = {};
 #pragma unroll
-  for (int u = 0; u < 8; ++u)
-    a[u] = c0 + u < nch ? item_slot<ROWS>(items, row, c0 + u, h) : u32x4_t{0u, 0u, 0u, 0u};
-}
-
-// acc += the products of those chunks with 32 query columns, `col(c)` giving the lane's query
-// slot of chunk c.
-template <int CT, typename Q>
-__device__ __forceinline__ void score_chunks(const u32x4_t (&a)[8], int c0, int nch, Q col, f32x16_t& acc) {
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    if (c0 + u >= nch) break;
-    const u32x4_t b = col(c0 + u);
+  for (int c = 0; c < NCH; ++c) {
     if constexpr (CT == MIPS_BF16) {
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[u]),
-                                                    __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[c]),
+                                                    __builtin_bit_cast(bf16x8_t, q[c]), acc, 0, 0, 0);
     } else {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[u][t]), __uint_as_float(b[t]), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[c][t]), __uint_as_float(q[c][t]), acc, 0, 0, 0);
     }
   }
-}
-
-// Scores of one query (slots in LDS, for every column) with 32 rows, lane (l, h) giving row l
-// and its first 8 chunks: the accumulation of the statistics pass, chunk by chunk, so bitwise
-// its scores. Returns row (lane & 31)'s score in every lane.
-template <int CT, bool ROWS>
-__device__ __forceinline__ float score_row(const FinishArgs& A, const u32x4_t* q, int64_t row, float* scr,
-                                           u32x4_t (&a)[8]) {
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int nch = (A.items.row_b + 31) / 32;
-  f32x16_t acc = {};
-  score_chunks<CT>(a, 0, nch, [&](int c) { return q[2 * c + h]; }, acc);
-  for (int c0 = 8; c0 < nch; c0 += 8) {
-    load_chunks<ROWS>(A.items, row, c0, nch, a);
-    score_chunks<CT>(a, c0, nch, [&](int c) { return q[2 * c + h]; }, acc);
-  }
-  // every column holds the query's scores: lanes 0 and 32 give the rows of their half
-  if ((lane & 31) == 0) {
+  float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) scr[acc_row(i, lane)] = acc[i];
-  }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  const float s = scr[lane & 31];
-  __builtin_amdgcn_wave_barrier();
+  for (int i = 0; i < 16; ++i) s = acc_row(i, lane) == (lane & 31) ? acc[i] : s;
   return s;
 }
 
-__device__ __forceinline__ float logit(const FinishArgs& A, float s, int64_t row) {
+__device__ __forceinline__ float logit(const FinishArgs& A, float s, float bias) {
   const float l = __fmul_rn(s, A.scale);
-  return A.bias ? __fadd_rn(l, A.bias[row]) : l;
+  return A.bias ? __fadd_rn(l, bias) : l;
 }
 
 __device__ __forceinline__ bool excluded(const FinishArgs& A, int q, int64_t row) {
@@ -133,18 +107,22 @@ __device__ __forceinline__ bool excluded(const FinishArgs& A, int q, int64_t row
   return (A.exclude[(int64_t)q * A.exclude_words + (row >> 5)] >> (row & 31)) & 1u;
 }
 
-// Slot (chunk c, half h) of a query's row, in the order of the item rows' slots.
-__device__ __forceinline__ u32x4_t query_slot(const FinishArgs& A, int64_t b, int c, int h) {
+// The lane's halves of a query's chunks, in the order of the item rows'.
+template <int NCH>
+__device__ __forceinline__ void query_chunks(const FinishArgs& A, int64_t b, u32x4_t (&q)[NCH]) {
+  const int h = (threadIdx.x & 63) >> 5;
   const uint8_t* row = A.queries.p + b * A.queries.stride_b;
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (A.packed_f32) {
-    const uint32_t* r = (const uint32_t*)row + 8 * c + h;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = r[2 * e];
-  } else if (32 * c + 16 * h < A.queries.row_b) {
-    v = *(const u32x4_t*)(row + 32 * c + 16 * h);
+  for (int c = 0; c < NCH; ++c) {
+    q[c] = u32x4_t{0u, 0u, 0u, 0u};
+    if (A.packed_f32) {
+      const uint32_t* r = (const uint32_t*)row + 8 * c + h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[c][e] = r[2 * e];
+    } else if (32 * c + 16 * h < A.queries.row_b) {
+      q[c] = *(const u32x4_t*)(row + 32 * c + 16 * h);
+    }
   }
-  return v;
 }
 
 // Statistics of a query over some items; join() adds those of others.
@@ -181,10 +159,10 @@ __device__ __forceinline__ void read_ids(const FinishArgs& A, int64_t at, bool& 
 // Without alternatives: one workgroup per 32 queries. Eight threads a query join the slices'
 // statistics; then each wave scores 32 (query, id) pairs at a time, pair i's item as row i and
 // its query as column i of one matrix product, whose diagonal holds the scores.
-template <int CT, bool ROWS>
+template <int CT, bool ROWS, int NCH>
 __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
   __shared__ float s_lse[kFrag];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int b0 = blockIdx.x * kFrag, nb = min(kFrag, A.b - b0);
   {
     const int q = t >> 3, sub = t & 7;
@@ -204,7 +182,6 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
     }
   }
   __syncthreads();
-  const int nch = (A.items.row_b + 31) / 32;
   for (int p0 = wave * kFrag; p0 < nb * A.g; p0 += 4 * kFrag) {
     const int p = min(p0 + (lane & 31), nb * A.g - 1);  // this lane's pair
     const int64_t at = (int64_t)b0 * A.g + p;
@@ -212,17 +189,14 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
     int64_t row;
     read_ids(A, at, pad, row);
     const int bl = p / A.g;
-    f32x16_t acc = {};
-    for (int c0 = 0; c0 < nch; c0 += 8) {
-      u32x4_t a[8];
-      load_chunks<ROWS>(A.items, row, c0, nch, a);
-      score_chunks<CT>(a, c0, nch, [&](int c) { return query_slot(A, b0 + bl, c, h); }, acc);
-    }
-    float s = 0.0f;  // the diagonal: held by the lane of the pair's column whose half has its row
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = acc_row(i, lane) == (lane & 31) ? acc[i] : s;
-    if (((lane >> 2) & 1) == h && p0 + (lane & 31) < nb * A.g)
-      A.logprobs[at] = pad ? 0.0f : (excluded(A, b0 + bl, row) ? -INFINITY : logit(A, s, row) - s_lse[bl]);
+    u32x4_t a[NCH], q[NCH];
+    load_chunks<ROWS, NCH>(A.items, row, a);
+    query_chunks<NCH>(A, b0 + bl, q);
+    const float s = score_rows<CT, NCH>(a, q);
+    if (diagonal() && p0 + (lane & 31) < nb * A.g)
+      A.logprobs[at] = pad ? 0.0f
+                           : (excluded(A, b0 + bl, row) ? -INFINITY
+                                                        : logit(A, s, A.bias ? A.bias[row] : 0.0f) - s_lse[bl]);
   }
 }
 
@@ -234,12 +208,10 @@ constexpr int kIdsKept = 128;  // given ids that are read ahead
 constexpr int kKept = 4;       // keys that a thread keeps in registers
 constexpr int kPickCap = 256;  // candidates of a pick that are ranked by counting
 
-template <int CT, bool ROWS>
+template <int CT, bool ROWS, int NCH>
 __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];  // keys of the rescored rows
-  __shared__ u32x4_t q[64];        // the query: slot 2c + h
   __shared__ float4 red[kFinWaves];
-  __shared__ float scr[kFinWaves][kFrag];
   __shared__ uint64_t found[kPickCap];
   __shared__ __attribute__((aligned(16))) uint32_t maxima[kFinThreads];
   __shared__ uint64_t best[MIPS_ALTERNATIVES_MAX];
@@ -366,7 +338,6 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
   };
   uint64_t kept[kKept];
   keep(top_key, ntop, kept);
-  const int nch = (A.items.row_b + 31) / 32;
   const int ng = (A.g + kFrag - 1) / kFrag;  // blocks of given ids
   for (int i = t; i < min(A.g, kIdsKept); i += kFinThreads) {
     bool pad;
@@ -374,7 +345,8 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     read_ids(A, (int64_t)b * A.g + i, pad, row);
     s_ids[i] = pad ? -1 : (int32_t)row;
   }
-  for (int i = t; i < 2 * nch; i += kFinThreads) q[i] = query_slot(A, b, i >> 1, i & 1);
+  u32x4_t q[NCH];  // the query in every column
+  query_chunks<NCH>(A, b, q);
   Stats st;
   for (int s = t; s < A.nslices; s += kFinThreads) {
     const float4 p = A.part[(int64_t)s * A.b + b];
@@ -393,24 +365,24 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
 
   int r = pick(top_key, ntop, kept);
   if (A.gmax) {
-    if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.per;
+    if (t < r) list[t] = (int64_t)composite_id(best[t]) << A.per_log;
     __syncthreads();
     auto key = [&](int64_t i) __attribute__((always_inline)) {
-      const int64_t u = list[i / A.per] + i % A.per;
+      const int64_t u = list[i >> A.per_log] + (i & ((1 << A.per_log) - 1));
       return u < A.nruns ? run_key(bm[u * kFrag], u) : 0ull;
     };
-    const int64_t n = (int64_t)r * A.per;
+    const int64_t n = (int64_t)r << A.per_log;
     keep(key, n, kept);
     r = pick(key, n, kept);
   }
-  if (t < r) list[t] = (int64_t)composite_id(best[t]) * A.rm;  // first 32-row block of the run
+  if (t < r) list[t] = (int64_t)composite_id(best[t]) << A.rm_log;  // first 32-row block of the run
   __syncthreads();
   // The rows of the runs and the given ids, 32 a wave at a time; each wave's next block is on
   // its way while this one is scored.
   uint64_t* keys = (uint64_t*)dyn;
-  const int nb = r * A.rm;
+  const int nb = r << A.rm_log;
   auto row_of = [&](int i) __attribute__((always_inline)) -> int64_t {  // -1: padding
-    if (i < nb) return (list[i / A.rm] + i % A.rm) * kFrag + (lane & 31);
+    if (i < nb) return (list[i >> A.rm_log] + (i & ((1 << A.rm_log) - 1))) * kFrag + (lane & 31);
     const int g = (i - nb) * kFrag + (lane & 31);
     if (g >= A.g) return -1;
     if (g < kIdsKept) return s_ids[g];
@@ -419,31 +391,41 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     read_ids(A, (int64_t)b * A.g + g, pad, row);
     return pad ? -1 : row;
   };
-  u32x4_t ahead[8];
-  int64_t next = -1;
-  auto fetch = [&](int i) __attribute__((always_inline)) {
-    next = row_of(i);
-    load_chunks<ROWS>(A.items, max<int64_t>(0, min<int64_t>(next, A.items.n - 1)), 0, nch, ahead);
+  struct Block {
+    u32x4_t chunks[NCH];
+    int64_t row;
+    uint32_t word;
+    float bias;
   };
-  if (wave < nb + ng) fetch(wave);
-  for (int i = wave; i < nb + ng; i += kFinWaves) {
-    const int64_t row = next;
-    const bool live = row >= 0 && row < A.items.n;
-    const int64_t rl = live ? row : 0;
-    u32x4_t now[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) now[u] = ahead[u];
-    if (i + kFinWaves < nb + ng) fetch(i + kFinWaves);
-    const float s = score_row<CT, ROWS>(A, q, rl, scr[wave], now);
-    const bool out = live && excluded(A, b, rl);
-    const float l = logit(A, s, rl);
-    if (lane >= kFrag) continue;
+  auto fetch = [&](int i, Block& x) __attribute__((always_inline)) {
+    if (i >= nb + ng) return;
+    x.row = row_of(i);
+    const int64_t at = max<int64_t>(0, min<int64_t>(x.row, A.items.n - 1));
+    load_chunks<ROWS, NCH>(A.items, at, x.chunks);
+    x.word = A.exclude ? A.exclude[(int64_t)b * A.exclude_words + (at >> 5)] : 0u;
+    x.bias = A.bias ? A.bias[at] : 0.0f;
+  };
+  auto score = [&](int i, Block& x) __attribute__((always_inline)) {
+    if (i >= nb + ng) return;
+    const bool live = x.row >= 0 && x.row < A.items.n;
+    const bool out = live && ((x.word >> (x.row & 31)) & 1u);
+    const float l = logit(A, score_rows<CT, NCH>(x.chunks, q), x.bias);
+    if (!diagonal()) return;
     if (i < nb) {
-      keys[i * kFrag + lane] = live && !out ? composite(score_key(l), (uint32_t)rl) : 0ull;
+      keys[i * kFrag + (lane & 31)] = live && !out ? composite(score_key(l), (uint32_t)x.row) : 0ull;
     } else {
-      const int g = (i - nb) * kFrag + lane;
+      const int g = (i - nb) * kFrag + (lane & 31);
       if (g < A.g) A.logprobs[(int64_t)b * A.g + g] = !live ? 0.0f : (out ? -INFINITY : l - lse);
     }
+  };
+  Block x0, x1;
+  fetch(wave, x0);
+#pragma unroll 1
+  for (int i = wave; i < nb + ng; i += 2 * kFinWaves) {
+    fetch(i + kFinWaves, x1);
+    score(i, x0);
+    fetch(i + 2 * kFinWaves, x0);
+    score(i + kFinWaves, x1);
   }
   __syncthreads();
   auto row_key = [&](int64_t i) __attribute__((always_inline)) { return keys[i]; };
@@ -566,17 +548,26 @@ static int stats_dispatch(int dtype, int width, int nqf, bool rows, const StatsA
   return MIPS_ERR_UNSUPPORTED;
 }
 
-template <int CT, bool ROWS>
-static int launch_finish(const FinishArgs& A, int b, hipStream_t s) {
-  static const hipError_t attr =
-      hipFuncSetAttribute((const void*)finish_kernel<CT, ROWS>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                          kKeyBytes);
-  (void)attr;
+template <int CT, bool ROWS, int NCH>
+static int launch_finish_one(const FinishArgs& A, int b, hipStream_t s) {
   if (A.k == 0)
-    hipLaunchKernelGGL((pairs_kernel<CT, ROWS>), dim3((b + kFrag - 1) / kFrag), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((pairs_kernel<CT, ROWS, NCH>), dim3((b + kFrag - 1) / kFrag), dim3(256), 0, s, A);
   else
-    hipLaunchKernelGGL((finish_kernel<CT, ROWS>), dim3(b), dim3(kFinThreads), (size_t)A.k * A.rm * kFrag * 8, s, A);
+    hipLaunchKernelGGL((finish_kernel<CT, ROWS, NCH>), dim3(b), dim3(kFinThreads),
+                       ((size_t)A.k << A.rm_log) * kFrag * 8, s, A);
   return check_launch();
+}
+
+template <int CT, bool ROWS>
+static int launch_finish(const FinishArgs& A, int width, int b, hipStream_t s) {
+  switch (chunks_per_block(CT, width)) {
+    case 1: if constexpr (CT == MIPS_BF16) return launch_finish_one<CT, ROWS, 1>(A, b, s); break;
+    case 2: return launch_finish_one<CT, ROWS, 2>(A, b, s);
+    case 4: return launch_finish_one<CT, ROWS, 4>(A, b, s);
+    case 8: return launch_finish_one<CT, ROWS, 8>(A, b, s);
+    case 16: return launch_finish_one<CT, ROWS, 16>(A, b, s);
+  }
+  return MIPS_ERR_UNSUPPORTED;
 }
 
 // Sizes that both entry points share; MIPS_OK or a status.
@@ -683,16 +674,16 @@ int mips_logprobs(const void* queries, int64_t query_stride, int32_t b, const vo
     F.gmax = P.ngroups ? (float*)(ws + P.gmax) : nullptr;
     F.nruns = P.nruns;
     F.ngroups = P.ngroups;
-    F.per = P.per;
-    F.rm = stats_rm(dtype, P.width) << P.run_log;
+    while (1 << F.per_log < P.per) ++F.per_log;
+    F.rm_log = (stats_rm(dtype, P.width) == 2 ? 1 : 0) + P.run_log;
     F.logprobs = g > 0 ? out_logprobs + (int64_t)q0 * g : nullptr;
     F.lse = out_lse + q0;
     F.entropy = out_entropy ? out_entropy + q0 : nullptr;
     F.alt_ids = k > 0 ? out_alt_ids + (int64_t)q0 * k : nullptr;
     F.alt_logprobs = k > 0 ? out_alt_logprobs + (int64_t)q0 * k : nullptr;
     int rc;
-    if (dtype == MIPS_F32) rc = rows ? launch_finish<MIPS_F32, true>(F, nb, s) : launch_finish<MIPS_F32, false>(F, nb, s);
-    else rc = rows ? launch_finish<MIPS_BF16, true>(F, nb, s) : launch_finish<MIPS_BF16, false>(F, nb, s);
+    if (dtype == MIPS_F32) rc = rows ? launch_finish<MIPS_F32, true>(F, P.width, nb, s) : launch_finish<MIPS_F32, false>(F, P.width, nb, s);
+    else rc = rows ? launch_finish<MIPS_BF16, true>(F, P.width, nb, s) : launch_finish<MIPS_BF16, false>(F, P.width, nb, s);
     if (rc) return rc;
   }
   return MIPS_OK;
