@@ -152,42 +152,60 @@ static int launch_lookup(LookupArgs A, int id_bits, hipStream_t s) {
 // precede it, counted by comparing it with every other (t^2 comparisons spread over the
 // chip). Otherwise a least-significant-digit radix sort of 8-bit digits over at most
 // kSortBlocks contiguous ranges of tokens, two kernels a digit: the ranges' digit counts,
-// then every range scans all counts for its own offsets and scatters. Inside a range a wave
-// takes 64 keys at a time and ranks equal digits by ballots, which keeps the sort stable.
+// then every range adds up all counts for its own offsets and scatters. Inside a range each wave
+// has a contiguous part: it counts its digits, and with the waves' offsets known ranks 64 keys at a
+// time by ballots, which keeps the sort stable. The kernels are bound by latency; the
+// output's zeros are written beside all of them, a share each.
 constexpr int kRankMax = 8192;
 constexpr int kRankTokens = 16;  // tokens ranked per workgroup
 constexpr int kSortBlocks = 256;
-constexpr int kSortTile = 2048;  // tokens of a range, at least
-constexpr int kSortThreads = 256;
+constexpr int kSortTile = 4096;  // tokens of a range: a multiple of this
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t rows) {
   return (id < 0 || id >= rows) ? (uint32_t)rows : (uint32_t)id;
 }
 
-// Writes zeros to the dense gradient: workgroup w of nw clears its share of `bytes` (a
-// multiple of the element size) at p. Run by the first kernel of the gradient in workgroups
-// of its own, beside the sort.
+// Writes zeros to the dense gradient, rows [first, last): workgroup w of nblocks, of any size,
+// clears its share. Run in workgroups of their own beside the sort's.
 struct ZeroArgs {
   void* p;
-  int64_t rows, stride_b;  // rows and bytes between them
-  int64_t row_b;           // bytes of a row
-  int nblocks;             // workgroups that clear (0: accumulate into what is there)
+  int64_t first, last, stride_b;  // rows, and bytes between them
+  int64_t row_b;                  // bytes of a row
+  int nblocks;                    // workgroups that clear (0: accumulate into what is there)
 };
 
 __device__ __forceinline__ void zero_rows(const ZeroArgs& Z, int w) {
   const u32x4_t z = {0u, 0u, 0u, 0u};
-  if (Z.stride_b == Z.row_b && ((uintptr_t)Z.p & 15) == 0) {
-    const int64_t total = Z.rows * Z.row_b, n16 = total / 16;
-    u32x4_t* p = (u32x4_t*)Z.p;
-    for (int64_t i = (int64_t)w * 256 + threadIdx.x; i < n16; i += (int64_t)Z.nblocks * 256) p[i] = z;
-    if (w == 0 && threadIdx.x < (total & 15) / 2)
-      ((uint16_t*)Z.p)[n16 * 8 + threadIdx.x] = 0;
+  uint8_t* base = (uint8_t*)Z.p + Z.first * Z.stride_b;
+  const int64_t rows = Z.last - Z.first, nt = blockDim.x;
+  if (Z.stride_b == Z.row_b && ((uintptr_t)base & 15) == 0) {
+    const int64_t total = rows * Z.row_b, n16 = total / 16;
+    u32x4_t* p = (u32x4_t*)base;
+    for (int64_t i = (int64_t)w * nt + threadIdx.x; i < n16; i += (int64_t)Z.nblocks * nt) p[i] = z;
+    if (w == 0 && threadIdx.x < (total & 15) / 2) ((uint16_t*)base)[n16 * 8 + threadIdx.x] = 0;
   } else {
-    for (int64_t r = w; r < Z.rows; r += Z.nblocks) {
-      uint16_t* p = (uint16_t*)((uint8_t*)Z.p + r * Z.stride_b);
-      for (int64_t j = threadIdx.x; j < Z.row_b / 2; j += 256) p[j] = 0;
+    for (int64_t r = w; r < rows; r += Z.nblocks) {
+      uint16_t* p = (uint16_t*)(base + r * Z.stride_b);
+      for (int64_t j = threadIdx.x; j < Z.row_b / 2; j += nt) p[j] = 0;
     }
   }
+}
+
+// The part [i / n, (i + 1) / n) of the rows (multiples of 8, so that parts keep an alignment of
+// 16 bytes), in workgroups of nt threads: 64 bytes a thread at least, at most 1024 of them.
+static ZeroArgs zero_part(const ZeroArgs& Z, int i, int n, int nt) {
+  ZeroArgs P = Z;
+  P.first = i == 0 ? 0 : Z.last * i / n / 8 * 8;
+  P.last = i == n - 1 ? Z.last : Z.last * (i + 1) / n / 8 * 8;
+  if (Z.nblocks == 0 || P.last <= P.first) {
+    P.nblocks = 0;
+    return P;
+  }
+  const int64_t want = ((P.last - P.first) * Z.row_b + nt * 64 - 1) / (nt * 64);
+  P.nblocks = (int)(want < 1024 ? want : 1024);
+  return P;
 }
 
 struct RankArgs {
@@ -212,30 +230,40 @@ __global__ __launch_bounds__(256) void rank_sort_kernel(RankArgs A) {
   if (threadIdx.x < kRankTokens)
     mine[threadIdx.x] = t0 + (int)threadIdx.x < t ? key_of(id_at<IdT>(A.ids, t0 + threadIdx.x), A.rows) : 0u;
   __syncthreads();
+  // Token j precedes token i if its key is smaller, or equal with j < i: for tokens before this
+  // workgroup's, 2 key_j < 2 key_i + 1; for those behind it, 2 key_j + 1 < 2 key_i + 1 (keys are
+  // below 2^31); its own are compared by both. The counts are a wave's, kept on the scalar unit:
+  // one comparison a pair. Eight tokens a lane are on their way at a time.
   uint32_t k[kRankTokens], c[kRankTokens];
 #pragma unroll
   for (int i = 0; i < kRankTokens; ++i) {
-    k[i] = mine[i];
+    k[i] = 2u * mine[i] + 1u;
     c[i] = 0u;
   }
-  // token j precedes token i if its key is smaller, or equal with j < i. Tokens before this
-  // workgroup's precede at equal keys, tokens after it do not: one comparison with k + 1 or
-  // k; only the workgroup's own tokens need the test of j.
-  for (int j = threadIdx.x; j < t; j += 256) {
-    const uint32_t kj = key_of(id_at<IdT>(A.ids, j), A.rows);
-    const uint32_t adj = j < t0 ? 1u : 0u;
-    const int in = j - t0;
+  constexpr int kBatch = 8;
+  for (int j0 = 0; j0 < t; j0 += 256 * kBatch) {  // uniform
+    uint32_t kj[kBatch];
 #pragma unroll
-    for (int i = 0; i < kRankTokens; ++i) {
-      const uint32_t lim = k[i] + ((in >= 0 && in < i) ? 1u : adj);
-      c[i] += kj < lim ? 1u : 0u;
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + u * 256 + (int)threadIdx.x;
+      const bool other = j < t && (j < t0 || j >= t0 + kRankTokens);
+      kj[u] = other ? 2u * key_of(id_at<IdT>(A.ids, j), A.rows) + (j < t0 ? 0u : 1u) : 0xFFFFFFFFu;
     }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+      for (int i = 0; i < kRankTokens; ++i) c[i] += (uint32_t)__popcll(__ballot(kj[u] < k[i]));
   }
+  if (wave == 0) {
+    const bool own = lane < kRankTokens && t0 + lane < t;
+    const uint32_t kl = mine[lane < kRankTokens ? lane : 0];
 #pragma unroll
-  for (int i = 0; i < kRankTokens; ++i) {
+    for (int i = 0; i < kRankTokens; ++i)
+      c[i] += (uint32_t)__popcll(__ballot(own && (kl < mine[i] || (kl == mine[i] && lane < i))));
+  }
+  if (lane == 0) {
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) c[i] += __shfl_xor(c[i], o, kWave);
-    if (lane == 0) cnt[wave][i] = c[i];
+    for (int i = 0; i < kRankTokens; ++i) cnt[wave][i] = c[i];
   }
   __syncthreads();
   if (threadIdx.x < kRankTokens && t0 + (int)threadIdx.x < t) {
@@ -269,50 +297,72 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs A) {
     zero_rows(A.Z, (int)blockIdx.x - A.nb);
     return;
   }
-  __shared__ uint32_t hist[256];
-  hist[threadIdx.x] = 0u;
+  __shared__ uint32_t hist[4][256];  // four copies: fewer lanes meet in one counter
+  hist[threadIdx.x >> 8][threadIdx.x & 255] = 0u;
   __syncthreads();
   const int64_t i0 = blockIdx.x * A.per, i1 = min(A.t, i0 + A.per);
+#pragma unroll 4
   for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
-    atomicAdd(&hist[(sort_key<IdT>(A, i) >> A.shift) & 255u], 1u);
+    atomicAdd(&hist[threadIdx.x >> 8][(sort_key<IdT>(A, i) >> A.shift) & 255u], 1u);
   __syncthreads();
-  A.counts[blockIdx.x * 256 + threadIdx.x] = hist[threadIdx.x];
+  const int t = threadIdx.x;
+  if (t < 256) A.counts[blockIdx.x * 256 + t] = hist[0][t] + hist[1][t] + hist[2][t] + hist[3][t];
 }
 
 template <typename IdT>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs A) {
-  __shared__ uint32_t base[256];      // next place of each digit of this range
-  __shared__ uint32_t wcnt[4][256];   // a step's counts per wave and digit
+  if ((int)blockIdx.x >= A.nb) {
+    zero_rows(A.Z, (int)blockIdx.x - A.nb);
+    return;
+  }
+  __shared__ uint32_t off[kSortWaves][256];  // a wave's keys per digit, then its next place of each
+  __shared__ uint32_t part[2][4][256];
   __shared__ uint32_t wsum[4];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  // digit t: tokens of the ranges before this one, and of all ranges
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t i0 = blockIdx.x * A.per, i1 = min(A.t, i0 + A.per);
+  const int64_t w0 = i0 + wave * (A.per / kSortWaves), w1 = min(i1, w0 + A.per / kSortWaves);
+#pragma unroll
+  for (int w = 0; w < kSortWaves / 4; ++w) off[4 * w + (t >> 8)][t & 255] = 0u;
+  // digit t & 255: tokens of the ranges before this one and of all ranges, a quarter of the
+  // ranges a thread
   uint32_t before = 0u, all = 0u;
-#pragma unroll 8
-  for (int b = 0; b < A.nb; ++b) {
-    const uint32_t c = A.counts[b * 256 + t];
+#pragma unroll 16
+  for (int b = t >> 8; b < A.nb; b += 4) {
+    const uint32_t c = A.counts[b * 256 + (t & 255)];
     all += c;
     before += b < (int)blockIdx.x ? c : 0u;
   }
-  uint32_t incl = all;  // prefix over the digits
+  part[0][t >> 8][t & 255] = before;
+  part[1][t >> 8][t & 255] = all;
+  __syncthreads();
+#pragma unroll 4
+  for (int64_t i = w0 + lane; i < w1; i += kWave) atomicAdd(&off[wave][(sort_key<IdT>(A, i) >> A.shift) & 255u], 1u);
+  uint32_t incl = 0u;
+  if (t < 256) {  // prefix over the digits
+    before = part[0][0][t] + part[0][1][t] + part[0][2][t] + part[0][3][t];
+    all = part[1][0][t] + part[1][1][t] + part[1][2][t] + part[1][3][t];
+    incl = all;
 #pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint32_t u = __shfl_up(incl, o, kWave);
-    if (lane >= o) incl += u;
+    for (int o = 1; o < kWave; o <<= 1) {
+      const uint32_t u = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += u;
+    }
+    if (lane == kWave - 1) wsum[wave] = incl;
   }
-  if (lane == kWave - 1) wsum[wave] = incl;
   __syncthreads();
-  uint32_t off = incl - all;
-  for (int w = 0; w < wave; ++w) off += wsum[w];
-  base[t] = off + before;
+  if (t < 256) {
+    uint32_t p = incl - all + before;
+    for (int w = 0; w < wave; ++w) p += wsum[w];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = off[w][t];
+      off[w][t] = p;
+      p += c;
+    }
+  }
   __syncthreads();
-
-  const int64_t i0 = blockIdx.x * A.per, i1 = min(A.t, i0 + A.per);
-  for (int64_t s0 = i0; s0 < i1; s0 += kSortThreads) {  // uniform: every thread takes each step
-#pragma unroll
-    for (int w = 0; w < 4; ++w) wcnt[w][t] = 0u;
-    __syncthreads();
-    const int64_t i = s0 + t;
-    const bool on = i < i1;
+  for (int64_t s0 = w0; s0 < w1; s0 += kWave) {  // wave-uniform
+    const int64_t i = s0 + lane;
+    const bool on = i < w1;
     const uint32_t key = on ? sort_key<IdT>(A, i) : 0u;
     const uint32_t tok = !on ? 0u : (A.ids ? (uint32_t)i : A.toks_in[i]);
     const uint32_t dig = (key >> A.shift) & 255u;
@@ -324,16 +374,18 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs A) 
       same &= ((dig >> bit) & 1u) ? m : ~m;
     }
     const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
-    if (on && rank == 0u) wcnt[wave][dig] = (uint32_t)__popcll(same);
-    __syncthreads();
     if (on) {
-      uint32_t p = base[dig] + rank;
-      for (int w = 0; w < wave; ++w) p += wcnt[w][dig];
+      const uint32_t p = off[wave][dig] + rank;
       A.keys_out[p] = key;
       A.toks_out[p] = tok;
     }
-    __syncthreads();
-    base[t] += wcnt[0][t] + wcnt[1][t] + wcnt[2][t] + wcnt[3][t];
+    // this wave's counters alone, read above before they move on: one wave's LDS accesses stay
+    // in order, and the fences keep the compiler from reordering them
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (on && rank == 0u) off[wave][dig] += (uint32_t)__popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -438,59 +490,87 @@ __global__ __launch_bounds__(256) void segment_kernel(SegArgs A) {
   }
 }
 
-// One workgroup per chunk whose last segment began in it and goes on: adds that segment's
-// partial rows, 2^tpr_log lanes a row, the groups taking chunks in turn, then the groups'
-// sums in LDS in a fixed order.
+// Adds the partial rows of the segments that cross chunks. A group of 2^tpr_log lanes looks at
+// one chunk: a segment that began in it and goes on over at most kJoinShort chunks is added up
+// by the group, chunk after chunk. Longer ones (hot ids) are left to the whole workgroup, one
+// after the other: the groups take chunks in turn, then their sums are joined in LDS, in a fixed
+// order.
+constexpr int kJoinShort = 16;
+
 template <int DT, int OUT, bool VEC>
 __global__ __launch_bounds__(256) void join_kernel(SegArgs A) {
   constexpr int N = Unit<DT, VEC>::N;
   __shared__ float red[256 * N];
-  const int64_t c = blockIdx.x;
-  const int64_t last = (c + 1) * A.chunk - 1;  // this chunk's last token (a later chunk exists)
-  if (last + 1 >= A.t) return;
-  const uint32_t key = A.keys[last];
-  const int64_t first = c * A.chunk;
-  if (key == (uint32_t)A.rows || A.keys[last + 1] != key) return;
-  if (A.keys[first] == key && first > 0 && A.keys[first - 1] == key) return;  // began earlier
-  // end of the segment: the first token with a larger key
-  int64_t lo = last + 1, hi = A.t;
-  while (lo < hi) {
-    const int64_t m = (lo + hi) >> 1;
-    if (A.keys[m] > key) hi = m;
-    else lo = m + 1;
-  }
-  const int64_t c1 = (lo - 1) / A.chunk;  // chunk of the segment's last token
+  __shared__ int64_t long_c[256], long_end[256];
+  __shared__ int nlong;
   const int tpr = 1 << A.tpr_log;
   const int sub = threadIdx.x & (tpr - 1), g = threadIdx.x >> A.tpr_log, ng = 256 >> A.tpr_log;
-  for (int u0 = 0; u0 < A.nunit; u0 += tpr) {
-    const int u = u0 + sub;
-    float a[N] = {};
-    if (u < A.nunit) {
-      const int64_t j = (int64_t)u * N;
+  if (threadIdx.x == 0) nlong = 0;
+  __syncthreads();
+  auto add_rows = [&](int64_t c, int64_t from, int64_t to, int step, int64_t j, float (&a)[N]) __attribute__((always_inline)) {
 #pragma unroll 4
-      for (int64_t q = c + g; q <= c1; q += ng) {
-        const float* p = A.part + (2 * q + (q == c ? 1 : 0)) * A.d + j;
+    for (int64_t q = from; q <= to; q += step) {
+      const float* p = A.part + (2 * q + (q == c ? 1 : 0)) * A.d + j;
 #pragma unroll
-        for (int e = 0; e < N; ++e) a[e] += p[e];
+      for (int e = 0; e < N; ++e) a[e] += p[e];
+    }
+  };
+  const int64_t c = (int64_t)blockIdx.x * ng + g;
+  const int64_t last = (c + 1) * A.chunk - 1;  // the chunk's last token
+  if (last + 1 < A.t) {
+    const uint32_t key = A.keys[last], first = A.keys[c * A.chunk];
+    const bool earlier = first == key && c > 0 && A.keys[c * A.chunk - 1] == key;
+    if (key != (uint32_t)A.rows && A.keys[last + 1] == key && !earlier) {
+      // end of the segment: the first token with a larger key, near by or by bisection
+      int64_t lo = last + 1, hi = min(A.t, last + 1 + (int64_t)kJoinShort * A.chunk);
+      if (hi < A.t && A.keys[hi - 1] == key) {
+        lo = hi;
+        hi = A.t;
+      }
+      while (lo < hi) {
+        const int64_t m = (lo + hi) >> 1;
+        if (A.keys[m] > key) hi = m;
+        else lo = m + 1;
+      }
+      const int64_t end = (lo - 1) / A.chunk;  // chunk of the segment's last token
+      if (end - c <= kJoinShort) {
+        for (int u = sub; u < A.nunit; u += tpr) {
+          float a[N] = {};
+          add_rows(c, c, end, 1, (int64_t)u * N, a);
+          write_row<DT, OUT, VEC>(A, key, (int64_t)u * N, a);
+        }
+      } else if (sub == 0) {
+        const int at = atomicAdd(&nlong, 1);  // (their order changes no sum)
+        long_c[at] = c;
+        long_end[at] = end;
       }
     }
+  }
+  __syncthreads();
+  for (int s = 0; s < nlong; ++s) {
+    const int64_t lc = long_c[s], le = long_end[s];
+    const uint32_t key = A.keys[(lc + 1) * A.chunk];
+    for (int u0 = 0; u0 < A.nunit; u0 += tpr) {
+      const int u = u0 + sub;
+      float a[N] = {};
+      if (u < A.nunit) add_rows(lc, lc + g, le, ng, (int64_t)u * N, a);
 #pragma unroll
-    for (int e = 0; e < N; ++e) red[threadIdx.x * N + e] = a[e];
-    __syncthreads();
-    for (int h = ng >> 1; h >= 1; h >>= 1) {
-      if (g < h) {
+      for (int e = 0; e < N; ++e) red[threadIdx.x * N + e] = a[e];
+      __syncthreads();
+      for (int h = ng >> 1; h >= 1; h >>= 1) {
+        if (g < h) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          red[threadIdx.x * N + e] += red[(threadIdx.x + h * tpr) * N + e];
+          for (int e = 0; e < N; ++e) red[threadIdx.x * N + e] += red[(threadIdx.x + h * tpr) * N + e];
+        }
+        __syncthreads();
+      }
+      if (g == 0 && u < A.nunit) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) a[e] = red[threadIdx.x * N + e];
+        write_row<DT, OUT, VEC>(A, key, (int64_t)u * N, a);
       }
       __syncthreads();
     }
-    if (g == 0 && u < A.nunit) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) a[e] = red[threadIdx.x * N + e];
-      write_row<DT, OUT, VEC>(A, key, (int64_t)u * N, a);
-    }
-    __syncthreads();
   }
 }
 
@@ -514,7 +594,8 @@ static int launch_segments(SegArgs A, hipStream_t s) {
                      dim3(256), 0, s, A);
   if (const int rc = check_launch()) return rc;
   if (A.nchunk > 1) {
-    hipLaunchKernelGGL((join_kernel<DT, OUT, VEC>), dim3((unsigned)(A.nchunk - 1)), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((join_kernel<DT, OUT, VEC>), dim3((unsigned)((A.nchunk - 1 + groups - 1) / groups)), dim3(256),
+                       0, s, A);
     return check_launch();
   }
   return MIPS_OK;
@@ -541,6 +622,8 @@ static GradPlan grad_plan(int64_t t, int64_t rows, int d) {
   P.nb = (int)((t + kSortTile - 1) / kSortTile < kSortBlocks ? (t + kSortTile - 1) / kSortTile : kSortBlocks);
   if (P.nb < 1) P.nb = 1;
   P.per = (t + P.nb - 1) / P.nb;
+  P.per = (P.per + kSortTile - 1) / kSortTile * kSortTile;
+  P.nb = (int)((t + P.per - 1) / P.per);
   P.keys[0] = take((size_t)t * 4);
   P.toks[0] = take((size_t)t * 4);
   if (!rank) {
@@ -610,27 +693,22 @@ int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t
     P = grad_plan(t, rows, d);
     if (workspace_bytes < P.bytes) return MIPS_ERR_WORKSPACE;
   }
-  // workgroups that clear the output: 64 KiB each at least, at most 8 a compute unit
-  ZeroArgs Z{out, rows, out_stride * O, (int64_t)d * O, 0};
-  if (!accumulate) {
-    const int64_t want = (rows * d * O + 65535) / 65536;
-    Z.nblocks = (int)(want < 2048 ? want : 2048);
-  }
+  const ZeroArgs Z{out, 0, rows, out_stride * O, (int64_t)d * O, accumulate ? 0 : 1};
   uint8_t* ws = (uint8_t*)workspace;
   int src = 0;
   if (t == 0) {  // nothing but the zeros
-    if (Z.nblocks > 0) {
+    if (!accumulate) {
       RankArgs R{};
-      R.Z = Z;
-      hipLaunchKernelGGL(rank_sort_kernel<int32_t>, dim3(Z.nblocks), dim3(256), 0, s, R);
+      R.Z = zero_part(Z, 0, 1, 256);
+      hipLaunchKernelGGL(rank_sort_kernel<int32_t>, dim3(R.Z.nblocks), dim3(256), 0, s, R);
       return check_launch();
     }
     return MIPS_OK;
   }
   if (P.passes == 0) {
     RankArgs R{ids, t, rows, (uint32_t*)(ws + P.keys[0]), (uint32_t*)(ws + P.toks[0]),
-               (int)((t + kRankTokens - 1) / kRankTokens), Z};
-    const dim3 grid(R.nrank + Z.nblocks);
+               (int)((t + kRankTokens - 1) / kRankTokens), zero_part(Z, 0, 1, 256)};
+    const dim3 grid(R.nrank + R.Z.nblocks);
     if (id_bits == 32) hipLaunchKernelGGL(rank_sort_kernel<int32_t>, grid, dim3(256), 0, s, R);
     else hipLaunchKernelGGL(rank_sort_kernel<int64_t>, grid, dim3(256), 0, s, R);
     if (const int rc = check_launch()) return rc;
@@ -640,12 +718,13 @@ int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t
       SortArgs S{p == 0 ? ids : nullptr, t, rows, P.per, P.nb, 8 * p,
                  (const uint32_t*)(ws + P.keys[in]), (const uint32_t*)(ws + P.toks[in]),
                  (uint32_t*)(ws + P.keys[to]), (uint32_t*)(ws + P.toks[to]),
-                 (uint32_t*)(ws + P.counts), Z};
-      if (p > 0) S.Z.nblocks = 0;
-      const dim3 gc(P.nb + S.Z.nblocks), gs(P.nb);
+                 (uint32_t*)(ws + P.counts), zero_part(Z, 2 * p, 2 * P.passes, kSortThreads)};
+      const dim3 gc(P.nb + S.Z.nblocks);
       if (id_bits == 32) hipLaunchKernelGGL(sort_count_kernel<int32_t>, gc, dim3(kSortThreads), 0, s, S);
       else hipLaunchKernelGGL(sort_count_kernel<int64_t>, gc, dim3(kSortThreads), 0, s, S);
       if (const int rc = check_launch()) return rc;
+      S.Z = zero_part(Z, 2 * p + 1, 2 * P.passes, kSortThreads);
+      const dim3 gs(P.nb + S.Z.nblocks);
       if (id_bits == 32) hipLaunchKernelGGL(sort_scatter_kernel<int32_t>, gs, dim3(kSortThreads), 0, s, S);
       else hipLaunchKernelGGL(sort_scatter_kernel<int64_t>, gs, dim3(kSortThreads), 0, s, S);
       if (const int rc = check_launch()) return rc;

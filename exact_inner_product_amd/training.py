@@ -1,6 +1,7 @@
 """Python binding of libmips' training and evaluation operators: log probabilities over an item
-table, embedding lookup and its gradient, and gradient-norm clipping. Argument marshalling only, as in the package's other entry points: the
-work is in the HIP kernels behind include/mips.h.
+table and their gradient, embedding lookup and its gradient, and gradient-norm clipping.
+Argument marshalling only, as in the package's other entry points: the work is in the HIP
+kernels behind include/mips.h.
 """
 from __future__ import annotations
 
@@ -329,7 +330,8 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     dtypes = [t.dtype for t in tensors]
     if not set(dtypes) <= _CODES.keys():
         raise TypeError(f"tensors must be float32 or bfloat16, got {set(dtypes)}")
-    if {t.device for t in tensors} != {device}:
+    index = device.index
+    if not all([t.get_device() == index for t in tensors]):
         raise ValueError(f"tensors must all be on {device}")
     plain = all([t.is_contiguous() for t in tensors])
     if not plain:
@@ -340,7 +342,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     if out is None:
         dst = src
     else:
-        if {o.device for o in outs} != {device} or [o.dtype for o in outs] != dtypes or \
+        if not all([o.get_device() == index for o in outs]) or [o.dtype for o in outs] != dtypes or \
                 [o.shape for o in outs] != [t.shape for t in tensors] or \
                 (not (plain and all([o.is_contiguous() for o in outs])) and
                  [o.stride() for o in outs] != [t.stride() for t in tensors]):
