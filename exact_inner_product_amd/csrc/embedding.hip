@@ -7,6 +7,8 @@
 // few tokens, by launches). The gradient's sum is a segmented sum over the tokens sorted by
 // id: no atomics on floats, so that the same call gives the same bits, and a hot id's
 // thousands of tokens are split over many groups of lanes.
+#include <type_traits>
+
 #include "common.h"
 #include "host.h"
 
@@ -148,16 +150,12 @@ static int launch_lookup(LookupArgs A, int id_bits, hipStream_t s) {
 // sum, and so its rounding, follows from the ids alone. Ids outside [0, rows) take the key
 // `rows` and sort behind every row.
 //
-// Few tokens (t <= kRankMax): one kernel; a token's place is the number of tokens that
-// precede it, counted by comparing it with every other (t^2 comparisons spread over the
-// chip). Otherwise a least-significant-digit radix sort of 8-bit digits over at most
-// kSortBlocks contiguous ranges of tokens, two kernels a digit: the ranges' digit counts,
-// then every range adds up all counts for its own offsets and scatters. Inside a range each wave
-// has a contiguous part: it counts its digits, and with the waves' offsets known ranks 64 keys at a
-// time by ballots, which keeps the sort stable. The kernels are bound by latency; the
-// output's zeros are written beside all of them, a share each.
-constexpr int kRankMax = 8192;
-constexpr int kRankTokens = 16;  // tokens ranked per workgroup
+// (Few tokens are not sorted as a whole: see small_kernel.) A least-significant-digit radix sort
+// of 8-bit digits over at most kSortBlocks contiguous ranges of tokens, two kernels a digit:
+// the ranges' digit counts, then every range adds up all counts for its own offsets and
+// scatters. Inside a range each wave has a contiguous part: it counts its digits, and with the
+// waves' offsets known ranks 64 keys at a time by ballots, which keeps the sort stable. The
+// kernels are bound by latency; the output's zeros are written beside all of them, a share each.
 constexpr int kSortBlocks = 256;
 constexpr int kSortTile = 4096;  // tokens of a range: a multiple of this
 constexpr int kSortThreads = 1024;
@@ -208,72 +206,6 @@ static ZeroArgs zero_part(const ZeroArgs& Z, int i, int n, int nt) {
   return P;
 }
 
-struct RankArgs {
-  const void* ids;
-  int64_t t, rows;
-  uint32_t* keys;  // sorted
-  uint32_t* toks;
-  int nrank;       // workgroups that rank; the others clear the output
-  ZeroArgs Z;
-};
-
-template <typename IdT>
-__global__ __launch_bounds__(256) void rank_sort_kernel(RankArgs A) {
-  if ((int)blockIdx.x >= A.nrank) {
-    zero_rows(A.Z, (int)blockIdx.x - A.nrank);
-    return;
-  }
-  __shared__ uint32_t mine[kRankTokens];
-  __shared__ uint32_t cnt[4][kRankTokens];
-  const int t = (int)A.t, t0 = blockIdx.x * kRankTokens;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (threadIdx.x < kRankTokens)
-    mine[threadIdx.x] = t0 + (int)threadIdx.x < t ? key_of(id_at<IdT>(A.ids, t0 + threadIdx.x), A.rows) : 0u;
-  __syncthreads();
-  // Token j precedes token i if its key is smaller, or equal with j < i: for tokens before this
-  // workgroup's, 2 key_j < 2 key_i + 1; for those behind it, 2 key_j + 1 < 2 key_i + 1 (keys are
-  // below 2^31); its own are compared by both. The counts are a wave's, kept on the scalar unit:
-  // one comparison a pair. Eight tokens a lane are on their way at a time.
-  uint32_t k[kRankTokens], c[kRankTokens];
-#pragma unroll
-  for (int i = 0; i < kRankTokens; ++i) {
-    k[i] = 2u * mine[i] + 1u;
-    c[i] = 0u;
-  }
-  constexpr int kBatch = 8;
-  for (int j0 = 0; j0 < t; j0 += 256 * kBatch) {  // uniform
-    uint32_t kj[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int j = j0 + u * 256 + (int)threadIdx.x;
-      const bool other = j < t && (j < t0 || j >= t0 + kRankTokens);
-      kj[u] = other ? 2u * key_of(id_at<IdT>(A.ids, j), A.rows) + (j < t0 ? 0u : 1u) : 0xFFFFFFFFu;
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-#pragma unroll
-      for (int i = 0; i < kRankTokens; ++i) c[i] += (uint32_t)__popcll(__ballot(kj[u] < k[i]));
-  }
-  if (wave == 0) {
-    const bool own = lane < kRankTokens && t0 + lane < t;
-    const uint32_t kl = mine[lane < kRankTokens ? lane : 0];
-#pragma unroll
-    for (int i = 0; i < kRankTokens; ++i)
-      c[i] += (uint32_t)__popcll(__ballot(own && (kl < mine[i] || (kl == mine[i] && lane < i))));
-  }
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kRankTokens; ++i) cnt[wave][i] = c[i];
-  }
-  __syncthreads();
-  if (threadIdx.x < kRankTokens && t0 + (int)threadIdx.x < t) {
-    const int i = threadIdx.x;
-    const uint32_t r = cnt[0][i] + cnt[1][i] + cnt[2][i] + cnt[3][i];
-    A.keys[r] = mine[i];
-    A.toks[r] = (uint32_t)(t0 + i);
-  }
-}
-
 struct SortArgs {
   const void* ids;          // first pass: the ids; NULL afterwards
   int64_t t, rows;
@@ -285,6 +217,31 @@ struct SortArgs {
   uint32_t* counts;         // [nb][256]
   ZeroArgs Z;
 };
+
+// Lanes of the wave whose `bits` low bits of dig agree with this lane's, among those that are on.
+__device__ __forceinline__ uint64_t same_digit(uint32_t dig, int bits, bool on) {
+  uint64_t same = __ballot(on);
+  for (int bit = 0; bit < bits; ++bit) {
+    const uint64_t m = __ballot((dig >> bit) & 1u);
+    same &= ((dig >> bit) & 1u) ? m : ~m;
+  }
+  return same;
+}
+
+// The place of this lane's key: the wave's next place of its digit (`off`, in LDS, this wave's
+// alone) plus its rank among the lanes with the same digit. Moves the wave's places on.
+__device__ __forceinline__ uint32_t take_place(uint32_t* off, uint32_t dig, int bits, bool on) {
+  const uint64_t same = same_digit(dig, bits, on);
+  const uint32_t rank = (uint32_t)__popcll(same & ((1ull << (threadIdx.x & 63)) - 1ull));
+  const uint32_t p = on ? off[dig] + rank : 0u;
+  // one wave's LDS accesses stay in order; the fences keep the compiler from reordering them
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (on && rank == 0u) off[dig] += (uint32_t)__popcll(same);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return p;
+}
 
 template <typename IdT>
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& A, int64_t i) {
@@ -366,26 +323,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs A) 
     const uint32_t key = on ? sort_key<IdT>(A, i) : 0u;
     const uint32_t tok = !on ? 0u : (A.ids ? (uint32_t)i : A.toks_in[i]);
     const uint32_t dig = (key >> A.shift) & 255u;
-    // lanes of the wave with the same digit
-    uint64_t same = __ballot(on);
-#pragma unroll
-    for (int bit = 0; bit < 8; ++bit) {
-      const uint64_t m = __ballot((dig >> bit) & 1u);
-      same &= ((dig >> bit) & 1u) ? m : ~m;
-    }
-    const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
+    const uint32_t p = take_place(off[wave], dig, 8, on);
     if (on) {
-      const uint32_t p = off[wave][dig] + rank;
       A.keys_out[p] = key;
       A.toks_out[p] = tok;
     }
-    // this wave's counters alone, read above before they move on: one wave's LDS accesses stay
-    // in order, and the fences keep the compiler from reordering them
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (on && rank == 0u) off[wave][dig] += (uint32_t)__popcll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -574,6 +516,195 @@ __global__ __launch_bounds__(256) void join_kernel(SegArgs A) {
   }
 }
 
+// ------------------------------------------------------------------------- few tokens
+// One launch: a workgroup owns 2^rlog rows of the output. Its waves look through all ids, a
+// quarter each, and keep the tokens of its rows in token order; a counting sort in LDS by row
+// (stable, as above) puts a row's tokens in a run; groups of 2^tpr_log lanes sum a row each and
+// write it, zeros where it has no token. A row with many tokens is summed by all groups of the
+// workgroup in turns and joined in a fixed order. Every workgroup reads the ids, which costs
+// less than the launches it saves up to kSmallMax tokens.
+constexpr int kSmallMax = 16384;
+constexpr int kSmallRows = 1024;   // rows of a workgroup, at most
+constexpr int kSmallHot = 32;      // tokens of a row that one group sums by itself, at most
+constexpr int kSmallBatch = 16;    // id loads in flight a lane
+constexpr int kSmallSum = 8;       // row loads in flight a lane
+constexpr int kLdsBytes = 160 * 1024;
+
+struct SmallArgs {
+  SegArgs G;        // grad, rows, d, units, scale, output
+  const void* ids;
+  int rlog;
+};
+
+// LDS: the waves' tokens (and later the groups' sums, 256 units), and the sorted tokens.
+__host__ __device__ constexpr int small_list(int t) {
+  return (t + 255) / 256 * 256 * 4 > 8192 ? (t + 255) / 256 * 256 * 4 : 8192;
+}
+__host__ __device__ constexpr int small_lds(int t) { return small_list(t) + (t + 1) / 2 * 4; }
+constexpr int kSmallStatic = 22 * 1024;  // the rest of it
+
+template <int DT, int OUT, bool VEC, typename IdT>
+__global__ __launch_bounds__(256) void small_kernel(SmallArgs P) {
+  const SegArgs& A = P.G;
+  using U = Unit<DT, VEC>;
+  constexpr int N = U::N;
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ uint32_t off[4][kSmallRows];
+  __shared__ uint32_t start[kSmallRows + 1];
+  __shared__ uint32_t wsum[4];
+  __shared__ uint16_t hot[kSmallMax / kSmallHot];
+  __shared__ uint32_t nhot;
+  float* red = (float*)dyn;  // (the lists have been used by then)
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int n = (int)A.t, quarter = (n + 255) / 256 * 64, R = 1 << P.rlog;
+  const int64_t row0 = (int64_t)blockIdx.x << P.rlog;
+  const int64_t nrow = min<int64_t>(R, A.rows - row0);
+  uint32_t* list = (uint32_t*)dyn + wave * quarter;          // row within the workgroup << 14 | token
+  uint16_t* sorted = (uint16_t*)(dyn + small_list(n));
+  for (int i = t; i < 4 * R; i += 256) off[i >> P.rlog][i & (R - 1)] = 0u;
+  if (t == 0) nhot = 0u;
+  __syncthreads();
+
+  int m = 0;  // tokens kept by this wave
+  for (int i0 = wave * quarter; i0 < (wave + 1) * quarter; i0 += kWave * kSmallBatch) {
+    IdT id[kSmallBatch];
+#pragma unroll
+    for (int u = 0; u < kSmallBatch; ++u) {
+      const int i = i0 + u * kWave + lane;
+      id[u] = i < n && i < (wave + 1) * quarter ? ((const IdT*)P.ids)[i] : (IdT)-1;
+    }
+#pragma unroll
+    for (int u = 0; u < kSmallBatch; ++u) {
+      const int64_t r = (int64_t)id[u] - row0;
+      const bool on = id[u] >= 0 && r >= 0 && r < nrow;
+      const uint64_t mask = __ballot(on);
+      if (on) {
+        list[m + __popcll(mask & ((1ull << lane) - 1ull))] = (uint32_t)r << 14 | (uint32_t)(i0 + u * kWave + lane);
+        atomicAdd(&off[wave][r], 1u);
+      }
+      m += __popcll(mask);
+    }
+  }
+  __syncthreads();
+  // first places: rows 4 t .. 4 t + 3 of thread t, then the waves within a row
+  uint32_t cnt[4], all = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = 4 * t + e;
+    cnt[e] = r < R ? off[0][r] + off[1][r] + off[2][r] + off[3][r] : 0u;
+    all += cnt[e];
+  }
+  uint32_t incl = all;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint32_t x = __shfl_up(incl, o, kWave);
+    if (lane >= o) incl += x;
+  }
+  if (lane == kWave - 1) wsum[wave] = incl;
+  __syncthreads();
+  uint32_t p = incl - all;
+  for (int w = 0; w < wave; ++w) p += wsum[w];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = 4 * t + e;
+    if (r < R) {
+      start[r] = p;
+      if (r == R - 1) start[R] = p + cnt[e];
+      uint32_t q = p;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t c = off[w][r];
+        off[w][r] = q;
+        q += c;
+      }
+      if (cnt[e] > (uint32_t)kSmallHot) hot[atomicAdd(&nhot, 1u)] = (uint16_t)r;  // (their order changes no sum)
+    }
+    p += cnt[e];
+  }
+  __syncthreads();
+  for (int i0 = 0; i0 < m; i0 += kWave) {  // wave-uniform
+    const bool on = i0 + lane < m;
+    const uint32_t x = on ? list[i0 + lane] : 0u;
+    const uint32_t to = take_place(off[wave], x >> 14, P.rlog, on);
+    if (on) sorted[to] = (uint16_t)(x & 16383u);
+  }
+  __syncthreads();
+
+  const int tpr = 1 << A.tpr_log;
+  const int sub = t & (tpr - 1), g = t >> A.tpr_log, ng = 256 >> A.tpr_log;
+  // adds tokens from, from + step, .. below `to` of the sorted list
+  auto add_tokens = [&](uint32_t from, uint32_t to, uint32_t step, int64_t j, float (&a)[N]) __attribute__((always_inline)) {
+    for (uint32_t i = from; i < to; i += kSmallSum * step) {
+      float v[kSmallSum][N];
+#pragma unroll
+      for (int b = 0; b < kSmallSum; ++b)
+        if (i + b * step < to) U::load(A.grad, (int64_t)sorted[i + b * step] * A.grad_stride + j, v[b]);
+#pragma unroll
+      for (int b = 0; b < kSmallSum; ++b)
+        if (i + b * step < to)
+#pragma unroll
+          for (int e = 0; e < N; ++e) a[e] += v[b][e];
+    }
+  };
+  for (int r = g; r < nrow; r += ng) {
+    const uint32_t from = start[r], to = start[r + 1];
+    if (to - from > (uint32_t)kSmallHot || (to == from && A.accumulate)) continue;
+    for (int u = sub; u < A.nunit; u += tpr) {
+      float a[N] = {};
+      add_tokens(from, to, 1, (int64_t)u * N, a);
+      write_row<DT, OUT, VEC>(A, (uint32_t)(row0 + r), (int64_t)u * N, a);
+    }
+  }
+  for (uint32_t s = 0; s < nhot; ++s) {
+    const uint32_t r = hot[s];
+    for (int u0 = 0; u0 < A.nunit; u0 += tpr) {
+      const int u = u0 + sub;
+      float a[N] = {};
+      if (u < A.nunit) add_tokens(start[r] + g, start[r + 1], ng, (int64_t)u * N, a);
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < N; ++e) red[t * N + e] = a[e];
+      __syncthreads();
+      for (int h = ng >> 1; h >= 1; h >>= 1) {
+        if (g < h) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) red[t * N + e] += red[(t + h * tpr) * N + e];
+        }
+        __syncthreads();
+      }
+      if (g == 0 && u < A.nunit) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) a[e] = red[t * N + e];
+        write_row<DT, OUT, VEC>(A, (uint32_t)(row0 + r), (int64_t)u * N, a);
+      }
+    }
+  }
+}
+
+template <int DT, int OUT, bool VEC>
+static int launch_small(SegArgs G, const void* ids, int id_bits, hipStream_t s) {
+  G.nunit = G.d / Unit<DT, VEC>::N;
+  G.tpr_log = log2_lanes(G.nunit);
+  // rows of a workgroup: so many that all workgroups run at once (as many a compute unit as its
+  // LDS holds, at most 4), but at most kSmallRows
+  SmallArgs P{G, ids, 0};
+  const int fit = kLdsBytes / (small_lds((int)G.t) + kSmallStatic);
+  const int64_t most = (int64_t)device_cu_count() * (fit > 4 ? 4 : (fit < 1 ? 1 : fit));
+  while (P.rlog < 10 && ((G.rows - 1) >> P.rlog) + 1 > most) ++P.rlog;
+  static_assert(kSmallRows == 1 << 10, "rlog is at most 10");
+  static const hipError_t attr[2] = {
+      hipFuncSetAttribute((const void*)small_kernel<DT, OUT, VEC, int32_t>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                          small_lds(kSmallMax)),
+      hipFuncSetAttribute((const void*)small_kernel<DT, OUT, VEC, int64_t>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                          small_lds(kSmallMax))};
+  (void)attr;
+  const dim3 grid((unsigned)((G.rows + (1 << P.rlog) - 1) >> P.rlog));
+  const size_t lds = small_lds((int)G.t);
+  if (id_bits == 32) hipLaunchKernelGGL((small_kernel<DT, OUT, VEC, int32_t>), grid, dim3(256), lds, s, P);
+  else hipLaunchKernelGGL((small_kernel<DT, OUT, VEC, int64_t>), grid, dim3(256), lds, s, P);
+  return check_launch();
+}
+
 // Sorted tokens per group: enough groups to fill the chip (about 16 waves a compute unit) before
 // a group takes more than 8 tokens, at most 64.
 static int seg_chunk(int64_t t, int tpr_log) {
@@ -617,8 +748,11 @@ static GradPlan grad_plan(int64_t t, int64_t rows, int d) {
   };
   int bits = 1;  // keys 0 .. rows
   while ((int64_t(1) << bits) <= rows) ++bits;
-  const bool rank = t <= kRankMax;
-  P.passes = rank ? 0 : (bits + 7) / 8;
+  if (t <= kSmallMax) {
+    P.bytes = 256;
+    return P;
+  }
+  P.passes = (bits + 7) / 8;
   P.nb = (int)((t + kSortTile - 1) / kSortTile < kSortBlocks ? (t + kSortTile - 1) / kSortTile : kSortBlocks);
   if (P.nb < 1) P.nb = 1;
   P.per = (t + P.nb - 1) / P.nb;
@@ -626,11 +760,9 @@ static GradPlan grad_plan(int64_t t, int64_t rows, int d) {
   P.nb = (int)((t + P.per - 1) / P.per);
   P.keys[0] = take((size_t)t * 4);
   P.toks[0] = take((size_t)t * 4);
-  if (!rank) {
-    P.keys[1] = take((size_t)t * 4);
-    P.toks[1] = take((size_t)t * 4);
-    P.counts = take((size_t)P.nb * 256 * 4);
-  }
+  P.keys[1] = take((size_t)t * 4);
+  P.toks[1] = take((size_t)t * 4);
+  P.counts = take((size_t)P.nb * 256 * 4);
   // partial rows: two per chunk (rows in 16-byte units share the fewest lanes, and so have
   // the smallest chunks)
   const int chunk = seg_chunk(t, log2_lanes(d / 8));
@@ -668,7 +800,7 @@ int mips_embedding_lookup(const void* table, int32_t dtype, int64_t rows, int32_
 size_t mips_embedding_grad_workspace_size(int64_t t, int64_t rows, int32_t d) {
   if (t < 0 || t > MIPS_TOKENS_MAX || rows < 1 || rows > mips::kMaxRows || d < 1 || d > MIPS_EMBEDDING_D_MAX)
     return 0;
-  return t == 0 ? 256 : mips::grad_plan(t, rows, d).bytes;
+  return mips::grad_plan(t, rows, d).bytes;
 }
 
 int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t d,
@@ -688,31 +820,31 @@ int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t
                 !aligned(workspace, 256)))
     return MIPS_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
-  GradPlan P{};
-  if (t > 0) {
-    P = grad_plan(t, rows, d);
-    if (workspace_bytes < P.bytes) return MIPS_ERR_WORKSPACE;
-  }
-  const ZeroArgs Z{out, 0, rows, out_stride * O, (int64_t)d * O, accumulate ? 0 : 1};
+  const GradPlan P = grad_plan(t, rows, d);
+  if (t > 0 && workspace_bytes < P.bytes) return MIPS_ERR_WORKSPACE;
   uint8_t* ws = (uint8_t*)workspace;
+  SegArgs G{grad, grad_stride, nullptr, nullptr, t, rows, d, 0, 0, 0, scale, accumulate, out, out_stride, nullptr, 0};
+  const bool vec = aligned(grad, 16) && aligned(out, 16) && (grad_stride * E) % 16 == 0 &&
+                   (out_stride * O) % 16 == 0 && (d * E) % 16 == 0;
+  // the launcher of the operands' types and units: of few tokens, or of sorted ones
+  auto dispatch = [&](auto small) {
+    auto go = [&](auto dt, auto ot, auto v) {
+      constexpr int DT = decltype(dt)::value, OT = decltype(ot)::value;
+      constexpr bool V = decltype(v)::value;
+      if constexpr (decltype(small)::value) return launch_small<DT, OT, V>(G, ids, id_bits, s);
+      else return launch_segments<DT, OT, V>(G, s);
+    };
+    using F32 = std::integral_constant<int, MIPS_F32>;
+    using B16 = std::integral_constant<int, MIPS_BF16>;
+    if (grad_dtype == MIPS_F32) return vec ? go(F32{}, F32{}, std::true_type{}) : go(F32{}, F32{}, std::false_type{});
+    if (out_dtype == MIPS_BF16) return vec ? go(B16{}, B16{}, std::true_type{}) : go(B16{}, B16{}, std::false_type{});
+    return vec ? go(B16{}, F32{}, std::true_type{}) : go(B16{}, F32{}, std::false_type{});
+  };
+  if (t <= kSmallMax) return t == 0 && accumulate ? MIPS_OK : dispatch(std::true_type{});
+
+  const ZeroArgs Z{out, 0, rows, out_stride * O, (int64_t)d * O, accumulate ? 0 : 1};
   int src = 0;
-  if (t == 0) {  // nothing but the zeros
-    if (!accumulate) {
-      RankArgs R{};
-      R.Z = zero_part(Z, 0, 1, 256);
-      hipLaunchKernelGGL(rank_sort_kernel<int32_t>, dim3(R.Z.nblocks), dim3(256), 0, s, R);
-      return check_launch();
-    }
-    return MIPS_OK;
-  }
-  if (P.passes == 0) {
-    RankArgs R{ids, t, rows, (uint32_t*)(ws + P.keys[0]), (uint32_t*)(ws + P.toks[0]),
-               (int)((t + kRankTokens - 1) / kRankTokens), zero_part(Z, 0, 1, 256)};
-    const dim3 grid(R.nrank + R.Z.nblocks);
-    if (id_bits == 32) hipLaunchKernelGGL(rank_sort_kernel<int32_t>, grid, dim3(256), 0, s, R);
-    else hipLaunchKernelGGL(rank_sort_kernel<int64_t>, grid, dim3(256), 0, s, R);
-    if (const int rc = check_launch()) return rc;
-  } else {
+  {
     for (int p = 0; p < P.passes; ++p) {
       const int in = (p + 1) & 1, to = p & 1;  // pass 0 reads the ids and writes buffer 0
       SortArgs S{p == 0 ? ids : nullptr, t, rows, P.per, P.nb, 8 * p,
@@ -731,15 +863,10 @@ int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t
       src = to;
     }
   }
-  SegArgs G{grad, grad_stride, (const uint32_t*)(ws + P.keys[src]), (const uint32_t*)(ws + P.toks[src]),
-            t, rows, d, 0, 0, 0, scale, accumulate, out, out_stride, (float*)(ws + P.part), 0};
-  const bool vec = aligned(grad, 16) && aligned(out, 16) && (grad_stride * E) % 16 == 0 &&
-                   (out_stride * O) % 16 == 0 && (d * E) % 16 == 0;
-  if (grad_dtype == MIPS_F32)
-    return vec ? launch_segments<MIPS_F32, MIPS_F32, true>(G, s) : launch_segments<MIPS_F32, MIPS_F32, false>(G, s);
-  if (out_dtype == MIPS_BF16)
-    return vec ? launch_segments<MIPS_BF16, MIPS_BF16, true>(G, s) : launch_segments<MIPS_BF16, MIPS_BF16, false>(G, s);
-  return vec ? launch_segments<MIPS_BF16, MIPS_F32, true>(G, s) : launch_segments<MIPS_BF16, MIPS_F32, false>(G, s);
+  G.keys = (const uint32_t*)(ws + P.keys[src]);
+  G.toks = (const uint32_t*)(ws + P.toks[src]);
+  G.part = (float*)(ws + P.part);
+  return dispatch(std::false_type{});
 }
 
 }  // extern "C"

@@ -107,6 +107,9 @@ CASES = [
     ("zipf", 1000, 513, 100), ("padded", 300, 1000, 33), ("one", 3, 8192, 32), ("zipf", 65536, 8192, 64),
     ("zipf", 65535, 8193, 64), ("uniform", 255, 8200, 16), ("uniform", 256, 9001, 24), ("one", 70000, 20000, 128),
     ("padded", 50, 30000, 8), ("zipf", 100000, 120001, 64), ("uniform", 900000, 40000, 16), ("zipf", 200, 9000, 700),
+    ("zipf", 5000, 16384, 16), ("zipf", 5000, 16385, 16), ("uniform", 1 << 24, 17000, 1), ("padded", 70, 1100000, 8),
+    ("zipf", 3000, 1024, 64), ("uniform", 65536, 1025, 8), ("uniform", 1 << 22, 5000, 1), ("one", 1 << 23, 700, 1),
+    ("one", 600, 16384, 8), ("padded", 1025, 16000, 40),
 ]
 
 
@@ -218,4 +221,5 @@ def test_refusals():
         mips.embedding_grad(torch.zeros(3, 8, device=dev), ids, 4,
                             out=torch.zeros(4, 8, device=dev, dtype=torch.bfloat16))
     with pytest.raises(mips.MipsError, match="workspace too small"):
-        mips.embedding_grad(torch.zeros(3, 8, device=dev), ids, 4, workspace=mips.empty_workspace(256, dev))
+        mips.embedding_grad(torch.zeros(20000, 8, device=dev), ids[:1].repeat(20000), 4,
+                            workspace=mips.empty_workspace(256, dev))

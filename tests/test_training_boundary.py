@@ -45,7 +45,8 @@ def test_embedding_grad_refusals(L):
     for bad in (dict(dt=FP8), dict(dt=F32, odt=BF16), dict(bits=8), dict(rows=1 << 31), dict(t=(1 << 30) + 1),
                 dict(d=16385, stride=16385, ostride=16385)):
         assert call(**bad) == UNSUPPORTED, bad
-    assert call(wsb=256) == WORKSPACE
+    assert call(wsb=128) == WORKSPACE
+    assert call(t=20000, wsb=256) == WORKSPACE
 
 
 def test_embedding_grad_workspace(L):
@@ -56,7 +57,7 @@ def test_embedding_grad_workspace(L):
     last = 0
     for t in (1, 8, 100, 8192, 8193, 100000, 1 << 20):
         n = size(t, 1000, 64)
-        assert n >= 8 * t and n >= last
+        assert n >= (8 * t if t > 16384 else 1) and n >= last  # (few tokens are sorted in LDS)
         last = n
 
 
