@@ -41,9 +41,13 @@ struct Unit {
       }
     }
   }
+  template <bool NT = false>
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[N]) {
     if constexpr (DT == MIPS_F32) {
-      if constexpr (VEC)
+      typedef float f32x4_t __attribute__((ext_vector_type(4)));
+      if constexpr (VEC && NT)
+        __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (f32x4_t*)((float*)p + i));
+      else if constexpr (VEC)
         *(float4*)((float*)p + i) = make_float4(v[0], v[1], v[2], v[3]);
       else
         ((float*)p)[i] = v[0];
@@ -53,7 +57,8 @@ struct Unit {
         bf16x8_t o;
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
-        *(bf16x8_t*)((uint16_t*)p + i) = o;
+        if constexpr (NT) __builtin_nontemporal_store(o, (bf16x8_t*)((uint16_t*)p + i));
+        else *(bf16x8_t*)((uint16_t*)p + i) = o;
       } else {
         ((__bf16*)p)[i] = (__bf16)v[0];
       }
@@ -112,7 +117,7 @@ __global__ __launch_bounds__(256) void lookup_kernel(LookupArgs A) {
 #pragma unroll
         for (int e = 0; e < U::N; ++e) v[u][e] *= A.scale;
       }
-      U::store(A.out, t * A.d + (int64_t)j * U::N, v[u]);
+      U::template store<true>(A.out, t * A.d + (int64_t)j * U::N, v[u]);
     }
   }
 }
@@ -181,7 +186,7 @@ __device__ __forceinline__ void zero_rows(const ZeroArgs& Z, int w) {
   if (Z.stride_b == Z.row_b && ((uintptr_t)base & 15) == 0) {
     const int64_t total = rows * Z.row_b, n16 = total / 16;
     u32x4_t* p = (u32x4_t*)base;
-    for (int64_t i = (int64_t)w * nt + threadIdx.x; i < n16; i += (int64_t)Z.nblocks * nt) p[i] = z;
+    for (int64_t i = (int64_t)w * nt + threadIdx.x; i < n16; i += (int64_t)Z.nblocks * nt) __builtin_nontemporal_store(z, p + i);
     if (w == 0 && threadIdx.x < (total & 15) / 2) ((uint16_t*)base)[n16 * 8 + threadIdx.x] = 0;
   } else {
     for (int64_t r = w; r < rows; r += Z.nblocks) {

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void clip_kernel(NormArgs A) {
           bf16x8_t v;
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = (__bf16)(y[e] * coef);  // rounded to nearest even
-          *(bf16x8_t*)o = v;
+          __builtin_nontemporal_store(v, (bf16x8_t*)o);
         } else {
           o[0] = (__bf16)(y[0] * coef);
         }
@@ -154,7 +154,8 @@ __global__ __launch_bounds__(256) void clip_kernel(NormArgs A) {
     } else {
       for_units<false>(T.x, i0, i1, vec, [&](const float* y, int n, int64_t at) __attribute__((always_inline)) {
         float* o = (float*)T.out + at;
-        if (n == 4) *(float4*)o = make_float4(y[0] * coef, y[1] * coef, y[2] * coef, y[3] * coef);
+        typedef float f32x4_t __attribute__((ext_vector_type(4)));
+        if (n == 4) __builtin_nontemporal_store(f32x4_t{y[0] * coef, y[1] * coef, y[2] * coef, y[3] * coef}, (f32x4_t*)o);
         else o[0] = y[0] * coef;
       });
     }
