@@ -20,17 +20,21 @@ namespace mips {
 template <int DT, bool VEC>
 struct Unit {
   static constexpr int N = VEC ? (DT == MIPS_F32 ? 4 : 8) : 1;
+  template <bool NT = false>  // NT: past the caches, for what is not used again soon
   static __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[N]) {
     if constexpr (DT == MIPS_F32) {
       if constexpr (VEC) {
-        const float4 x = *(const float4*)((const float*)p + i);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        const u32x4_t* q = (const u32x4_t*)((const float*)p + i);
+        const u32x4_t x = NT ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(x[j]);
       } else {
         v[0] = ((const float*)p)[i];
       }
     } else {
       if constexpr (VEC) {
-        const u32x4_t x = *(const u32x4_t*)((const uint16_t*)p + i);
+        const u32x4_t* q = (const u32x4_t*)((const uint16_t*)p + i);
+        const u32x4_t x = NT ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[2 * j] = __uint_as_float(x[j] << 16);
@@ -417,7 +421,7 @@ __global__ __launch_bounds__(256) void segment_kernel(SegArgs A) {
       for (int b = 0; b < kSegBatch; ++b) {
         const int64_t ib = i + b < i1 ? i + b : i1 - 1;
         k[b] = A.keys[ib];
-        U::load(A.grad, (int64_t)A.toks[ib] * A.grad_stride + j, v[b]);
+        U::template load<true>(A.grad, (int64_t)A.toks[ib] * A.grad_stride + j, v[b]);
       }
 #pragma unroll
       for (int b = 0; b < kSegBatch; ++b) {

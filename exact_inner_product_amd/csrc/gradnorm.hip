@@ -59,8 +59,8 @@ __device__ __forceinline__ int tensor_of(const NormArgs& A, uint32_t c) {
 }
 
 // Calls f(values, count, element index) for this thread's elements of [i0, i1) of x: 16-byte
-// loads where x is aligned, four of them in flight per thread.
-template <bool BF16, typename F>
+// loads where x is aligned, four of them in flight per thread. LAST: x is not read again.
+template <bool BF16, bool LAST, typename F>
 __device__ __forceinline__ void for_units(const void* x, int64_t i0, int64_t i1, bool vec, F f) {
   constexpr int N = BF16 ? 8 : 4;
   constexpr int kBatch = 4;
@@ -72,7 +72,8 @@ __device__ __forceinline__ void for_units(const void* x, int64_t i0, int64_t i1,
       u32x4_t v[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        v[u] = b + u * 256 < nv ? p[b + u * 256] : u32x4_t{0u, 0u, 0u, 0u};
+        v[u] = b + u * 256 < nv ? (LAST ? __builtin_nontemporal_load(p + b + u * 256) : p[b + u * 256])
+                                : u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (b + u * 256 >= nv) break;
@@ -111,8 +112,8 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs A) {
     auto add = [&](const float* y, int n, int64_t) __attribute__((always_inline)) {
       for (int e = 0; e < n; ++e) s = fma((double)y[e], (double)y[e], s);
     };
-    if ((A.bf16 >> i) & 1u) for_units<true>(T.x, i0, i1, vec, add);
-    else for_units<false>(T.x, i0, i1, vec, add);
+    if ((A.bf16 >> i) & 1u) for_units<true, false>(T.x, i0, i1, vec, add);
+    else for_units<false, false>(T.x, i0, i1, vec, add);
   }
   s = block_sum(s, red);
   if (threadIdx.x == 0) A.part[blockIdx.x] = s;
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(256) void clip_kernel(NormArgs A) {
     const int64_t i1 = min(T.n, i0 + kNormChunk);
     const bool vec = (((uintptr_t)T.x | (uintptr_t)T.out) & 15) == 0;
     if ((A.bf16 >> i) & 1u) {
-      for_units<true>(T.x, i0, i1, vec, [&](const float* y, int n, int64_t at) __attribute__((always_inline)) {
+      for_units<true, true>(T.x, i0, i1, vec, [&](const float* y, int n, int64_t at) __attribute__((always_inline)) {
         __bf16* o = (__bf16*)T.out + at;
         if (n == 8) {
           bf16x8_t v;
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(256) void clip_kernel(NormArgs A) {
         }
       });
     } else {
-      for_units<false>(T.x, i0, i1, vec, [&](const float* y, int n, int64_t at) __attribute__((always_inline)) {
+      for_units<false, true>(T.x, i0, i1, vec, [&](const float* y, int n, int64_t at) __attribute__((always_inline)) {
         float* o = (float*)T.out + at;
         typedef float f32x4_t __attribute__((ext_vector_type(4)));
         if (n == 4) __builtin_nontemporal_store(f32x4_t{y[0] * coef, y[1] * coef, y[2] * coef, y[3] * coef}, (f32x4_t*)o);
