@@ -530,8 +530,8 @@ __global__ __launch_bounds__(256) void join_kernel(SegArgs A) {
 // quarter each, and keep the tokens of its rows in token order; a counting sort in LDS by row
 // (stable, as above) puts a row's tokens in a run; groups of 2^tpr_log lanes sum a row each and
 // write it, zeros where it has no token. A row with many tokens is summed by all groups of the
-// workgroup in turns and joined in a fixed order. Every workgroup reads the ids, which costs
-// less than the launches it saves up to kSmallMax tokens.
+// workgroup in turns and joined in a fixed order. Every workgroup reads the ids; small_pays() says
+// when that costs less than the launches it saves.
 constexpr int kSmallMax = 16384;
 constexpr int kSmallRows = 1024;   // rows of a workgroup, at most
 constexpr int kSmallHot = 32;      // tokens of a row that one group sums by itself, at most
@@ -551,6 +551,25 @@ __host__ __device__ constexpr int small_list(int t) {
 }
 __host__ __device__ constexpr int small_lds(int t) { return small_list(t) + (t + 1) / 2 * 4; }
 constexpr int kSmallStatic = 22 * 1024;  // the rest of it
+
+// Workgroups that run at once: as many a compute unit as its LDS holds, at most 4.
+static int64_t small_resident(int t) {
+  const int fit = kLdsBytes / (small_lds(t) + kSmallStatic);
+  return (int64_t)device_cu_count() * (fit > 4 ? 4 : (fit < 1 ? 1 : fit));
+}
+
+// Whether the gradient takes one launch. Each round of workgroups reads all ids, so the tokens
+// times the rounds decide (all at once on one card, sorted against one launch, in microseconds):
+// 8000 tokens of 1M x 128 rows in bf16, 2 rounds, 69 : 50; 16,000 of 262,144, 1 round, 51 : 36;
+// 4000 of 4M x 64, 6 rounds, 109 : 101; 8000 of 4M x 64, 8 rounds, 114 : 131; 16,000 of 1M x 128,
+// 4 rounds, 71 : 104.
+constexpr int64_t kSmallRounds = 32768;
+static bool small_pays(int64_t t, int64_t rows) {
+  if (t > kSmallMax) return false;
+  const int64_t most = small_resident((int)t);
+  const int64_t rounds = ((rows + kSmallRows - 1) / kSmallRows + most - 1) / most;
+  return t * rounds <= kSmallRounds;
+}
 
 template <int DT, int OUT, bool VEC, typename IdT>
 __global__ __launch_bounds__(256) void small_kernel(SmallArgs P) {
@@ -584,8 +603,8 @@ __global__ __launch_bounds__(256) void small_kernel(SmallArgs P) {
     }
 #pragma unroll
     for (int u = 0; u < kSmallBatch; ++u) {
-      const int64_t r = (int64_t)id[u] - row0;
-      const bool on = id[u] >= 0 && r >= 0 && r < nrow;
+      const uint64_t r = (uint64_t)(int64_t)id[u] - (uint64_t)row0;  // (ids before row0 wrap to the far end)
+      const bool on = id[u] >= 0 && r < (uint64_t)nrow;
       const uint64_t mask = __ballot(on);
       if (on) {
         list[m + __popcll(mask & ((1ull << lane) - 1ull))] = (uint32_t)r << 14 | (uint32_t)(i0 + u * kWave + lane);
@@ -694,11 +713,9 @@ template <int DT, int OUT, bool VEC>
 static int launch_small(SegArgs G, const void* ids, int id_bits, hipStream_t s) {
   G.nunit = G.d / Unit<DT, VEC>::N;
   G.tpr_log = log2_lanes(G.nunit);
-  // rows of a workgroup: so many that all workgroups run at once (as many a compute unit as its
-  // LDS holds, at most 4), but at most kSmallRows
+  // rows of a workgroup: so many that all workgroups run at once, but at most kSmallRows
   SmallArgs P{G, ids, 0};
-  const int fit = kLdsBytes / (small_lds((int)G.t) + kSmallStatic);
-  const int64_t most = (int64_t)device_cu_count() * (fit > 4 ? 4 : (fit < 1 ? 1 : fit));
+  const int64_t most = small_resident((int)G.t);
   while (P.rlog < 10 && ((G.rows - 1) >> P.rlog) + 1 > most) ++P.rlog;
   static_assert(kSmallRows == 1 << 10, "rlog is at most 10");
   static const hipError_t attr[2] = {
@@ -757,7 +774,7 @@ static GradPlan grad_plan(int64_t t, int64_t rows, int d) {
   };
   int bits = 1;  // keys 0 .. rows
   while ((int64_t(1) << bits) <= rows) ++bits;
-  if (t <= kSmallMax) {
+  if (small_pays(t, rows)) {
     P.bytes = 256;
     return P;
   }
@@ -849,7 +866,7 @@ int mips_embedding_grad(const void* grad, int32_t grad_dtype, int64_t t, int32_t
     if (out_dtype == MIPS_BF16) return vec ? go(B16{}, B16{}, std::true_type{}) : go(B16{}, B16{}, std::false_type{});
     return vec ? go(B16{}, F32{}, std::true_type{}) : go(B16{}, F32{}, std::false_type{});
   };
-  if (t <= kSmallMax) return t == 0 && accumulate ? MIPS_OK : dispatch(std::true_type{});
+  if (small_pays(t, rows)) return t == 0 && accumulate ? MIPS_OK : dispatch(std::true_type{});
 
   const ZeroArgs Z{out, 0, rows, out_stride * O, (int64_t)d * O, accumulate ? 0 : 1};
   int src = 0;

@@ -110,6 +110,7 @@ CASES = [
     ("zipf", 5000, 16384, 16), ("zipf", 5000, 16385, 16), ("uniform", 1 << 24, 17000, 1), ("padded", 70, 1100000, 8),
     ("zipf", 3000, 1024, 64), ("uniform", 65536, 1025, 8), ("uniform", 1 << 22, 5000, 1), ("one", 1 << 23, 700, 1),
     ("one", 600, 16384, 8), ("padded", 1025, 16000, 40),
+    ("zipf", 1 << 21, 16000, 8), ("uniform", 1 << 23, 9000, 1),  # few tokens, sorted: many rows
 ]
 
 
