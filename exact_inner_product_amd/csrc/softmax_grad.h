@@ -19,6 +19,28 @@ namespace mips {
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 
+// Lane l of four neighbours gives v[0..3] of column l and gets columns 0..3 of v[l]. All lanes of the
+// wave take part.
+__device__ __forceinline__ void quad_transpose(float (&v)[4], int lane) {
+  auto from = [](float x, auto perm) __attribute__((always_inline)) {
+    constexpr int ctrl = decltype(perm)::value;
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), ctrl, 0xF, 0xF, true));
+  };
+  constexpr std::integral_constant<int, 0xB1> next{};  // of lane l ^ 1
+  constexpr std::integral_constant<int, 0x4E> over{};  // of lane l ^ 2
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {  // rows e and e + 1: columns of this lane and the next
+    const float got = from(odd ? v[e] : v[e + 1], next);
+    const float a = odd ? got : v[e], b = odd ? v[e + 1] : got;
+    v[e] = a, v[e + 1] = b;
+  }
+  const float g0 = from(high ? v[0] : v[2], over), g1 = from(high ? v[1] : v[3], over);
+  const float a = high ? v[2] : v[0], b = high ? v[3] : v[1];
+  v[0] = high ? g0 : a, v[1] = high ? g1 : b;
+  v[2] = high ? a : g0, v[3] = high ? b : g1;
+}
+
 // Streamed rows in LDS: 16-byte slot s of row j is kept at slot s ^ swz(j). Eight consecutive
 // rows' equal slots (the operand of the scores, one row a lane) then lie in eight different
 // 16-byte columns, and four consecutive rows' equal slot pairs (the transposed read of the
@@ -367,28 +389,38 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
     }
   }
 
-  // rows acc_row(i, lane) of the wave's tile, column 32 d + col
+  // A lane holds rows acc_row(i, lane) of column 32 d + col. Four registers of four neighbouring
+  // lanes are transposed, so that lane l stores four columns of row l & 3 at once.
   const int d_live = A.own.row_b / E;
   uint32_t dead = 0u;  // excluded items have no gradient
   if (ITEMS && shared_mask && own0 < A.own.n) dead = A.exclude[own0 >> 5];
+  const bool direct = ITEMS && A.nsplit == 1;
+  if (!direct || A.out != nullptr) {  // (else only the bias' gradient was asked for)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = acc_row(i, lane);
-    const int64_t row = own0 + r;
-    if (row >= A.own.n) continue;
+    for (int q = 0; q < 4; ++q) {
+      const int r = 8 * q + 4 * h + (col & 3);
+      const int64_t row = own0 + r;
+      const bool none = (dead >> r) & 1u;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const int c = 32 * d + col;
-      if (c >= d_live) continue;
-      const float v = ((dead >> r) & 1u) ? 0.0f : sum[d][i];
-      if (A.nsplit > 1 || !ITEMS)
-        A.part[((int64_t)split * A.own.n + row) * d_live + c] = v;
-      else if (A.out == nullptr)
-        continue;  // only the bias' gradient was asked for
-      else if (CT == MIPS_F32)
-        ((float*)A.out)[row * d_live + c] = v * A.scale;
-      else
-        ((__bf16*)A.out)[row * d_live + c] = (__bf16)(v * A.scale);
+      for (int d = 0; d < DT; ++d) {
+        const int c = 32 * d + (col & ~3);
+        const bool on = row < A.own.n && c < d_live;
+        float v[4] = {sum[d][4 * q], sum[d][4 * q + 1], sum[d][4 * q + 2], sum[d][4 * q + 3]};
+        quad_transpose(v, lane);
+        if (!on) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : v[e];
+        if (!direct) {
+          *(float4*)(A.part + ((int64_t)split * A.own.n + row) * d_live + c) = make_float4(v[0], v[1], v[2], v[3]);
+        } else if constexpr (CT == MIPS_F32) {
+          *(float4*)((float*)A.out + row * d_live + c) =
+              make_float4(v[0] * A.scale, v[1] * A.scale, v[2] * A.scale, v[3] * A.scale);
+        } else {
+          typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+          *(bf16x4_t*)((__bf16*)A.out + row * d_live + c) = bf16x4_t{
+              (__bf16)(v[0] * A.scale), (__bf16)(v[1] * A.scale), (__bf16)(v[2] * A.scale), (__bf16)(v[3] * A.scale)};
+        }
+      }
     }
   }
   if constexpr (ITEMS && EXTRA) {
