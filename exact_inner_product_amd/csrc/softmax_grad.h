@@ -413,12 +413,14 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
         if (!direct) {
           *(float4*)(A.part + ((int64_t)split * A.own.n + row) * d_live + c) = make_float4(v[0], v[1], v[2], v[3]);
         } else if constexpr (CT == MIPS_F32) {
-          *(float4*)((float*)A.out + row * d_live + c) =
-              make_float4(v[0] * A.scale, v[1] * A.scale, v[2] * A.scale, v[3] * A.scale);
+          typedef float f32x4_t __attribute__((ext_vector_type(4)));
+          __builtin_nontemporal_store(f32x4_t{v[0] * A.scale, v[1] * A.scale, v[2] * A.scale, v[3] * A.scale},
+                                      (f32x4_t*)((float*)A.out + row * d_live + c));
         } else {
           typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-          *(bf16x4_t*)((__bf16*)A.out + row * d_live + c) = bf16x4_t{
-              (__bf16)(v[0] * A.scale), (__bf16)(v[1] * A.scale), (__bf16)(v[2] * A.scale), (__bf16)(v[3] * A.scale)};
+          __builtin_nontemporal_store(bf16x4_t{(__bf16)(v[0] * A.scale), (__bf16)(v[1] * A.scale),
+                                               (__bf16)(v[2] * A.scale), (__bf16)(v[3] * A.scale)},
+                                      (bf16x4_t*)((__bf16*)A.out + row * d_live + c));
         }
       }
     }
