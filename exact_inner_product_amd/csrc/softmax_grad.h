@@ -44,7 +44,10 @@ __device__ __forceinline__ void quad_transpose(float (&v)[4], int lane) {
 // Streamed rows in LDS: 16-byte slot s of row j is kept at slot s ^ swz(j). Eight consecutive
 // rows' equal slots (the operand of the scores, one row a lane) then lie in eight different
 // 16-byte columns, and four consecutive rows' equal slot pairs (the transposed read of the
-// second product) in four different 32-byte ones: both read without bank conflicts.
+// second product) in four different 32-byte ones: both read at 128 bytes a cycle, half of what LDS
+// can do. Four swizzle bits reach all of it (64 of 145 LDS cycles per 32 x 32 block gone), but need
+// more address arithmetic, and the pass, bound by its matrix and vector instructions, was no
+// faster: 592 + 491 us against 583 + 486 (items + queries, 4096 x 250,000 x 128).
 __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 1); }
 
 // One workgroup = grad_waves waves of 32 own rows each, one split of the streamed rows. A wave
@@ -61,6 +64,14 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 //     (bf16), or element by element (f32).
 // In bf16 the weights are rounded to bf16 for step 3, to nearest: an independent relative error
 // of at most 2^-8 each, under sums that are rounded to bf16 themselves. Sums are in binary32.
+//
+// What bounds it: matrix and vector instructions together, which share a SIMD's issue. Per 32 x 32
+// block of a width of 128 in bf16, 17 products of 32 cycles and about 70 vector instructions, 16 of
+// them exp2 (8 cycles each): at 4096 x 250,000 x 128 the queries' pass takes 456-486 us (1.08-1.15
+// PFLOP/s of its two products) with the matrix pipes busy 57% and the vector units 43% of the
+// cycles; the items' pass 540-583 us (47% and 40%; it also looks for targets and signs). In f32
+// the products bound it (32 x 32 x 2, 64 cycles each). A small batch is latency: 1000 x 1000 x 64
+// in f32 takes 14.5 + 11.5 us, 4096 x 8192 x 128 in bf16 31 + 30 us.
 //
 // Step 1 of the next 32 rows is interleaved with step 2 of these, chunk by chunk, so that the
 // matrix pipe works under the exponentials. Tiles of 64 streamed rows go through three LDS
@@ -390,7 +401,8 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
   }
 
   // A lane holds rows acc_row(i, lane) of column 32 d + col. Four registers of four neighbouring
-  // lanes are transposed, so that lane l stores four columns of row l & 3 at once.
+  // lanes are transposed, so that lane l stores four columns of row l & 3 at once (items' pass of
+  // 452 x 860,000 x 16: 177 us, with a store per column 206).
   const int d_live = A.own.row_b / E;
   uint32_t dead = 0u;  // excluded items have no gradient
   if (ITEMS && shared_mask && own0 < A.own.n) dead = A.exclude[own0 >> 5];
