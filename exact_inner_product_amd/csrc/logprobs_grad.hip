@@ -65,22 +65,10 @@ struct JoinArgs {
   float scale;
   const float* sign;  // a factor per row, or NULL
   void* out;          // [rows, d]
-  const int32_t* tgt; // queries' pass: the targets' rows are added here, unrounded
-  const float* gval;
-  int g;
-  Table items;
   int ways_log;       // 2^ways_log threads share four columns of a row
 };
 
-template <int DT>
-__device__ __forceinline__ float4 load4(const uint8_t* row, int c) {
-  if (DT == MIPS_F32) return *(const float4*)(row + 4 * c);
-  const uint2 v = *(const uint2*)(row + 2 * c);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xFFFF0000u));
-}
-
-// Four columns of a row: the splits' sums, the targets' rows, the scale and the one rounding to
+// Four columns of a row: the splits' sums, the scale and the one rounding to
 // the operands' type. Way w of the threads that share them adds splits w, w + ways, ..; the ways are
 // joined in a fixed order in LDS. Of many splits it is bound by the latency of the loads: 256
 // splits of 160 x 128 sums take 23.8 us by one way, 14.0, 9.4 and 8.0 by 2, 4 and 8 (and 8.0 by 16);
@@ -110,13 +98,6 @@ __global__ __launch_bounds__(256) void join_rows_kernel(JoinArgs A) {
   if (A.sign) {
     const float k = A.sign[row];
     v.x *= k, v.y *= k, v.z *= k, v.w *= k;
-  }
-  for (int g = 0; g < A.g; ++g) {
-    const int32_t t = A.tgt[row * A.g + g];
-    if (t < 0) continue;
-    const float k = A.gval[row * A.g + g];
-    const float4 y = load4<DT>(A.items.p + (int64_t)t * A.items.stride_b, c);
-    v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
   }
   v.x *= A.scale, v.y *= A.scale, v.z *= A.scale, v.w *= A.scale;
   if (DT == MIPS_F32) {
@@ -321,7 +302,7 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
     A.bias_part = grad_bias ? (float*)(ws + P.bias_part) : nullptr;
     if (const int rc = grad_dispatch(dtype, P.width, true, extra, A, s)) return rc;
     if (grad_items && P.i.nsplit > 1) {
-      const JoinArgs J{A.part, P.i.nsplit, n, d, scale, nullptr, grad_items, nullptr, nullptr, 0, ti, 0};
+      const JoinArgs J{A.part, P.i.nsplit, n, d, scale, nullptr, grad_items, 0};
       if (const int rc = launch_join(J, dtype, s)) return rc;
     }
     if (grad_bias) {
@@ -340,7 +321,7 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
     A.part = (float*)(ws + P.part);
     A.bias_part = nullptr;
     if (const int rc = grad_dispatch(dtype, P.width, false, extra, A, s)) return rc;
-    const JoinArgs J{A.part, P.q.nsplit, b, d, scale, extra ? nullptr : T.sign, grad_queries, T.tgt, T.gval, g, ti, 0};
+    const JoinArgs J{A.part, P.q.nsplit, b, d, scale, extra ? nullptr : T.sign, grad_queries, 0};
     if (const int rc = launch_join(J, dtype, s)) return rc;
   }
   return MIPS_OK;

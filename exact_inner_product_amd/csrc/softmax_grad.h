@@ -63,7 +63,10 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 //     other operand takes the streamed rows in the same order, transposed by the LDS read
 //     (bf16), or element by element (f32).
 // In bf16 the weights are rounded to bf16 for step 3, to nearest: an independent relative error
-// of at most 2^-8 each, under sums that are rounded to bf16 themselves. Sums are in binary32.
+// of at most 2^-8 each, under sums that are rounded to bf16 themselves. What is rounded is the whole
+// weight: both passes add the targets' gradients in step 2. A target with nearly all of the
+// probability has a weight of nearly 0, the difference of g and p g; with p g rounded by itself, the
+// queries' gradients were off by several times their size. Sums are in binary32.
 //
 // What bounds it: matrix and vector instructions together, which share a SIMD's issue. Per 32 x 32
 // block of a width of 128 in bf16, 17 products of 32 cycles and about 70 vector instructions, 16 of
@@ -138,8 +141,10 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
   // the lane's own terms
   const float masked_add = kMasked * A.inv_scx;
   float my_add = 0.0f, my_coef = 0.0f, my_hent = 0.0f;
+  bool flip = false;  // this query's sums are of -w: its coefficient is negative (plain)
   if constexpr (!ITEMS) {
     my_add = live ? A.q.add[own_c] : kMasked;
+    if (!EXTRA) flip = (A.q.neg[own_c >> 5] >> (own_c & 31)) & 1u;
     if (EXTRA) my_coef = live ? A.q.coef[own_c] : 0.0f;
     if (EXTRA) my_hent = live ? A.q.hent[own_c] : 0.0f;
   } else {
@@ -147,6 +152,20 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
   }
 
   const int64_t t_begin = (int64_t)split * A.ntiles / A.nsplit, t_end = (int64_t)(split + 1) * A.ntiles / A.nsplit;
+
+  // Queries' pass: the lane's query has no target below this row that has not been passed yet. The
+  // blocks come in the rows' order, so that one comparison a block finds the few that hold a target.
+  // visit() calls f(row, its gradient) for the targets in [first, end), in the order given, and moves on.
+  int32_t target = INT32_MAX;
+  auto visit = [&](int32_t first, int32_t end, auto f) __attribute__((always_inline)) {
+    target = INT32_MAX;
+    for (int g = 0; g < A.q.g; ++g) {
+      const int32_t t = A.q.tgt[own_c * A.q.g + g];
+      if (t >= end) target = min(target, t);
+      else if (t >= first) f(t, A.q.gval[own_c * A.q.g + g]);
+    }
+  };
+  if (!ITEMS && live) visit(0, (int32_t)(t_begin * kGradTile), [](int32_t, float) {});
 
   // ---- staging
   u32x4_t ld[NLD];
@@ -343,6 +362,18 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
 #pragma unroll
         for (int i = 0; i < 16; ++i) dbias += w[i];
       }
+    } else {
+      // targets of this wave's queries among the block's items, as rare: row r of the block is
+      // register 4 (r >> 3) + (r & 3) of half (r >> 2) & 1
+      const int32_t first = (int32_t)(tile * kGradTile) + jb * 32;
+      if (__ballot(target < first + 32) != 0ull && target < first + 32)
+        visit(first, first + 32, [&](int32_t t, float v) __attribute__((always_inline)) {
+          const int r = t - first;
+          const int at = ((r >> 2) & 1) == h ? 4 * (r >> 3) + (r & 3) : -1;
+          v = flip ? -v : v;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] += i == at ? v : 0.0f;
+        });
     }
     between();
     // sums += w^T Y
