@@ -66,7 +66,10 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 // of at most 2^-8 each, under sums that are rounded to bf16 themselves. What is rounded is the whole
 // weight: both passes add the targets' gradients in step 2. A target with nearly all of the
 // probability has a weight of nearly 0, the difference of g and p g; with p g rounded by itself, the
-// queries' gradients were off by several times their size. Sums are in binary32.
+// queries' gradients were off by several times their size. Blocks with a target in them take step 3
+// a second time, for what the first rounding left: a target's weight is most of its item's gradient,
+// and would double that gradient's error (of 250,000 items by 4096 queries 0.4% of the blocks have
+// a target). Sums are in binary32.
 //
 // What bounds it: matrix and vector instructions together, which share a SIMD's issue. Per 32 x 32
 // block of a width of 128 in bf16, 17 products of 32 cycles and about 70 vector instructions, 16 of
@@ -291,6 +294,7 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
       if (!EXTRA) negw = vneg[buf * (kGradTile / 32) + jb];
     }
     float w[16];
+    bool target_here = false;  // a target's weight in the block; uniform over the wave
     float ck[16], hk[16];
     if constexpr (EXTRA && ITEMS) {
 #pragma unroll
@@ -348,6 +352,7 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
       for (int g = 0; g < A.q.g; ++g) {
         const int32_t tgt = g == 0 ? tgt0 : vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
         uint32_t hits = (uint32_t)__ballot(tgt >= own0 && tgt < own0 + 32);
+        target_here |= hits != 0u;
         while (hits != 0u) {
           const int j = __builtin_ctz(hits);
           hits &= hits - 1u;
@@ -366,7 +371,8 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
       // targets of this wave's queries among the block's items, as rare: row r of the block is
       // register 4 (r >> 3) + (r & 3) of half (r >> 2) & 1
       const int32_t first = (int32_t)(tile * kGradTile) + jb * 32;
-      if (__ballot(target < first + 32) != 0ull && target < first + 32)
+      target_here = __ballot(target < first + 32) != 0ull;
+      if (target_here && target < first + 32)
         visit(first, first + 32, [&](int32_t t, float v) __attribute__((always_inline)) {
           const int r = t - first;
           const int at = ((r >> 2) & 1) == h ? 4 * (r >> 3) + (r & 3) : -1;
@@ -387,6 +393,17 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
         for (int d = 0; d < DT; ++d)
           sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               wa, kb == 0 && d < kAhead ? ahead[d < kAhead ? d : 0] : read_columns(kb, d), sum[d], 0, 0, 0);
+      }
+      if (__builtin_expect(target_here, 0)) {  // the weights' next eight bits
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          bf16x8_t wa;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) wa[e] = (__bf16)(w[8 * kb + e] - (float)(__bf16)w[8 * kb + e]);
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, read_columns(kb, d), sum[d], 0, 0, 0);
+        }
       }
     } else {
 #pragma unroll

@@ -76,3 +76,22 @@ def test_weights_keep_what_the_formula_leaves(b, n, d, g, sign, confident, extra
     got = mips.item_logprobs_backward(gl.to(dev), *args, f, scale=scale, need_bias=extra)
     check(got[0], *dq, "queries")
     check(got[1], *di, "items")
+
+
+@pytest.mark.parametrize("b,n,d,g", [(64, 500, 64, 1), (300, 2000, 128, 1), (90, 777, 256, 3), (20, 9000, 32, 1),
+                                     (700, 700, 24, 1)])
+@pytest.mark.parametrize("extra", [False, True])
+def test_a_targets_weight_is_kept_to_16_bits(b, n, d, g, extra):
+    """It is most of its item's gradient: 2^-16 of it may be lost, 2^-8 of the others."""
+    dev = _dev()
+    print(f"logprobs grad precision at targets b={b} n={n} d={d} g={g} extra={extra}", flush=True)
+    rng = np.random.default_rng(b + n)
+    items, q = grid(rng, n, d, "bf16"), grid(rng, b, d, "bf16")
+    ids = torch.from_numpy(rng.integers(0, n, (b, g)))
+    gl = torch.from_numpy(rng.uniform(-1.5, 1.5, (b, g)).astype(np.float32))
+    dq, di, _ = bounds(q, items, 10.0, ids, gl, 2.0 ** -16)
+    args = [x.to(dev) for x in (q, items, ids)]
+    f = mips.item_logprobs(*args, scale=10.0)
+    got = mips.item_logprobs_backward(gl.to(dev), *args, f, scale=10.0, need_bias=extra)
+    check(got[0], *dq, "queries")
+    check(got[1], *di, "items")
