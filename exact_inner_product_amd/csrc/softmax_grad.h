@@ -193,6 +193,9 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
         if (EXTRA) lc = A.q.hent[r];
       } else {
         la = r >= A.str.n ? masked_add : (A.bias ? A.bias[r] * kLog2e * A.inv_scx : 0.0f);
+        // a bias that masks its item (-inf, the lowest float) stays finite: -inf would make NaN of
+        // its parts and of its product with the zeros beside the ones (a NaN bias stays NaN)
+        la = la < masked_add ? masked_add : la;
         law = shared_mask && r < A.str.n ? A.exclude[r >> 5] >> (r & 31) : 0u;
       }
     }

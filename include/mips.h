@@ -431,7 +431,7 @@ MIPS_API int mips_clip_grad_norm(const void *const *tensors, void *const *outs,
  *                MIPS_PACKED as mips_prepare_corpus. Rows are 16-byte aligned (base and
  *                stride) and at most 2^25 bytes apart.
  *   dtype        MIPS_F32 or MIPS_BF16, of queries and items.
- *   bias         device float [n] or NULL.
+ *   bias         device float [n] or NULL. -INFINITY and the lowest float mask an item: p = 0.
  *   exclude, exclude_row_words   as mips_topk: ids whose bit is set have probability 0,
  *                whatever their rows hold (NaN and infinities included).
  *   scale        MIPS_SCALE_MIN .. MIPS_SCALE_MAX.
