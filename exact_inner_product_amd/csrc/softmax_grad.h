@@ -318,7 +318,9 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
         if constexpr (EXTRA) {
           float k = ITEMS ? ck[i] : my_coef;
           if (A.use_hent) k = fmaf(t, ITEMS ? hk[i] : my_hent, k);
-          w[i] = ((bits >> i) & 1u) ? 0.0f : w[i] * k;
+          // (0 log 0 = 0: log2 p of a masked item may be -inf)
+          const bool none = ((bits >> i) & 1u) || (A.use_hent && w[i] == 0.0f);
+          w[i] = none ? 0.0f : w[i] * k;
         }
         asm volatile("" : "+v"(w[i]));  // computed here, under these products
       }

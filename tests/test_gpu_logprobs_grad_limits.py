@@ -97,3 +97,42 @@ def test_masking_biases_at_the_scales_limits(dtype, scale):
         refs, r = gradients64(q, items, scale, ids, gl, None, bias)
         check(got, refs, r, dtype == "bf16")
     assert all(torch.isfinite(x.float()).all() for x in got)
+
+
+@pytest.mark.parametrize("dtype,b,n,d", SHAPES)
+@pytest.mark.parametrize("kind", ["inf", "lowest", "both"])
+def test_masking_biases_with_entropy(dtype, b, n, d, kind):
+    """0 log 0 = 0: neither the pass that owns the items nor the one that streams them makes it a NaN.
+    The forward pass' entropy is given from 64 bits."""
+    dev = _dev()
+    print(f"logprobs grad entropy, masking bias {kind} {dtype} b={b} n={n} d={d}", flush=True)
+    rng = np.random.default_rng(n + d + len(kind))
+    q, items, bias, ids, gl = inputs(rng, dtype, b, n, d, kind)
+    gh = torch.from_numpy(rng.uniform(-1, 1, b).astype(np.float32))
+    gh[::4] = 0.0
+    refs, r = gradients64(q, items, 10.0, ids, gl, gh, bias)
+    l = logits64(q, items, 10.0, bias).astype(np.float64)
+    l[l < -1e30] = -np.inf
+    lp = l - np.logaddexp.reduce(l, axis=1, keepdims=True)
+    entropy = torch.from_numpy((-(np.exp(lp) * np.where(np.isfinite(lp), lp, 0)).sum(1)).astype(np.float32))
+    args = [x.to(dev) for x in (q, items, ids)]
+    f = mips.item_logprobs(*args, scale=10.0, bias=bias.to(dev), entropy=False)
+    f.entropy = entropy.to(dev)
+    got = mips.item_logprobs_backward(gl.to(dev), *args, f, scale=10.0, bias=bias.to(dev), grad_entropy=gh.to(dev),
+                                      need_bias=True)
+    check(got, refs, r, dtype == "bf16")
+
+
+def test_large_entropy_gradients_of_masked_items():
+    """h log p overflows where log p is that of a masked item; p = 0 all the same."""
+    dev = _dev()
+    rng = np.random.default_rng(9)
+    q, items, bias, _, _ = inputs(rng, "bf16", 40, 300, 64, "both")
+    low = bias < -1e30
+    q, items, bias = q.to(dev), items.to(dev), bias.to(dev)
+    f = mips.item_logprobs(q, items, scale=5.0, bias=bias)
+    f.entropy = torch.ones(40, device=dev)
+    dq, di, db = mips.item_logprobs_backward(None, q, items, None, f, scale=5.0, bias=bias, need_bias=True,
+                                             grad_entropy=torch.full((40,), 1e12, device=dev))
+    assert torch.isfinite(dq.float()).all() and torch.isfinite(di.float()).all() and torch.isfinite(db).all()
+    assert (di[low] == 0).all() and (db[low] == 0).all()
