@@ -180,7 +180,9 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
       const int e = i * NT + threadIdx.x, j = e / SL, s = e % SL;
-      const int64_t r = tile * kGradTile + j;
+      // Padding queries, of weight 0, hold the last one's row: zeros would make NaN of the score
+      // with an item's row of infinities.
+      const int64_t r = ITEMS ? min(tile * kGradTile + j, A.str.n - 1) : tile * kGradTile + j;
       ld[i] = u32x4_t{0u, 0u, 0u, 0u};
       if (r < A.str.n && 16 * s < A.str.row_b) ld[i] = *(const u32x4_t*)(A.str.p + r * A.str.stride_b + 16 * s);
       if (!ITEMS && shared_mask) lw[i] = r < A.str.n ? A.exclude[r >> 5] : 0u;

@@ -136,3 +136,24 @@ def test_large_entropy_gradients_of_masked_items():
                                              grad_entropy=torch.full((40,), 1e12, device=dev))
     assert torch.isfinite(dq.float()).all() and torch.isfinite(di.float()).all() and torch.isfinite(db).all()
     assert (di[low] == 0).all() and (db[low] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 16), ("bf16", 64)])
+def test_scores_of_minus_infinity_with_entropy(dtype, d):
+    """Items of p = 0 by their own rows have no gradient either (the queries' would multiply 0 with
+    those rows)."""
+    dev = _dev()
+    rng = np.random.default_rng(d)
+    b, n = 50, 200
+    q, items = grid(rng, b, d, dtype), grid(rng, n, d, dtype)
+    q[:, 0] = q[:, 0].abs() + 2.0 ** -8
+    low = np.arange(n) % 3 == 0
+    items[torch.from_numpy(low), 0] = -float("inf")
+    gh = torch.from_numpy(rng.uniform(-1, 1, b).astype(np.float32)).to(dev)
+    q, items = q.to(dev), items.to(dev)
+    f = mips.item_logprobs(q, items, scale=5.0)
+    f.entropy = torch.ones(b, device=dev)
+    _, di, db = mips.item_logprobs_backward(None, q, items, None, f, scale=5.0, grad_entropy=gh, need_queries=False,
+                                            need_bias=True)
+    for x in (di.float().cpu(), db.cpu()):
+        assert torch.isfinite(x).all() and (x[low] == 0).all() and (x[~low] != 0).any()
