@@ -305,6 +305,18 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
         }
         if constexpr (NQF > 1) __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (ENT) {
+        // A logit of -inf (a bias that masks, a row of infinities) has e = 0 and made e t a NaN; it
+        // adds 0. Rare, so the sum is taken again where it came out NaN; a NaN of its own stays one.
+        if (__builtin_expect(__ballot(x0 + x1 != x0 + x1) != 0ull, 0)) {
+          x0 = x1 = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 16 * RM; ++k) {
+            const float t = fmaf(cur[k >> 4][k & 15], A.scx, -m);
+            x0 = fmaf(__builtin_amdgcn_exp2f(t), fmaxf(t, kMasked), x0);
+          }
+        }
+      }
       st[(SV * f + 0) * kWave] = m;
       st[(SV * f + 1) * kWave] = z + (z0 + z1);
       if constexpr (ENT) st[(SV * f + 2) * kWave] = x + (x0 + x1);

@@ -1,0 +1,68 @@
+"""Log probabilities where logits are infinite, of the lowest value or NaN: biases that mask items,
+scores of -inf, rows of NaN, and queries that such values leave without an item.
+
+Definitions as in tests/test_gpu_logprobs.py, whose tolerances hold: a logit of -inf (or far below
+every other one) has probability 0 and adds 0 to the entropy, so the finite logits alone decide the
+sums and the bounds. The log probability of an item with the lowest finite bias is that bias: what is
+subtracted is below its last place."""
+import numpy as np
+import pytest
+import torch
+
+import exact_inner_product_amd as mips
+from tests.test_gpu_logprobs import check, grid, logits64
+
+pytestmark = pytest.mark.gpu
+LOWEST = float(np.finfo(np.float32).min)
+
+
+def _dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return torch.device("cuda:0")
+
+
+def masking_bias(rng, n, kind, share=0.4):
+    """(bias, which items it masks): -inf, the lowest float, or both in turn."""
+    low = rng.random(n) < share
+    bias = rng.uniform(-8, 8, n).astype(np.float32)
+    bias[low] = {"inf": -np.inf, "lowest": LOWEST, "both": np.where(np.arange(low.sum()) % 2, -np.inf, LOWEST)}[kind]
+    return torch.from_numpy(bias), low
+
+
+SHAPES = [("f32", 5, 333, 16), ("bf16", 40, 2000, 64), ("bf16", 300, 1000, 128), ("f32", 70, 70000, 32),
+          ("bf16", 9, 3333, 256), ("bf16", 600, 90000, 16)]
+
+
+@pytest.mark.parametrize("dtype,b,n,d", SHAPES)
+@pytest.mark.parametrize("kind", ["inf", "lowest", "both"])
+def test_entropy_under_masking_biases(dtype, b, n, d, kind):
+    dev = _dev()
+    print(f"logprobs masking bias {kind} {dtype} b={b} n={n} d={d}", flush=True)
+    rng = np.random.default_rng(n + len(kind))
+    items, q = grid(rng, n, d, dtype), grid(rng, b, d, dtype)
+    bias, low = masking_bias(rng, n, kind)
+    low[:64] = True  # whole tiles too
+    bias[:64] = -np.inf if kind != "lowest" else LOWEST
+    ids = torch.from_numpy(np.flatnonzero(~low)[rng.integers(0, (~low).sum(), (b, 2))]).to(torch.int32)
+    r = mips.item_logprobs(q.to(dev), items.to(dev), ids.to(dev), scale=10.0, bias=bias.to(dev))
+    l = logits64(q, items, 10.0, bias)
+    l[:, low] = -np.inf
+    check(r, l, ids)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 16), ("bf16", 64), ("bf16", 128)])
+def test_entropy_with_scores_of_minus_infinity(dtype, d):
+    """Items whose rows hold -inf against queries that are positive there: p = 0 without a bias."""
+    dev = _dev()
+    rng = np.random.default_rng(d)
+    items, q = grid(rng, 3000, d, dtype), grid(rng, 40, d, dtype)
+    q[:, 0] = q[:, 0].abs() + 2.0 ** -8
+    low = rng.random(3000) < 0.3
+    low[:32] = True
+    items[torch.from_numpy(low), 0] = -float("inf")
+    ids = torch.from_numpy(np.flatnonzero(~low)[:80].reshape(40, 2))
+    r = mips.item_logprobs(q.to(dev), items.to(dev), ids.to(dev), scale=10.0)
+    l = logits64(q, torch.where(torch.from_numpy(low)[:, None], 0, items), 10.0)
+    l[:, low] = -np.inf
+    check(r, l, ids)
