@@ -269,9 +269,11 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       if (__builtin_expect(__ballot(mn > m + kSlack) != 0ull, 0)) {
         if (mn > m) {
           const float g = __builtin_amdgcn_exp2f(m - mn);
-          // (a sum over masked values alone is dropped here, whatever it holds)
-          x = g > 0.0f ? g * (x - (mn - m) * z) : 0.0f;
-          z = g > 0.0f ? g * z : 0.0f;
+          // (a sum over masked values alone is dropped here, infinite or not; NaN came from an eligible
+          // item, in a tile that held nothing else, and stays)
+          const float kept = z == z ? 0.0f : z;
+          x = g > 0.0f ? g * (x - (mn - m) * z) : kept;
+          z = g > 0.0f ? g * z : kept;
           m = mn;
         }
       }

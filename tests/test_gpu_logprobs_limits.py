@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import exact_inner_product_amd as mips
-from tests.test_gpu_logprobs import check, grid, logits64
+from tests.test_gpu_logprobs import bitmap, check, grid, logits64
 
 pytestmark = pytest.mark.gpu
 LOWEST = float(np.finfo(np.float32).min)
@@ -66,3 +66,44 @@ def test_entropy_with_scores_of_minus_infinity(dtype, d):
     l = logits64(q, torch.where(torch.from_numpy(low)[:, None], 0, items), 10.0)
     l[:, low] = -np.inf
     check(r, l, ids)
+
+
+@pytest.mark.parametrize("first", [0, 9984, 19968])
+@pytest.mark.parametrize("what", ["rows", "bias"])
+@pytest.mark.parametrize("k", [0, 4])
+def test_a_block_of_nan_reaches_every_query(first, what, k):
+    """So many queries that a wave takes several tiles of 64 items: the NaN are in its first, a middle
+    or the last one, as whole rows or biases."""
+    dev = _dev()
+    rng = np.random.default_rng(3)
+    n, b, d = 20032, 2100, 64
+    items, q = grid(rng, n, d, "bf16").to(dev), grid(rng, b, d, "bf16").to(dev)
+    bias = torch.zeros(n, device=dev)
+    if what == "rows":
+        items[first:first + 64] = float("nan")
+    else:
+        bias[first:first + 64] = float("nan")
+    ids = torch.full((b, 1), 5000, device=dev)
+    r = mips.item_logprobs(q, items, ids, scale=10.0, bias=bias if what == "bias" else None, alternatives=k)
+    assert torch.isnan(r.logsumexp).all() and torch.isnan(r.entropy).all() and torch.isnan(r.logprobs).all()
+    # few queries over many items, f32, and a single wide tile of a wave
+    items, q = grid(rng, 300000, 16, "f32").to(dev), grid(rng, 3, 16, "f32").to(dev)
+    items[first:first + 64] = float("nan")
+    r = mips.item_logprobs(q, items, scale=10.0, alternatives=k)
+    assert torch.isnan(r.logsumexp).all() and torch.isnan(r.entropy).all()
+
+
+def test_nan_rows_behind_a_bitmap_stay_out():
+    """The block of NaN is excluded for some queries: those are finite, the others NaN."""
+    dev = _dev()
+    rng = np.random.default_rng(6)
+    n, b, d = 5000, 70, 64
+    items, q = grid(rng, n, d, "bf16"), grid(rng, b, d, "bf16")
+    held = items.clone()
+    held[:64] = float("nan")
+    mask = np.zeros((b, n), bool)
+    mask[::2, :64] = True
+    r = mips.item_logprobs(q.to(dev), held.to(dev), scale=10.0, exclude=bitmap(mask).to(dev))
+    assert torch.isnan(r.logsumexp[1::2]).all() and torch.isnan(r.entropy[1::2]).all()
+    even = mips.ItemLogprobs(None, r.logsumexp[::2], r.entropy[::2], None, None)
+    check(even, logits64(q, items, 10.0, None, mask)[::2])
