@@ -102,6 +102,9 @@ __device__ __forceinline__ float logit(const FinishArgs& A, float s, float bias)
   return A.bias ? __fadd_rn(l, bias) : l;
 }
 
+// Of a query that is left without an item (lse -inf, by bitmap or biases) every item's is -inf.
+__device__ __forceinline__ float log_prob(float l, float lse) { return lse == -INFINITY ? -INFINITY : l - lse; }
+
 __device__ __forceinline__ bool excluded(const FinishArgs& A, int q, int64_t row) {
   if (!A.exclude) return false;
   return (A.exclude[(int64_t)q * A.exclude_words + (row >> 5)] >> (row & 31)) & 1u;
@@ -197,7 +200,7 @@ __global__ __launch_bounds__(256) void pairs_kernel(FinishArgs A) {
     if (diagonal() && p0 + (lane & 31) < nb * A.g)
       A.logprobs[at] = pad ? 0.0f
                            : (excluded(A, b0 + bl, row) ? -INFINITY
-                                                        : logit(A, s, A.bias ? A.bias[row] : 0.0f) - s_lse[bl]);
+                                                        : log_prob(logit(A, s, A.bias ? A.bias[row] : 0.0f), s_lse[bl]));
   }
 }
 
@@ -419,7 +422,7 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
       keys[i * kFrag + (lane & 31)] = live && !out ? composite(score_key(l), (uint32_t)x.row) : 0ull;
     } else {
       const int g = (i - nb) * kFrag + (lane & 31);
-      if (g < A.g) A.logprobs[(int64_t)b * A.g + g] = !live ? 0.0f : (out ? -INFINITY : l - lse);
+      if (g < A.g) A.logprobs[(int64_t)b * A.g + g] = !live ? 0.0f : (out ? -INFINITY : log_prob(l, lse));
     }
   };
   Block x0, x1;

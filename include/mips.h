@@ -441,7 +441,8 @@ MIPS_API int mips_clip_grad_norm(const void *const *tensors, void *const *outs,
  *   out_logprobs device float [b, g]; out_lse device float [b]; out_entropy device float [b]
  *                or NULL; out_alt_ids device int32 [b, k] and out_alt_logprobs device float
  *                [b, k]: largest first, missing ones (-1, -INFINITY).
- *                A query without an eligible item has lse -INFINITY and entropy 0.
+ *                A query without an eligible item, or whose eligible logits are all below -6e29
+ *                (-INFINITY among them), has lse and log probabilities -INFINITY and entropy 0.
  *   workspace    device, 256-byte aligned, mips_logprobs_workspace_size bytes (it depends on
  *                the device's compute units; 0 for unsupported sizes). Calls that share one
  *                must be ordered.

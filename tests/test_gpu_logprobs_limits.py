@@ -107,3 +107,34 @@ def test_nan_rows_behind_a_bitmap_stay_out():
     assert torch.isnan(r.logsumexp[1::2]).all() and torch.isnan(r.entropy[1::2]).all()
     even = mips.ItemLogprobs(None, r.logsumexp[::2], r.entropy[::2], None, None)
     check(even, logits64(q, items, 10.0, None, mask)[::2])
+
+
+@pytest.mark.parametrize("k", [0, 5])
+@pytest.mark.parametrize("kind", ["inf", "lowest", "both"])
+def test_given_ids_of_masked_items(kind, k):
+    """logp = l - lse: -inf, or the lowest float itself."""
+    dev = _dev()
+    rng = np.random.default_rng(1)
+    n, b = 777, 37
+    items, q = grid(rng, n, 64, "bf16"), grid(rng, b, 64, "bf16")
+    bias, low = masking_bias(rng, n, kind)
+    ids = torch.from_numpy(np.flatnonzero(low)[rng.integers(0, low.sum(), (b, 3))])
+    r = mips.item_logprobs(q.to(dev), items.to(dev), ids.to(dev), scale=10.0, bias=bias.to(dev), alternatives=k)
+    assert torch.equal(r.logprobs.cpu(), bias[ids])
+
+
+@pytest.mark.parametrize("k", [0, 5])
+@pytest.mark.parametrize("kind", ["inf", "lowest"])
+def test_biases_that_leave_nothing(kind, k):
+    """As under a bitmap that leaves nothing: lse and log probabilities -inf, entropy 0, no alternatives."""
+    dev = _dev()
+    rng = np.random.default_rng(2)
+    n, b = 700, 35
+    items, q = grid(rng, n, 32, "bf16").to(dev), grid(rng, b, 32, "bf16").to(dev)
+    bias = torch.full((n,), -np.inf if kind == "inf" else LOWEST, device=dev)
+    ids = torch.from_numpy(rng.integers(-1, n, (b, 2))).to(dev)
+    r = mips.item_logprobs(q, items, ids, scale=10.0, bias=bias, alternatives=k)
+    assert (r.logsumexp == -np.inf).all() and (r.entropy == 0).all()
+    assert torch.equal(r.logprobs, torch.where(ids < 0, 0.0, -np.inf).float())
+    if k:
+        assert (r.alt_ids == -1).all() and (r.alt_logprobs == -np.inf).all()
