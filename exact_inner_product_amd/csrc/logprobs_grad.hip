@@ -18,17 +18,19 @@ struct TermsArgs {
   int32_t* tgt;
 };
 
-// One thread per query: the terms of QueryTerms (bound by launch and latency: 4 us for 4096 queries). A target outside [0, n) is padding and an
-// excluded one has a constant log probability: neither has a gradient.
+// One thread per query: the terms of QueryTerms (bound by launch and latency: 4 us for 4096
+// queries). A target outside [0, n) is padding, and an excluded one, or any of a query that is left
+// without an item, has a constant log probability: none of them has a gradient.
 __global__ __launch_bounds__(256) void terms_kernel(TermsArgs A) {
   const int b = blockIdx.x * 256 + threadIdx.x;
   if (b >= A.bpad) return;
   float sum = 0.0f;
+  const bool some = b < A.b && A.lse[b] != -INFINITY;
   for (int g = 0; g < A.g; ++g) {
     const int64_t at = (int64_t)b * A.g + g;
     int64_t id = -1;
     float v = 0.0f;
-    if (b < A.b) {
+    if (some) {
       id = A.id_bits == 32 ? (int64_t)((const int32_t*)A.ids)[at] : ((const int64_t*)A.ids)[at];
       if (id < 0 || id >= A.n) id = -1;
       else if (A.exclude && ((A.exclude[(int64_t)b * A.exclude_words + (id >> 5)] >> (id & 31)) & 1u)) id = -1;
@@ -39,7 +41,7 @@ __global__ __launch_bounds__(256) void terms_kernel(TermsArgs A) {
     sum += v;
   }
   float add = kMasked, coef = 0.0f, hent = 0.0f;
-  if (b < A.b && A.lse[b] != -INFINITY) {
+  if (some) {
     coef = -sum;
     if (A.grad_entropy) {
       const float h = A.grad_entropy[b];

@@ -471,8 +471,8 @@ MIPS_API int mips_logprobs(const void *queries, int64_t query_stride, int32_t b,
  *   w_bj = sum_i G_bi [ids_bi = j] - p_bj (sum_i G_bi + H'_b (log p_bj + entropy_b)),
  *   grad_queries[b] = scale sum_j w_bj items[j],  grad_items[j] = scale sum_b w_bj queries[b],
  *   grad_bias[j] = sum_b w_bj,
- * over the eligible items; padding and excluded targets have no gradient. The scores are computed
- * again, once for each of the two sums, and never written. Sums are in binary32 in a fixed
+ * over the eligible items; padding and excluded targets, and queries of lse -INFINITY, have no
+ * gradient. The scores are computed again, once for each of the two sums, and never written. Sums are in binary32 in a fixed
  * order (the same call gives the same bits); with MIPS_BF16 the weights w are rounded to bf16
  * before they multiply the rows, and the gradients to bf16 at the end.
  *   queries .. g   as the forward call's; g at most MIPS_TARGETS_MAX, n at most 2^30. An item that the shared

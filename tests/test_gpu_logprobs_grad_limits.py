@@ -157,3 +157,34 @@ def test_scores_of_minus_infinity_with_entropy(dtype, d):
                                             need_bias=True)
     for x in (di.float().cpu(), db.cpu()):
         assert torch.isfinite(x).all() and (x[low] == 0).all() and (x[~low] != 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["inf", "lowest"])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_queries_that_biases_leave_without_an_item(dtype, kind, entropy):
+    """No gradient, as under a bitmap that leaves nothing; also where only some queries are left so."""
+    dev = _dev()
+    rng = np.random.default_rng(4)
+    b, n, d = 70, 150, 32
+    q, items = grid(rng, b, d, dtype).to(dev), grid(rng, n, d, dtype).to(dev)
+    ids = torch.from_numpy(rng.integers(0, n, (b, 2))).to(dev)
+    gl = torch.ones(b, 2, device=dev)
+    gh = torch.ones(b, device=dev) if entropy else None
+    bias = torch.full((n,), -np.inf if kind == "inf" else LOWEST, device=dev)
+    f = mips.item_logprobs(q, items, ids, scale=5.0, bias=bias)
+    got = mips.item_logprobs_backward(gl, q, items, ids, f, scale=5.0, bias=bias, grad_entropy=gh, need_bias=True)
+    assert all((x == 0).all() for x in got)
+    # every item masked but number 7, which a bitmap takes from the odd queries
+    bias[7] = 0.0
+    words = torch.zeros((b, (n + 31) // 32), dtype=torch.int32, device=dev)
+    words[1::2, 0] = 1 << 7
+    kw = dict(scale=5.0, bias=bias, exclude=words)
+    f = mips.item_logprobs(q, items, ids, **kw)
+    dq, di, db = mips.item_logprobs_backward(gl, q, items, ids, f, grad_entropy=gh, need_bias=True, **kw)
+    assert (dq[1::2] == 0).all() and torch.isfinite(dq.float()).all() and torch.isfinite(di.float()).all()
+    # even queries have p_7 = 1, and so w = sum_i g_i ([id_i = j] - [j = 7])
+    want = torch.zeros(n, device=dev)
+    want.index_add_(0, ids[::2].reshape(-1), torch.ones(b, device=dev))
+    want[7] -= float(b)
+    assert (db - want).abs().max() <= 1e-3
