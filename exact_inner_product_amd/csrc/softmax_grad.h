@@ -67,9 +67,10 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 // weight: both passes add the targets' gradients in step 2. A target with nearly all of the
 // probability has a weight of nearly 0, the difference of g and p g; with p g rounded by itself, the
 // queries' gradients were off by several times their size. Blocks with a target in them take step 3
-// a second time, for what the first rounding left: a target's weight is most of its item's gradient,
-// and would double that gradient's error (of 250,000 items by 4096 queries 0.4% of the blocks have
-// a target). Sums are in binary32.
+// a second time, for what the first rounding left of the targets' weights: one is most of its item's
+// gradient, and would double that gradient's error (of 250,000 items by 4096 queries 0.4% of the
+// blocks have a target). The other weights stay as they are, so that what a row gets does not depend
+// on its neighbours. Sums are in binary32.
 //
 // What bounds it: matrix and vector instructions together, which share a SIMD's issue. Per 32 x 32
 // block of a width of 128 in bf16, 17 products of 32 cycles and about 70 vector instructions, 16 of
@@ -299,7 +300,8 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
       if (!EXTRA) negw = vneg[buf * (kGradTile / 32) + jb];
     }
     float w[16];
-    bool target_here = false;  // a target's weight in the block; uniform over the wave
+    uint32_t targets = 0u;     // bit i: register i's weight has a target's gradient
+    bool target_here = false;  // whether any lane's has; uniform over the wave
     float ck[16], hk[16];
     if constexpr (EXTRA && ITEMS) {
 #pragma unroll
@@ -366,6 +368,7 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
           const int to = __builtin_amdgcn_readlane(tgt, j) - (int)own0 + 32 * ((j >> 2) & 1);
           const float v = lane == to ? A.q.gval[(tile * kGradTile + jb * 32 + j) * A.q.g + g] : 0.0f;
           const int at = 4 * (j >> 3) + (j & 3);
+          targets |= lane == to ? 1u << at : 0u;
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] += i == at ? v : 0.0f;
         }
@@ -384,6 +387,7 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
           const int r = t - first;
           const int at = ((r >> 2) & 1) == h ? 4 * (r >> 3) + (r & 3) : -1;
           v = flip ? -v : v;
+          targets |= at >= 0 ? 1u << at : 0u;
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] += i == at ? v : 0.0f;
         });
@@ -401,12 +405,15 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
           sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               wa, kb == 0 && d < kAhead ? ahead[d < kAhead ? d : 0] : read_columns(kb, d), sum[d], 0, 0, 0);
       }
-      if (__builtin_expect(target_here, 0)) {  // the weights' next eight bits
+      if (__builtin_expect(target_here, 0)) {  // the next eight bits of the targets' weights
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           bf16x8_t wa;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) wa[e] = (__bf16)(w[8 * kb + e] - (float)(__bf16)w[8 * kb + e]);
+          for (int e = 0; e < 8; ++e) {
+            const float x = w[8 * kb + e];
+            wa[e] = (targets >> (8 * kb + e)) & 1u ? (__bf16)(x - (float)(__bf16)x) : (__bf16)0.0f;
+          }
 #pragma unroll
           for (int d = 0; d < DT; ++d)
             sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, read_columns(kb, d), sum[d], 0, 0, 0);
