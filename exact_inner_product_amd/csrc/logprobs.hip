@@ -8,7 +8,8 @@
 // one and a lower id. The same holds for groups of runs. So the finish pass picks the k best
 // groups, among their runs the k best, scores those runs' rows again with the same matrix
 // instructions (bitwise the same scores) and picks the k best rows: exact, with ties by the
-// lowest id, at the cost of k runs of rows a query instead of a second pass over the table.
+// lowest id, at the cost of k runs of rows a query instead of a second pass over the table. Logits of
+// NaN, -inf and down to kLeastLogit are no candidates, neither as a run's maximum nor as a row.
 #include "host.h"
 #include "softmax_api.h"
 
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(kFinThreads) void finish_kernel(FinishArgs A) {
     const float l = logit(A, score_rows<CT, NCH>(x.chunks, q), x.bias);
     if (!diagonal()) return;
     if (i < nb) {
-      keys[i * kFrag + (lane & 31)] = live && !out ? composite(score_key(l), (uint32_t)x.row) : 0ull;
+      keys[i * kFrag + (lane & 31)] = live && !out && l > kLeastLogit ? composite(score_key(l), (uint32_t)x.row) : 0ull;
     } else {
       const int g = (i - nb) * kFrag + (lane & 31);
       if (g < A.g) A.logprobs[(int64_t)b * A.g + g] = !live ? 0.0f : (out ? -INFINITY : log_prob(l, lse));

@@ -257,7 +257,7 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
         const int in_run = (int)(i_tile & (run - 1));
         const float v3 = in_run == 0 ? v2 : fmaxf(v2, st[(SV * f + 3) * kWave]);
         st[(SV * f + 3) * kWave] = v3;
-        const float l = v3 * A.scx <= kEmpty ? -INFINITY : (A.bias ? v3 : v3 * A.scale);
+        const float l0 = A.bias ? v3 : v3 * A.scale, l = l0 > kLeastLogit ? l0 : -INFINITY;
         // the store is unconditional, out of the buffer's range where nothing is to be stored (the
         // upper lanes, the earlier tiles): one that may or may not be issued makes the compiler's
         // wait counts for the item loads behind it inexact

@@ -23,6 +23,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // that no eligible item has been seen; what was summed until then is dropped.
 constexpr float kMasked = -1e30f;
 constexpr float kEmpty = -0.9e30f;
+// The same bound for a logit. One that is not above it (NaN and -inf among them) is no alternative:
+// in a run's maximum and in the row's own key alike, so that what is listed does not depend on
+// which rows happen to be scored again.
+constexpr float kLeastLogit = kEmpty * kLn2;
 
 // The exponents' reference is not the exact running maximum: it follows when a value exceeds it
 // by kSlack (log2 units), so that the rescaling branch is taken a few times per slice instead

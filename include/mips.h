@@ -417,7 +417,9 @@ MIPS_API int mips_clip_grad_norm(const void *const *tensors, void *const *outs,
  *   lse_b = log sum over the eligible items j of exp(l_bj),
  *   out_logprobs[b][i] = l_bj - lse_b for j = ids[b][i],
  *   out_entropy[b] = - sum_j p_bj log p_bj,  p_bj = exp(l_bj - lse_b),
- *   alternatives: the k eligible items of the largest l_bj, ties by the lowest id.
+ *   alternatives: the k eligible items of the largest l_bj, ties by the lowest id; an item whose
+ *   logit is NaN or below -6e29 (-INFINITY among them) is none.
+ * A logit that is NaN or +INFINITY makes its query's lse, entropy and log probabilities NaN.
  * The scores are never written to memory. scale is 1 / temperature; the bias is, for
  * instance, - log q of a sampled softmax ("Two-Tower Retrieval at Industrial Scale", the logQ
  * correction).

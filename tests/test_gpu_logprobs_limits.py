@@ -138,3 +138,43 @@ def test_biases_that_leave_nothing(kind, k):
     assert torch.equal(r.logprobs, torch.where(ids < 0, 0.0, -np.inf).float())
     if k:
         assert (r.alt_ids == -1).all() and (r.alt_logprobs == -np.inf).all()
+
+
+@pytest.mark.parametrize("dtype,b,n,d", SHAPES)
+@pytest.mark.parametrize("kind", ["inf", "lowest", "both"])
+@pytest.mark.parametrize("left", [3, None])
+def test_alternatives_under_masking_biases(dtype, b, n, d, kind, left):
+    """Masked items are no alternatives, wherever they lie; fewer live items than alternatives too."""
+    dev = _dev()
+    print(f"logprobs alternatives, masking bias {kind} {dtype} b={b} n={n} d={d} left={left}", flush=True)
+    rng = np.random.default_rng(n + len(kind))
+    items, q = grid(rng, n, d, dtype), grid(rng, b, d, dtype)
+    bias, low = masking_bias(rng, n, kind)
+    if left:
+        keep = rng.permutation(n)[:left]
+        low[:] = True
+        low[keep] = False
+        bias[:] = torch.where(torch.arange(n) % 2 == 0, LOWEST, -np.inf) if kind == "both" else bias[bias < -1e30][0]
+        bias[torch.from_numpy(keep)] = torch.arange(left).float()
+    r = mips.item_logprobs(q.to(dev), items.to(dev), scale=10.0, bias=bias.to(dev), entropy=False, alternatives=17)
+    l = logits64(q, items, 10.0, bias)
+    l[:, low] = -np.inf
+    check(r, l, None, 17)
+
+
+def test_nan_logits_are_no_alternatives():
+    """The others keep their order; their log probabilities are NaN, as the log-sum-exp is."""
+    dev = _dev()
+    rng = np.random.default_rng(5)
+    for n, d in ((700, 64), (90000, 16)):
+        items, q = grid(rng, n, d, "bf16"), grid(rng, 40, d, "bf16")
+        bad = rng.random(n) < 0.02
+        bad[64:128] = True
+        held = items.clone()
+        held[torch.from_numpy(bad)] = float("nan")
+        r = mips.item_logprobs(q.to(dev), held.to(dev), scale=5.0, alternatives=9)
+        l = logits64(q, items, 5.0)
+        l[:, bad] = -np.inf
+        want = np.lexsort((np.broadcast_to(np.arange(n), l.shape), -l), axis=1)[:, :9]
+        assert np.array_equal(r.alt_ids.cpu().numpy(), want)
+        assert torch.isnan(r.logsumexp).all() and torch.isnan(r.alt_logprobs).all()
