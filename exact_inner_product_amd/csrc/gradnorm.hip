@@ -1,7 +1,7 @@
 // gradnorm.hip -- the global norm of a model's gradients and clipping by it (gfx950).
 //
 //   norm = sqrt(sum over all tensors of sum x^2),  coef = min(1, max_norm / (norm + 1e-6)),
-//   x <- coef * x.
+//   x <- coef * x;  coef = 1 where max_norm is infinite.
 //
 // Both passes are bound by memory traffic: x is read for the norm, and read and written for
 // the scaling (a set of tensors that fits the caches is read from memory once). Squares are
@@ -129,8 +129,9 @@ __global__ __launch_bounds__(256) void clip_kernel(NormArgs A) {
   double s = 0.0;
   for (int i = threadIdx.x; i < A.nall; i += 256) s += A.all[i];
   const double norm = sqrt(block_sum(s, red));
-  // coef in binary32 as the values it scales; a NaN norm gives a NaN coef, an infinite one 0
-  const float q = (float)((double)A.max_norm / (norm + 1e-6));
+  // coef in binary32 as the values it scales; a NaN norm gives a NaN coef, an infinite one 0. Without
+  // a bound on the norm it is 1, whatever the norm is (inf / inf would be NaN)
+  const float q = isinf(A.max_norm) ? 1.0f : (float)((double)A.max_norm / (norm + 1e-6));
   const float coef = q < 1.0f ? q : (q != q ? q : 1.0f);
   if (A.norm && blockIdx.x == 0 && threadIdx.x == 0) *A.norm = (float)norm;
   const uint32_t total = A.chunk0[A.nt];

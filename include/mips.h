@@ -399,7 +399,8 @@ MIPS_API int mips_embedding_grad(const void *grad, int32_t grad_dtype, int64_t t
  *               element counts (0 .. 2^38) and MIPS_F32 or MIPS_BF16. outs[i] may equal
  *               tensors[i] (scaled in place; not written when the factor is 1) and may not
  *               otherwise overlap any tensor. 16-byte aligned pairs move in 16-byte units.
- *   max_norm    >= 0; infinity only takes the norm (and copies).
+ *   max_norm    >= 0; infinity only takes the norm (and copies): the factor is 1, whatever the
+ *               norm, infinite and NaN ones included.
  *   out_norm    device float [1].
  *   workspace   device, 256-byte aligned, mips_clip_workspace_size(ntensors) bytes.
  * Errors: INVALID_ARG, UNSUPPORTED (a dtype), WORKSPACE, HIP.

@@ -145,3 +145,20 @@ def test_refusals():
         mips.clip_grad_norm([t], 1.0, out=[t.bfloat16()])
     with pytest.raises(mips.MipsError, match="workspace too small"):
         mips.clip_grad_norm([t], 1.0, workspace=mips.empty_workspace(256, dev))
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_an_infinite_max_norm_only_takes_the_norm(bad, dtype):
+    """Gradients that overflowed are left (and copied) bit by bit, whatever the norm."""
+    dev = _dev()
+    ts = [torch.randn(70001, device=dev).to(dtype), torch.randn(33, 7, device=dev).to(dtype)]
+    ts[0][4321] = bad
+    keep = [t.clone() for t in ts]
+    as_ints = lambda t: t.view(torch.int32 if dtype == torch.float32 else torch.int16)  # noqa: E731
+    norm, got = mips.clip_grad_norm(ts, math.inf, out=[torch.zeros_like(t) for t in ts])
+    assert math.isnan(float(norm)) if math.isnan(bad) else float(norm) == math.inf
+    assert all(torch.equal(as_ints(a), as_ints(b)) for a, b in zip(got, keep))
+    norm, _ = mips.clip_grad_norm(ts, math.inf)
+    assert math.isnan(float(norm)) if math.isnan(bad) else float(norm) == math.inf
+    assert all(torch.equal(as_ints(a), as_ints(b)) for a, b in zip(ts, keep))
