@@ -205,18 +205,18 @@ def item_logprobs_backward(grad_logprobs: Optional[torch.Tensor], queries: torch
         raise TypeError("the gradient needs a table of rows, not a packed index")
     b, dev, width = q.shape[0], q.device, queries.shape[1]
     g = 0 if ids is None else ids.shape[1]
-    lse, ent = forward.logsumexp, forward.entropy
+    lse, ent = forward.logsumexp, forward.entropy if grad_entropy is not None else None
     if grad_entropy is not None and ent is None:
         raise ValueError("grad_entropy needs the forward pass' entropy")
     if (ids is None) != (grad_logprobs is None):
         raise ValueError("grad_logprobs and ids go together")
     for name, t, shape in (("grad_logprobs", grad_logprobs, (b, g)), ("grad_entropy", grad_entropy, (b,)),
-                           ("logsumexp", lse, (b,))):
+                           ("logsumexp", lse, (b,)), ("entropy", ent, (b,))):
         if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
             raise ValueError(f"{name} must be float32 {list(shape)}, got {t.dtype} {tuple(t.shape)}")
-    _on_gpu(dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, logsumexp=lse)
-    grad_logprobs = None if grad_logprobs is None else grad_logprobs.contiguous()
-    grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
+    _on_gpu(dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, logsumexp=lse, entropy=ent)
+    grad_logprobs, grad_entropy, lse, ent = (None if t is None else t.contiguous()
+                                             for t in (grad_logprobs, grad_entropy, lse, ent))
     dq = torch.empty((b, d), dtype=q.dtype, device=dev) if need_queries else None
     di = torch.empty((n, d), dtype=q.dtype, device=dev) if need_items else None
     db = torch.empty((n,), dtype=torch.float32, device=dev) if need_bias else None

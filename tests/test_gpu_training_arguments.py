@@ -1,0 +1,53 @@
+"""What the training operators' Python calls check and lay out before a kernel reads it."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import exact_inner_product_amd as mips
+from tests.test_gpu_logprobs import grid
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return torch.device("cuda:0")
+
+
+def softmax_call(dev, dtype="bf16", b=20, n=100, d=32):
+    rng = np.random.default_rng(0)
+    q, items = grid(rng, b, d, dtype).to(dev), grid(rng, n, d, dtype).to(dev)
+    ids = torch.from_numpy(rng.integers(0, n, (b, 2))).to(dev)
+    gl = torch.from_numpy(rng.standard_normal((b, 2)).astype(np.float32)).to(dev)
+    gh = torch.from_numpy(rng.standard_normal(b).astype(np.float32)).to(dev)
+    return q, items, ids, gl, gh, mips.item_logprobs(q, items, ids, scale=3.0)
+
+
+def test_strided_results_of_the_forward_call():
+    """The log-sum-exp and the entropy as columns of one tensor, and as every second row of another."""
+    dev = _dev()
+    q, items, ids, gl, gh, f = softmax_call(dev)
+    want = mips.item_logprobs_backward(gl, q, items, ids, f, scale=3.0, grad_entropy=gh)
+    plain = mips.item_logprobs_backward(gl, q, items, ids, f, scale=3.0)
+    both = torch.stack([f.logsumexp, f.entropy], 1)
+    wide = torch.full((2, 40), 7.0, device=dev)
+    wide[0, ::2], wide[1, ::2] = f.logsumexp, f.entropy
+    for lse, ent in ((both[:, 0], both[:, 1]), (wide[0, ::2], wide[1, ::2])):
+        g = dataclasses.replace(f, logsumexp=lse, entropy=ent)
+        got = mips.item_logprobs_backward(gl, q, items, ids, g, scale=3.0, grad_entropy=gh)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        got = mips.item_logprobs_backward(gl, q, items, ids, g, scale=3.0)
+        assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+
+
+def test_an_entropy_that_does_not_fit_is_refused():
+    dev = _dev()
+    q, items, ids, gl, gh, f = softmax_call(dev)
+    for bad in (f.entropy[:-1], f.entropy[:, None], f.entropy.bfloat16(), f.entropy.double(), f.entropy.cpu()):
+        g = dataclasses.replace(f, entropy=bad)
+        with pytest.raises(ValueError):
+            mips.item_logprobs_backward(gl, q, items, ids, g, scale=3.0, grad_entropy=gh)
+        mips.item_logprobs_backward(gl, q, items, ids, g, scale=3.0)  # not used, not looked at
