@@ -107,7 +107,7 @@ def _exclude_words(exclude: Optional[torch.Tensor], n: int, b: int) -> Tuple[Opt
     raise ValueError(f"exclude must be [>= {words}] or [{b}, >= {words}], got {tuple(exclude.shape)}")
 
 
-def _softmax_args(queries, items, ids, bias, exclude, model_version=None):
+def _softmax_args(queries, items, ids, bias, exclude, workspace, model_version=None):
     """Checked and laid out operands of the softmax entry points: (queries, items pointer,
     layout, item stride, n, d, dtype code, ids, id bits, bias, exclude, exclude words)."""
     if queries.dim() != 2 or queries.shape[0] < 1:
@@ -133,7 +133,7 @@ def _softmax_args(queries, items, ids, bias, exclude, model_version=None):
         d = (width + per - 1) // per * per
         held = _operand(items, d)
         stride = _row_stride(held)
-    _on_gpu(queries.device, items=held, ids=ids, bias=bias, exclude=exclude)
+    _on_gpu(queries.device, items=held, ids=ids, bias=bias, exclude=exclude, workspace=workspace)
     queries = _operand(queries, d)
     bits = 32
     if ids is not None:
@@ -163,7 +163,7 @@ def item_logprobs(queries: torch.Tensor, items: Union[torch.Tensor, Corpus], ids
     exclude: bitmap as topk's; excluded items have probability 0.
     """
     q, held, layout, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(
-        queries, items, ids, bias, exclude, model_version)
+        queries, items, ids, bias, exclude, workspace, model_version)
     b, dev = q.shape[0], q.device
     g = 0 if ids is None else ids.shape[1]
     f32 = dict(dtype=torch.float32, device=dev)
@@ -200,7 +200,8 @@ def item_logprobs_backward(grad_logprobs: Optional[torch.Tensor], queries: torch
     result of item_logprobs on the same arguments (its logsumexp, and its entropy with
     grad_entropy). Up to TARGETS_MAX ids a query.
     """
-    q, held, _, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(queries, items, ids, bias, exclude)
+    q, held, _, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(
+        queries, items, ids, bias, exclude, workspace)
     if isinstance(items, Corpus):
         raise TypeError("the gradient needs a table of rows, not a packed index")
     b, dev, width = q.shape[0], q.device, queries.shape[1]

@@ -51,3 +51,18 @@ def test_an_entropy_that_does_not_fit_is_refused():
         with pytest.raises(ValueError):
             mips.item_logprobs_backward(gl, q, items, ids, g, scale=3.0, grad_entropy=gh)
         mips.item_logprobs_backward(gl, q, items, ids, g, scale=3.0)  # not used, not looked at
+
+
+def test_a_workspace_on_the_host_is_refused():
+    dev = _dev()
+    q, items, ids, gl, _, f = softmax_call(dev)
+    host = torch.empty(1 << 24, dtype=torch.uint8)
+    calls = (lambda ws: mips.item_logprobs(q, items, ids, workspace=ws),
+             lambda ws: mips.item_logprobs(q, items, ids, alternatives=3, workspace=ws),
+             lambda ws: mips.item_logprobs_backward(gl, q, items, ids, f, workspace=ws),
+             lambda ws: mips.embedding_grad(torch.zeros(20, 2, 8, device=dev), ids, 100, workspace=ws),
+             lambda ws: mips.clip_grad_norm([q], 1.0, workspace=ws))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(host)
+        call(host.to(dev))
