@@ -277,7 +277,8 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, scale: floa
     flat, bits = _ids_arg(ids)
     t, d = flat.numel(), grad.shape[-1]
     g = _rows_arg(grad.reshape(t, d))
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((rows, d), dtype=grad.dtype, device=grad.device)
     elif tuple(out.shape) != (rows, d) or (d > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < d):
         raise ValueError(f"out must be [{rows}, {d}] with contiguous rows, got {tuple(out.shape)}")
@@ -292,6 +293,8 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, scale: floa
                                      float(scale), int(accumulate), _ptr(out), _code(out, "out"),
                                      _row_stride(out), _ptr(workspace), workspace.numel(),
                                      _stream(grad.device)), "mips_embedding_grad")
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out
 
 
@@ -357,4 +360,6 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
                                      words(*[_CODES[t] for t in dtypes]), n, float(max_norm), _ptr(norm),
                                      _ptr(workspace), workspace.numel(), _stream(device)),
            "mips_clip_grad_norm")
+    # written through their addresses: autograd would not notice a saved tensor that changed
+    torch.autograd.graph.increment_version(outs)
     return norm, outs

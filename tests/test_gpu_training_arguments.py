@@ -66,3 +66,30 @@ def test_a_workspace_on_the_host_is_refused():
         with pytest.raises(ValueError):
             call(host)
         call(host.to(dev))
+
+
+def test_autograd_notices_what_is_written_in_place():
+    """As after torch's own in-place operations: a backward pass that saved the tensor refuses."""
+    dev = _dev()
+
+    def refused(write, rg=torch.ones(30, 8, device=dev)):
+        t = rg.clone().requires_grad_()
+        x = t * 1.0
+        y = (x * x).sum()  # saves x
+        write(x.detach())
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            y.backward()
+
+    ids = torch.zeros(4, dtype=torch.int32, device=dev)
+    grad = torch.ones(4, 8, device=dev)
+    refused(lambda x: mips.clip_grad_norm([x], 1.0))
+    refused(lambda x: mips.clip_grad_norm([torch.ones_like(x)], 1.0, out=[x]))
+    refused(lambda x: mips.embedding_grad(grad, ids, 30, out=x))
+    refused(lambda x: mips.embedding_grad(grad, ids, 30, out=x, accumulate=True))
+    # what is only read stays as it was
+    x = torch.ones(30, 8, device=dev)
+    version = x._version
+    mips.clip_grad_norm([x], 1.0, out=[torch.empty_like(x)])
+    mips.embedding_lookup(x, ids)
+    mips.embedding_grad(x, torch.zeros(30, dtype=torch.int32, device=dev), 5)
+    assert x._version == version
