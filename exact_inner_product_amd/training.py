@@ -309,6 +309,11 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+def _same_strides(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether elements of equal indices lie at equal places (a and b have the same shape)."""
+    return a.numel() == 0 or all(n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
+
+
 def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
                    out: Optional[Sequence[torch.Tensor]] = None,
                    workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, List[torch.Tensor]]:
@@ -349,7 +354,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         if not all([o.get_device() == index for o in outs]) or [o.dtype for o in outs] != dtypes or \
                 [o.shape for o in outs] != [t.shape for t in tensors] or \
                 (not (plain and all([o.is_contiguous() for o in outs])) and
-                 [o.stride() for o in outs] != [t.stride() for t in tensors]):
+                 not all(_same_strides(o, t) for o, t in zip(outs, tensors))):
             raise ValueError("out tensors must have their tensors' device, shapes, types and strides")
         dst = [o.data_ptr() for o in outs]
     pointers, sizes, words = C.c_void_p * n, C.c_int64 * n, C.c_int32 * n

@@ -162,3 +162,17 @@ def test_an_infinite_max_norm_only_takes_the_norm(bad, dtype):
     norm, _ = mips.clip_grad_norm(ts, math.inf)
     assert math.isnan(float(norm)) if math.isnan(bad) else float(norm) == math.inf
     assert all(torch.equal(as_ints(a), as_ints(b)) for a, b in zip(ts, keep))
+
+
+def test_the_stride_of_a_single_element_does_not_matter():
+    """out may have any stride along an axis of length 1, also beside a permuted tensor."""
+    dev = _dev()
+    ts = [torch.randn(33, 7, device=dev).t(), torch.randn(1, 5, device=dev).t()]
+    out = [torch.empty(33, 7, device=dev).t(), torch.empty(5, 1, device=dev)]
+    assert ts[1].stride() != out[1].stride()
+    total, coef = _exact(ts, 1.0)
+    norm, got = mips.clip_grad_norm(ts, 1.0, out=out)
+    assert abs(float(norm) - total) <= total * 2.0 ** -23
+    _check(got, ts, coef)
+    with pytest.raises(ValueError):
+        mips.clip_grad_norm(ts, 1.0, out=[torch.empty(7, 33, device=dev), out[1]])
