@@ -301,6 +301,8 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, scale: floa
 # ------------------------------------------------------------------------- clipping
 def _dense(t: torch.Tensor) -> bool:
     """Whether t's elements fill one run of memory, in any order of its axes."""
+    if t.numel() == 0:
+        return True
     want = 1
     for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n != 1), key=lambda x: x[1]):
         if stride != want:

@@ -164,6 +164,20 @@ def test_an_infinite_max_norm_only_takes_the_norm(bad, dtype):
     assert all(torch.equal(as_ints(a), as_ints(b)) for a, b in zip(ts, keep))
 
 
+def test_empty_tensors_among_permuted_ones():
+    """A tensor without elements is dense whatever its strides: also beside one that is permuted."""
+    dev = _dev()
+    ts = [torch.randn(33, 7, device=dev).t(), torch.empty(5, 0, device=dev), torch.empty(0, 5, device=dev).t()]
+    keep = ts[0].clone(memory_format=torch.preserve_format)
+    total, coef = _exact(ts[:1], 1.0)
+    norm, got = mips.clip_grad_norm(ts, 1.0)
+    assert abs(float(norm) - total) <= total * 2.0 ** -23
+    _check(got[:1], [keep], coef)
+    out = [torch.empty_like(t) for t in ts]
+    norm2, got2 = mips.clip_grad_norm([keep, *ts[1:]], 1.0, out=out)
+    assert float(norm2) == float(norm) and torch.equal(got2[0], got[0])
+
+
 def test_the_stride_of_a_single_element_does_not_matter():
     """out may have any stride along an axis of length 1, also beside a permuted tensor."""
     dev = _dev()
