@@ -145,3 +145,24 @@ def test_limits_match_the_binding():
     limits = dict(re.findall(r"#define (MIPS_\w+_MAX) (\d+)", text))
     assert int(limits["MIPS_ALTERNATIVES_MAX"]) == mips.ALTERNATIVES_MAX
     assert int(limits["MIPS_TARGETS_MAX"]) == mips.TARGETS_MAX
+
+
+def test_the_stream_handle_has_a_public_source(monkeypatch):
+    """Without torch's internal function the handle comes from the current stream's object."""
+    import types
+
+    import torch
+
+    from exact_inner_product_amd import training
+    asked = []
+
+    def current_stream(device):
+        asked.append(device)
+        return types.SimpleNamespace(cuda_stream=77)
+
+    monkeypatch.setattr(torch.cuda, "current_stream", current_stream)
+    monkeypatch.setattr(training, "_raw_stream", None)
+    device = torch.device("cuda", 0)
+    assert training._stream(device) == 77 and asked == [device]
+    monkeypatch.setattr(training, "_raw_stream", lambda index: 100 + index)
+    assert training._stream(device) == 100 and len(asked) == 1
