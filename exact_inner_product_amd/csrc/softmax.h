@@ -119,12 +119,21 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
   }
   constexpr int SV = stats_values(MODE);
   float* st = (float*)(lds + (size_t)QB * D * E) + (size_t)wave * NQF * SV * kWave + lane;
-  for (int f = 0; f < NQF; ++f) {
-    st[(SV * f + 0) * kWave] = kMasked;
-    st[(SV * f + 1) * kWave] = 0.0f;
-    st[(SV * f + 2) * kWave] = 0.0f;
-  }
+  auto clear = [&]() __attribute__((always_inline)) {
+    for (int f = 0; f < NQF; ++f) {
+      st[(SV * f + 0) * kWave] = kMasked;
+      st[(SV * f + 1) * kWave] = 0.0f;
+      st[(SV * f + 2) * kWave] = 0.0f;
+    }
+  };
+  clear();
   __syncthreads();
+  // A logit of -inf has e = 0 and would make e t a NaN in the entropy's sum. Biases are bounded from
+  // below as they are loaded, so what is left are rows of infinities: a wave that finds such a NaN at
+  // its end takes its tiles again with every logit bounded, in the branch of the masks. (A call of
+  // 4096 x 250,000 x 128 with the entropy: 338 us without any of this, 345 so, 363 with each tile's sum
+  // tested.)
+  bool bounded = false;
 
   // Tiles go in runs of 2^run_log consecutive ones, a wave's runs kStatsWaves apart: the run
   // is the unit of the maxima. Tile i of this wave, of `count`:
@@ -175,9 +184,6 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
     const int cc = c + kLook;
     bq[c % kLook] = ((const u32x4_t*)(lds + (size_t)(cc < NCH ? f : follow) * BLK) + lane)[(cc % NCH) * 64];
   };
-#pragma unroll
-  for (int c = 0; c < kLook; ++c) bq[c] = ((const u32x4_t*)lds + lane)[c * 64];
-
   auto compute_stage = [&](const u32x4_t (&a)[RM][NCH], uint32_t xraw, int64_t i_tile) __attribute__((always_inline)) {
     const int64_t tile = tile_of(i_tile);
     // words of the tile's blocks, rows past n set; uniform
@@ -190,6 +196,7 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       word[r] = w;
       any |= w;
     }
+    if (ENT && bounded) any = ~0u;
     // the tile's biases: rows 8q + 4 (lane >> 5) + (0..3) for q = 0..3 (rows past n read 0 and
     // are masked); kept for all fragments where the registers allow it
     constexpr bool kKeepBias = RM == 1 && NCH <= 8;
@@ -205,7 +212,10 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
           const u32x4_t v = __builtin_bit_cast(
               u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (lane >> 5) * 16 + q * 32, 0, 0));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) bv[r][4 * q + e] = __uint_as_float(v[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float x = __uint_as_float(v[e]);
+            bv[r][4 * q + e] = ENT && x < A.vmask ? A.vmask : x;  // (one that masks, for the entropy: see bounded)
+          }
         }
       }
     };
@@ -232,6 +242,12 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
                                    (((word[r] >> (b0 + 4)) & 1u) ? 0xFFFFFFFF00000000ull : 0ull);
             cur[r][i] = __builtin_amdgcn_inverse_ballot_w64(lanes) ? A.vmask : cur[r][i];
           }
+        }
+        if (ENT && bounded) {
+#pragma unroll
+          for (int r = 0; r < RM; ++r)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) cur[r][i] = cur[r][i] < A.vmask ? A.vmask : cur[r][i];
         }
       }
       if (A.exclude_words != 0) {  // this column's own words
@@ -307,18 +323,6 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
         }
         if constexpr (NQF > 1) __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (ENT) {
-        // A logit of -inf (a bias that masks, a row of infinities) has e = 0 and made e t a NaN; it
-        // adds 0. Rare, so the sum is taken again where it came out NaN; a NaN of its own stays one.
-        if (__builtin_expect(__ballot(x0 + x1 != x0 + x1) != 0ull, 0)) {
-          x0 = x1 = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 16 * RM; ++k) {
-            const float t = fmaf(cur[k >> 4][k & 15], A.scx, -m);
-            x0 = fmaf(__builtin_amdgcn_exp2f(t), fmaxf(t, kMasked), x0);
-          }
-        }
-      }
       st[(SV * f + 0) * kWave] = m;
       st[(SV * f + 1) * kWave] = z + (z0 + z1);
       if constexpr (ENT) st[(SV * f + 2) * kWave] = x + (x0 + x1);
@@ -344,8 +348,10 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
 
   u32x4_t a[NS][RM][NCH];
   uint32_t xw[NS];
-  int64_t i = 0;
-  if (count > 0) {
+  while (count > 0) {
+    int64_t i = 0;
+#pragma unroll
+    for (int c = 0; c < kLook; ++c) bq[c] = ((const u32x4_t*)lds + lane)[c * 64];
     unroll_for<NS - 1>([&](auto uc) __attribute__((always_inline)) {
       constexpr int u = decltype(uc)::value;
       load_stage(a[u], xw[u], tile_of(i + u));
@@ -365,6 +371,13 @@ __global__ __launch_bounds__(kStatsThreads) __attribute__((amdgpu_waves_per_eu(2
       while (!(step(std::integral_constant<int, 0>{}) || step(std::integral_constant<int, 1>{})))
         i += NS;
     }
+    if (!ENT || bounded) break;
+    for (int f = 0; f < nfr; ++f) {
+      const float z = st[(SV * f + 1) * kWave], x = st[(SV * f + 2) * kWave];
+      bounded |= __ballot(x != x && z == z) != 0ull;
+    }
+    if (!bounded) break;
+    clear();
   }
   __syncthreads();
 
