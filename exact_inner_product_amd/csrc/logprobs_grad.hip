@@ -18,30 +18,23 @@ struct TermsArgs {
   int32_t* tgt;
 };
 
-// One thread per query: the terms of QueryTerms (bound by launch and latency: 4 us for 4096
-// queries). A target outside [0, n) is padding, and an excluded one, or any of a query that is left
-// without an item, has a constant log probability: none of them has a gradient.
-__global__ __launch_bounds__(256) void terms_kernel(TermsArgs A) {
-  const int b = blockIdx.x * 256 + threadIdx.x;
-  if (b >= A.bpad) return;
-  float sum = 0.0f;
-  const bool some = b < A.b && A.lse[b] != -INFINITY;
-  for (int g = 0; g < A.g; ++g) {
-    const int64_t at = (int64_t)b * A.g + g;
-    int64_t id = -1;
-    float v = 0.0f;
-    if (some) {
-      id = A.id_bits == 32 ? (int64_t)((const int32_t*)A.ids)[at] : ((const int64_t*)A.ids)[at];
-      if (id < 0 || id >= A.n) id = -1;
-      else if (A.exclude && ((A.exclude[(int64_t)b * A.exclude_words + (id >> 5)] >> (id & 31)) & 1u)) id = -1;
-      if (id >= 0) v = A.grad_logprobs[at];
-    }
-    A.tgt[at] = (int32_t)id;
-    A.gval[at] = v;
-    sum += v;
-  }
+// The target of query b at ids[at] and its gradient. One outside [0, n) is padding, and an excluded
+// one, or any of a query that is left without an item, has a constant log probability: none of them has
+// a gradient.
+__device__ __forceinline__ int32_t read_target(const TermsArgs& A, int b, int64_t at, float& v) {
+  v = 0.0f;
+  if (b >= A.b || A.lse[b] == -INFINITY) return kNoTarget;
+  const int64_t id = A.id_bits == 32 ? (int64_t)((const int32_t*)A.ids)[at] : ((const int64_t*)A.ids)[at];
+  if (id < 0 || id >= A.n) return kNoTarget;
+  if (A.exclude && ((A.exclude[(int64_t)b * A.exclude_words + (id >> 5)] >> (id & 31)) & 1u)) return kNoTarget;
+  v = A.grad_logprobs[at];
+  return (int32_t)id;
+}
+
+// Query b's terms, given the sum of its targets' gradients.
+__device__ __forceinline__ float write_terms(const TermsArgs& A, int b, float sum) {
   float add = kMasked, coef = 0.0f, hent = 0.0f;
-  if (some) {
+  if (b < A.b && A.lse[b] != -INFINITY) {
     coef = -sum;
     if (A.grad_entropy) {
       const float h = A.grad_entropy[b];
@@ -55,9 +48,54 @@ __global__ __launch_bounds__(256) void terms_kernel(TermsArgs A) {
   A.coef[b] = coef;
   A.hent[b] = hent;
   A.sign[b] = coef < 0.0f ? -1.0f : 1.0f;
+  return coef;
+}
+
+// The terms of QueryTerms (bound by launch and latency: 4 us for 4096 queries). With one target at
+// most, a thread a query, 64 of them a wave.
+__global__ __launch_bounds__(256) void terms_kernel(TermsArgs A) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= A.bpad) return;
+  float v = 0.0f;
+  if (A.g > 0) {
+    A.tgt[b] = read_target(A, b, b, v);
+    A.gval[b] = v;
+  }
+  const float coef = write_terms(A, b, v);
   const uint64_t neg = __ballot(coef < 0.0f);  // (bpad is a multiple of 64: whole waves get here)
   if ((threadIdx.x & 31) == 0) A.neg[b >> 5] = (uint32_t)(neg >> (threadIdx.x & 32));
 }
+
+// With more, a lane a target: a wave sorts a query's targets by their ranks, for the queries' pass to
+// walk through. A workgroup takes 32 queries, so that it has a whole word of signs.
+constexpr int kSortedThreads = 1024;
+__global__ __launch_bounds__(kSortedThreads) void sorted_terms_kernel(TermsArgs A) {
+  __shared__ int negative[kFrag];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = wave; i < kFrag; i += kSortedThreads / kWave) {
+    const int b = blockIdx.x * kFrag + i;
+    const int64_t at = (int64_t)b * A.g;
+    float v = 0.0f;
+    const int32_t t = lane < A.g ? read_target(A, b, at + lane, v) : kNoTarget;
+    int rank = 0;
+    for (int j = 0; j < A.g; ++j) {
+      const int32_t o = __builtin_amdgcn_readlane(t, j);
+      rank += o < t || (o == t && j < lane) ? 1 : 0;
+    }
+    if (lane < A.g) {
+      A.tgt[at + rank] = t;
+      A.gval[at + rank] = v;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
+    if (lane == 0) negative[i] = write_terms(A, b, v) < 0.0f;
+  }
+  __syncthreads();
+  const uint32_t neg = (uint32_t)__ballot(lane < kFrag && negative[lane % kFrag]);
+  if (threadIdx.x == 0) A.neg[blockIdx.x] = neg;
+}
+static_assert(MIPS_TARGETS_MAX <= kWave, "a lane for each target of a query");
 
 struct JoinArgs {
   const float* part;  // [nsplit][rows][d]
@@ -278,7 +316,8 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
   TermsArgs T{lse, entropy, grad_logprobs, grad_entropy, ids, id_bits, b, P.bpad, g, n, exclude, exclude_row_words,
               extra, (float*)(ws + P.add), (float*)(ws + P.coef), (float*)(ws + P.hent), (float*)(ws + P.sign),
               (float*)(ws + P.gval), (uint32_t*)(ws + P.neg), (int32_t*)(ws + P.tgt)};
-  hipLaunchKernelGGL(terms_kernel, dim3((P.bpad + 255) / 256), dim3(256), 0, s, T);
+  if (g <= 1) hipLaunchKernelGGL(terms_kernel, dim3((P.bpad + 255) / 256), dim3(256), 0, s, T);
+  else hipLaunchKernelGGL(sorted_terms_kernel, dim3(P.bpad / kFrag), dim3(kSortedThreads), 0, s, T);
   if (const int rc = check_launch()) return rc;
 
   const Table tq{(const uint8_t*)queries, query_stride * E, b, d * E};
@@ -291,7 +330,6 @@ int mips_logprobs_backward(const void* queries, int64_t query_stride, int32_t b,
   A.scale = scale;
   A.scx = scale * kLog2e;
   A.inv_scx = 1.0f / A.scx;
-  A.use_hent = grad_entropy != nullptr;
 
   if (grad_items || grad_bias) {
     A.own = ti;

@@ -101,12 +101,13 @@ namespace mips {
 // add_j = bias_j log2 e. The streamed rows' addend is divided by scx and enters the scores'
 // products as one more 16-byte chunk, against a chunk of ones. Queries are padded to a multiple
 // of kGradTile with addends of kMasked.
+constexpr int32_t kNoTarget = 0x7FFFFFFF;
 struct QueryTerms {
   const float* add;      // add_b
   const float* coef;
-  const float* hent;
+  const float* hent;     // 0 without an entropy gradient
   const uint32_t* neg;   // bit b & 31 of word b >> 5: coef_b < 0 (plain)
-  const int32_t* tgt;    // [b][g]; -1: no target
+  const int32_t* tgt;    // [b][g], ascending for each query; kNoTarget: none
   const float* gval;     // [b][g]
   int g;
 };
@@ -118,7 +119,6 @@ struct GradArgs {
   const uint32_t* exclude;
   int64_t exclude_words;
   float scale, scx, inv_scx;
-  int use_hent;
   int nown, nsplit;          // own tiles and splits of the streamed rows
   int64_t ntiles;            // tiles of streamed rows
   void* out;                 // [own.n, d] of the operands' type; nsplit == 1

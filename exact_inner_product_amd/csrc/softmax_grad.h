@@ -63,14 +63,12 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 //     other operand takes the streamed rows in the same order, transposed by the LDS read
 //     (bf16), or element by element (f32).
 // In bf16 the weights are rounded to bf16 for step 3, to nearest: an independent relative error
-// of at most 2^-8 each, under sums that are rounded to bf16 themselves. What is rounded is the whole
-// weight: both passes add the targets' gradients in step 2. A target with nearly all of the
-// probability has a weight of nearly 0, the difference of g and p g; with p g rounded by itself, the
-// queries' gradients were off by several times their size. Blocks with a target in them take step 3
-// a second time, for what the first rounding left of the targets' weights: one is most of its item's
-// gradient, and would double that gradient's error (of 250,000 items by 4096 queries 0.4% of the
-// blocks have a target). The other weights stay as they are, so that what a row gets does not depend
-// on its neighbours. Sums are in binary32.
+// of at most 2^-8 each, under sums that are rounded to bf16 themselves. The targets' weights g - p G
+// are not: with nearly all of the probability a target has a weight of nearly 0, of which the rounding
+// of p G leaves nothing, and with little its weight is most of its item's gradient, whose error the
+// rounding would double. So step 3 takes - p G of a target as of any other row, and g and what the
+// rounding left are added as one more product in binary32, of one row each (4096 targets among
+// 250,000 items: 0.4% of the blocks hold one). Sums are in binary32.
 //
 // What bounds it: matrix and vector instructions together, which share a SIMD's issue. Per 32 x 32
 // block of a width of 128 in bf16, 17 products of 32 cycles and about 70 vector instructions, 16 of
@@ -157,24 +155,32 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
 
   const int64_t t_begin = (int64_t)split * A.ntiles / A.nsplit, t_end = (int64_t)(split + 1) * A.ntiles / A.nsplit;
 
-  // Queries' pass: the lane's query has no target below this row that has not been passed yet. The
-  // blocks come in the rows' order, so that one comparison a block finds the few that hold a target.
-  // visit() calls f(row, its gradient) for the targets in [first, end), in the order given, and moves on.
-  int32_t target = INT32_MAX;
-  auto visit = [&](int32_t first, int32_t end, auto f) __attribute__((always_inline)) {
-    target = INT32_MAX;
-    for (int g = 0; g < A.q.g; ++g) {
-      const int32_t t = A.q.tgt[own_c * A.q.g + g];
-      if (t >= end) target = min(target, t);
-      else if (t >= first) f(t, A.q.gval[own_c * A.q.g + g]);
+  // Queries' pass: the next target of the lane's query with its gradient, and the one after it, which
+  // is on its way when it is needed. Targets and blocks come in the rows' order, so that one comparison
+  // a block finds the few that hold a target.
+  int32_t target = kNoTarget, target2 = kNoTarget;
+  float target_grad = 0.0f, target_grad2 = 0.0f;
+  int64_t target_at = own_c * A.q.g, target_end = target_at + A.q.g;  // of the one after
+  auto next_target = [&]() __attribute__((always_inline)) {
+    target = target2, target_grad = target_grad2, target2 = kNoTarget;
+    if (++target_at < target_end) {
+      target2 = A.q.tgt[target_at];
+      target_grad2 = flip ? -A.q.gval[target_at] : A.q.gval[target_at];
     }
   };
-  if (!ITEMS && live) visit(0, (int32_t)(t_begin * kGradTile), [](int32_t, float) {});
+  if (!ITEMS && live) {
+    int passed = 0;
+#pragma unroll 8
+    for (int g = 0; g < A.q.g; ++g) passed += A.q.tgt[own_c * A.q.g + g] < t_begin * kGradTile ? 1 : 0;
+    target_at += passed - 1;
+    next_target();
+    next_target();
+  }
 
   // ---- staging
   u32x4_t ld[NLD];
   float la = 0.0f, lb = 0.0f, lc = 0.0f;
-  int32_t lt = -1;
+  int32_t lt = kNoTarget;
   uint32_t lw[NLD], law = 0u, ln = 0u;
   const bool shared_mask = A.exclude != nullptr && A.exclude_words == 0;
   auto stage_load = [&](int64_t tile) __attribute__((always_inline)) {
@@ -183,9 +189,9 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
       const int e = i * NT + threadIdx.x, j = e / SL, s = e % SL;
       // Padding queries, of weight 0, hold the last one's row: zeros would make NaN of the score
       // with an item's row of infinities.
-      const int64_t r = ITEMS ? min(tile * kGradTile + j, A.str.n - 1) : tile * kGradTile + j;
+      const int64_t r = ITEMS ? min((int)tile * kGradTile + j, (int)A.str.n - 1) : tile * kGradTile + j;
       ld[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (r < A.str.n && 16 * s < A.str.row_b) ld[i] = *(const u32x4_t*)(A.str.p + r * A.str.stride_b + 16 * s);
+      if ((ITEMS || r < A.str.n) && 16 * s < A.str.row_b) ld[i] = *(const u32x4_t*)(A.str.p + r * A.str.stride_b + 16 * s);
       if (!ITEMS && shared_mask) lw[i] = r < A.str.n ? A.exclude[r >> 5] : 0u;
     }
     if (threadIdx.x < kGradTile) {
@@ -293,15 +299,13 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
       }
     }
     // the block's first targets and signs, read ahead of the products
-    int32_t tgt0 = -1;
+    int32_t tgt0 = kNoTarget;
     uint32_t negw = 0u;
     if constexpr (ITEMS) {
       if (A.q.g > 0) tgt0 = vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g];
       if (!EXTRA) negw = vneg[buf * (kGradTile / 32) + jb];
     }
     float w[16];
-    uint32_t targets = 0u;     // bit i: register i's weight has a target's gradient
-    bool target_here = false;  // whether any lane's has; uniform over the wave
     float ck[16], hk[16];
     if constexpr (EXTRA && ITEMS) {
 #pragma unroll
@@ -320,11 +324,9 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
         const float t = fmaf(s[i], A.scx, my_add);
         w[i] = __builtin_amdgcn_exp2f(t);
         if constexpr (EXTRA) {
-          float k = ITEMS ? ck[i] : my_coef;
-          if (A.use_hent) k = fmaf(t, ITEMS ? hk[i] : my_hent, k);
-          // (0 log 0 = 0: log2 p of a masked item may be -inf)
-          const bool none = ((bits >> i) & 1u) || (A.use_hent && w[i] == 0.0f);
-          w[i] = none ? 0.0f : w[i] * k;
+          // 0 log 0 = 0: log2 p of a masked item may be -inf, but below -126 its p is 0
+          const float k = fmaf(fmaxf(t, -200.0f), ITEMS ? hk[i] : my_hent, ITEMS ? ck[i] : my_coef);
+          w[i] = ((bits >> i) & 1u) ? 0.0f : w[i] * k;
         }
         asm volatile("" : "+v"(w[i]));  // computed here, under these products
       }
@@ -346,6 +348,33 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
 #pragma unroll
       for (int d = 0; d < kAhead; ++d) ahead[d] = read_columns(0, d);
     }
+    // A target, own row `own_r` and streamed row `str_r` of the block (both uniform): its gradient v
+    // and, in bf16, what the rounding of its weight will leave go to the sums as a multiple of the
+    // streamed row, in binary32. The weight is register 4 (str_r >> 3) + (str_r & 3) of lane own_r of
+    // half (str_r >> 2) & 1, the sums' row the register of the same form of own_r, in one half's lanes.
+    auto add_target = [&](int own_r, int str_r, float v) __attribute__((always_inline)) {
+      const int at = 4 * (str_r >> 3) + (str_r & 3), holder = own_r + 32 * ((str_r >> 2) & 1);
+      if constexpr (CT == MIPS_BF16) {
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x = i == at ? w[i] : x;
+        const float rounded = (float)(__bf16)x;
+        v += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x - rounded), holder));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = i == at && lane == holder ? rounded : w[i];  // (an id given twice)
+      }
+      float row[DT];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const int byte = (32 * d + col) * E;
+        const uint8_t* q = y + str_r * RB + (((byte >> 4) ^ (swz(str_r) & (SL - 1))) << 4) + (byte & 15);
+        if constexpr (CT == MIPS_BF16) row[d] = bf16_to_f32(*(const uint16_t*)q);
+        else row[d] = *(const float*)q;
+      }
+      const float k = own_r == lane ? v : 0.0f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) sum[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(k, row[d], sum[d], 0, 0, 0);
+    };
     if constexpr (ITEMS) {
       if constexpr (!EXTRA) {
         // the queries whose coefficient is negative (none, or all, in most losses)
@@ -356,41 +385,35 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
           for (int i = 0; i < 16; ++i) w[i] = ((nb >> i) & 1u) ? -w[i] : w[i];
         }
       }
-      // targets among this wave's items: rare, so one ballot a target column, and the pairs it
-      // finds one by one: row j of the block is register 4 (j >> 3) + (j & 3) of half (j >> 2) & 1
-      for (int g = 0; g < A.q.g; ++g) {
-        const int32_t tgt = g == 0 ? tgt0 : vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
-        uint32_t hits = (uint32_t)__ballot(tgt >= own0 && tgt < own0 + 32);
-        target_here |= hits != 0u;
-        while (hits != 0u) {
-          const int j = __builtin_ctz(hits);
-          hits &= hits - 1u;
-          const int to = __builtin_amdgcn_readlane(tgt, j) - (int)own0 + 32 * ((j >> 2) & 1);
-          const float v = lane == to ? A.q.gval[(tile * kGradTile + jb * 32 + j) * A.q.g + g] : 0.0f;
-          const int at = 4 * (j >> 3) + (j & 3);
-          targets |= lane == to ? 1u << at : 0u;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] += i == at ? v : 0.0f;
-        }
-      }
       if (EXTRA && A.bias_part) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dbias += w[i];
       }
+      // targets among this wave's items: rare, so one ballot a target column, and the pairs it
+      // finds one by one
+      for (int g = 0; g < A.q.g; ++g) {
+        const int32_t tgt = g == 0 ? tgt0 : vtgt[(buf * kGradTile + jb * 32 + col) * A.q.g + g];
+        uint32_t hits = (uint32_t)__ballot(tgt >= own0 && tgt < own0 + 32);
+        while (hits != 0u) {
+          const int j = __builtin_ctz(hits);
+          hits &= hits - 1u;
+          const int r = __builtin_amdgcn_readlane(tgt, j) - (int)own0;
+          const float v = A.q.gval[(tile * kGradTile + jb * 32 + j) * A.q.g + g];
+          add_target(r, j, v);
+          if (EXTRA && A.bias_part) dbias += lane == r ? v : 0.0f;
+        }
+      }
     } else {
-      // targets of this wave's queries among the block's items, as rare: row r of the block is
-      // register 4 (r >> 3) + (r & 3) of half (r >> 2) & 1
+      // targets of this wave's queries among the block's items, as rare
       const int32_t first = (int32_t)(tile * kGradTile) + jb * 32;
-      target_here = __ballot(target < first + 32) != 0ull;
-      if (target_here && target < first + 32)
-        visit(first, first + 32, [&](int32_t t, float v) __attribute__((always_inline)) {
-          const int r = t - first;
-          const int at = ((r >> 2) & 1) == h ? 4 * (r >> 3) + (r & 3) : -1;
-          v = flip ? -v : v;
-          targets |= at >= 0 ? 1u << at : 0u;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] += i == at ? v : 0.0f;
-        });
+      uint32_t hits = (uint32_t)__ballot(target < first + 32);
+      while (hits != 0u) {
+        const int r = __builtin_ctz(hits);
+        const int j = __builtin_amdgcn_readlane(target, r) - first;
+        add_target(r, j, __int_as_float(__builtin_amdgcn_readlane(__float_as_int(target_grad), r)));
+        if (col == r) next_target();
+        hits = (uint32_t)__ballot(target < first + 32);
+      }
     }
     between();
     // sums += w^T Y
@@ -404,20 +427,6 @@ __attribute__((amdgpu_waves_per_eu(grad_wps(CT, D), grad_wps(CT, D)))) void grad
         for (int d = 0; d < DT; ++d)
           sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               wa, kb == 0 && d < kAhead ? ahead[d < kAhead ? d : 0] : read_columns(kb, d), sum[d], 0, 0, 0);
-      }
-      if (__builtin_expect(target_here, 0)) {  // the next eight bits of the targets' weights
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          bf16x8_t wa;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = w[8 * kb + e];
-            wa[e] = (targets >> (8 * kb + e)) & 1u ? (__bf16)(x - (float)(__bf16)x) : (__bf16)0.0f;
-          }
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            sum[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, read_columns(kb, d), sum[d], 0, 0, 0);
-        }
       }
     } else {
 #pragma unroll
