@@ -158,7 +158,7 @@ static int launch_lookup(LookupArgs A, int id_bits, hipStream_t s) {
 
 // ------------------------------------------------------------------ sorting the tokens
 // The (id, token) pairs sorted by id, equal ids in token order: the order of the segmented
-// sum, and so its rounding, follows from the ids alone. Ids outside [0, rows) take the key
+// sum, and so its rounding, follows from the ids and sizes alone. Ids outside [0, rows) take the key
 // `rows` and sort behind every row.
 //
 // (Few tokens are not sorted as a whole: see small_kernel.) A least-significant-digit radix sort

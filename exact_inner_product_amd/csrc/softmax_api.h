@@ -133,7 +133,7 @@ constexpr int kGradBufs = 3;   // tiles in LDS: this one, the next, and the one 
 __host__ __device__ constexpr int grad_wps(int ct, int d) { return d * elem_bytes(ct) > 256 ? 1 : 2; }
 // Waves of a workgroup: in bf16 eight, which share each tile of streamed rows (four, in two
 // workgroups a unit, moved twice the rows through LDS: 506 us against 456 for the queries of
-// 4096 x 250,000 x 128); in f32, bound by its products, four: twice the workgroups for small
+// 4096 x 250,000 x 128 at the time); in f32, bound by its products, four: twice the workgroups for small
 // batches (1000 x 1000 x 64: 15.5 us against 20.8).
 __host__ __device__ constexpr int grad_waves(int ct, int d) { return ct == MIPS_BF16 && grad_wps(ct, d) == 2 ? 8 : 4; }
 // Workgroups that run on a compute unit at once.

@@ -72,11 +72,12 @@ __device__ __forceinline__ int swz(int j) { return ((j & 3) << 1) | ((j >> 2) & 
 //
 // What bounds it: matrix and vector instructions together, which share a SIMD's issue. Per 32 x 32
 // block of a width of 128 in bf16, 17 products of 32 cycles and about 70 vector instructions, 16 of
-// them exp2 (8 cycles each): at 4096 x 250,000 x 128 the queries' pass takes 456-486 us (1.08-1.15
-// PFLOP/s of its two products) with the matrix pipes busy 57% and the vector units 43% of the
-// cycles; the items' pass 540-583 us (47% and 40%; it also looks for targets and signs). In f32
-// the products bound it (32 x 32 x 2, 64 cycles each). A small batch is latency: 1000 x 1000 x 64
-// in f32 takes 14.5 + 11.5 us, 4096 x 8192 x 128 in bf16 31 + 30 us.
+// them exp2 (8 cycles each): at 4096 x 250,000 x 128 the queries' pass takes 485 us (1.08 PFLOP/s of
+// its two products) with the matrix pipes busy 54% and the vector units 41% of the cycles; the items'
+// pass 568 us (45% and 38%; it also looks for signs, and for targets by their ids). In f32 the products
+// bound it (32 x 32 x 2, 64 cycles each). A small batch is latency: 1000 x 1000 x 64 in f32 takes
+// 14 + 13.5 us, 4096 x 8192 x 128 in bf16 34 + 34 us, of which targets are about a tenth (12% of the
+// blocks hold one).
 //
 // Step 1 of the next 32 rows is interleaved with step 2 of these, chunk by chunk, so that the
 // matrix pipe works under the exponentials. Tiles of 64 streamed rows go through three LDS

@@ -162,10 +162,12 @@ def item_logprobs(queries: torch.Tensor, items: Union[torch.Tensor, Corpus], ids
     `alternatives` most likely items (ties by the lowest id).
 
     queries: float32 or bfloat16 [b, d]; items: [n, d] of the same type (any strides; rows that
-    are not 16-byte aligned are copied first), d up to 128 (float32) or 256 (bfloat16), or an
+    are not 16-byte aligned are copied first, in every call: a table of 250,000 x 100 bfloat16 takes
+    390 us where 104 wide it takes 298), d up to 128 (float32) or 256 (bfloat16), or an
     f32 or bf16 Corpus. ids: int32/int64 [b, g]; an id outside [0, n) is padding (0).
-    scale: 1 / temperature, positive. bias: float32 [n], e.g. -log q of a sampled softmax.
-    exclude: bitmap as topk's; excluded items have probability 0.
+    scale: 1 / temperature, positive. bias: float32 [n], e.g. -log q of a sampled softmax; -inf and
+    the lowest float mask an item (p = 0). exclude: bitmap as topk's; excluded items have
+    probability 0. A logit of NaN or +inf makes its query's results NaN; one of -inf is no alternative.
     """
     q, held, layout, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(
         queries, items, ids, bias, exclude, workspace, model_version)
@@ -203,7 +205,8 @@ def item_logprobs_backward(grad_logprobs: Optional[torch.Tensor], queries: torch
     grad_logprobs: float32 [b, g], the gradient of each log probability (a loss that is the
     mean of -log p of one target has -1/b); grad_entropy: float32 [b] or None. `forward` is the
     result of item_logprobs on the same arguments (its logsumexp, and its entropy with
-    grad_entropy). Up to TARGETS_MAX ids a query.
+    grad_entropy). Up to TARGETS_MAX ids a query. Rows that a shared bitmap excludes may hold
+    anything; with one bitmap per query all rows must be finite.
     """
     q, held, _, stride, n, d, code, ids, bits, bias, exclude, words = _softmax_args(
         queries, items, ids, bias, exclude, workspace)
@@ -267,7 +270,8 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, rows: int, scale: floa
                    out: Optional[torch.Tensor] = None, accumulate: bool = False,
                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of embedding_lookup for its table: [rows, d], row v being scale times the
-    sum of grad over the tokens with id v (binary32, in token order: reproducible bit by bit).
+    sum of grad over the tokens with id v (binary32, in an order that follows from the ids, sizes
+    and device: the same call gives the same bits).
 
     grad: float32 or bfloat16 [*ids.shape, d]; ids as embedding_lookup's (ids outside
     [0, rows) take no part). out: [rows, d] of grad's type or float32 (default: a new tensor
@@ -329,7 +333,8 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     shapes, types and strides). Nothing waits for the GPU.
 
     tensors: float32 or bfloat16, mixed as they come, each dense (its elements fill one run of
-    memory). max_norm: >= 0; math.inf only takes the norm.
+    memory), none overlapping another. max_norm: >= 0; math.inf only takes the norm, and leaves (or
+    copies) the tensors as they are, whatever it is.
     """
     tensors = list(tensors)
     outs = tensors if out is None else list(out)

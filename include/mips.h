@@ -343,7 +343,8 @@ MIPS_API int mips_merge_interests(const float *in_scores, const int32_t *in_ids,
 /* ---------------------------------------------------------------------------------------
  * Training: the steps around the search that make and use the vectors. The conventions
  * above hold, with these of their own: matrices are row-major with a row stride in
- * elements; NaN and infinities are allowed and propagate as in the formulas.
+ * elements; NaN and infinities are allowed and propagate as in the formulas, or as each entry
+ * point says.
  */
 
 /* Largest width of an embedding row, and most tokens of one mips_embedding_grad call. */
@@ -369,8 +370,9 @@ MIPS_API int mips_embedding_lookup(const void *table, int32_t dtype, int64_t row
 /*
  * mips_embedding_grad -- the gradient of mips_embedding_lookup for the table:
  * out[v] = scale * sum of grad[i] over the tokens i with ids[i] = v, zero rows for ids that
- * no token has. The tokens are sorted by id (stably) and summed in binary32 in that order:
- * the same call gives the same bits. Ids outside [0, rows) take no part.
+ * no token has. Sums are in binary32 without atomics, in an order that follows from the call's
+ * ids, sizes and device alone (a hot id's tokens are added in several parts): the same call gives
+ * the same bits. Ids outside [0, rows) take no part.
  *   grad        device, [t, d] of grad_dtype MIPS_F32 or MIPS_BF16, grad_stride >= d.
  *   ids         device, int32 or int64 [t]; t 0 .. MIPS_TOKENS_MAX.
  *   rows        1 .. 2^31 - 64.
@@ -475,12 +477,13 @@ MIPS_API int mips_logprobs(const void *queries, int64_t query_stride, int32_t b,
  *   grad_queries[b] = scale sum_j w_bj items[j],  grad_items[j] = scale sum_b w_bj queries[b],
  *   grad_bias[j] = sum_b w_bj,
  * over the eligible items; padding and excluded targets, and queries of lse -INFINITY, have no
- * gradient. The scores are computed again, once for each of the two sums, and never written. Sums are in binary32 in a fixed
- * order (the same call gives the same bits); with MIPS_BF16 the weights w are rounded to bf16
- * before they multiply the rows, and the gradients to bf16 at the end.
- *   queries .. g   as the forward call's; g at most MIPS_TARGETS_MAX, n at most 2^30. An item that the shared
- *               bitmap excludes may hold anything; with one bitmap per query, the rows must be
- *               finite (a row may be excluded for some queries and not for others).
+ * gradient, and p log p is 0 where p is. The scores are computed again, once for each of the two
+ * sums, and never written. Sums are in binary32 in a fixed order (the same call gives the same
+ * bits). With MIPS_BF16 the weights are rounded to bf16 before they multiply the rows, those of
+ * targets excepted, and the gradients to bf16 at the end.
+ *   queries .. g   as the forward call's; g at most MIPS_TARGETS_MAX, n at most 2^30. An item that
+ *               the shared bitmap excludes may hold anything; with one bitmap per query, the rows
+ *               must be finite (a row may be excluded for some queries and not for others).
  *   lse, entropy   device float [b], the forward call's (entropy only with grad_entropy).
  *   grad_logprobs  device float [b, g]; grad_entropy device float [b] or NULL.
  *   grad_queries   device, [b, d] contiguous of dtype, or NULL: not wanted; grad_items device,
