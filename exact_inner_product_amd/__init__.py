@@ -33,6 +33,9 @@ EXPORTS = (
     "mips_clip_workspace_size", "mips_clip_grad_norm",
     "mips_logprobs_workspace_size", "mips_logprobs",
     "mips_logprobs_backward_workspace_size", "mips_logprobs_backward",
+    "mips_gated_scan_carries", "mips_gated_scan_workspace_size", "mips_gated_scan", "mips_gated_scan_backward",
+    "mips_gated_step", "mips_dropout",
+    "mips_pool_workspace_size", "mips_pool_normalize", "mips_pool_normalize_backward",
 )
 MERGE_MAX_LISTS = 64
 MAX_MASKS = 4  # result sets of one mips_topk_masks pass
@@ -107,6 +110,22 @@ def lib() -> C.CDLL:
         L.mips_logprobs_backward.argtypes = [p, i64, i32, p, i64, i64, i32, i32, p, p, i64, f32, p, i32, i32,
                                              p, p, p, p, p, p, p, p, sz, p]
         for f in (L.mips_logprobs, L.mips_logprobs_backward, L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
+            f.restype = C.c_int
+        u64 = C.c_uint64
+        L.mips_gated_scan_carries.argtypes = [p, i32]
+        L.mips_gated_scan_carries.restype = i64
+        L.mips_gated_scan_workspace_size.argtypes = [p, i32]
+        L.mips_gated_scan_workspace_size.restype = sz
+        L.mips_gated_scan.argtypes = [p, i32, i32, p, p, p, p, p, p, p, p, sz, p]
+        L.mips_gated_scan_backward.argtypes = [p, i32, i32, p, p, p, p, p, p, p, p, p, p, p, p, sz, p]
+        L.mips_gated_step.argtypes = [p, i64, p, i64, p, i64, i32, i32, i32, p, i64, p, i64, i64, p, i32, p, p]
+        L.mips_dropout.argtypes = [p, i32, i64, C.c_double, u64, u64, p, p, p, p]
+        L.mips_pool_workspace_size.argtypes = [p, i32]
+        L.mips_pool_workspace_size.restype = sz
+        L.mips_pool_normalize.argtypes = [p, i32, i32, p, i32, p, p, p, p, sz, p]
+        L.mips_pool_normalize_backward.argtypes = [p, i32, i32, p, i64, i32, p, p, p, p]
+        for f in (L.mips_gated_scan, L.mips_gated_scan_backward, L.mips_gated_step, L.mips_dropout,
+                  L.mips_pool_normalize, L.mips_pool_normalize_backward):
             f.restype = C.c_int
         for f in (L.mips_l2_normalize, L.mips_prepare_corpus, L.mips_topk, L.mips_topk_noalloc,
                   L.mips_topk_ranges,
@@ -493,3 +512,5 @@ def set_timing_events(before, after) -> None:
 
 from .training import (ALTERNATIVES_MAX, TARGETS_MAX, ItemLogprobs, clip_grad_norm, embedding_grad,  # noqa: E402
                        embedding_lookup, item_logprobs, item_logprobs_backward)
+from .histories import (EVENTS_MAX, GatedScan, Pooled, dropout, gated_scan, gated_scan_backward, gated_step,  # noqa: E402
+                        pool_normalize, pool_normalize_backward)

@@ -20,7 +20,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmips.so")
 SOURCES = ["api.hip", "normalize.hip", "topk.hip", "merge.hip", "noalloc.hip",
            "embedding.hip", "gradnorm.hip", "logprobs.hip",
-           "logprobs_grad.hip"]
+           "logprobs_grad.hip", "scan.hip", "scan_grad.hip", "events.hip", "dropout.hip", "pool.hip"]
 
 # (dtype macro, width) pairs of the score pass; must match corpus_d_supported in host.h
 SCORE_UNITS = ([("MIPS_F32", d) for d in (16, 32, 64, 128)] +

@@ -1,0 +1,178 @@
+// events.hip -- the gated recurrence for single events against a table of states (gfx950).
+//
+// For events e in order: row = rows[e], h = a_e state[row] + b_e x_e, state[row] = h, out[e] = h.
+// A row that several events name gets them one after another: the first of them does the work
+// of all, so that no two workgroups touch one row. To find out, every workgroup looks through all
+// events' rows once (4 bytes each, from the caches) against a small table of hashes of its own.
+#include "scan.h"
+
+namespace mips {
+
+constexpr int kEventThreads = 256;
+constexpr int kEventsMost = 64;        // events of a workgroup
+constexpr uint32_t kFilterBits = 2048;
+constexpr uint32_t kHitsMost = 1024;   // later events of a workgroup's rows that are kept in LDS
+
+struct EventArgs {
+  const void *x, *forget, *gate;
+  int64_t x_stride, forget_stride, gate_stride;
+  const float* state;
+  float* out;       // [rows, d], may be `state`
+  int64_t state_stride, out_stride;
+  int64_t table;    // rows of it
+  const void* ids;
+  int32_t wide;
+  int32_t b, d;
+  int32_t own;      // events of a workgroup
+  int32_t lanes_log2;
+  void* h;          // [b, d]
+};
+
+__device__ __forceinline__ int64_t event_row(const EventArgs& A, int64_t e) {
+  return A.wide ? ((const int64_t*)A.ids)[e] : (int64_t)((const int32_t*)A.ids)[e];
+}
+__device__ __forceinline__ uint32_t row_hash(int64_t row) {
+  return ((uint32_t)row * 2654435761u + (uint32_t)(row >> 32) * 40503u) >> (32 - 11);
+}
+
+// The first event after e, below b, whose row is `row`, or b: all lanes of a group together. `hits` are the
+// workgroup's later events (their own event << 16 | event), in any order, if they are all there.
+__device__ __forceinline__ int32_t next_event(const EventArgs& A, const uint32_t* hits, uint32_t nhits, int i,
+                                              int64_t row, int32_t e, int lanes, int lane) {
+  if (nhits <= kHitsMost) {
+    uint32_t best = 0xFFFFFFFFu;
+    for (uint32_t k = lane; k < nhits; k += lanes) {
+      const uint32_t v = hits[k];
+      if ((int)(v >> 16) == i && (int32_t)(v & 0xFFFFu) > e) best = min(best, v & 0xFFFFu);
+    }
+    for (int o = lanes >> 1; o >= 1; o >>= 1) best = min(best, (uint32_t)__shfl_xor((int)best, o));
+    return best == 0xFFFFFFFFu ? A.b : (int32_t)best;
+  }
+  const int shift = (threadIdx.x & 63) & ~(lanes - 1);
+  const uint64_t group = (lanes == 64 ? ~uint64_t(0) : (uint64_t(1) << lanes) - 1) << shift;
+  for (int32_t at = e + 1; at < A.b; at += lanes) {
+    const bool same = at + lane < A.b && event_row(A, at + lane) == row;
+    const uint64_t m = __ballot(same) & group;  // this group's lanes are here together
+    if (m) return at + (__ffsll((unsigned long long)m) - 1 - shift);
+  }
+  return A.b;
+}
+
+template <typename T, bool GATE, bool VEC>
+__global__ __launch_bounds__(kEventThreads) void events_kernel(EventArgs A) {
+  __shared__ int64_t own[kEventsMost];
+  __shared__ uint32_t earlier[kEventsMost], later[kEventsMost];
+  __shared__ uint32_t filter[kFilterBits / 32];
+  __shared__ uint32_t hits[kHitsMost], nhits;
+  const int tid = threadIdx.x;
+  const int32_t e0 = (int32_t)blockIdx.x * A.own;
+  const int count = min(A.own, A.b - e0);
+  for (int i = tid; i < (int)kFilterBits / 32; i += kEventThreads) filter[i] = 0;
+  if (tid == 0) nhits = 0;
+  if (tid < count) {
+    own[tid] = event_row(A, e0 + tid);
+    earlier[tid] = later[tid] = 0;
+  }
+  __syncthreads();
+  if (tid < count) {
+    const uint32_t v = row_hash(own[tid]);
+    atomicOr(&filter[v >> 5], 1u << (v & 31));
+  }
+  __syncthreads();
+  for (int32_t e = tid; e < A.b; e += kEventThreads) {
+    const int64_t row = event_row(A, e);
+    const uint32_t v = row_hash(row);
+    if (!((filter[v >> 5] >> (v & 31)) & 1u)) continue;
+    for (int i = 0; i < count; ++i) {
+      if (own[i] != row) continue;
+      if (e < e0 + i) {
+        earlier[i] = 1;  // every writer writes the same
+      } else if (e > e0 + i) {
+        later[i] = 1;
+        const uint32_t k = atomicAdd(&nhits, 1u);
+        if (k < kHitsMost) hits[k] = (uint32_t)i << 16 | (uint32_t)e;
+      }
+    }
+  }
+  __syncthreads();
+
+  const int lanes = 1 << A.lanes_log2, lane = tid & (lanes - 1);
+  for (int i = tid >> A.lanes_log2; i < count; i += kEventThreads >> A.lanes_log2) {
+    const int64_t row = own[i];
+    const bool inside = row >= 0 && row < A.table;
+    if (inside && earlier[i]) continue;
+    for (int base = 0; base < A.d; base += lanes * 4) {
+      const int c0 = base + lane * 4, live = min(4, A.d - c0);  // live <= 0: only looks for events
+      float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (!inside) {
+        if (live > 0) store4<VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, h);
+        continue;
+      }
+      if (live > 0) load4<VEC>(A.state + row * A.state_stride + c0, live, h);
+      for (int32_t e = e0 + i; e < A.b;) {
+        if (live > 0) {
+          Raw<T> x, f, g;
+          raw_load<VEC>((const T*)A.x + e * A.x_stride + c0, live, &x);
+          raw_load<VEC>((const T*)A.forget + e * A.forget_stride + c0, live, &f);
+          if (GATE) raw_load<VEC>((const T*)A.gate + e * A.gate_stride + c0, live, &g);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float a, na, b, nb;
+            sigmoids(f.at(c), &a, &na);
+            b = na;
+            if (GATE) sigmoids(g.at(c), &b, &nb);
+            h[c] = fmaf(a, h[c], b * x.at(c));
+          }
+          store4<VEC>((T*)A.h + (int64_t)e * A.d + c0, live, h);
+        }
+        if (!later[i]) break;
+        e = next_event(A, hits, nhits, i, row, e, lanes, lane);
+      }
+      if (live > 0) store4<VEC>(A.out + row * A.out_stride + c0, live, h);
+    }
+  }
+}
+
+}  // namespace mips
+
+using namespace mips;
+
+extern "C" int mips_gated_step(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride,
+                               const void* gate, int64_t gate_stride, int32_t dtype, int32_t b, int32_t d,
+                               const float* state, int64_t state_stride, float* out_state, int64_t out_stride,
+                               int64_t rows, const void* ids, int32_t id_bits, void* out, void* stream) {
+  if (b < 0 || d < 1 || rows < 1 || x_stride < d || forget_stride < d || (gate && gate_stride < d) ||
+      state_stride < d || out_stride < d)
+    return MIPS_ERR_INVALID_ARG;
+  if ((dtype != MIPS_F32 && dtype != MIPS_BF16) || (id_bits != 32 && id_bits != 64) || d > MIPS_EMBEDDING_D_MAX ||
+      b > MIPS_EVENTS_MAX)
+    return MIPS_ERR_UNSUPPORTED;
+  if (b == 0) return MIPS_OK;
+  const int E = elem_bytes(dtype);
+  if (!x || !forget || !state || !out_state || !ids || !out || !aligned(x, E) || !aligned(forget, E) || !aligned(gate, E) ||
+      !aligned(out, E) || !aligned(state, 4) || !aligned(out_state, 4) || !aligned(ids, id_bits / 8) ||
+      (out_state == state && out_stride != state_stride))
+    return MIPS_ERR_INVALID_ARG;
+  EventArgs A{x, forget, gate, x_stride, forget_stride, gate_stride, state, out_state, state_stride, out_stride,
+              rows, ids, id_bits == 64, b, d, 0, 0, out};
+  A.lanes_log2 = d > 128 ? 6 : d > 64 ? 5 : d > 32 ? 4 : d > 16 ? 3 : 2;
+  // a workgroup's events: one round of its threads, or as many as keep its look through all
+  // events below the cost of its own
+  const int round = kEventThreads >> A.lanes_log2;
+  int own = round;
+  while (own < kEventsMost && (int64_t)b / own > 512) own *= 2;
+  A.own = own < kEventsMost ? own : kEventsMost;
+  const int64_t strides = x_stride | forget_stride | (gate ? gate_stride : 0);
+  const bool vec = d % 4 == 0 && strides % 4 == 0 && state_stride % 4 == 0 && aligned(x, 4 * E) && aligned(forget, 4 * E) &&
+                   aligned(gate, 4 * E) && aligned(out, 4 * E) && aligned(state, 16) && out_stride % 4 == 0 &&
+                   aligned(out_state, 16);
+  void (*kernel)(EventArgs) = nullptr;
+  if (dtype == MIPS_F32)
+    kernel = gate ? (vec ? events_kernel<float, true, true> : events_kernel<float, true, false>)
+                  : (vec ? events_kernel<float, false, true> : events_kernel<float, false, false>);
+  else
+    kernel = gate ? (vec ? events_kernel<__bf16, true, true> : events_kernel<__bf16, true, false>)
+                  : (vec ? events_kernel<__bf16, false, true> : events_kernel<__bf16, false, false>);
+  hipLaunchKernelGGL(kernel, dim3((b + A.own - 1) / A.own), dim3(kEventThreads), 0, (hipStream_t)stream, A);
+  return check_launch();
+}

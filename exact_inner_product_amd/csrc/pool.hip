@@ -1,0 +1,374 @@
+// pool.hip -- the mean of a sequence's rows, L2-normalised, and its gradient (gfx950).
+//
+//   m = sum of the rows / their number (0 without rows),  n = sqrt(max(sum m^2, 1e-12)),  u = m / n
+//   dm = (g - u (u . g)) / n, or g / n where the sum is below 1e-12;  each row's gradient dm / number
+//
+// Bound by reading the rows, and by writing their gradients. (Normalisation as the index's: sum
+// over all channels, 1e-12 under the root: recsys_two_tower_model.py:69, 73-76, 1287-1306.)
+#include "sequences.h"
+
+namespace mips {
+
+constexpr int kPoolThreads = 256;  // four waves, each on its own
+constexpr int kPoolWaves = kPoolThreads / 64;
+constexpr float kPoolEps = 1e-12f;
+
+struct PoolArgs {
+  Sequences S;
+  Rows x;           // forward: the rows
+  int32_t d;
+  int32_t lanes;    // of a row, 8 channels each, 1 to 64
+  int32_t normalize;
+  uint32_t chunk;   // rows of a wave
+  uint32_t chunks;
+  float* part;      // [chunks][2][d]: sums of the sequence that a chunk goes on with, of the one it leaves open
+  void* vectors;    // [b, d]
+  float* mean;      // [b, d]
+  float* norm;      // [b]
+  const void* grad; // backward: [b, d], grad_stride apart
+  int64_t grad_stride;
+  void* dx;         // [n, d]
+};
+
+// The rows of sequence s: [*begin, *end) in the numbering of sequences.h.
+__device__ __forceinline__ void sequence_rows(const Sequences& S, int64_t s, uint32_t* begin, uint32_t* end) {
+  if (S.t) {
+    *begin = (uint32_t)s * S.t;
+    *end = *begin + (S.lengths ? index_at(S.lengths, S.wide, s, S.t) : S.t);
+  } else {
+    *begin = index_at(S.offsets, S.wide, s, S.n);
+    *end = index_at(S.offsets, S.wide, s + 1, S.n);
+    if (*end < *begin) *end = *begin;
+  }
+}
+
+// Calls f(s, begin, end) for the sequences with rows in [r0, r1), those of a wave together. Dense ones
+// come with rows of padding or none too, packed ones only with rows.
+template <typename F>
+__device__ __forceinline__ void for_sequences(const Sequences& S, uint32_t r0, uint32_t r1, F f) {
+  uint32_t begin, end;
+  if (S.t) {
+    for (uint32_t s = r0 / S.t; s < (uint32_t)S.b && s * S.t < r1; ++s) {
+      sequence_rows(S, s, &begin, &end);
+      f((int32_t)s, begin, end);
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t s0 = lower_bound(S, r0);
+  s0 = s0 > 0 ? s0 - 1 : 0;
+  for (; s0 < S.b; s0 += 64) {
+    begin = end = ~0u;
+    if (s0 + lane < S.b) sequence_rows(S, s0 + lane, &begin, &end);
+    uint64_t m = __ballot(begin < end && begin < r1 && end > r0);
+    while (m) {
+      const int k = __ffsll((unsigned long long)m) - 1;
+      m &= m - 1;
+      f((int32_t)(s0 + k), (uint32_t)__shfl((int)begin, k), (uint32_t)__shfl((int)end, k));
+    }
+    if ((uint32_t)__shfl((int)begin, 63) >= r1) break;  // this one and all behind it
+  }
+}
+
+// Eight channels of a row, 16-byte loads with VEC (bf16: one, f32: two).
+template <typename T, bool VEC>
+__device__ __forceinline__ void row8(const T* p, int live, float* v) {
+  typedef T v8_t __attribute__((ext_vector_type(8), aligned(16)));
+  if constexpr (VEC) {
+    const v8_t q = *(const v8_t*)p;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = (float)q[c];
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = c < live ? (float)p[c] : 0.0f;
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void put8(T* p, int live, const float* v) {
+  typedef T v8_t __attribute__((ext_vector_type(8), aligned(16)));
+  if constexpr (VEC) {
+    v8_t q;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) q[c] = (T)v[c];
+    *(v8_t*)p = q;
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < live) p[c] = (T)v[c];
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// sum m^2 -> the norm (NaN stays NaN).
+__device__ __forceinline__ float pool_norm(const PoolArgs& A, float square) {
+  if (!A.normalize) return 1.0f;
+  return sqrtf(square < kPoolEps ? kPoolEps : square);
+}
+
+// One wave a chunk: the sums of its sequences; those that lie whole in it are finished.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kPoolThreads) void pool_kernel(PoolArgs A) {
+  const uint32_t chunk = blockIdx.x * kPoolWaves + (threadIdx.x >> 6);
+  if (chunk >= A.chunks) return;
+  const uint32_t r0 = chunk * A.chunk, r1 = min(r0 + A.chunk, A.S.n);
+  const int lane = threadIdx.x & 63, lanes = A.lanes, slots = 64 / lanes, slot = lane / lanes;
+  const int at = (lane & (lanes - 1)) * 8;
+  for_sequences(A.S, r0, r1, [&](int32_t s, uint32_t begin, uint32_t end) {
+    const uint32_t lo = max(begin, r0), hi = min(end, r1);
+    const bool whole = begin >= r0 && end <= r1;
+    const float inv = end > begin ? 1.0f / (float)(end - begin) : 0.0f;
+    float square = 0.0f, sum[8];
+    for (int c0 = 0; c0 < A.d; c0 += lanes * 8) {
+      const int c = c0 + at, live = min(8, A.d - c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+      if (live > 0) {
+        const T* p = (const T*)A.x.p + (A.S.t ? s * A.x.extra : 0) + c;
+        uint32_t r = lo + slot;
+        for (; r + 3 * slots < hi; r += 4 * slots) {
+          float v[4][8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) row8<T, VEC>(p + (int64_t)(r + k * slots) * A.x.row, live, v[k]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += (v[0][e] + v[1][e]) + (v[2][e] + v[3][e]);
+        }
+        for (; r < hi; r += slots) {
+          float v[8];
+          row8<T, VEC>(p + (int64_t)r * A.x.row, live, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        }
+      }
+      for (int o = lanes; o < 64; o <<= 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], o);
+      }
+      if (slot || live <= 0) continue;
+      if (!whole) {
+        float* q = A.part + ((int64_t)chunk * 2 + (begin < r0 ? 0 : 1)) * A.d + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < live) q[e] = sum[e];
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum[e] *= inv;
+        square = fmaf(sum[e], sum[e], square);
+      }
+      float* q = A.mean + (int64_t)s * A.d + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < live) q[e] = sum[e];
+    }
+    if (!whole) return;
+    const float n = pool_norm(A, wave_sum(square));
+    if (lane == 0) A.norm[s] = n;
+    if (slot) return;
+    for (int c0 = 0; c0 < A.d; c0 += lanes * 8) {
+      const int c = c0 + at, live = min(8, A.d - c);
+      if (live <= 0) continue;
+      if (A.d > lanes * 8) {  // several spans: this lane wrote them above
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = e < live ? A.mean[(int64_t)s * A.d + c + e] : 0.0f;
+      }
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = sum[e] / n;
+      put8<T, VEC>((T*)A.vectors + (int64_t)s * A.d + c, live, v);
+    }
+  });
+}
+
+// One workgroup a sequence: those that lie in several chunks, and packed ones without rows.
+template <typename T>
+__global__ __launch_bounds__(kPoolThreads) void pool_join_kernel(PoolArgs A) {
+  __shared__ float red[kPoolWaves];
+  const int tid = threadIdx.x;
+  const int64_t s = blockIdx.x;
+  uint32_t begin, end;
+  sequence_rows(A.S, s, &begin, &end);
+  const uint32_t k0 = begin / A.chunk, k1 = end > begin ? (end - 1) / A.chunk : k0;
+  if (k0 == k1 && (end > begin || A.S.t)) return;
+  const float inv = end > begin ? 1.0f / (float)(end - begin) : 0.0f;
+  float square = 0.0f;
+  for (int c = tid; c < A.d; c += kPoolThreads) {
+    float sum = 0.0f;
+    if (end > begin) {
+      // the first chunk left it open, unless it starts there: then it was gone on with as in the others
+      sum = A.part[((int64_t)k0 * 2 + 1) * A.d + c];
+      for (uint32_t k = k0 + 1; k <= k1; ++k) sum += A.part[(int64_t)k * 2 * A.d + c];
+    }
+    sum *= inv;
+    A.mean[s * A.d + c] = sum;
+    square = fmaf(sum, sum, square);
+  }
+  square = wave_sum(square);
+  if ((tid & 63) == 0) red[tid >> 6] = square;
+  __syncthreads();
+  const float n = pool_norm(A, (red[0] + red[1]) + (red[2] + red[3]));
+  if (tid == 0) A.norm[s] = n;
+  for (int c = tid; c < A.d; c += kPoolThreads)  // this thread wrote these
+    ((T*)A.vectors)[s * A.d + c] = (T)(A.mean[s * A.d + c] / n);
+}
+
+// One wave a chunk of rows, each sequence's row of gradients computed again for every chunk.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kPoolThreads) void pool_grad_kernel(PoolArgs A) {
+  const uint32_t chunk = blockIdx.x * kPoolWaves + (threadIdx.x >> 6);
+  if (chunk >= A.chunks) return;
+  const uint32_t r0 = chunk * A.chunk, r1 = min(r0 + A.chunk, A.S.n);
+  const int lane = threadIdx.x & 63, lanes = A.lanes, slots = 64 / lanes, slot = lane / lanes;
+  const int at = (lane & (lanes - 1)) * 8;
+  // rows [lo, hi) of dx as v, channels c ..
+  auto fill = [&](uint32_t lo, uint32_t hi, int c, int live, const float* v) {
+    for (uint32_t r = lo + slot; r < hi; r += slots) put8<T, VEC>((T*)A.dx + (int64_t)r * A.d + c, live, v);
+  };
+  auto zeros = [&](uint32_t lo, uint32_t hi) {
+    const float v[8] = {};
+    for (int c = at; c < A.d; c += lanes * 8) fill(lo, hi, c, min(8, A.d - c), v);
+  };
+  for_sequences(A.S, r0, r1, [&](int32_t s, uint32_t begin, uint32_t end) {
+    if (A.S.t) zeros(max(end, r0), min(begin + A.S.t, r1));
+    if (end <= r0) return;
+    const float* m = A.mean + (int64_t)s * A.d;
+    const T* g = (const T*)A.grad + s * A.grad_stride;
+    const float n = A.norm[s], inv = 1.0f / (float)(end - begin);
+    float dot = 0.0f, square = 0.0f;
+    if (A.normalize) {
+      for (int c = lane; c < A.d; c += 64) {
+        dot = fmaf(m[c], (float)g[c], dot);
+        square = fmaf(m[c], m[c], square);
+      }
+      dot = wave_sum(dot);
+      square = wave_sum(square);
+    }
+    // u (u . g) = m (m . g) / n^2, away where the root is that of 1e-12
+    const float along = A.normalize && !(square < kPoolEps) ? dot / n / n : 0.0f;
+    for (int c0 = 0; c0 < A.d; c0 += lanes * 8) {
+      const int c = c0 + at, live = min(8, A.d - c);
+      if (live <= 0) continue;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < live ? ((float)g[c + e] - m[c + e] * along) / n * inv : 0.0f;
+      fill(max(begin, r0), min(end, r1), c, live, v);
+    }
+  });
+  if (!A.S.t) {  // packed rows of no sequence
+    zeros(r0, min(r1, index_at(A.S.offsets, A.S.wide, 0, A.S.n)));
+    zeros(max(r0, index_at(A.S.offsets, A.S.wide, A.S.b, A.S.n)), r1);
+  }
+}
+
+// Rows of a wave: whole sequences where dense ones are short, else a length that leaves waves
+// enough to fill the card and few parts to join.
+static uint32_t pool_chunk(const Sequences& S) {
+  if (S.t && S.t <= 256) return S.t >= 32 ? S.t : 32 / S.t * S.t;
+  const uint32_t rows = S.n / 4096;
+  return rows < 64 ? 64 : (rows > 1024 ? 1024 : rows);
+}
+static bool pool_joins(const Sequences& S) { return !(S.t && S.t <= 256); }
+static int pool_lanes(int32_t d) {
+  int lanes = 1;
+  while (lanes < 64 && lanes * 8 < d) lanes *= 2;
+  return lanes;
+}
+static size_t pool_bytes(const Sequences& S, int32_t d) {
+  if (!pool_joins(S)) return 256;
+  const uint32_t chunk = pool_chunk(S);
+  return 256 + ((size_t)S.n + chunk - 1) / chunk * 2 * d * sizeof(float);
+}
+
+}  // namespace mips
+
+using namespace mips;
+
+extern "C" {
+
+size_t mips_pool_workspace_size(const mips_sequences* seq, int32_t d) {
+  Sequences S;
+  if (check_sequences(seq, &S) != MIPS_OK || d < 1 || d > MIPS_EMBEDDING_D_MAX) return 0;
+  return pool_bytes(S, d);
+}
+
+int mips_pool_normalize(const mips_sequences* seq, int32_t d, int32_t dtype, const mips_rows* x, int32_t normalize,
+                        void* vectors, float* mean, float* norm, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  PoolArgs A{};
+  if (const int rc = check_sequences(seq, &A.S)) return rc;
+  if (d < 1) return MIPS_ERR_INVALID_ARG;
+  if (d > MIPS_EMBEDDING_D_MAX || (dtype != MIPS_F32 && dtype != MIPS_BF16)) return MIPS_ERR_UNSUPPORTED;
+  if (const int rc = check_rows(x, A.S, d, dtype, &A.x)) return rc;
+  const int E = elem_bytes(dtype);
+  const bool joins = pool_joins(A.S);
+  if (!vectors || !mean || !norm || !aligned(vectors, E) || !aligned(mean, 4) || !aligned(norm, 4) ||
+      !aligned(workspace, 256) || (joins && !workspace))
+    return MIPS_ERR_INVALID_ARG;
+  if (joins && workspace_bytes < pool_bytes(A.S, d)) return MIPS_ERR_WORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  A.d = d;
+  A.lanes = pool_lanes(d);
+  A.normalize = normalize != 0;
+  A.chunk = pool_chunk(A.S);
+  A.chunks = (uint32_t)(((uint64_t)A.S.n + A.chunk - 1) / A.chunk);
+  A.part = (float*)workspace;
+  A.vectors = vectors;
+  A.mean = mean;
+  A.norm = norm;
+  const int64_t step = 16 / E;
+  const bool vec = d % 8 == 0 && A.x.row % step == 0 && A.x.extra % step == 0 && aligned(A.x.p, 16) && aligned(vectors, 16);
+  if (A.chunks) {
+    const dim3 grid((A.chunks + kPoolWaves - 1) / kPoolWaves);
+    if (dtype == MIPS_F32)
+      hipLaunchKernelGGL((vec ? pool_kernel<float, true> : pool_kernel<float, false>), grid, dim3(kPoolThreads), 0, s, A);
+    else
+      hipLaunchKernelGGL((vec ? pool_kernel<__bf16, true> : pool_kernel<__bf16, false>), grid, dim3(kPoolThreads), 0, s, A);
+    if (const int rc = check_launch()) return rc;
+  }
+  if (joins) {
+    if (dtype == MIPS_F32) hipLaunchKernelGGL(pool_join_kernel<float>, dim3(A.S.b), dim3(kPoolThreads), 0, s, A);
+    else hipLaunchKernelGGL(pool_join_kernel<__bf16>, dim3(A.S.b), dim3(kPoolThreads), 0, s, A);
+    return check_launch();
+  }
+  return MIPS_OK;
+}
+
+int mips_pool_normalize_backward(const mips_sequences* seq, int32_t d, int32_t dtype, const void* grad,
+                                 int64_t grad_stride, int32_t normalize, const float* mean, const float* norm,
+                                 void* grad_x, void* stream) {
+  PoolArgs A{};
+  if (const int rc = check_sequences(seq, &A.S)) return rc;
+  if (d < 1 || grad_stride < d) return MIPS_ERR_INVALID_ARG;
+  if (d > MIPS_EMBEDDING_D_MAX || (dtype != MIPS_F32 && dtype != MIPS_BF16)) return MIPS_ERR_UNSUPPORTED;
+  const int E = elem_bytes(dtype);
+  if (!grad || !mean || !norm || (A.S.n > 0 && !grad_x) || !aligned(grad, E) || !aligned(mean, 4) || !aligned(norm, 4) ||
+      !aligned(grad_x, E))
+    return MIPS_ERR_INVALID_ARG;
+  if (A.S.n == 0) return MIPS_OK;
+  A.d = d;
+  A.lanes = pool_lanes(d);
+  A.normalize = normalize != 0;
+  A.mean = (float*)mean;
+  A.norm = (float*)norm;
+  A.grad = grad;
+  A.grad_stride = grad_stride;
+  A.dx = grad_x;
+  A.chunk = 32;  // rows that share one row's gradient; more leave too few waves
+  while (A.chunk < 1024 && A.S.n / A.chunk > 65536) A.chunk *= 2;
+  A.chunks = (uint32_t)(((uint64_t)A.S.n + A.chunk - 1) / A.chunk);
+  const bool vec = d % 8 == 0 && aligned(grad_x, 16);
+  const dim3 grid((A.chunks + kPoolWaves - 1) / kPoolWaves);
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == MIPS_F32)
+    hipLaunchKernelGGL((vec ? pool_grad_kernel<float, true> : pool_grad_kernel<float, false>), grid, dim3(kPoolThreads), 0, s, A);
+  else
+    hipLaunchKernelGGL((vec ? pool_grad_kernel<__bf16, true> : pool_grad_kernel<__bf16, false>), grid, dim3(kPoolThreads), 0, s, A);
+  return check_launch();
+}
+
+}  // extern "C"

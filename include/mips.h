@@ -16,7 +16,10 @@
  * mips_merge_topk and mips_merge_interests (merges of sorted result lists);
  * mips_type_bitmap (per-type exclusion bitmaps); status strings and a timing hook.
  * For training and evaluation: mips_logprobs and its gradient
- * mips_logprobs_backward; mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm.
+ * mips_logprobs_backward; mips_embedding_lookup and mips_embedding_grad, mips_clip_grad_norm. For
+ * a user tower that reads a history of events: mips_gated_scan with its gradient
+ * mips_gated_scan_backward and its form for single events mips_gated_step, mips_dropout,
+ * mips_pool_normalize and mips_pool_normalize_backward.
  *
  * Conventions shared by every entry point:
  *  - All buffers are caller-owned (except the static scratch array of
@@ -506,6 +509,141 @@ MIPS_API int mips_logprobs_backward(const void *queries, int64_t query_stride, i
                                     const float *grad_entropy, void *grad_queries,
                                     void *grad_items, float *grad_bias, void *workspace,
                                     size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Histories: the user tower's operators over sequences of events. The conventions of the training
+ * entry points hold. A sequence's rows come in one of three forms:
+ *   dense    [b, t, d]: b sequences of t rows (offsets and lengths NULL);
+ *   padded   the same with lengths, int32 or int64 [b] on the device, clamped to [0, t]: rows behind
+ *            a sequence's length are padding;
+ *   packed   [n, d], sequence s having the rows offsets[s] .. offsets[s + 1] - 1: offsets int32
+ *            or int64 [b + 1] on the device, not decreasing, in [0, n]. Rows before the first
+ *            offset and behind the last one are padding. Offsets outside [0, n] are clamped;
+ *            decreasing ones give meaningless results (no access leaves the buffers).
+ * Padding is never read as data (it may hold anything, NaN included); in outputs it is 0.
+ */
+typedef struct mips_sequences {
+  int32_t b;           /* sequences, 1 .. MIPS_B_MAX */
+  int32_t index_bits;  /* 32 or 64, of offsets or lengths */
+  int64_t t;           /* dense and padded: rows a sequence, >= 1; b * t <= MIPS_TOKENS_MAX */
+  int64_t n;           /* packed: rows, 0 .. MIPS_TOKENS_MAX */
+  const void *offsets; /* device, or NULL */
+  const void *lengths; /* device, or NULL; not with offsets */
+} mips_sequences;
+
+/* An input tensor over such rows: unit stride along d, row_stride >= d elements from a row to the
+ * next one, seq_stride >= d (dense and padded) from a sequence to the next one. */
+typedef struct mips_rows {
+  const void *data; /* device */
+  int64_t row_stride;
+  int64_t seq_stride;
+} mips_rows;
+
+/*
+ * mips_gated_scan -- a gated linear recurrence along each sequence, per channel, in binary32:
+ *   h_r = a_r h_{r-1} + b_r x_r,  a = sigmoid(forget),  b = sigmoid(gate), or 1 - a without a gate,
+ * from initial (or 0) before the first row. Rows are cut into tiles whose states are joined in an
+ * order that follows from the sizes alone: the same call gives the same bits. A state that is not
+ * finite makes those behind it in its sequence and channel not finite.
+ *   x, forget, gate   rows of dtype MIPS_F32 or MIPS_BF16; gate may be NULL.  d 1 .. 16384.
+ *   initial      device float [b, d] or NULL.
+ *   states       device, contiguous rows of dtype in the layout of the input ([b, t, d] or [n, d]):
+ *                every h, rounded once; or NULL.
+ *   last         device float [b, d]: the state behind the last row; initial (or 0) without rows.
+ *   carries      device float [mips_gated_scan_carries(seq, d), d]: states between tiles, for the
+ *                gradient; may be NULL where that is 0. The number follows from the sizes alone.
+ *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0 for unsupported
+ *                sizes), may be NULL where there are no carries. Calls that share one must be ordered.
+ * Rows whose elements lie in aligned groups of four (d, strides and pointers) move so, others one by one.
+ * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, index_bits, d, b or
+ * rows above their limits), WORKSPACE, HIP.
+ */
+MIPS_API int64_t mips_gated_scan_carries(const mips_sequences *seq, int32_t d);
+MIPS_API size_t mips_gated_scan_workspace_size(const mips_sequences *seq, int32_t d);
+MIPS_API int mips_gated_scan(const mips_sequences *seq, int32_t d, int32_t dtype, const mips_rows *x,
+                             const mips_rows *forget, const mips_rows *gate, const float *initial,
+                             void *states, float *last, float *carries, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * mips_gated_scan_backward -- the gradient of mips_gated_scan. With G the gradient of the states and,
+ * added at a sequence's last row, of the last one, D_r = G_r + a_{r+1} D_{r+1}:
+ *   grad_x = D b,  grad_forget = D (h_{r-1} - x) a (1 - a) without a gate,  D h_{r-1} a (1 - a)
+ *   and grad_gate = D x b (1 - b) with one,  grad_initial = a D at the first row (grad_last
+ *   without rows).
+ * States are computed again in binary32 from the inputs and the carries, not read.
+ *   seq .. initial, carries   as the forward call's (d, sizes and lengths decide the carries' places).
+ *   grad_states   rows of dtype or NULL; grad_last  device float [b, d] or NULL; one of them at least.
+ *   grad_x, grad_forget, grad_gate   device, contiguous rows of dtype, written whole (grad_gate
+ *                 with a gate only); grad_initial  device float [b, d] or NULL: not wanted.
+ *   workspace     as mips_gated_scan.
+ * Errors: as mips_gated_scan; INVALID_ARG without any gradient.
+ */
+MIPS_API int mips_gated_scan_backward(const mips_sequences *seq, int32_t d, int32_t dtype, const mips_rows *x,
+                                      const mips_rows *forget, const mips_rows *gate, const float *initial,
+                                      const mips_rows *grad_states, const float *grad_last,
+                                      const float *carries, void *grad_x, void *grad_forget, void *grad_gate,
+                                      float *grad_initial, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/*
+ * mips_gated_step -- the recurrence for single events against a table of states: for events e in
+ * order, with r = ids[e], state[r] = a_e state[r] + b_e x_e and out[e] = state[r]. Events of one row
+ * are applied one after another in their order. An id outside [0, rows) is padding: out[e] = 0.
+ *   x, forget, gate   device, [b, d] of dtype, strides >= d; gate may be NULL.
+ *   b            0 .. MIPS_EVENTS_MAX (0 enqueues nothing).
+ *   state        device float [rows, d], state_stride >= d.
+ *   out_state    device float [rows, d]: the rows that events name are written, others are left as
+ *                they are; either `state` itself with the same stride, or no overlap.
+ *   ids          device, int32 or int64 [b].
+ *   out          device, [b, d] contiguous of dtype.
+ * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, id_bits, d > 16384,
+ * b > MIPS_EVENTS_MAX), HIP.
+ */
+#define MIPS_EVENTS_MAX 65536
+MIPS_API int mips_gated_step(const void *x, int64_t x_stride, const void *forget, int64_t forget_stride,
+                             const void *gate, int64_t gate_stride, int32_t dtype, int32_t b, int32_t d,
+                             const float *state, int64_t state_stride, float *out_state, int64_t out_stride,
+                             int64_t rows, const void *ids, int32_t id_bits, void *out, void *stream);
+
+/*
+ * mips_dropout -- out = residual + (kept ? x * 65536 / (65536 - c) : 0), c = p * 65536 rounded to
+ * the nearest integer (p is taken in steps of 2^-16). Element i is kept if its 16 random bits are at
+ * least c: half-word i % 8, low halves first, of the four words of Philox4x32-10 with the counter
+ * (i / 8 mod 2^32, i / 8 / 2^32, offset mod 2^32, offset / 2^32) and the key (seed mod 2^32, seed / 2^32).
+ * The same call on the gradient is the gradient for x. Dropped elements count as 0 whatever they hold.
+ *   x, out       device, [n] of dtype; out may be x or residual.  n 0 .. 2^40.
+ *   p            0 .. 1; all elements are dropped at 1.
+ *   counter      device uint64 [1], added to the offset (mod 2^64) when the kernel runs, or NULL: a
+ *                captured graph draws new numbers when it is replayed with another value there.
+ *   residual     device, [n] of dtype, or NULL.
+ * Errors: INVALID_ARG (NULL, n, p, alignment), UNSUPPORTED (dtype, n), HIP.
+ */
+MIPS_API int mips_dropout(const void *x, int32_t dtype, int64_t n, double p, uint64_t seed, uint64_t offset,
+                          const uint64_t *counter, const void *residual, void *out, void *stream);
+
+/*
+ * mips_pool_normalize -- per sequence the mean m of its rows (0 without rows), and, with normalize,
+ * m / sqrt(max(sum m^2, 1e-12)) as mips_l2_normalize's rows. Sums in binary32, in an order that
+ * follows from sizes, offsets and lengths.
+ *   x            rows of dtype MIPS_F32 or MIPS_BF16.  d 1 .. 16384.
+ *   vectors      device, [b, d] contiguous of dtype; mean device float [b, d]; norm device float
+ *                [b]: the root (1 without normalize). The latter two are what the gradient needs.
+ *   workspace    device, 256-byte aligned, mips_pool_workspace_size bytes (0 for unsupported sizes).
+ * mips_pool_normalize_backward -- its gradient: with g that of the vectors and u = m / norm,
+ *   grad_x = (g - u (u . g)) / norm / rows of the sequence (g / norm / rows where the sum is below
+ *   1e-12; g / rows without normalize), one row for all of a sequence's.
+ *   grad         device, [b, d] of dtype, grad_stride >= d.
+ *   grad_x       device, contiguous rows of dtype, written whole.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP as above.
+ */
+MIPS_API size_t mips_pool_workspace_size(const mips_sequences *seq, int32_t d);
+MIPS_API int mips_pool_normalize(const mips_sequences *seq, int32_t d, int32_t dtype, const mips_rows *x,
+                                 int32_t normalize, void *vectors, float *mean, float *norm, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+MIPS_API int mips_pool_normalize_backward(const mips_sequences *seq, int32_t d, int32_t dtype, const void *grad,
+                                          int64_t grad_stride, int32_t normalize, const float *mean,
+                                          const float *norm, void *grad_x, void *stream);
 
 /*
  * mips_set_timing_events -- profiling hook (host, per calling thread). When both are

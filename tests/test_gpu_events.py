@@ -1,0 +1,135 @@
+"""The recurrence for single events against a table of states, against a plain loop in 64 bits
+(bounds: histories_check; an event's state has been through as many rows as its row had events)."""
+import numpy as np
+import pytest
+import torch
+
+import exact_inner_product_amd as mips
+from tests import histories_check as hc
+from tests.histories_check import DT
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return torch.device("cuda:0")
+
+
+def make(kind, b, v, d, dtype, gate, seed=0):
+    rng = np.random.default_rng(seed + b + v + d)
+    f32 = lambda *s, m=0.0, k=1.0: torch.from_numpy((rng.standard_normal(s) * k + m).astype(np.float32))  # noqa: E731
+    if kind == "one":
+        rows = np.full(b, v // 2)
+    elif kind == "pairs":
+        rows = np.arange(b) // 2 % v
+    elif kind == "few":
+        rows = rng.integers(0, min(v, 5), b)
+    elif kind == "padded":
+        rows = rng.integers(-3, v + 3, b)
+    else:
+        rows = rng.integers(0, v, b)
+    return dict(x=f32(b, d).to(DT[dtype]), forget=f32(b, d, m=1.0, k=2.0).to(DT[dtype]),
+                gate=f32(b, d, k=2.0).to(DT[dtype]) if gate else None, state=f32(v, d), rows=torch.from_numpy(rows))
+
+
+def reference(c):
+    x, f = c["x"].double().numpy(), c["forget"].double().numpy()
+    a, _, ka, w, _, kb = hc.gates(f, None if c["gate"] is None else c["gate"].double().numpy())
+    table = c["state"].double().numpy().copy()
+    err, mag = np.zeros_like(table), np.abs(table)
+    h, he = np.zeros_like(x), np.zeros_like(x)
+    for e, r in enumerate(c["rows"].tolist()):
+        if not 0 <= r < len(table):
+            continue
+        err[r] = a[e] * err[r] + (np.maximum(ka[e], kb[e]) + 4) * hc.U * (a[e] * mag[r] + w[e] * np.abs(x[e]))
+        mag[r] = a[e] * mag[r] + w[e] * np.abs(x[e])
+        table[r] = a[e] * table[r] + w[e] * x[e]
+        h[e], he[e] = table[r], err[r] + 1e-36
+    return h, he, table, err
+
+
+CASES = [("any", 1, 1, 1), ("any", 16, 1000, 64), ("any", 1000, 300, 128), ("padded", 300, 100, 33), ("few", 700, 20, 16),
+         ("one", 900, 3, 128), ("pairs", 4096, 2048, 16), ("any", 513, 60, 260), ("padded", 5, 2, 1024), ("any", 64, 10, 4),
+         ("one", 3000, 9, 20), ("few", 5000, 5, 8), ("any", 20000, 700, 8), ("any", 65536, 100000, 4), ("one", 65536, 2, 16)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,b,v,d", CASES)
+def test_step(kind, b, v, d, dtype):
+    dev = _dev()
+    print(f"step {kind} b={b} v={v} d={d} {dtype}", flush=True)
+    for gate in (False, True):
+        c = make(kind, b, v, d, dtype, gate)
+        p = {k: None if t is None else t.to(dev) for k, t in c.items()}
+        h, he, table, te = reference(c)
+        kept = p["state"].clone()
+        into = torch.full_like(kept, 7.0)
+        got = mips.gated_step(p["x"], p["forget"], p["state"], p["rows"].to(torch.int32), p["gate"], out=into)
+        assert torch.equal(p["state"], kept)
+        hc.within(got, h, he, "states")
+        named = torch.zeros(v, dtype=torch.bool)
+        named[[r for r in c["rows"].tolist() if 0 <= r < v]] = True
+        assert (into[~named.to(dev)] == 7.0).all()      # rows without an event are left as they were
+        hc.within(into[named.to(dev)], table[named.numpy()], te[named.numpy()] + 1e-36, "table")
+        again = mips.gated_step(p["x"], p["forget"], p["state"], p["rows"], p["gate"])  # in place, int64
+        assert torch.equal(again, got) and torch.equal(p["state"][named.to(dev)], into[named.to(dev)])
+        assert torch.equal(p["state"][~named.to(dev)], kept[~named.to(dev)])
+
+
+def test_steps_make_the_scan():
+    """A history event by event ends in the states of the scan over it, to their bounds."""
+    dev = _dev()
+    b, t, d = 50, 30, 64
+    rng = np.random.default_rng(0)
+    x, f, g = (torch.from_numpy(rng.standard_normal((b, t, d)).astype(np.float32)) for _ in range(3))
+    want = mips.gated_scan(x.to(dev), f.to(dev), g.to(dev))
+    state = torch.zeros(80, d, device=dev)
+    rows = torch.randperm(80, device=dev)[:b]
+    steps = [mips.gated_step(x[:, i].to(dev), f[:, i].to(dev), state, rows, g[:, i].to(dev)) for i in range(t)]
+    flat = [v.double().numpy().reshape(-1, d) for v in (x, f, g)]
+    _, e, _, le = hc.scan(*flat, [(s * t, s * t + t) for s in range(b)], None)
+    assert (np.abs((torch.stack(steps, 1) - want.states).cpu().double().numpy()).reshape(-1, d) <= 2 * e).all()
+    assert (np.abs((state[rows] - want.last).cpu().double().numpy()) <= 2 * le).all()
+
+
+def test_strides_and_alignment():
+    dev = _dev()
+    for dtype in ("f32", "bf16"):
+        c = make("any", 200, 50, 64, dtype, True)
+        p = {k: t.to(dev) for k, t in c.items()}
+        first = p["state"].clone()
+        want = mips.gated_step(p["x"], p["forget"], first, p["rows"], p["gate"])
+        for k, shift in ((4, 4), (3, 1)):
+            cut = []
+            for t in (p["x"], p["forget"], p["gate"], p["state"]):
+                big = torch.full((t.shape[0], t.shape[1] + k + 1), float("nan"), dtype=t.dtype, device=dev)
+                cut.append(big[:, shift:shift + t.shape[1]])
+                cut[-1].copy_(t)
+            got = mips.gated_step(cut[0], cut[1], cut[3], p["rows"], cut[2])
+            assert torch.equal(got, want) and torch.equal(cut[3], first)
+        got = mips.gated_step(p["x"], p["forget"], p["state"].clone(), p["rows"].repeat_interleave(2)[::2], p["gate"])
+        assert torch.equal(got, want)
+
+
+def test_offsets_past_32_bits():
+    """Rows beyond 2^32 bytes and 2^31 elements of a table."""
+    dev = _dev()
+    v, d = 9_000_000, 256
+    table = torch.empty(v, d, device=dev)
+    rows = torch.tensor([v - 1, 3, 8_400_001, v - 1], device=dev)
+    table[rows] = 2.0
+    x, f = torch.ones(4, d, device=dev), torch.zeros(4, d, device=dev)
+    h = mips.gated_step(x, f, table, rows)
+    assert h[:, 0].tolist() == [1.5, 1.5, 1.5, 1.25] and table[rows, d - 1].tolist() == [1.25, 1.5, 1.5, 1.25]
+
+
+def test_autograd_notices_the_table():
+    dev = _dev()
+    t = torch.ones(30, 8, device=dev, requires_grad=True)
+    state = t * 1.0
+    y = (state * state).sum()
+    mips.gated_step(torch.ones(2, 8, device=dev), torch.ones(2, 8, device=dev), state.detach(), torch.tensor([0, 1], device=dev))
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        y.backward()

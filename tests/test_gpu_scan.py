@@ -1,0 +1,263 @@
+"""The gated recurrence over sequences and its gradient against a plain loop in 64 bits; the bounds
+are derived in histories_check."""
+import numpy as np
+import pytest
+import torch
+
+import exact_inner_product_amd as mips
+from tests import histories_check as hc
+from tests.histories_check import DT
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return torch.device("cuda:0")
+
+
+def _lengths(kind, b, t, rng):
+    n = rng.integers(0, t + 1, b)
+    if kind == "none":
+        n[:] = 0
+    elif kind == "ends":
+        n[0], n[-1] = 0, t
+    elif kind == "holes":
+        n[rng.random(b) < 0.6] = 0
+    return n
+
+
+def make(layout, b, t, d, dtype, gate, initial, seed=0, lens="ends"):
+    """Inputs on the CPU: a dict of tensors and how they are laid out."""
+    rng = np.random.default_rng(seed + b * 1000 + t * 10 + d)
+    c = dict(layout=layout, b=b, t=t, d=d, lengths=None, offsets=None)
+    shape = (b, t, d)
+    if layout == "padded":
+        c["lengths"] = torch.from_numpy(_lengths(lens, b, t, rng))
+    if layout == "packed":
+        n = _lengths(lens, b, t, rng)
+        before, after = (3, 2) if lens == "ends" else (0, 0)  # rows of no sequence
+        off = before + np.concatenate([[0], np.cumsum(n)])
+        c["offsets"] = torch.from_numpy(off)
+        shape = (int(off[-1]) + after, d)
+    t32 = lambda *s, m=0.0, k=1.0: torch.from_numpy((rng.standard_normal(s) * k + m).astype(np.float32))  # noqa: E731
+    c["x"] = t32(*shape).to(DT[dtype])
+    c["forget"] = t32(*shape, m=1.5, k=2.0).to(DT[dtype])
+    c["gate"] = t32(*shape, k=2.0).to(DT[dtype]) if gate else None
+    c["initial"] = t32(b, d) if initial else None
+    c["gs"], c["gl"] = t32(*shape).to(DT[dtype]), t32(b, d)
+    c["seqs"] = hc.spans(layout, shape, c["lengths"], c["offsets"])
+    return c
+
+
+def flat(v):
+    return None if v is None else v.double().numpy().reshape(-1, v.shape[-1])
+
+
+def place(c, dev, index=torch.int32):
+    """The case on the GPU."""
+    out = {k: (v.to(dev) if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    for k in ("lengths", "offsets"):
+        out[k] = None if out[k] is None else out[k].to(index)
+    return out
+
+
+def run(c, dev, states=True, grads=("gs", "gl"), index=torch.int32):
+    p = place(c, dev, index)
+    at = dict(lengths=p["lengths"], offsets=p["offsets"], initial=p["initial"])
+    f = mips.gated_scan(p["x"], p["forget"], p["gate"], states=states, **at)
+    g = mips.gated_scan_backward(p["gs"] if "gs" in grads else None, p["gl"] if "gl" in grads else None, p["x"], p["forget"],
+                                 p["gate"], f, **at)
+    return f, g
+
+
+def check(c, f, g, grads=("gs", "gl")):
+    x, ff, gg, init = (flat(c[k]) for k in ("x", "forget", "gate", "initial"))
+    h, e, last, le = hc.scan(x, ff, gg, c["seqs"], init)
+    if f.states is not None:
+        assert f.states.shape == c["x"].shape and f.states.dtype == c["x"].dtype
+        pad = np.ones(len(x), dtype=bool)
+        for lo, hi in c["seqs"]:
+            pad[lo:hi] = False
+        assert not f.states.reshape(-1, c["d"])[torch.from_numpy(pad).to(f.states.device)].any()
+        hc.within(f.states, h, e, "states")
+    hc.within(f.last, last, le, "last")
+    want = hc.scan_grad(x, ff, gg, c["seqs"], init, flat(c["gs"]) if "gs" in grads else None, flat(c["gl"]) if "gl" in grads else None)
+    for name, got, w in zip(("grad_x", "grad_forget", "grad_gate", "grad_initial"), g, want):
+        if got is None:
+            assert (name == "grad_gate" and gg is None) or (name == "grad_initial" and init is None)
+            continue
+        hc.within(got, w[0], w[1], name)
+
+
+CASES = [
+    # layout, b, t, d
+    ("dense", 1, 1, 1), ("dense", 3, 1, 128), ("dense", 300, 1, 16), ("dense", 1, 2, 4), ("dense", 5, 7, 3),
+    ("dense", 1, 50, 64), ("dense", 40, 50, 16), ("dense", 9, 127, 128), ("dense", 4, 128, 132), ("dense", 4, 129, 128),
+    ("dense", 2, 300, 100), ("dense", 3, 1000, 16), ("dense", 1, 2500, 30), ("dense", 2, 1500, 260), ("dense", 1, 700, 64),
+    ("padded", 1, 1, 8), ("padded", 7, 20, 33), ("padded", 30, 127, 128), ("padded", 6, 400, 64), ("padded", 3, 900, 128),
+    ("padded", 500, 3, 16), ("packed", 1, 1, 16), ("packed", 1, 300, 128), ("packed", 40, 60, 100), ("packed", 12, 500, 128),
+    ("packed", 2000, 3, 32), ("packed", 3, 2500, 16), ("packed", 30, 200, 1), ("packed", 5, 700, 260),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout,b,t,d", CASES)
+def test_scan(layout, b, t, d, dtype):
+    dev = _dev()
+    for gate, initial in ((False, False), (True, True)):
+        print(f"scan {layout} b={b} t={t} d={d} {dtype} gate={gate} initial={initial}", flush=True)
+        c = make(layout, b, t, d, dtype, gate, initial)
+        check(c, *run(c, dev))
+
+
+@pytest.mark.parametrize("lens", ["none", "holes"])
+@pytest.mark.parametrize("layout,b,t,d", [("padded", 9, 40, 64), ("padded", 9, 400, 64), ("packed", 9, 40, 64),
+                                          ("packed", 3000, 9, 128), ("packed", 200, 400, 20)])
+def test_sequences_without_rows(layout, b, t, d, lens):
+    dev = _dev()
+    print(f"scan {lens} {layout} b={b} t={t} d={d}", flush=True)
+    c = make(layout, b, t, d, "f32", True, True, lens=lens)
+    check(c, *run(c, dev, index=torch.int64))
+    c = make(layout, b, t, d, "bf16", False, False, lens=lens)
+    check(c, *run(c, dev))
+
+
+@pytest.mark.parametrize("layout,b,t,d", [("dense", 3, 40, 64), ("dense", 2, 600, 128), ("padded", 8, 200, 100), ("packed", 8, 200, 64)])
+def test_parts_of_the_gradient(layout, b, t, d):
+    """Only the last state's gradient, only the states'; without states the last ones stay the same."""
+    dev = _dev()
+    print(f"parts {layout} b={b} t={t} d={d}", flush=True)
+    c = make(layout, b, t, d, "bf16", False, True)
+    f, g = run(c, dev)
+    for grads in (("gl",), ("gs",)):
+        f2, g2 = run(c, dev, states=False, grads=grads)
+        assert f2.states is None and torch.equal(f2.last, f.last) and torch.equal(f2.carries, f.carries)
+        check(c, f2, g2, grads)
+
+
+@pytest.mark.parametrize("layout,b,t,d", [("dense", 2, 50, 64), ("dense", 3, 700, 64), ("padded", 5, 200, 128), ("packed", 5, 300, 36)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strides(layout, b, t, d, dtype):
+    """Views with wider rows, gaps between sequences, rows that are not aligned, turned and broadcast ones."""
+    dev = _dev()
+    print(f"strides {layout} b={b} t={t} d={d} {dtype}", flush=True)
+    c = make(layout, b, t, d, dtype, True, True)
+    p = place(c, dev)
+    at = dict(lengths=p["lengths"], offsets=p["offsets"], initial=p["initial"])
+    f = mips.gated_scan(p["x"], p["forget"], p["gate"], **at)
+    want = mips.gated_scan_backward(p["gs"], p["gl"], p["x"], p["forget"], p["gate"], f, **at)
+
+    def wide(v, k, shift):  # [..., rows + 3, d + k] cut back
+        big = torch.full((*v.shape[:-2], v.shape[-2] + 3, v.shape[-1] + k), float("nan"), dtype=v.dtype, device=dev)
+        cut = big[..., 1:1 + v.shape[-2], shift:shift + v.shape[-1]]
+        cut.copy_(v)
+        return cut
+
+    def turned(v):
+        return v.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+    for change in (lambda v: wide(v, 8, 4), lambda v: wide(v, 3, 1), turned):
+        x, fg, gt, gs = (change(p[k]) for k in ("x", "forget", "gate", "gs"))
+        f2 = mips.gated_scan(x, fg, gt, **at)
+        g2 = mips.gated_scan_backward(gs, p["gl"], x, fg, gt, f2, **at)
+        assert torch.equal(f2.states, f.states) and torch.equal(f2.last, f.last)
+        assert all(torch.equal(u, v) for u, v in zip(g2, want))
+    one = p["gs"].reshape(-1, d)[:1].expand(p["gs"].numel() // d, d).reshape(p["gs"].shape)
+    broad = p["gs"].reshape(-1, d)[:1].expand(*p["gs"].shape)
+    g2 = mips.gated_scan_backward(broad, p["gl"], p["x"], p["forget"], p["gate"], f, **at)
+    g3 = mips.gated_scan_backward(one.contiguous(), p["gl"], p["x"], p["forget"], p["gate"], f, **at)
+    assert all(torch.equal(u, v) for u, v in zip(g2, g3))
+
+
+@pytest.mark.parametrize("layout,b,t,d", [("padded", 6, 90, 64), ("padded", 4, 600, 128), ("packed", 6, 150, 64)])
+def test_padding_may_hold_anything(layout, b, t, d):
+    dev = _dev()
+    print(f"padding {layout} b={b} t={t} d={d}", flush=True)
+    c = make(layout, b, t, d, "bf16", True, True)
+    f, g = run(c, dev)
+    pad = torch.ones(c["x"].numel() // d, dtype=torch.bool)
+    for lo, hi in c["seqs"]:
+        pad[lo:hi] = False
+    for bad in (float("nan"), float("inf"), -float("inf"), torch.finfo(torch.bfloat16).min):
+        c2 = dict(c)
+        for k in ("x", "forget", "gate", "gs"):
+            c2[k] = c[k].clone()
+            c2[k].view(-1, d)[pad] = bad
+        f2, g2 = run(c2, dev)
+        assert torch.equal(f2.states, f.states) and torch.equal(f2.last, f.last)
+        assert all(torch.equal(u, v) for u, v in zip(g2, g))
+
+
+def test_nan_stays_in_its_sequence_and_channel():
+    dev = _dev()
+    for layout, b, t, d in (("dense", 6, 40, 64), ("dense", 4, 700, 64), ("packed", 7, 300, 128)):
+        print(f"nan {layout}", flush=True)
+        c = make(layout, b, t, d, "f32", False, False)
+        f, g = run(c, dev)
+        lo, hi = next((lo, hi) for lo, hi in c["seqs"][1:] if hi - lo > 5)
+        for bad in (float("nan"), float("inf")):
+            c2 = dict(c)
+            c2["x"] = c["x"].clone()
+            c2["x"].view(-1, d)[lo + 3, 5] = bad
+            f2, g2 = run(c2, dev)
+            h, h2 = f.states.view(-1, d), f2.states.view(-1, d)
+            hit = torch.zeros_like(h, dtype=torch.bool)
+            hit[lo + 3:hi, 5] = True
+            assert not torch.isfinite(h2[hit]).any() and torch.equal(h2[~hit], h[~hit])
+            # the gradient for x does not depend on x
+            assert torch.equal(g2[0], g[0])
+            same = ~hit
+            assert torch.equal(g2[1].view(-1, d)[same], g[1].view(-1, d)[same])
+
+
+def test_extreme_gates():
+    """Gates that are exactly 0 and 1: a state that is kept for good, and one that is replaced."""
+    dev = _dev()
+    for t in (90, 1500):
+        c = make("dense", 2, t, 64, "f32", False, True)
+        c["forget"][0] = float("inf")       # kept
+        c["forget"][1] = -float("inf")      # replaced
+        f, g = run(c, dev)
+        assert torch.equal(f.states[0].cpu(), c["initial"][0].expand(t, 64))
+        assert torch.equal(f.states[1].cpu(), c["x"][1])
+        assert not g[0][0].any() and not g[1].any()
+        want = c["gs"].clone()
+        want[1, -1] += c["gl"][1]
+        assert torch.equal(g[0][1].cpu(), want[1])
+        c["forget"][0], c["forget"][1] = 300.0, -300.0
+        f, _ = run(c, dev)
+        assert torch.equal(f.states[0].cpu(), c["initial"][0].expand(t, 64)) and torch.equal(f.states[1].cpu(), c["x"][1])
+
+
+def test_same_call_same_bits():
+    dev = _dev()
+    for layout, b, t, d in (("dense", 2, 9000, 64), ("packed", 700, 90, 128), ("dense", 1, 40000, 16)):
+        c = make(layout, b, t, d, "bf16", True, True)
+        f, g = run(c, dev)
+        for _ in range(4):
+            f2, g2 = run(c, dev)
+            assert torch.equal(f2.states, f.states) and torch.equal(f2.last, f.last) and torch.equal(f2.carries, f.carries)
+            assert all(torch.equal(u, v) for u, v in zip(g2, g))
+
+
+def test_broken_offsets_stay_in_bounds():
+    """Decreasing offsets and ones outside the rows: results are meaningless, neighbours are not touched."""
+    dev = _dev()
+    n, d = 1000, 64
+    big = torch.randn(3, n, d, device=dev)
+    for off in ([5, -7, 2000, 3, 10 ** 9, 600, 1000], [1000, 0], [0, 0, 0, 0], [-1, -1], [n + 5, n + 9], [900, 100, 900, 100]):
+        o = torch.tensor(off, dtype=torch.int32, device=dev)
+        print(f"offsets {off}", flush=True)
+        f = mips.gated_scan(big[0], big[1], offsets=o)
+        g = mips.gated_scan_backward(big[2], None, big[0], big[1], None, f, offsets=o)
+        p = mips.pool_normalize(big[0], offsets=o)
+        mips.pool_normalize_backward(p.vectors, big[0].shape, p, offsets=o)
+        torch.cuda.synchronize()
+        assert f.last.shape == (len(off) - 1, d) and g[0].shape == (n, d)
+    padded = torch.tensor([-5, 400, 7], dtype=torch.int64, device=dev)
+    x = torch.randn(3, 300, d, device=dev)
+    want = mips.gated_scan(x, x, lengths=torch.tensor([0, 300, 7], device=dev))
+    got = mips.gated_scan(x, x, lengths=padded)
+    assert torch.equal(got.states, want.states) and torch.equal(got.last, want.last)
