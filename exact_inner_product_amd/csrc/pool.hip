@@ -30,46 +30,6 @@ struct PoolArgs {
   void* dx;         // [n, d]
 };
 
-// The rows of sequence s: [*begin, *end) in the numbering of sequences.h.
-__device__ __forceinline__ void sequence_rows(const Sequences& S, int64_t s, uint32_t* begin, uint32_t* end) {
-  if (S.t) {
-    *begin = (uint32_t)s * S.t;
-    *end = *begin + (S.lengths ? index_at(S.lengths, S.wide, s, S.t) : S.t);
-  } else {
-    *begin = index_at(S.offsets, S.wide, s, S.n);
-    *end = index_at(S.offsets, S.wide, s + 1, S.n);
-    if (*end < *begin) *end = *begin;
-  }
-}
-
-// Calls f(s, begin, end) for the sequences with rows in [r0, r1), those of a wave together. Dense ones
-// come with rows of padding or none too, packed ones only with rows.
-template <typename F>
-__device__ __forceinline__ void for_sequences(const Sequences& S, uint32_t r0, uint32_t r1, F f) {
-  uint32_t begin, end;
-  if (S.t) {
-    for (uint32_t s = r0 / S.t; s < (uint32_t)S.b && s * S.t < r1; ++s) {
-      sequence_rows(S, s, &begin, &end);
-      f((int32_t)s, begin, end);
-    }
-    return;
-  }
-  const int lane = threadIdx.x & 63;
-  int64_t s0 = lower_bound(S, r0);
-  s0 = s0 > 0 ? s0 - 1 : 0;
-  for (; s0 < S.b; s0 += 64) {
-    begin = end = ~0u;
-    if (s0 + lane < S.b) sequence_rows(S, s0 + lane, &begin, &end);
-    uint64_t m = __ballot(begin < end && begin < r1 && end > r0);
-    while (m) {
-      const int k = __ffsll((unsigned long long)m) - 1;
-      m &= m - 1;
-      f((int32_t)(s0 + k), (uint32_t)__shfl((int)begin, k), (uint32_t)__shfl((int)end, k));
-    }
-    if ((uint32_t)__shfl((int)begin, 63) >= r1) break;  // this one and all behind it
-  }
-}
-
 // Eight channels of a row, 16-byte loads with VEC (bf16: one, f32: two).
 template <typename T, bool VEC>
 __device__ __forceinline__ void row8(const T* p, int live, float* v) {

@@ -10,28 +10,34 @@
 
 #include "sequences.h"
 
+// Products and sums are joined where fmaf says so and nowhere else: the variants for aligned and other
+// rows, compiled apart, give the same bits.
+#pragma clang fp contract(off)
+
 namespace mips {
 
-constexpr int kTileThreadRows = 4096;  // rows of a tile times lanes a row
-constexpr int kTileRowsMost = 1024;
+constexpr int kTileThreads = 512;
+constexpr int kLongRun = 8;  // rows of a thread: forward in bf16
+constexpr int kRun = 4;      // forward in f32, and backward, which have to hold more of each
 
-// Lanes a row (4 channels each) and their logarithm: 4, 8, 16 or 32, of widths up to 16, 32, 64, any.
+// Lanes a row (4 channels each): 4, 8, 16 or 32, of widths up to 16, 32, 64, any.
 inline int scan_lanes_log2(int32_t d) { return d > 64 ? 5 : d > 32 ? 4 : d > 16 ? 3 : 2; }
-inline int tile_rows(int32_t d) { return kTileThreadRows >> scan_lanes_log2(d); }
 
-// How a call's rows are cut. Dense sequences of at most a tile's rows lie whole in tiles of a
-// multiple of their length: no state passes between tiles. Else the tiles are chained.
+// How a call's rows are cut. Dense sequences that fit in a tile lie whole in tiles of a multiple of
+// their length: no state passes between tiles. Else the tiles are chained.
 struct Tiling {
   uint32_t rows;      // of a tile
   uint32_t tiles;
   uint32_t columns;   // tiles side by side along the channels
   int lanes_log2;
+  int threads;        // of a workgroup: 512 or 1024
   bool chained;
 };
-inline Tiling tiling_of(const Sequences& S, int32_t d) {
+inline Tiling tiling_of(const Sequences& S, int32_t d, int run, int threads) {
   Tiling T;
   T.lanes_log2 = scan_lanes_log2(d);
-  T.rows = (uint32_t)tile_rows(d);
+  T.threads = threads;
+  T.rows = (uint32_t)(threads * run) >> T.lanes_log2;
   const bool whole = S.t && S.t <= T.rows;
   if (whole) T.rows = T.rows / S.t * S.t;
   T.tiles = S.n ? (S.n + T.rows - 1) / T.rows : 1u;
@@ -40,6 +46,15 @@ inline Tiling tiling_of(const Sequences& S, int32_t d) {
   T.columns = ((uint32_t)d + width - 1) / width;
   return T;
 }
+// 512 threads by 4 rows each; twice the threads where that makes sequences lie whole in a tile.
+inline Tiling short_tiling(const Sequences& S, int32_t d) {
+  const Tiling T = tiling_of(S, d, kRun, kTileThreads), W = tiling_of(S, d, kRun, 2 * kTileThreads);
+  return T.chained && S.t && !W.chained ? W : T;
+}
+inline Tiling forward_tiling(const Sequences& S, int32_t d, int32_t dtype) {
+  return dtype == MIPS_BF16 ? tiling_of(S, d, kLongRun, kTileThreads) : short_tiling(S, d);
+}
+inline Tiling backward_tiling(const Sequences& S, int32_t d) { return short_tiling(S, d); }
 
 // ------------------------------------------------------------------------------ gates
 // sigmoid(v) and sigmoid(-v), each exact to a few units in the last place (1 - sigmoid(v) would
@@ -65,88 +80,239 @@ __device__ __forceinline__ void compose(float a0, float b0, float a1, float b1, 
 __device__ __forceinline__ float apply(float a, float b, float h) { return a < 0.0f ? b : fmaf(a, h, b); }
 
 // -------------------------------------------------------------------- chain of tiles
-// Each tile and channel has a 64-bit word: empty, the tile's own map (A, B), or, once it is known,
-// the state behind the tile. It is written and read with relaxed atomics of one word, value and
-// meaning together, so nothing else has to be ordered. Tiles are handed out by a counter, in the
-// chain's order: what a workgroup waits for belongs to workgroups that run already, each of which writes
-// its map before it waits, and the first tile waits for nothing; so every wait ends, whatever the
-// order in which the card starts workgroups.
+// Each tile and channel has a 64-bit word: empty, or the tile's map (A, B), a constant one where the
+// state is cut inside. So has each group of kGroup tiles, written by its last tile; when that knows the
+// state behind the group, it is written over the group's map, as a constant. Words are written and read with
+// relaxed atomics, value and meaning together, so nothing else has to be ordered.
 //
-// The state before a tile is always the same left fold, h <- A h + B over the maps since the nearest
-// known state, which is itself that fold: results do not depend on how far a tile had to look back.
-constexpr uint32_t kEmpty = 0xFFFFFFFFu;   // A of a word that is not written yet
-constexpr uint32_t kState = 0x80000000u;   // A of a word that holds a state
-constexpr int kWindow = 8;                 // words looked at together
+// Tiles are handed out by a counter, one a column of channels, in the chain's order: what a workgroup waits for
+// are words of tiles handed out before its own, to workgroups that run already. The first of the
+// unfinished tiles finds all it waits for, so every wait ends, whatever the order in which the card
+// starts workgroups. A tile's word is written before anything is waited for, a group's after a wait
+// for its tiles' words alone: no wait follows from another along the chain.
+//
+// The state before a tile is always the same fold, h <- A h + B over groups and then over tiles of its
+// own group: constants only cut it short. Results do not depend on what was known when.
+constexpr uint32_t kEmpty = 0xFFFFFFFFu;     // A of a word that is not written yet
+constexpr uint32_t kConstant = 0x80000000u;  // A of a constant map
+constexpr uint32_t kGroup = 16;
 
-__device__ __forceinline__ uint64_t chain_word(uint32_t a, float b) {
-  return ((uint64_t)a << 32) | __float_as_uint(b);
-}
-__device__ __forceinline__ void chain_put(uint64_t* w, uint64_t v) {
-  __hip_atomic_store(w, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+struct Chain {
+  uint64_t* tiles;   // the same for all threads, as the rest but `channel`: scalar registers
+  uint64_t* groups;
+  int64_t stride;    // from a tile's words to the next one's
+  uint32_t channel;
+};
+
+__device__ __forceinline__ void chain_put(uint64_t* w, float a, float b) {
+  // a product of gates has no sign; the sign that a NaN may have is taken away
+  const uint32_t m = a < 0.0f ? kConstant : (a == a ? __float_as_uint(a) : 0x7FC00000u);
+  __hip_atomic_store(w, ((uint64_t)m << 32) | __float_as_uint(b), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint64_t chain_get(const uint64_t* w) {
   return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint64_t chain_map(float a, float b) {
-  // a product of gates has no sign; the sign that a NaN may have is taken away
-  return chain_word(a == a ? __float_as_uint(a) : 0x7FC00000u, b);
-}
 
-// The state before tile `k` >= 1 of a chain whose words lie `stride` apart.
-__device__ __forceinline__ float chain_state(const uint64_t* words, int64_t stride, uint32_t k) {
-  uint64_t w[kWindow];
-  int64_t at = (int64_t)k - 1;
-  int64_t found = -1;
-  while (found < 0) {  // tile 0 holds a state: the walk ends there at the latest
-    const int64_t low = at - (kWindow - 1) > 0 ? at - (kWindow - 1) : 0;
+// A link of the chain, all threads of a workgroup together. Thread `i` below `channels` has its channel's map
+// (a, b) of tile k; it gets the state before the tile, or 0 if the tile needs none (its map is then taken as
+// the constant b). `source`: the tile that the state comes from, one that is constant because the sequence begins
+// there, or k; the same for all threads. The other threads fetch words with it: those of the
+// group's tiles and of the kGroup groups before it are asked for at once, so that a link costs one
+// trip to memory where nothing is late.
+template <int THREADS>
+__device__ __forceinline__ float chain_link(const Chain& C, uint32_t k, uint32_t source, int channels, float a, float b) {
+  __shared__ uint64_t tiles[kGroup][128], groups[kGroup][128];
+  constexpr int PARTS = THREADS / 128, EACH = kGroup / PARTS;
+  const int tid = threadIdx.x, i = tid & 127, part = tid >> 7;
+  const uint32_t group = k / kGroup, begin = group * kGroup, before = k - begin;
+  const bool closes = before == kGroup - 1;
+  const bool owner = tid < channels, needs = source < k;
+  if (!needs) a = kForgets;
+  if (owner) chain_put(C.tiles + k * C.stride + C.channel, a, b);
+  if (!needs && !closes) return 0.0f;
+  uint64_t* own = C.groups + group * C.stride + C.channel;
+  const uint32_t low = source > begin && !closes ? source - begin : 0u;  // tiles low .. before - 1 of the group
+  const uint32_t depth = group - min(source / kGroup, group);            // groups before it
+  const uint32_t asked = min(depth, kGroup);                             // at once, the nearest first
+  uint64_t tw[EACH], gw[EACH];
+  if (i < channels) {
 #pragma unroll
-    for (int j = 0; j < kWindow; ++j) w[j] = chain_get(words + (at - j > low ? at - j : low) * stride);
+    for (int j = 0; j < EACH; ++j) {
+      const uint32_t t = part + j * PARTS;
+      if (t >= low && t < before) tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
+      if (t < asked) gw[j] = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
+    }
 #pragma unroll
-    for (int j = 0; j < kWindow; ++j) {
-      if (found >= 0) continue;
-      const int64_t i = at - j > low ? at - j : low;
-      while ((uint32_t)(w[j] >> 32) == kEmpty) {
+    for (int j = 0; j < EACH; ++j) {
+      const uint32_t t = part + j * PARTS;
+      if (t < low || t >= before) continue;
+      while ((uint32_t)(tw[j] >> 32) == kEmpty) {
         __builtin_amdgcn_s_sleep(1);
-        w[j] = chain_get(words + i * stride);
+        tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
       }
-      if ((uint32_t)(w[j] >> 32) == kState) found = i;
-    }
-    if (found < 0) at = low - 1;
-  }
-  float h = 0.0f;
-  if (at == (int64_t)k - 1) {  // the words are at hand
-#pragma unroll
-    for (int j = kWindow - 1; j >= 0; --j) {
-      const int64_t i = at - j;
-      if (i < found) continue;
-      const uint32_t a = (uint32_t)(w[j] >> 32);
-      const float b = __uint_as_float((uint32_t)w[j]);
-      h = a == kState ? b : fmaf(__uint_as_float(a), h, b);
-    }
-    return h;
-  }
-  for (int64_t i0 = found; i0 < (int64_t)k; i0 += kWindow) {  // none of these is empty any more
-#pragma unroll
-    for (int j = 0; j < kWindow; ++j) w[j] = chain_get(words + (i0 + j < (int64_t)k ? i0 + j : i0) * stride);
-#pragma unroll
-    for (int j = 0; j < kWindow; ++j) {
-      if (i0 + j >= (int64_t)k) continue;
-      const uint32_t a = (uint32_t)(w[j] >> 32);
-      const float b = __uint_as_float((uint32_t)w[j]);
-      h = a == kState ? b : fmaf(__uint_as_float(a), h, b);
+      tiles[t][i] = tw[j];
     }
   }
-  return h;
+  __syncthreads();
+  float ga = 1.0f, gb = 0.0f, va = 0.0f, vb = 0.0f;  // of the group's tiles before this one, and with it
+  if (owner) {
+    for (uint32_t t = low; t < before; ++t) {
+      const uint32_t m = (uint32_t)(tiles[t][i] >> 32);
+      compose(ga, gb, m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)tiles[t][i]), &ga, &gb);
+    }
+    compose(ga, gb, a, b, &va, &vb);
+    if (closes) chain_put(own, va, vb);
+  }
+  if (!needs) return 0.0f;
+  if (asked == 0) return apply(ga, gb, 0.0f);
+  if (i < channels) {
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      const uint32_t t = part + j * PARTS;
+      if (t >= asked) continue;
+      while ((uint32_t)(gw[j] >> 32) == kEmpty) {
+        __builtin_amdgcn_s_sleep(1);
+        gw[j] = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
+      }
+      groups[t][i] = gw[j];
+    }
+  }
+  __syncthreads();
+  if (!owner) return 0.0f;
+  // back to the nearest constant (the source's group is one), and forward again
+  float v = 0.0f;
+  uint32_t t = 0;
+  while (t < asked && (uint32_t)(groups[t][i] >> 32) != kConstant) ++t;
+  if (t == asked && asked < depth) {  // further back than the words at hand
+    uint32_t from = group - asked;
+    uint64_t w;
+    do {
+      --from;
+      do w = chain_get(C.groups + from * C.stride + C.channel);
+      while ((uint32_t)(w >> 32) == kEmpty);
+    } while (from > group - depth && (uint32_t)(w >> 32) != kConstant);
+    for (; from < group - asked; ++from) {
+      w = chain_get(C.groups + from * C.stride + C.channel);
+      const uint32_t m = (uint32_t)(w >> 32);
+      v = apply(m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)w), v);
+    }
+  }
+  for (t = t < asked ? t + 1 : asked; t > 0; --t) {
+    const uint32_t m = (uint32_t)(groups[t - 1][i] >> 32);
+    v = apply(m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)groups[t - 1][i]), v);
+  }
+  if (closes && !(va < 0.0f)) chain_put(own, kForgets, apply(va, vb, v));
+  return apply(ga, gb, v);
 }
 
-// Empties the words and sets the counter to 0 (a kernel: a memset node replays wrongly in graphs).
-__global__ void chain_clear_kernel(uint64_t* words, uint64_t count, uint32_t* counter);
-
-// Workspace of a chained call: the counter, then the words [tiles][columns * width].
-inline size_t chain_bytes(const Tiling& T) {
-  return T.chained ? 256 + (size_t)T.tiles * T.columns * (4u << T.lanes_log2) * 8 : 0;
+// Workspace: the columns' counters (an atomic a tile on one address takes 12 ns, so they lie apart); of packed
+// rows, what is known of each (to the end of the last tile); of chained tiles the words of tiles and of
+// groups, [columns * width] each.
+constexpr int kCounterPitch = 64;
+struct ScanSpace {
+  uint32_t* counters;
+  int32_t* info;
+  uint64_t* words;
+  uint64_t count;  // of words
+  size_t bytes;
+};
+inline ScanSpace scan_space(const Sequences& S, const Tiling& T, void* workspace) {
+  ScanSpace W;
+  uint8_t* p = (uint8_t*)workspace;
+  W.counters = (uint32_t*)p;
+  p += (size_t)T.columns * kCounterPitch * 4;
+  W.info = S.offsets ? (int32_t*)p : nullptr;
+  if (S.offsets) p += ((size_t)T.tiles * T.rows * 4 + 255) / 256 * 256;
+  W.words = (uint64_t*)p;
+  W.count = T.chained ? (uint64_t)(T.tiles + (T.tiles + kGroup - 1) / kGroup) * T.columns * (4u << T.lanes_log2) : 0;
+  W.bytes = (size_t)(p - (uint8_t*)workspace) + W.count * 8;
+  return W;
 }
-int chain_clear(const Tiling& T, void* workspace, hipStream_t s);
+// The launch before a scan of packed or chained rows: empties the words, sets the counters to 0 (a
+// kernel: a memset node replays wrongly in graphs), describes packed rows, and writes rows of
+// `of_none` ([b, d]; NULL: not wanted) for packed sequences without rows: those of `as`, or 0.
+int scan_begin(const Sequences& S, const Tiling& T, const ScanSpace& W, int32_t d, const float* as, float* of_none,
+               hipStream_t s);
+
+// The tile of this workgroup, the block'th of a call, in its column; the same for all its threads.
+__device__ __forceinline__ uint32_t chain_ticket(uint32_t* counters, uint32_t column) {
+  __shared__ uint32_t ticket;
+  if (threadIdx.x == 0) ticket = atomicAdd(counters + column * kCounterPitch, 1u);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(ticket);
+}
+
+// --------------------------------------------------------- across a wave's two halves
+// v of the lane 32 lower or the lane itself, and of the lane itself or 32 higher: one instruction for
+// both, against two through LDS.
+__device__ __forceinline__ void halves(float v, float* low, float* high) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  *low = __uint_as_float(r[0]);
+  *high = __uint_as_float(r[1]);
+}
+
+// Of four channels, from each lane's run's map (ra, rb): that of the whole wave, (wa, wb), and that of the
+// wave's runs before the lane's, (ea, eb). BACK: the argument comes from the last run, not the first.
+// CUTS: some may be constant (six instructions to compose two of them, not two).
+template <bool BACK, bool CUTS>
+__device__ __forceinline__ void wave_maps(const float* ra, const float* rb, int lane, int lanes, float* ea, float* eb,
+                                          float* wa, float* wb) {
+  const int in = lane & 31;
+  const bool behind = BACK ? lane < 32 : lane >= 32;  // the other half's runs come before this one's
+  float xa[4], xb[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    xa[c] = ra[c];
+    xb[c] = rb[c];
+    ea[c] = 1.0f;
+    eb[c] = 0.0f;
+  }
+  if (lanes < 32) {
+    for (int o = lanes; o < 32; o <<= 1) {
+      const bool has = BACK ? in + o < 32 : in >= o;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float pa = BACK ? __shfl_down(xa[c], o, 32) : __shfl_up(xa[c], o, 32);
+        const float pb = BACK ? __shfl_down(xb[c], o, 32) : __shfl_up(xb[c], o, 32);
+        if (has) compose(pa, pb, xa[c], xb[c], &xa[c], &xb[c]);
+      }
+    }
+    const bool edge = BACK ? in + lanes >= 32 : in < lanes;
+    const int total = (BACK ? 0 : 32 - lanes) + (lane & (lanes - 1));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float pa = BACK ? __shfl_down(xa[c], lanes, 32) : __shfl_up(xa[c], lanes, 32);
+      const float pb = BACK ? __shfl_down(xb[c], lanes, 32) : __shfl_up(xb[c], lanes, 32);
+      if (!edge) {
+        ea[c] = pa;
+        eb[c] = pb;
+      }
+      xa[c] = __shfl(xa[c], total, 32);
+      xb[c] = __shfl(xb[c], total, 32);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float la, lb, ua, ub;
+    halves(xa[c], &la, &ua);
+    halves(xb[c], &lb, &ub);
+    const float oa = BACK ? ua : la, ob = BACK ? ub : lb, ta = BACK ? la : ua, tb = BACK ? lb : ub;
+    if (CUTS) {
+      compose(oa, ob, ta, tb, &wa[c], &wb[c]);
+      if (behind) compose(oa, ob, ea[c], eb[c], &ea[c], &eb[c]);
+    } else {
+      wa[c] = oa * ta;
+      wb[c] = fmaf(ta, ob, tb);
+      if (lanes == 32) {
+        ea[c] = behind ? oa : 1.0f;
+        eb[c] = behind ? ob : 0.0f;
+      } else if (behind) {
+        eb[c] = fmaf(ea[c], ob, eb[c]);
+        ea[c] = oa * ea[c];
+      }
+    }
+  }
+}
 
 // -------------------------------------------------------------------- four channels
 template <bool VEC>
@@ -175,10 +341,16 @@ template <> struct Raw<__bf16> {
   }
 };
 
+// Makes the compiler forget what it has computed from v or r, so that it does so again where it is needed
+// rather than keep it in registers.
+__device__ __forceinline__ uint32_t again(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 template <typename T>
-__device__ __forceinline__ void raw_zero(Raw<T>* r) {
+__device__ __forceinline__ void raw_again(Raw<T>* r) {
 #pragma unroll
-  for (unsigned c = 0; c < sizeof(r->v) / 4; ++c) r->v[c] = 0;
+  for (unsigned c = 0; c < sizeof(r->v) / 4; ++c) asm volatile("" : "+v"(r->v[c]));
 }
 // `live` channels (1 to 4) of a row at p; 4 and aligned with VEC.
 template <bool VEC>
@@ -198,6 +370,143 @@ __device__ __forceinline__ void raw_load(const __bf16* p, int live, Raw<__bf16>*
     r->v[1] = (live > 2 ? (uint32_t)u[2] : 0u) | (live > 3 ? (uint32_t)u[3] << 16 : 0u);
   }
 }
+// Rows of a run that are not inner ones of a sequence, a bit each, 8 a kind, in one register.
+struct Marks {
+  uint32_t bits;
+  __device__ __forceinline__ bool any() const { return bits != 0; }
+  __device__ __forceinline__ bool pad(int t) const { return (bits >> t) & 1u; }            // of no sequence: 0
+  __device__ __forceinline__ bool beyond(int t) const { return (bits >> (8 + t)) & 1u; }   // and not this tile's
+  __device__ __forceinline__ bool cut(int t) const { return (bits >> (16 + t)) & 1u; }     // pad, or a first row
+  __device__ __forceinline__ bool final(int t) const { return (bits >> (24 + t)) & 1u; }
+  __device__ __forceinline__ bool first(int t) const { return cut(t) && !pad(t); }
+};
+// The sequence of a row that has one.
+__device__ __forceinline__ int64_t row_sequence(const Sequences& S, const int32_t* packed, uint32_t r) {
+  return S.t ? r / S.t : (uint32_t)packed[r] >> 2;
+}
+template <int R>
+__device__ __forceinline__ Marks run_marks(const Sequences& S, const int32_t* packed, uint32_t r0, uint32_t rows,
+                                           uint32_t at) {
+  const uint32_t r = r0 + at;
+  uint32_t pad = 0, cut = 0, final = 0;
+  const uint32_t here = at < rows ? min(rows - at, (uint32_t)R) : 0u;
+  const uint32_t beyond = ((1u << R) - 1u) & ~((1u << here) - 1u);
+  if (!S.t) {
+#pragma unroll
+    for (int t = 0; t < R; t += 4) {
+      const i32x4_t v = *(const i32x4_t*)(packed + r + t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // (a row that broken offsets leave out has whatever lay there)
+        pad |= (uint32_t)((uint32_t)v[e] >= (uint32_t)S.b << 2) << (t + e);
+        cut |= (uint32_t)(v[e] & kFirst) << (t + e);
+        final |= (uint32_t)(v[e] & kFinal) >> 1 << (t + e);
+      }
+    }
+  } else {
+    uint32_t s = r / S.t, pos = r - s * S.t;
+    if (!S.lengths) {
+      if (pos > 0 && pos + R < S.t && !beyond) return Marks{0u};
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        cut |= (uint32_t)(pos == 0) << t;
+        pos = pos + 1 == S.t ? 0 : pos + 1;
+        final |= (uint32_t)(pos == 0) << t;
+      }
+    } else {
+      uint32_t len = 0;
+      for (uint32_t t = 0; t < here; ++t) {
+        if (t == 0 || pos == 0) len = index_at(S.lengths, S.wide, s, S.t);
+        cut |= (uint32_t)(pos == 0) << t;
+        pad |= (uint32_t)(pos >= len) << t;
+        final |= (uint32_t)(pos + 1 == len) << t;
+        if (++pos == S.t) {
+          pos = 0;
+          ++s;
+        }
+      }
+    }
+  }
+  pad |= beyond;
+  final &= ~pad;
+  return Marks{pad | beyond << 8 | (cut | pad) << 16 | final << 24};
+}
+
+// The tile where the sequence of row r0 begins, the first of tile k, in whose chain k's state is then found;
+// k itself if no sequence goes on from the tile before.
+__device__ __forceinline__ uint32_t chain_source(const Sequences& S, const int32_t* packed, uint32_t r0, uint32_t rows, uint32_t k) {
+  if (k == 0) return 0;
+  uint32_t begin, end;
+  int64_t s;
+  if (S.t) {
+    s = r0 / S.t;
+  } else {
+    const uint32_t v = (uint32_t)packed[r0];
+    if (v >= (uint32_t)S.b << 2) return k;  // padding
+    s = v >> 2;
+  }
+  sequence_rows(S, s, &begin, &end);
+  return begin < r0 && r0 < end ? begin / rows : k;
+}
+// Backward: the step of the tile where the sequence of row r, the last of step k's tile, ends. Step 0 is the last tile.
+__device__ __forceinline__ uint32_t chain_source_back(const Sequences& S, const int32_t* packed, uint32_t r, uint32_t rows,
+                                                      uint32_t tiles, uint32_t k) {
+  if (k == 0) return 0;
+  uint32_t begin, end;
+  int64_t s;
+  if (S.t) {
+    s = r / S.t;
+  } else {
+    const uint32_t v = (uint32_t)packed[r];
+    if (v >= (uint32_t)S.b << 2) return k;
+    s = v >> 2;
+  }
+  sequence_rows(S, s, &begin, &end);
+  return begin <= r && r + 1 < end ? tiles - 1 - (end - 1) / rows : k;
+}
+
+// A run of a tensor: rows `row` .. of the tile [r0, r0 + rows), channels `channel` .. of those from c0
+// on. There is no branch around a load: for rows beyond the tile and padding one is loaded that is
+// there (the run's first, or the tile's last), and not looked at.
+//
+// Sequences without gaps between them, tiles below 2^31 bytes: a scalar address and 32-bit offsets.
+template <bool VEC, typename T, int R>
+__device__ __forceinline__ void load_flat(const Rows& src, uint32_t r0, uint32_t rows, uint32_t row, int c0,
+                                          uint32_t channel, int live, Marks skip, Raw<T> (&out)[R]) {
+  const uint8_t* base = (const uint8_t*)((const T*)src.p + (int64_t)r0 * src.row + c0);
+  const uint32_t bytes = (uint32_t)src.row * sizeof(T);
+  const uint32_t first = (row < rows ? row : rows - 1) * bytes + channel * (uint32_t)sizeof(T);
+  uint32_t at = first;
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    raw_load<VEC>((const T*)(base + (skip.pad(t) ? first : at)), live, &out[t]);
+    at += bytes;
+  }
+}
+inline bool rows_flat(const Rows& r, const Tiling& T, int32_t dtype) {
+  return r.extra == 0 && (int64_t)T.rows * r.row * elem_bytes(dtype) < int64_t(1) << 31;
+}
+// Any others, dense ones (packed rows have no gaps and a bounded stride).
+template <bool VEC, typename T, int R>
+__device__ __forceinline__ void load_gaps(const Sequences& S, const Rows& src, uint32_t r0, uint32_t rows, uint32_t row,
+                                          int c0, uint32_t channel, int live, Marks skip, Raw<T> (&out)[R]) {
+  const uint32_t r = r0 + (row < rows ? row : rows - 1), s = r / S.t;
+  const T* p = (const T*)src.p + (int64_t)r * src.row + (int64_t)s * src.extra + c0 + channel;
+  const T* first = p;
+  uint32_t left = (s + 1) * S.t - r;  // rows of this sequence
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    raw_load<VEC>(skip.pad(t) ? first : p, live, &out[t]);
+    if (row + t + 1 < rows) {
+      p += src.row;
+      if (--left == 0) {
+        p += src.extra;
+        left = S.t;
+      }
+    }
+  }
+}
+
 template <bool VEC>
 __device__ __forceinline__ void store4(float* p, int live, const float* v) {
   typedef float f32x4_t __attribute__((ext_vector_type(4)));

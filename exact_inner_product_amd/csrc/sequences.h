@@ -26,12 +26,6 @@ struct Rows {
   int64_t extra;  // dense: sequence stride - t * row stride
 };
 
-// What is said about a row of a tile.
-constexpr uint32_t kFirst = 1, kFinal = 2;  // of its sequence
-constexpr uint32_t kPad = 4;                // of no sequence: nothing is read, zeros are written
-constexpr uint32_t kBeyond = 8;             // not this tile's: nothing is read or written
-constexpr uint32_t kCut = kFirst | kPad | kBeyond;
-
 // Where the offsets are broken (decreasing, negative, past the rows), results are meaningless but
 // every access stays in bounds: offsets are clamped to [0, n] and only compared with rows.
 __device__ __forceinline__ uint32_t index_at(const void* p, int wide, int64_t i, uint32_t most) {
@@ -57,57 +51,49 @@ __device__ __forceinline__ int32_t lower_bound(const Sequences& S, uint32_t r) {
   return lo;
 }
 
-// Marks the rows [r0, r0 + rows) of a tile, all threads of the workgroup: kind[i], and for first and
-// final rows their sequence. empty(s) is called by one thread for every sequence without rows
-// that this tile answers for (where it would lie; the last tile for those behind the rows).
-// Ends with a barrier. kind has `space` entries; those from `rows` on are kBeyond.
-template <int THREADS, typename F>
-__device__ __forceinline__ void mark_rows(const Sequences& S, uint32_t r0, uint32_t rows, uint32_t space, bool last,
-                                          uint8_t* kind, int32_t* first, int32_t* final, F empty) {
-  const uint32_t tid = threadIdx.x;
+// The rows of sequence s: [*begin, *end) in the numbering above.
+__device__ __forceinline__ void sequence_rows(const Sequences& S, int64_t s, uint32_t* begin, uint32_t* end) {
   if (S.t) {
-    for (uint32_t i = tid; i < space; i += THREADS) {
-      uint32_t k = kBeyond;
-      if (i < rows) {
-        const uint32_t r = r0 + i, s = r / S.t, pos = r - s * S.t;
-        const uint32_t len = S.lengths ? index_at(S.lengths, S.wide, s, S.t) : S.t;
-        k = pos >= len ? kPad : ((pos == 0 ? kFirst : 0u) | (pos + 1 == len ? kFinal : 0u));
-        if (pos == 0 && len == 0) empty((int32_t)s);
-        first[i] = final[i] = (int32_t)s;
-      }
-      kind[i] = (uint8_t)k;
+    *begin = (uint32_t)s * S.t;
+    *end = *begin + (S.lengths ? index_at(S.lengths, S.wide, s, S.t) : S.t);
+  } else {
+    *begin = index_at(S.offsets, S.wide, s, S.n);
+    *end = index_at(S.offsets, S.wide, s + 1, S.n);
+    if (*end < *begin) *end = *begin;
+  }
+}
+
+// Calls f(s, begin, end) for the sequences with rows in [r0, r1), those of a wave together. Dense ones
+// come with rows of padding or none too, packed ones only with rows.
+template <typename F>
+__device__ __forceinline__ void for_sequences(const Sequences& S, uint32_t r0, uint32_t r1, F f) {
+  uint32_t begin, end;
+  if (S.t) {
+    for (uint32_t s = r0 / S.t; s < (uint32_t)S.b && s * S.t < r1; ++s) {
+      sequence_rows(S, s, &begin, &end);
+      f((int32_t)s, begin, end);
     }
-    __syncthreads();
     return;
   }
-  // the rows from offsets[0] to offsets[b] belong to sequences
-  const uint32_t begin = index_at(S.offsets, S.wide, 0, S.n), end = index_at(S.offsets, S.wide, S.b, S.n);
-  for (uint32_t i = tid; i < space; i += THREADS) {
-    const uint32_t r = r0 + i;
-    kind[i] = (uint8_t)(i >= rows ? kBeyond : (r < begin || r >= end ? kPad : 0u));
-    first[i] = final[i] = -1;
-  }
-  __shared__ int32_t from;
-  if (tid < 64) {
-    const int32_t k = lower_bound(S, r0);
-    if (tid == 0) from = k > 0 ? k - 1 : 0;  // the sequence that r0 may lie inside of
-  }
-  __syncthreads();
-  for (int64_t s = (int64_t)from + tid; s < S.b; s += THREADS) {
-    const uint32_t o0 = index_at(S.offsets, S.wide, s, S.n), o1 = index_at(S.offsets, S.wide, s + 1, S.n);
-    if (o0 >= r0 + rows && !last) break;
-    if (o1 <= o0) {
-      if (o0 >= r0) empty((int32_t)s);
-      continue;
+  const int lane = threadIdx.x & 63;
+  int64_t s0 = lower_bound(S, r0);
+  s0 = s0 > 0 ? s0 - 1 : 0;
+  for (; s0 < S.b; s0 += 64) {
+    begin = end = ~0u;
+    if (s0 + lane < S.b) sequence_rows(S, s0 + lane, &begin, &end);
+    uint64_t m = __ballot(begin < end && begin < r1 && end > r0);
+    while (m) {
+      const int k = __ffsll((unsigned long long)m) - 1;
+      m &= m - 1;
+      f((int32_t)(s0 + k), (uint32_t)__shfl((int)begin, k), (uint32_t)__shfl((int)end, k));
     }
-    if (o0 >= r0 && o0 < r0 + rows) first[o0 - r0] = (int32_t)s;
-    if (o1 > r0 && o1 <= r0 + rows) final[o1 - 1 - r0] = (int32_t)s;
+    if ((uint32_t)__shfl((int)begin, 63) >= r1) break;  // this one and all behind it
   }
-  __syncthreads();
-  for (uint32_t i = tid; i < rows; i += THREADS)
-    kind[i] |= (uint8_t)((first[i] >= 0 ? kFirst : 0u) | (final[i] >= 0 ? kFinal : 0u));
-  __syncthreads();
 }
+
+// What is kept of a packed row: its sequence << 2, | kFirst and kFinal where it is its sequence's first and
+// last one; kPad for a row of no sequence.
+constexpr int32_t kFirst = 1, kFinal = 2, kPad = -1;
 
 // ------------------------------------------------------------------------------- host
 // Checks a mips_sequences and makes a Sequences of it; MIPS_OK or an error.

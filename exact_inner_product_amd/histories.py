@@ -20,6 +20,7 @@ from . import MipsError, _check, empty_workspace, lib
 from .training import _code, _ids_arg, _on_gpu, _ptr, _row_stride, _rows_arg, _stream
 
 EVENTS_MAX = 65536  # events of one gated_step call
+PACKED_STRIDE_MAX = 524288  # elements between packed rows that are used in place
 
 
 class _Sequences(C.Structure):
@@ -64,6 +65,8 @@ def _rows(x: torch.Tensor) -> Tuple[torch.Tensor, _Rows]:
     """x, or a copy where its rows are not runs of memory that do not overlap, and its description."""
     if x.dim() == 2:
         x = _rows_arg(x)
+        if _row_stride(x) > PACKED_STRIDE_MAX:
+            x = x.contiguous()
         return x, _Rows(x.data_ptr(), _row_stride(x), 0)
     b, t, d = x.shape
     row, seq = x.stride(1) if t > 1 else d, x.stride(0) if b > 1 else t * d
@@ -133,7 +136,7 @@ def gated_scan(x: torch.Tensor, forget: torch.Tensor, gate: Optional[torch.Tenso
     out = GatedScan(torch.empty(x.shape, dtype=x.dtype, device=dev) if states else None,
                     torch.empty((b, d), dtype=torch.float32, device=dev),
                     torch.empty((tiles, d), dtype=torch.float32, device=dev))
-    if tiles:
+    if tiles or offsets is not None:
         workspace = _workspace(lib().mips_gated_scan_workspace_size, seq, d, "mips_gated_scan_workspace_size",
                                workspace, dev)
     _check(lib().mips_gated_scan(C.byref(seq), d, code, C.byref(xr), C.byref(fr), None if gr is None else C.byref(gr),
@@ -175,7 +178,7 @@ def gated_scan_backward(grad_states: Optional[torch.Tensor], grad_last: Optional
     dx, df = (torch.empty(x.shape, dtype=x.dtype, device=dev) for _ in range(2))
     dg = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
     di = torch.empty((b, d), dtype=torch.float32, device=dev) if initial is not None else None
-    if tiles:
+    if tiles or offsets is not None:
         workspace = _workspace(lib().mips_gated_scan_workspace_size, seq, d, "mips_gated_scan_workspace_size",
                                workspace, dev)
     _check(lib().mips_gated_scan_backward(

@@ -532,7 +532,9 @@ typedef struct mips_sequences {
 } mips_sequences;
 
 /* An input tensor over such rows: unit stride along d, row_stride >= d elements from a row to the
- * next one, seq_stride >= d (dense and padded) from a sequence to the next one. */
+ * next one (packed: at most MIPS_PACKED_STRIDE_MAX), seq_stride >= d (dense and padded) from a
+ * sequence to the next one. */
+#define MIPS_PACKED_STRIDE_MAX 524288
 typedef struct mips_rows {
   const void *data; /* device */
   int64_t row_stride;
@@ -553,7 +555,8 @@ typedef struct mips_rows {
  *   carries      device float [mips_gated_scan_carries(seq, d), d]: states between tiles, for the
  *                gradient; may be NULL where that is 0. The number follows from the sizes alone.
  *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0 for unsupported
- *                sizes), may be NULL where there are no carries. Calls that share one must be ordered.
+ *                sizes), may be NULL for dense and padded rows without carries. Calls that share one must
+ *                be ordered.
  * Rows whose elements lie in aligned groups of four (d, strides and pointers) move so, others one by one.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, index_bits, d, b or
  * rows above their limits), WORKSPACE, HIP.
