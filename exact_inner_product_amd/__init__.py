@@ -112,9 +112,9 @@ def lib() -> C.CDLL:
         for f in (L.mips_logprobs, L.mips_logprobs_backward, L.mips_embedding_lookup, L.mips_embedding_grad, L.mips_clip_grad_norm):
             f.restype = C.c_int
         u64 = C.c_uint64
-        L.mips_gated_scan_carries.argtypes = [p, i32]
+        L.mips_gated_scan_carries.argtypes = [p, i32, i32]
         L.mips_gated_scan_carries.restype = i64
-        L.mips_gated_scan_workspace_size.argtypes = [p, i32]
+        L.mips_gated_scan_workspace_size.argtypes = [p, i32, i32]
         L.mips_gated_scan_workspace_size.restype = sz
         L.mips_gated_scan.argtypes = [p, i32, i32, p, p, p, p, p, p, p, p, sz, p]
         L.mips_gated_scan_backward.argtypes = [p, i32, i32, p, p, p, p, p, p, p, p, p, p, p, p, sz, p]

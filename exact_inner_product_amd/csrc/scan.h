@@ -17,8 +17,8 @@
 namespace mips {
 
 constexpr int kTileThreads = 512;
-constexpr int kLongRun = 8;  // rows of a thread: forward in bf16
-constexpr int kRun = 4;      // forward in f32, and backward, which have to hold more of each
+// Rows of a thread, a run: of what it holds of each, eight fit in its registers in bf16 and four in f32.
+template <typename T> constexpr int kRun = sizeof(T) == 2 ? 8 : 4;
 
 // Lanes a row (4 channels each): 4, 8, 16 or 32, of widths up to 16, 32, 64, any.
 inline int scan_lanes_log2(int32_t d) { return d > 64 ? 5 : d > 32 ? 4 : d > 16 ? 3 : 2; }
@@ -46,25 +46,24 @@ inline Tiling tiling_of(const Sequences& S, int32_t d, int run, int threads) {
   T.columns = ((uint32_t)d + width - 1) / width;
   return T;
 }
-// 512 threads by 4 rows each; twice the threads where that makes sequences lie whole in a tile.
-inline Tiling short_tiling(const Sequences& S, int32_t d) {
-  const Tiling T = tiling_of(S, d, kRun, kTileThreads), W = tiling_of(S, d, kRun, 2 * kTileThreads);
+inline Tiling scan_tiling(const Sequences& S, int32_t d, int32_t dtype) {
+  if (dtype == MIPS_BF16) return tiling_of(S, d, kRun<__bf16>, kTileThreads);
+  // f32: twice the threads where that makes sequences lie whole in a tile
+  const Tiling T = tiling_of(S, d, kRun<float>, kTileThreads), W = tiling_of(S, d, kRun<float>, 2 * kTileThreads);
   return T.chained && S.t && !W.chained ? W : T;
 }
-inline Tiling forward_tiling(const Sequences& S, int32_t d, int32_t dtype) {
-  return dtype == MIPS_BF16 ? tiling_of(S, d, kLongRun, kTileThreads) : short_tiling(S, d);
-}
-inline Tiling backward_tiling(const Sequences& S, int32_t d) { return short_tiling(S, d); }
+// Runs of all tiles.
+inline int64_t scan_runs(const Tiling& T) { return (int64_t)T.tiles * (T.threads >> T.lanes_log2); }
 
 // ------------------------------------------------------------------------------ gates
 // sigmoid(v) and sigmoid(-v), each exact to a few units in the last place (1 - sigmoid(v) would
-// not be): with e = exp(-|v|) they are 1 / (1 + e) and e / (1 + e).
+// not be): with e = exp(-v) they are 1 / (1 + e) and e / (1 + e). e is at most 2^126, so that the second is
+// not inf 0 (values of the first below 2^-126 are held there); a NaN stays one.
 __device__ __forceinline__ void sigmoids(float v, float* up, float* down) {
-  const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(v));
+  const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-1.44269504f * v, 126.0f));
   const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  const float q = e * r;
-  *up = v < 0.0f ? q : r;
-  *down = v < 0.0f ? r : q;
+  *up = r;
+  *down = e * r;
 }
 
 // --------------------------------------------------------------------- affine maps
@@ -242,76 +241,66 @@ __device__ __forceinline__ uint32_t chain_ticket(uint32_t* counters, uint32_t co
   return __builtin_amdgcn_readfirstlane(ticket);
 }
 
-// --------------------------------------------------------- across a wave's two halves
-// v of the lane 32 lower or the lane itself, and of the lane itself or 32 higher: one instruction for
-// both, against two through LDS.
-__device__ __forceinline__ void halves(float v, float* low, float* high) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  *low = __uint_as_float(r[0]);
-  *high = __uint_as_float(r[1]);
-}
-
-// Of four channels, from each lane's run's map (ra, rb): that of the whole wave, (wa, wb), and that of the
-// wave's runs before the lane's, (ea, eb). BACK: the argument comes from the last run, not the first.
-// CUTS: some may be constant (six instructions to compose two of them, not two).
-template <bool BACK, bool CUTS>
-__device__ __forceinline__ void wave_maps(const float* ra, const float* rb, int lane, int lanes, float* ea, float* eb,
-                                          float* wa, float* wb) {
-  const int in = lane & 31;
-  const bool behind = BACK ? lane < 32 : lane >= 32;  // the other half's runs come before this one's
-  float xa[4], xb[4];
+// -------------------------------------------------------------- runs of half a wave
+// The maps that threads of a channel take states through are those of half waves: with 32 lanes a row of
+// one run. With fewer, the runs of a half are joined by shuffles first; what a run gets of what reaches its half
+// waits in LDS meanwhile (registers are short), as it is needed only again behind the chain.
+//
+// Writes the half's map of this lane's four channels into `maps`. BACK: the argument comes from the last run.
+template <int THREADS, bool BACK>
+__device__ __forceinline__ void half_maps(const float* ra, const float* rb, int lanes, float2 (*maps)[128], float4 (*inner)[2]) {
+  const int tid = threadIdx.x, in = tid & 31, ch = (tid & (lanes - 1)) * 4;
+  if (lanes == 32) {
+    float4* p = (float4*)&maps[tid >> 5][ch];
+    p[0] = float4{ra[0], rb[0], ra[1], rb[1]};
+    p[1] = float4{ra[2], rb[2], ra[3], rb[3]};
+    return;
+  }
+  float xa[4], xb[4], ea[4], eb[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     xa[c] = ra[c];
     xb[c] = rb[c];
-    ea[c] = 1.0f;
-    eb[c] = 0.0f;
   }
-  if (lanes < 32) {
-    for (int o = lanes; o < 32; o <<= 1) {
-      const bool has = BACK ? in + o < 32 : in >= o;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float pa = BACK ? __shfl_down(xa[c], o, 32) : __shfl_up(xa[c], o, 32);
-        const float pb = BACK ? __shfl_down(xb[c], o, 32) : __shfl_up(xb[c], o, 32);
-        if (has) compose(pa, pb, xa[c], xb[c], &xa[c], &xb[c]);
-      }
-    }
-    const bool edge = BACK ? in + lanes >= 32 : in < lanes;
-    const int total = (BACK ? 0 : 32 - lanes) + (lane & (lanes - 1));
+  for (int o = lanes; o < 32; o <<= 1) {
+    const bool has = BACK ? in + o < 32 : in >= o;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float pa = BACK ? __shfl_down(xa[c], lanes, 32) : __shfl_up(xa[c], lanes, 32);
-      const float pb = BACK ? __shfl_down(xb[c], lanes, 32) : __shfl_up(xb[c], lanes, 32);
-      if (!edge) {
-        ea[c] = pa;
-        eb[c] = pb;
-      }
-      xa[c] = __shfl(xa[c], total, 32);
-      xb[c] = __shfl(xb[c], total, 32);
+      const float pa = BACK ? __shfl_down(xa[c], o, 32) : __shfl_up(xa[c], o, 32);
+      const float pb = BACK ? __shfl_down(xb[c], o, 32) : __shfl_up(xb[c], o, 32);
+      if (has) compose(pa, pb, xa[c], xb[c], &xa[c], &xb[c]);
     }
   }
+  const bool edge = BACK ? in + lanes >= 32 : in < lanes;  // nothing of the half before it
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    float la, lb, ua, ub;
-    halves(xa[c], &la, &ua);
-    halves(xb[c], &lb, &ub);
-    const float oa = BACK ? ua : la, ob = BACK ? ub : lb, ta = BACK ? la : ua, tb = BACK ? lb : ub;
-    if (CUTS) {
-      compose(oa, ob, ta, tb, &wa[c], &wb[c]);
-      if (behind) compose(oa, ob, ea[c], eb[c], &ea[c], &eb[c]);
-    } else {
-      wa[c] = oa * ta;
-      wb[c] = fmaf(ta, ob, tb);
-      if (lanes == 32) {
-        ea[c] = behind ? oa : 1.0f;
-        eb[c] = behind ? ob : 0.0f;
-      } else if (behind) {
-        eb[c] = fmaf(ea[c], ob, eb[c]);
-        ea[c] = oa * ea[c];
-      }
-    }
+    const float pa = BACK ? __shfl_down(xa[c], lanes, 32) : __shfl_up(xa[c], lanes, 32);
+    const float pb = BACK ? __shfl_down(xb[c], lanes, 32) : __shfl_up(xb[c], lanes, 32);
+    ea[c] = edge ? 1.0f : pa;
+    eb[c] = edge ? 0.0f : pb;
   }
+  inner[tid][0] = float4{ea[0], ea[1], ea[2], ea[3]};
+  inner[tid][1] = float4{eb[0], eb[1], eb[2], eb[3]};
+  if (BACK ? in < lanes : in + lanes >= 32) {
+    float4* p = (float4*)&maps[tid >> 5][ch];
+    p[0] = float4{xa[0], xb[0], xa[1], xb[1]};
+    p[1] = float4{xa[2], xb[2], xa[3], xb[3]};
+  }
+}
+// What reaches this lane's run, of what reaches its half.
+__device__ __forceinline__ void half_reach(const float (*reach)[128], const float4 (*inner)[2], int lanes, float* v) {
+  const int tid = threadIdx.x;
+  const float4 r = *(const float4*)&reach[tid >> 5][(tid & (lanes - 1)) * 4];
+  v[0] = r.x;
+  v[1] = r.y;
+  v[2] = r.z;
+  v[3] = r.w;
+  if (lanes == 32) return;
+  const float4 a = inner[tid][0], b = inner[tid][1];
+  v[0] = apply(a.x, b.x, v[0]);
+  v[1] = apply(a.y, b.y, v[1]);
+  v[2] = apply(a.z, b.z, v[2]);
+  v[3] = apply(a.w, b.w, v[3]);
 }
 
 // -------------------------------------------------------------------- four channels
@@ -341,12 +330,10 @@ template <> struct Raw<__bf16> {
   }
 };
 
-// Makes the compiler forget what it has computed from v or r, so that it does so again where it is needed
+// Makes the compiler forget what it has computed from r, so that it does so again where it is needed
 // rather than keep it in registers.
-__device__ __forceinline__ uint32_t again(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
+// Has v computed here, not where it is used, with all it comes from in registers until then.
+__device__ __forceinline__ void here(float* v) { asm volatile("" : "+v"(*v)); }
 template <typename T>
 __device__ __forceinline__ void raw_again(Raw<T>* r) {
 #pragma unroll
@@ -379,6 +366,8 @@ struct Marks {
   __device__ __forceinline__ bool cut(int t) const { return (bits >> (16 + t)) & 1u; }     // pad, or a first row
   __device__ __forceinline__ bool final(int t) const { return (bits >> (24 + t)) & 1u; }
   __device__ __forceinline__ bool first(int t) const { return cut(t) && !pad(t); }
+  // Whether a lane of the wave has one at row t: what few rows need is done for those.
+  __device__ __forceinline__ bool wave_has(int t) const { return __any((bits >> t) & 0x01010101u); }
 };
 // The sequence of a row that has one.
 __device__ __forceinline__ int64_t row_sequence(const Sequences& S, const int32_t* packed, uint32_t r) {

@@ -1,6 +1,8 @@
 // scan.hip -- the gated linear recurrence over sequences, forward (gfx950). scan.h has the method.
 //
 // One pass: forget logits, inputs (and gate logits) are read once and the states written once.
+#include <type_traits>
+
 #include "scan.h"
 
 namespace mips {
@@ -11,26 +13,39 @@ struct ScanArgs {
   const float* initial;  // [b, d] or NULL
   void* states;          // [n, d] or NULL
   float* last;           // [b, d]
-  float* carries;        // [the gradient's tiles, d], or NULL: it needs none
+  float* carries;        // [runs of all tiles, d] or NULL: the state before each run
   const int32_t* info;   // packed rows
   uint64_t* words;       // chained calls: of tiles, then of groups
   uint32_t* counters;
   int32_t d;
   int32_t lanes_log2;
   uint32_t rows, tiles, columns;
-  uint32_t half;         // rows of the gradient's tiles
   uint32_t block0;       // of this launch
   int32_t chained;
   int32_t flat;          // load_flat serves
 };
 
-template <typename T, bool GATE, bool VEC, int R, int THREADS>
-__global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
-  constexpr int WAVES = THREADS / 64;
-  __shared__ float2 maps[WAVES][128];
-  __shared__ __attribute__((aligned(16))) float entry[WAVES][128];  // the state before each wave's rows
+// Row r is padding: if a padded sequence without rows would begin there, its last state is its initial one.
+__device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t channel, int live) {
+  const uint32_t s = r / A.S.t;
+  if (r != s * A.S.t) return;
+  const int64_t i = (int64_t)s * A.d + channel;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < live) A.last[i + c] = A.initial ? A.initial[i + c] : 0.0f;
+}
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// STATES: every state is wanted, and held until the one before the run is known. Else a run keeps its map and, of
+// a sequence that goes on from the run before, the map up to its final row: registers for half as
+// many waves again, where this is bound by latency (4096 x 127 x 128 with lengths: 72 -> 45 us).
+template <typename T, bool GATE, bool VEC, bool STATES, int THREADS>
+__global__ __launch_bounds__(THREADS, STATES || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
+  constexpr int R = kRun<T>, HALVES = THREADS / 32;
+  __shared__ __attribute__((aligned(16))) float2 maps[HALVES][128];
+  __shared__ __attribute__((aligned(16))) float entry[HALVES][128];  // the state before each half wave's rows
+  __shared__ float4 inner[THREADS][2];
+
+  const int tid = threadIdx.x;
   const uint32_t job = A.block0 + blockIdx.x, column = job % A.columns;
   const uint32_t tile = A.chained ? chain_ticket(A.counters, column) : job / A.columns;
   const uint32_t r0 = tile * A.rows;
@@ -38,7 +53,7 @@ __global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
   const int width = 4 << A.lanes_log2;
   const int c0 = column * width;                        // the tile's first channel
   const int lanes = 1 << A.lanes_log2;
-  const int ch = (lane & (lanes - 1)) * 4;              // this thread's first channel in the tile
+  const int ch = (tid & (lanes - 1)) * 4;              // this thread's first channel in the tile
   const int live = min(4, A.d - c0 - ch);               // <= 0: none
   const uint32_t at = (uint32_t)(tid >> A.lanes_log2) * R;  // its first row in the tile
   const int64_t channel = c0 + ch;
@@ -52,13 +67,16 @@ __global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
   const uint32_t source = A.chained ? chain_source(A.S, A.info, r0, A.rows, tile) : 0;
 
   // the run from a state of 0: P the product of the gates so far, h the state
-  float P[R][4], h[R][4];
-  int cut = R;  // the first row that does not see the state before the run
+  constexpr int KEPT = STATES ? R : 1;
+  float P[KEPT][4], h[KEPT][4];
+  float fP[4], fh[4];    // those of `ends`, the final row that sees the state before the run, without STATES
+  int ends = R;
+  int cut = R;           // the first row that does not see the state before the run
+#pragma unroll
+  for (int t = 0; t < KEPT; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) P[t][c] = h[t][c] = 0.0f;
   if (idle) {
-#pragma unroll
-    for (int t = 0; t < R; ++t)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) P[t][c] = h[t][c] = 0.0f;
     cut = 0;
   } else {
     Raw<T> x[R], f[R], g[R];
@@ -71,15 +89,23 @@ __global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
       load_gaps<VEC>(A.S, A.x, r0, rows, at, c0, from, some, marks, x);
       if (GATE) load_gaps<VEC>(A.S, A.gate, r0, rows, at, c0, from, some, marks, g);
     }
-    if (special) {
+    auto run = [&](auto plain) __attribute__((always_inline)) {
+      constexpr bool PLAIN = decltype(plain)::value;  // no row of the wave begins or ends a sequence, or is padding
+      float p[4], v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        p[c] = 1.0f;
+        v[c] = 0.0f;
+      }
 #pragma unroll
       for (int t = 0; t < R; ++t) {
-        if (marks.cut(t)) cut = min(cut, t);
-        float init[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (A.initial && live > 0 && marks.first(t)) {
-          const float* p = A.initial + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel;
+        const bool has = !PLAIN && marks.wave_has(t);
+        if (has && marks.cut(t)) {
+          cut = min(cut, t);
+          const bool init = A.initial && live > 0 && marks.first(t);
+          const float* q = init ? A.initial + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel : nullptr;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) init[c] = c < live ? p[c] : 0.0f;
+          for (int c = 0; c < 4; ++c) v[c] = init && c < live ? q[c] : 0.0f;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -87,48 +113,58 @@ __global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
           sigmoids(f[t].at(c), &a, &na);
           b = na;
           if (GATE) sigmoids(g[t].at(c), &b, &nb);
-          const float prev = marks.cut(t) ? init[c] : (t ? h[t - 1][c] : 0.0f);
-          const float v = fmaf(a, prev, b * x[t].at(c));
-          h[t][c] = marks.pad(t) ? 0.0f : v;
-          P[t][c] = t ? P[t - 1][c] * a : a;
+          v[c] = fmaf(a, v[c], b * x[t].at(c));
+          p[c] *= a;
+          if (has && marks.pad(t)) v[c] = 0.0f;
+          if (STATES) {
+            P[STATES ? t : 0][c] = p[c];
+            h[STATES ? t : 0][c] = v[c];
+            here(&P[STATES ? t : 0][c]);
+            here(&h[STATES ? t : 0][c]);
+          }
+        }
+        if (!STATES && has && marks.final(t)) {
+          if (t < cut) {
+            ends = t;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              fP[c] = p[c];
+              fh[c] = v[c];
+            }
+          } else if (live > 0) {
+            float* q = A.last + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (c < live) q[c] = v[c];
+          }
         }
       }
-    } else {
-#pragma unroll
-      for (int t = 0; t < R; ++t)
+      if (!STATES) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float a, na, b, nb;
-          sigmoids(f[t].at(c), &a, &na);
-          b = na;
-          if (GATE) sigmoids(g[t].at(c), &b, &nb);
-          h[t][c] = t ? fmaf(a, h[t - 1][c], b * x[t].at(c)) : b * x[t].at(c);
-          P[t][c] = t ? P[t - 1][c] * a : a;
+          P[0][c] = p[c];
+          h[0][c] = v[c];
         }
-    }
+      }
+    };
+    if (special) run(std::false_type{});
+    else run(std::true_type{});
   }
 
-  // maps of the runs before this one, within the wave and then the tile
-  float ra[4];
+  float ra[4];  // the run's map
 #pragma unroll
-  for (int c = 0; c < 4; ++c) ra[c] = cut < R ? kForgets : P[R - 1][c];
-  float ea[4], eb[4], wa[4], wb[4];
-  if (special) wave_maps<false, true>(ra, h[R - 1], lane, lanes, ea, eb, wa, wb);
-  else wave_maps<false, false>(ra, h[R - 1], lane, lanes, ea, eb, wa, wb);
-  if (lane < lanes) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) maps[wave][ch + c] = float2{wa[c], wb[c]};
-  }
+  for (int c = 0; c < 4; ++c) ra[c] = cut < R ? kForgets : P[KEPT - 1][c];
+  half_maps<THREADS, false>(ra, h[KEPT - 1], lanes, maps, inner);
   __syncthreads();
-  // one thread a channel takes the state through the waves (all threads doing so for their own
-  // wave would be a tenth of the kernel's instructions)
+  // one thread a channel takes the state through the half waves (all threads doing so for their own
+  // would be a tenth of the kernel's instructions)
   const int channels = min(width, A.d - c0);
   float v = 0.0f;
   if (A.chained) {
     float a = 1.0f, b = 0.0f;
     if (tid < channels) {
 #pragma unroll 4
-      for (int w = 0; w < WAVES; ++w) compose(a, b, maps[w][tid].x, maps[w][tid].y, &a, &b);
+      for (int w = 0; w < HALVES; ++w) compose(a, b, maps[w][tid].x, maps[w][tid].y, &a, &b);
     }
     const int64_t stride = (int64_t)A.columns * width;
     const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
@@ -136,7 +172,7 @@ __global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
   }
   if (tid < channels) {
 #pragma unroll 4
-    for (int w = 0; w < WAVES; ++w) {
+    for (int w = 0; w < HALVES; ++w) {
       entry[w][tid] = v;
       v = apply(maps[w][tid].x, maps[w][tid].y, v);
     }
@@ -144,44 +180,48 @@ __global__ __launch_bounds__(THREADS, 4) void scan_kernel(ScanArgs A) {
   __syncthreads();
   if (live <= 0) return;
   float state[4];  // before the run
-#pragma unroll
-  for (int c = 0; c < 4; ++c) state[c] = apply(ea[c], eb[c], entry[wave][ch + c]);
+  half_reach(entry, inner, lanes, state);
 
-  if (A.carries && at % A.half == 0 && at < rows) {  // where a tile of the gradient begins
-    float* p = A.carries + ((int64_t)tile * (A.rows / A.half) + at / A.half) * A.d + channel;
+  if (A.carries && at < rows)
+    store4<VEC>(A.carries + ((int64_t)tile * (THREADS >> A.lanes_log2) + (tid >> A.lanes_log2)) * A.d + channel, live, state);
+  if (!STATES) {
+    if (!special) return;
+    if (ends < R) {
+      float* p = A.last + row_sequence(A.S, A.info, r0 + at + ends) * A.d + channel;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < live) p[c] = state[c];
+      for (int c = 0; c < 4; ++c)
+        if (c < live) p[c] = fmaf(fP[c], state[c], fh[c]);
+    }
+    if (!A.S.lengths) return;
+#pragma unroll 1
+    for (int t = 0; t < R; ++t)
+      if (marks.pad(t) && !marks.beyond(t)) none_last(A, r0 + at + t, channel, live);
+    return;
   }
   uint8_t* base = (uint8_t*)((T*)A.states + (int64_t)r0 * A.d + c0);
   uint32_t out = (at * (uint32_t)A.d + ch) * (uint32_t)sizeof(T);
-  if (!special) {
-    if (!A.states) return;
+  auto write = [&](auto plain) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
     for (int t = 0; t < R; ++t, out += (uint32_t)A.d * sizeof(T)) {
+      constexpr int K = STATES;
       float v[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = fmaf(P[t][c], state[c], h[t][c]);
+      for (int c = 0; c < 4; ++c) v[c] = PLAIN || t < cut ? fmaf(P[K * t][c], state[c], h[K * t][c]) : h[K * t][c];
+      const bool has = !PLAIN && marks.wave_has(t);
+      if (has && marks.beyond(t)) continue;
       store4<VEC>((T*)(base + out), live, v);
+      if (!has) continue;
+      if (A.S.lengths && marks.pad(t)) none_last(A, r0 + at + t, channel, live);
+      if (!marks.final(t)) continue;
+      float* p = A.last + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < live) p[c] = v[c];
     }
-    return;
-  }
-#pragma unroll
-  for (int t = 0; t < R; ++t, out += (uint32_t)A.d * sizeof(T)) {
-    if (marks.beyond(t)) continue;
-    float v[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = t < cut ? fmaf(P[t][c], state[c], h[t][c]) : h[t][c];
-    if (A.states) store4<VEC>((T*)(base + out), live, v);
-    const uint32_t r = r0 + at + t;
-    // a padded sequence without rows: where its first one would lie
-    const bool none = A.S.lengths && marks.pad(t) && r % A.S.t == 0;
-    if (!none && !marks.final(t)) continue;
-    const int64_t i = row_sequence(A.S, A.info, r) * A.d + channel;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < live) A.last[i + c] = !none ? v[c] : (A.initial ? A.initial[i + c] : 0.0f);
-  }
+  };
+  if (special) write(std::false_type{});
+  else write(std::true_type{});
 }
 
 struct BeginArgs {
@@ -277,21 +317,13 @@ int check_rows(const mips_rows* r, const Sequences& S, int32_t d, int32_t dtype,
   return MIPS_OK;
 }
 
-template <typename T, int R, int THREADS>
-static void (*scan_variant(bool gate, bool vec))(ScanArgs) {
-  return gate ? (vec ? scan_kernel<T, true, true, R, THREADS> : scan_kernel<T, true, false, R, THREADS>)
-              : (vec ? scan_kernel<T, false, true, R, THREADS> : scan_kernel<T, false, false, R, THREADS>);
-}
-
-// Bytes that both directions of a call need; the tiles of the gradient if they are chained, else 0.
-static size_t scan_bytes(const Sequences& S, int32_t d) {
-  const size_t f = scan_space(S, forward_tiling(S, d, MIPS_BF16), nullptr).bytes;
-  const size_t b = scan_space(S, backward_tiling(S, d), nullptr).bytes;  // and forward in f32
-  return f > b ? f : b;
-}
-static uint32_t scan_carries(const Sequences& S, int32_t d) {
-  const Tiling B = backward_tiling(S, d);
-  return B.chained ? B.tiles : 0;
+template <typename T, int THREADS>
+static void (*scan_variant(bool gate, bool vec, bool states))(ScanArgs) {
+  if (states)
+    return gate ? (vec ? scan_kernel<T, true, true, true, THREADS> : scan_kernel<T, true, false, true, THREADS>)
+                : (vec ? scan_kernel<T, false, true, true, THREADS> : scan_kernel<T, false, false, true, THREADS>);
+  return gate ? (vec ? scan_kernel<T, true, true, false, THREADS> : scan_kernel<T, true, false, false, THREADS>)
+              : (vec ? scan_kernel<T, false, true, false, THREADS> : scan_kernel<T, false, false, false, THREADS>);
 }
 
 }  // namespace mips
@@ -300,16 +332,18 @@ using namespace mips;
 
 extern "C" {
 
-int64_t mips_gated_scan_carries(const mips_sequences* seq, int32_t d) {
+int64_t mips_gated_scan_carries(const mips_sequences* seq, int32_t d, int32_t dtype) {
   Sequences S;
-  if (check_sequences(seq, &S) != MIPS_OK || d < 1 || d > MIPS_EMBEDDING_D_MAX) return -1;
-  return scan_carries(S, d);
+  if (check_sequences(seq, &S) != MIPS_OK || d < 1 || d > MIPS_EMBEDDING_D_MAX || (dtype != MIPS_F32 && dtype != MIPS_BF16))
+    return -1;
+  return scan_runs(scan_tiling(S, d, dtype));
 }
 
-size_t mips_gated_scan_workspace_size(const mips_sequences* seq, int32_t d) {
+size_t mips_gated_scan_workspace_size(const mips_sequences* seq, int32_t d, int32_t dtype) {
   Sequences S;
-  if (check_sequences(seq, &S) != MIPS_OK || d < 1 || d > MIPS_EMBEDDING_D_MAX) return 0;
-  return scan_bytes(S, d);
+  if (check_sequences(seq, &S) != MIPS_OK || d < 1 || d > MIPS_EMBEDDING_D_MAX || (dtype != MIPS_F32 && dtype != MIPS_BF16))
+    return 0;
+  return scan_space(S, scan_tiling(S, d, dtype), nullptr).bytes;
 }
 
 int mips_gated_scan(const mips_sequences* seq, int32_t d, int32_t dtype, const mips_rows* x, const mips_rows* forget,
@@ -324,36 +358,34 @@ int mips_gated_scan(const mips_sequences* seq, int32_t d, int32_t dtype, const m
   if (gate) {
     if (const int rc = check_rows(gate, A.S, d, dtype, &A.gate)) return rc;
   }
-  const Tiling T = forward_tiling(A.S, d, dtype);
-  const bool carried = scan_carries(A.S, d) > 0;
+  const Tiling T = scan_tiling(A.S, d, dtype);
   if (!last || !aligned(last, 4) || !aligned(initial, 4) || !aligned(states, elem_bytes(dtype)) ||
-      !aligned(workspace, 256) || ((T.chained || A.S.offsets) && !workspace) || (carried && !carries) || !aligned(carries, 4))
+      !aligned(workspace, 256) || ((T.chained || A.S.offsets) && !workspace) || !aligned(carries, 4))
     return MIPS_ERR_INVALID_ARG;
-  if ((T.chained || A.S.offsets) && workspace_bytes < scan_bytes(A.S, d)) return MIPS_ERR_WORKSPACE;
+  const ScanSpace W = scan_space(A.S, T, workspace);
+  if ((T.chained || A.S.offsets) && workspace_bytes < W.bytes) return MIPS_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   A.initial = initial;
   A.states = states;
   A.last = last;
-  A.carries = carried ? carries : nullptr;
-  A.half = carried ? backward_tiling(A.S, d).rows : T.rows;
+  A.carries = carries;
   A.d = d;
   A.lanes_log2 = T.lanes_log2;
   A.rows = T.rows;
   A.tiles = T.tiles;
   A.columns = T.columns;
   A.chained = T.chained;
-  const ScanSpace W = scan_space(A.S, T, workspace);
   A.info = W.info;
   A.words = W.words;
   A.counters = W.counters;
   if (const int rc = scan_begin(A.S, T, W, d, initial, last, s)) return rc;
   const bool vec = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
-                   (!gate || rows_by_four(A.gate, d, dtype)) && aligned(states, 4 * elem_bytes(dtype));
+                   (!gate || rows_by_four(A.gate, d, dtype)) && aligned(states, 4 * elem_bytes(dtype)) && aligned(carries, 16);
   A.flat = rows_flat(A.x, T, dtype) && rows_flat(A.forget, T, dtype) && (!gate || rows_flat(A.gate, T, dtype));
   void (*kernel)(ScanArgs) = nullptr;
-  if (dtype == MIPS_BF16) kernel = scan_variant<__bf16, kLongRun, kTileThreads>(gate != nullptr, vec);
-  else if (T.threads == kTileThreads) kernel = scan_variant<float, kRun, kTileThreads>(gate != nullptr, vec);
-  else kernel = scan_variant<float, kRun, 2 * kTileThreads>(gate != nullptr, vec);
+  if (dtype == MIPS_BF16) kernel = scan_variant<__bf16, kTileThreads>(gate != nullptr, vec, states != nullptr);
+  else if (T.threads == kTileThreads) kernel = scan_variant<float, kTileThreads>(gate != nullptr, vec, states != nullptr);
+  else kernel = scan_variant<float, 2 * kTileThreads>(gate != nullptr, vec, states != nullptr);
   const uint64_t jobs = (uint64_t)T.tiles * T.columns, most = kMaxGridBlocks / 2;  // up to 1024 threads each
   for (uint64_t j = 0; j < jobs; j += most) {
     A.block0 = (uint32_t)j;

@@ -6,7 +6,12 @@
 //   dinitial = a D at the first row.
 // What flows backward is u_r = a_r (G_r + u_{r+1}), again a composition of affine maps, from the
 // last tile to the first. The states h_{r-1} are not read: they follow from the inputs, which are
-// needed anyway, and the state before the tile, which the forward call left in binary32.
+// needed anyway, and the state before the run, which the forward call left in binary32 (an eighth of a
+// bf16 tensor's rows, and a quarter of its bytes; taking the states from tile to tile here as well, by maps
+// as the gradient, was a third more instructions, and they are what bounds this kernel).
+//
+// A run's rows are gone through twice: forward, for the factor of D in dforget and the run's map of u, and,
+// when it is known what flows in from behind, backward for D.
 #include <type_traits>
 
 #include "scan.h"
@@ -18,7 +23,7 @@ struct ScanGradArgs {
   Rows x, forget, gate, grad;
   const float* initial;    // [b, d] or NULL
   const float* grad_last;  // [b, d] or NULL
-  const float* carries;    // [tiles, d], chained calls
+  const float* carries;    // [runs of all tiles, d]: the state before each run
   void *dx, *dforget, *dgate;
   float* dinitial;         // [b, d] or NULL
   const int32_t* info;     // packed rows
@@ -33,12 +38,12 @@ struct ScanGradArgs {
 
 template <typename T, bool GATE, bool VEC, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
-  constexpr int R = kRun, WAVES = THREADS / 64;
-  __shared__ float2 maps[WAVES][128];   // of the state, forward
-  __shared__ float2 flows[WAVES][128];  // of the gradient, backward
-  __shared__ __attribute__((aligned(16))) float entry[WAVES][128], leave[WAVES][128];  // what each wave's rows start from
+  constexpr int R = kRun<T>, HALVES = THREADS / 32;
+  __shared__ __attribute__((aligned(16))) float2 flows[HALVES][128];  // maps of the gradient, backward
+  __shared__ __attribute__((aligned(16))) float leave[HALVES][128];   // what flows into each half wave's rows from behind
+  __shared__ float4 inner[THREADS][2];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x;
   const uint32_t job = A.block0 + blockIdx.x, column = job % A.columns;
   const uint32_t step = A.chained ? chain_ticket(A.counters, column) : job / A.columns;
   const uint32_t tile = A.tiles - 1 - step;
@@ -47,31 +52,22 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   const int width = 4 << A.lanes_log2;
   const int c0 = column * width;
   const int lanes = 1 << A.lanes_log2;
-  const int ch = (lane & (lanes - 1)) * 4;
+  const int ch = (tid & (lanes - 1)) * 4;
   const int live = min(4, A.d - c0 - ch);
   const uint32_t at = (uint32_t)(tid >> A.lanes_log2) * R;
   const int64_t channel = c0 + ch;
   const uint32_t from = live > 0 ? ch : 0;
   const int some = live > 0 ? live : 1;
-  const uint32_t mine = tid - 128;  // the channel that this thread takes the state of through the waves
-  const float state_in = A.chained && mine < (uint32_t)min(width, A.d - c0) ? A.carries[(int64_t)tile * A.d + c0 + mine] : 0.0f;
   const uint32_t source = A.chained ? chain_source_back(A.S, A.info, r0 + rows - 1, A.rows, A.tiles, step) : 0;
 
   const Marks marks = run_marks<R>(A.S, A.info, r0, rows, at);
   const bool special = __any(marks.any());
   const bool idle = special && __all((marks.bits & ((1u << R) - 1u)) == (1u << R) - 1u);  // a wave of padding
   Raw<T> x[R], f[R], g[R], G[R];
-  if (!A.grad.p || idle) {
+  float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the state before the run, then before each row
 #pragma unroll
-    for (int t = 0; t < R; ++t) G[t] = Raw<T>{};
-  }
-  if (idle) {
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      x[t] = f[t] = Raw<T>{};
-      if (GATE) g[t] = Raw<T>{};
-    }
-  } else {
+  for (int t = 0; t < R; ++t) x[t] = f[t] = g[t] = G[t] = Raw<T>{};
+  if (!idle) {
     if (A.flat) {
       load_flat<VEC>(A.forget, r0, rows, at, c0, from, some, marks, f);
       load_flat<VEC>(A.x, r0, rows, at, c0, from, some, marks, x);
@@ -83,6 +79,8 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
       if (GATE) load_gaps<VEC>(A.S, A.gate, r0, rows, at, c0, from, some, marks, g);
       if (A.grad.p) load_gaps<VEC>(A.S, A.grad, r0, rows, at, c0, from, some, marks, G);
     }
+    if (at < rows)
+      load4<VEC>(A.carries + ((int64_t)tile * (THREADS >> A.lanes_log2) + (tid >> A.lanes_log2)) * A.d + c0 + from, some, h);
   }
 
   // [b, d] floats at a row's sequence, for the rows that have one
@@ -92,94 +90,69 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
     for (int c = 0; c < 4; ++c) v[c] = c < live ? p[c] : 0.0f;
   };
 
-  // maps of the run, both taken along with its rows: the state's, h -> ma h + mb, and the gradient's,
-  // where row t's map of what flows in from behind, v -> a (G + v), goes inside those before it
-  float a[R][4], na[R][4];
-  float ea[4], eb[4], la[4], lb[4];  // what reaches the run of what reaches the wave
-  {
-    float ma[4], mb[4], fa[4], fb[4];
+  // forward: q, by which D is multiplied for dforget, and the run's map of what flows in from behind, v -> fa v + fb
+  // (row t's own, v -> a (G + v), goes inside those before it)
+  float q[R][4], fa[4], fb[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      ma[c] = fa[c] = 1.0f;
-      mb[c] = fb[c] = 0.0f;
-    }
-    if (special) {
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const bool pad = marks.pad(t);
-        float init[4] = {0.0f, 0.0f, 0.0f, 0.0f}, end[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (A.initial && live > 0 && marks.first(t)) row4(A.initial, at + t, init);
-        if (A.grad_last && live > 0 && marks.final(t)) row4(A.grad_last, at + t, end);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float b, nb;
-          sigmoids(f[t].at(c), &a[t][c], &na[t][c]);
-          b = na[t][c];
-          if (GATE) sigmoids(g[t].at(c), &b, &nb);
-          const float u = b * x[t].at(c);
-          if (marks.cut(t)) {
-            ma[c] = kForgets;
-            mb[c] = pad ? 0.0f : fmaf(a[t][c], init[c], u);
-          } else {
-            mb[c] = fmaf(a[t][c], mb[c], u);
-            ma[c] = ma[c] < 0.0f ? kForgets : ma[c] * a[t][c];
-          }
-          if (!(fa[c] < 0.0f)) {  // no sequence of the run has ended yet
-            const float p = fa[c] * a[t][c];
-            if (pad) {
-              fa[c] = kForgets;
-            } else if (marks.final(t)) {
-              fb[c] = fmaf(p, G[t].at(c) + end[c], fb[c]);
-              fa[c] = kForgets;
-            } else {
-              fb[c] = fmaf(p, G[t].at(c), fb[c]);
-              fa[c] = p;
-            }
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < R; ++t)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float b, nb;
-          sigmoids(f[t].at(c), &a[t][c], &na[t][c]);
-          b = na[t][c];
-          if (GATE) sigmoids(g[t].at(c), &b, &nb);
-          mb[c] = fmaf(a[t][c], mb[c], b * x[t].at(c));
-          ma[c] *= a[t][c];
-          fb[c] = fmaf(ma[c], G[t].at(c), fb[c]);
-        }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) fa[c] = ma[c];
-    }
-    auto exchange = [&](auto cuts) __attribute__((always_inline)) {
-      constexpr bool CUTS = decltype(cuts)::value;
-      float wa[4], wb[4];
-      wave_maps<false, CUTS>(ma, mb, lane, lanes, ea, eb, wa, wb);
-      if (lane < lanes) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) maps[wave][ch + c] = float2{wa[c], wb[c]};
-      }
-      wave_maps<true, CUTS>(fa, fb, lane, lanes, la, lb, wa, wb);
-      if (lane < lanes) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) flows[wave][ch + c] = float2{wa[c], wb[c]};
-      }
-    };
-    if (special) exchange(std::true_type{});
-    else exchange(std::false_type{});
+  for (int c = 0; c < 4; ++c) {
+    fa[c] = idle ? kForgets : 1.0f;
+    fb[c] = 0.0f;
   }
+  auto forward = [&](auto plain) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value;  // no row of the wave begins or ends a sequence, or is padding
+    bool ended = false;  // a sequence of the run has: what lies behind belongs to others
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      const bool has = !PLAIN && marks.wave_has(t);
+      if (has) {
+        ended = ended || marks.pad(t);
+        if (marks.cut(t)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) h[c] = 0.0f;
+          if (A.initial && live > 0 && marks.first(t)) row4(A.initial, at + t, h);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float up, down, b, nb;
+        sigmoids(f[t].at(c), &up, &down);
+        b = down;
+        if (GATE) sigmoids(g[t].at(c), &b, &nb);
+        const float xx = x[t].at(c);
+        q[t][c] = up * down * (GATE ? h[c] : h[c] - xx);
+        here(&q[t][c]);
+        h[c] = fmaf(up, h[c], b * xx);
+        fa[c] *= up;
+        fb[c] = !PLAIN && ended ? fb[c] : fmaf(fa[c], G[t].at(c), fb[c]);
+      }
+      if (has && !ended && marks.final(t)) {
+        ended = true;
+        if (A.grad_last && live > 0) {
+          float end[4];
+          row4(A.grad_last, at + t, end);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) fb[c] = fmaf(fa[c], end[c], fb[c]);
+        }
+      }
+      if (t & 1) __builtin_amdgcn_sched_barrier(0);  // rows that are computed at once take registers
+    }
+    if (!PLAIN && ended) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) fa[c] = kForgets;
+    }
+  };
+  if (!special) forward(std::true_type{});
+  else if (!idle) forward(std::false_type{});
+  half_maps<THREADS, true>(fa, fb, lanes, flows, inner);
   __syncthreads();
-  // one thread a channel takes the gradient backward through the waves, another the state forward
+  // one thread a channel takes the gradient through the half waves
   const int channels = min(width, A.d - c0);
   float v = 0.0f;
   if (A.chained) {
     float ta = 1.0f, tb = 0.0f;
     if (tid < channels) {
 #pragma unroll 4
-      for (int w = WAVES - 1; w >= 0; --w) compose(ta, tb, flows[w][tid].x, flows[w][tid].y, &ta, &tb);
+      for (int w = HALVES - 1; w >= 0; --w) compose(ta, tb, flows[w][tid].x, flows[w][tid].y, &ta, &tb);
     }
     const int64_t stride = (int64_t)A.columns * width;
     const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
@@ -187,105 +160,98 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   }
   if (tid < channels) {
 #pragma unroll 4
-    for (int w = WAVES - 1; w >= 0; --w) {
+    for (int w = HALVES - 1; w >= 0; --w) {
       leave[w][tid] = v;
       v = apply(flows[w][tid].x, flows[w][tid].y, v);
-    }
-  } else if (tid >= 128 && tid - 128 < channels) {
-    v = state_in;
-#pragma unroll 4
-    for (int w = 0; w < WAVES; ++w) {
-      entry[w][tid - 128] = v;
-      v = apply(maps[w][tid - 128].x, maps[w][tid - 128].y, v);
     }
   }
   __syncthreads();
   if (live <= 0) return;
-  float h[4], u[4];  // the state before the run, the gradient that flows into it from behind
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    h[c] = apply(ea[c], eb[c], entry[wave][ch + c]);
-    u[c] = apply(la[c], lb[c], leave[wave][ch + c]);
-  }
-  if (GATE) {
-#pragma unroll
-    for (int t = 0; t < R; ++t) raw_again(&g[t]);
-  }
   const int64_t tile0 = (int64_t)r0 * A.d + c0;
   const uint32_t pitch = (uint32_t)A.d * sizeof(T), out0 = at * pitch + ch * (uint32_t)sizeof(T);
-  auto gradients = [&](auto plain) __attribute__((always_inline)) {
-    constexpr bool PLAIN = decltype(plain)::value;  // no row of the wave begins or ends a sequence, or is padding
-    // backward first: D is used up, and what flows on, v = a D, takes the place of G
-    float v[R][4];
+  // Row r is padding: the last state of a padded sequence without rows is its initial one
+  auto none = [&](uint32_t r) __attribute__((always_inline)) {
+    const uint32_t s = r / A.S.t;
+    if (r != s * A.S.t) return;
+    const int64_t i = (int64_t)s * A.d + channel;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < live) A.dinitial[i + c] = A.grad_last ? A.grad_last[i + c] : 0.0f;
+  };
+  if (idle) {
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int t = 0; t < R; ++t) {
+      if (marks.beyond(t)) continue;
+      const uint32_t out = out0 + t * pitch;
+      store4<VEC>((T*)((uint8_t*)((T*)A.dx + tile0) + out), live, zero);
+      store4<VEC>((T*)((uint8_t*)((T*)A.dforget + tile0) + out), live, zero);
+      if (GATE) store4<VEC>((T*)((uint8_t*)((T*)A.dgate + tile0) + out), live, zero);
+      if (A.S.lengths && A.dinitial) none(r0 + at + t);
+    }
+    return;
+  }
+  float u[4];  // what flows into the run from behind, then into each row
+  half_reach(leave, inner, lanes, u);
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    raw_again(&f[t]);
+    raw_again(&G[t]);
+    if (GATE) {
+      raw_again(&g[t]);
+      raw_again(&x[t]);
+    }
+  }
+  auto backward = [&](auto plain) __attribute__((always_inline)) {
+    constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
     for (int t = R - 1; t >= 0; --t) {
-      const bool pad = !PLAIN && marks.pad(t);
-      if (!PLAIN && marks.final(t)) {
+      const bool has = !PLAIN && marks.wave_has(t);
+      const bool pad = has && marks.pad(t);
+      if (has && marks.final(t)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) u[c] = 0.0f;
         if (A.grad_last) row4(A.grad_last, at + t, u);
       }
-      float dx[4], dg[4];
+      float dx[4], df[4], dg[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float D = G[t].at(c) + u[c];
-        float b = na[t][c], nb;
+        float up, down, b, nb;
+        sigmoids(f[t].at(c), &up, &down);
+        b = down;
         if (GATE) {
           sigmoids(g[t].at(c), &b, &nb);
-          dg[c] = pad ? 0.0f : D * x[t].at(c) * b * nb;
+          dg[c] = D * x[t].at(c) * b * nb;
         }
-        dx[c] = pad ? 0.0f : D * b;
-        u[c] = pad ? 0.0f : a[t][c] * D;
-        v[t][c] = u[c];
+        dx[c] = D * b;
+        df[c] = D * q[t][c];
+        u[c] = up * D;
+        if (pad) dx[c] = df[c] = dg[c] = u[c] = 0.0f;
       }
-      if (!PLAIN && marks.beyond(t)) continue;
+      if (t & 1) __builtin_amdgcn_sched_barrier(0);
+      if (has && marks.beyond(t)) continue;
       const uint32_t out = out0 + t * pitch;
       store4<VEC>((T*)((uint8_t*)((T*)A.dx + tile0) + out), live, dx);
+      store4<VEC>((T*)((uint8_t*)((T*)A.dforget + tile0) + out), live, df);
       if (GATE) store4<VEC>((T*)((uint8_t*)((T*)A.dgate + tile0) + out), live, dg);
-      if (PLAIN || !A.dinitial) continue;
-      const uint32_t r = r0 + at + t;
-      // a padded sequence without rows, where its first one would lie: its last state is the initial one
-      const bool none = A.S.lengths && pad && r % A.S.t == 0;
-      if (!none && !marks.first(t)) continue;
-      const int64_t i = row_sequence(A.S, A.info, r) * A.d + channel;
+      if (!has || !A.dinitial) continue;
+      if (pad && A.S.lengths) none(r0 + at + t);
+      if (!marks.first(t)) continue;
+      float* p = A.dinitial + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (c < live) A.dinitial[i + c] = !none ? u[c] : (A.grad_last ? A.grad_last[i + c] : 0.0f);
-    }
-    if (GATE) {
-#pragma unroll
-      for (int t = 0; t < R; ++t) raw_again(&g[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      if (!PLAIN && marks.cut(t)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) h[c] = 0.0f;
-        if (A.initial && marks.first(t)) row4(A.initial, at + t, h);
-      }
-      float df[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float xx = x[t].at(c);
-        df[c] = !PLAIN && marks.pad(t) ? 0.0f : v[t][c] * na[t][c] * (GATE ? h[c] : h[c] - xx);
-        float b = na[t][c], nb;
-        if (GATE) sigmoids(g[t].at(c), &b, &nb);
-        h[c] = fmaf(a[t][c], h[c], b * xx);
-      }
-      if (PLAIN || !marks.beyond(t)) store4<VEC>((T*)((uint8_t*)((T*)A.dforget + tile0) + out0 + t * pitch), live, df);
+        if (c < live) p[c] = u[c];
     }
   };
-  if (special) gradients(std::false_type{});
-  else gradients(std::true_type{});
+  if (special) backward(std::false_type{});
+  else backward(std::true_type{});
 }
 
-template <int THREADS>
-static void (*grad_variant(int32_t dtype, bool gate, bool vec))(ScanGradArgs) {
-  if (dtype == MIPS_F32)
-    return gate ? (vec ? scan_grad_kernel<float, true, true, THREADS> : scan_grad_kernel<float, true, false, THREADS>)
-                : (vec ? scan_grad_kernel<float, false, true, THREADS> : scan_grad_kernel<float, false, false, THREADS>);
-  return gate ? (vec ? scan_grad_kernel<__bf16, true, true, THREADS> : scan_grad_kernel<__bf16, true, false, THREADS>)
-              : (vec ? scan_grad_kernel<__bf16, false, true, THREADS> : scan_grad_kernel<__bf16, false, false, THREADS>);
+template <typename T, int THREADS>
+static void (*grad_variant(bool gate, bool vec))(ScanGradArgs) {
+  return gate ? (vec ? scan_grad_kernel<T, true, true, THREADS> : scan_grad_kernel<T, true, false, THREADS>)
+              : (vec ? scan_grad_kernel<T, false, true, THREADS> : scan_grad_kernel<T, false, false, THREADS>);
 }
 
 }  // namespace mips
@@ -311,14 +277,15 @@ int mips_gated_scan_backward(const mips_sequences* seq, int32_t d, int32_t dtype
   if (grad_states) {
     if (const int rc = check_rows(grad_states, A.S, d, dtype, &A.grad)) return rc;
   }
-  const Tiling T = backward_tiling(A.S, d);
+  const Tiling T = scan_tiling(A.S, d, dtype);
   const int E = elem_bytes(dtype);
   if ((!grad_states && !grad_last) || (A.S.n > 0 && (!grad_x || !grad_forget || (gate && !grad_gate))) ||
       !aligned(grad_x, E) || !aligned(grad_forget, E) || !aligned(grad_gate, E) || !aligned(initial, 4) ||
       !aligned(grad_last, 4) || !aligned(grad_initial, 4) || !aligned(carries, 4) || !aligned(workspace, 256) ||
-      (T.chained && !carries) || ((T.chained || A.S.offsets) && !workspace))
+      !carries || ((T.chained || A.S.offsets) && !workspace))
     return MIPS_ERR_INVALID_ARG;
-  if ((T.chained || A.S.offsets) && workspace_bytes < scan_space(A.S, T, workspace).bytes) return MIPS_ERR_WORKSPACE;
+  const ScanSpace W = scan_space(A.S, T, workspace);
+  if ((T.chained || A.S.offsets) && workspace_bytes < W.bytes) return MIPS_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   A.initial = initial;
   A.grad_last = grad_last;
@@ -333,7 +300,6 @@ int mips_gated_scan_backward(const mips_sequences* seq, int32_t d, int32_t dtype
   A.tiles = T.tiles;
   A.columns = T.columns;
   A.chained = T.chained;
-  const ScanSpace W = scan_space(A.S, T, workspace);
   A.info = W.info;
   A.words = W.words;
   A.counters = W.counters;
@@ -341,11 +307,13 @@ int mips_gated_scan_backward(const mips_sequences* seq, int32_t d, int32_t dtype
   const uintptr_t V = 4 * E;
   const bool vec = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
                    (!gate || rows_by_four(A.gate, d, dtype)) && (!A.grad.p || rows_by_four(A.grad, d, dtype)) &&
-                   aligned(grad_x, V) && aligned(grad_forget, V) && aligned(grad_gate, V);
+                   aligned(carries, 16) && aligned(grad_x, V) && aligned(grad_forget, V) && aligned(grad_gate, V);
   A.flat = rows_flat(A.x, T, dtype) && rows_flat(A.forget, T, dtype) && (!gate || rows_flat(A.gate, T, dtype)) &&
            (!A.grad.p || rows_flat(A.grad, T, dtype));
-  void (*kernel)(ScanGradArgs) = T.threads == 1024 ? grad_variant<1024>(dtype, gate != nullptr, vec)
-                                                   : grad_variant<512>(dtype, gate != nullptr, vec);
+  void (*kernel)(ScanGradArgs) = nullptr;
+  if (dtype == MIPS_BF16) kernel = grad_variant<__bf16, kTileThreads>(gate != nullptr, vec);
+  else if (T.threads == kTileThreads) kernel = grad_variant<float, kTileThreads>(gate != nullptr, vec);
+  else kernel = grad_variant<float, 2 * kTileThreads>(gate != nullptr, vec);
   const uint64_t jobs = (uint64_t)T.tiles * T.columns, most = kMaxGridBlocks / 2;
   for (uint64_t j = 0; j < jobs; j += most) {
     A.block0 = (uint32_t)j;

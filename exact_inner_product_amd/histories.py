@@ -89,10 +89,10 @@ def _floats(shape: Tuple[int, int], **tensors) -> None:
             raise ValueError(f"{name} must be float32 {list(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _workspace(size, seq, d: int, what: str, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+def _workspace(what: str, seq, *sizes, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
     if workspace is not None:
         return workspace
-    nbytes = size(C.byref(seq), d)
+    nbytes = getattr(lib(), what)(C.byref(seq), *sizes)
     if nbytes == 0:
         raise MipsError(2, what)
     return empty_workspace(nbytes, device)
@@ -104,12 +104,19 @@ class GatedScan:
     """What gated_scan returns."""
     states: Optional[torch.Tensor]  # every state, of x's shape and type
     last: torch.Tensor              # float32 [b, d]: the state behind each sequence's last row
-    carries: torch.Tensor           # float32 [tiles, d]: states between tiles, for the gradient
+    carries: Optional[torch.Tensor]  # float32 [runs, d]: states between runs of rows, for the gradient
+
+
+def _runs(seq, d: int, code: int) -> int:
+    runs = lib().mips_gated_scan_carries(C.byref(seq), d, code)
+    if runs < 0:
+        raise MipsError(2, "mips_gated_scan_carries")
+    return runs
 
 
 def gated_scan(x: torch.Tensor, forget: torch.Tensor, gate: Optional[torch.Tensor] = None, *,
                offsets: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
-               initial: Optional[torch.Tensor] = None, states: bool = True,
+               initial: Optional[torch.Tensor] = None, states: bool = True, carries: bool = True,
                workspace: Optional[torch.Tensor] = None) -> GatedScan:
     """A gated linear recurrence along each sequence: h_r = a_r h_{r-1} + b_r x_r per channel, with
     a = sigmoid(forget) and b = sigmoid(gate), or 1 - a without a gate; in binary32.
@@ -117,8 +124,9 @@ def gated_scan(x: torch.Tensor, forget: torch.Tensor, gate: Optional[torch.Tenso
     x, forget, gate: float32 or bfloat16 [b, t, d] (with `lengths` [b]: padded) or, with
     `offsets` [b + 1], [n, d]; any strides (rows without unit stride along d, or that overlap, are
     copied first). initial: float32 [b, d], the state before each sequence (0 by default). With
-    states false only the last states are written. Padding is not read and has states of 0; a
-    sequence without rows has its initial state as its last one.
+    states false only the last states are written; with carries false the result has no gradient (they
+    are a quarter of x's bytes). Padding is not read and has states of 0; a sequence without rows has
+    its initial state as its last one.
     """
     seq, b, d, held = _sequences(x.shape, offsets, lengths)
     code = _code(x, "x")
@@ -130,19 +138,13 @@ def gated_scan(x: torch.Tensor, forget: torch.Tensor, gate: Optional[torch.Tenso
     forget, fr = _rows(forget)
     gate, gr = _rows(gate) if gate is not None else (None, None)
     initial = None if initial is None else initial.contiguous()
-    tiles = lib().mips_gated_scan_carries(C.byref(seq), d)
-    if tiles < 0:
-        raise MipsError(2, "mips_gated_scan_carries")
+    workspace = _workspace("mips_gated_scan_workspace_size", seq, d, code, workspace=workspace, device=dev)
     out = GatedScan(torch.empty(x.shape, dtype=x.dtype, device=dev) if states else None,
                     torch.empty((b, d), dtype=torch.float32, device=dev),
-                    torch.empty((tiles, d), dtype=torch.float32, device=dev))
-    if tiles or offsets is not None:
-        workspace = _workspace(lib().mips_gated_scan_workspace_size, seq, d, "mips_gated_scan_workspace_size",
-                               workspace, dev)
+                    torch.empty((_runs(seq, d, code), d), dtype=torch.float32, device=dev) if carries else None)
     _check(lib().mips_gated_scan(C.byref(seq), d, code, C.byref(xr), C.byref(fr), None if gr is None else C.byref(gr),
-                                 _ptr(initial), _ptr(out.states), _ptr(out.last), _ptr(out.carries) if tiles else None,
-                                 _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev)),
-           "mips_gated_scan")
+                                 _ptr(initial), _ptr(out.states), _ptr(out.last), _ptr(out.carries), _ptr(workspace),
+                                 workspace.numel(), _stream(dev)), "mips_gated_scan")
     return out
 
 
@@ -164,10 +166,9 @@ def gated_scan_backward(grad_states: Optional[torch.Tensor], grad_last: Optional
     _like(x, forget=forget, gate=gate, grad_states=grad_states)
     _floats((b, d), initial=initial, grad_last=grad_last)
     dev = x.device
-    tiles = lib().mips_gated_scan_carries(C.byref(seq), d)
-    if tiles < 0:
-        raise MipsError(2, "mips_gated_scan_carries")
-    _floats((tiles, d), carries=forward.carries)
+    if forward.carries is None:
+        raise ValueError("the gradient needs the forward pass' carries")
+    _floats((_runs(seq, d, code), d), carries=forward.carries)
     _on_gpu(dev, forget=forget, gate=gate, grad_states=grad_states, grad_last=grad_last, offsets=offsets,
             lengths=lengths, initial=initial, carries=forward.carries, workspace=workspace)
     x, xr = _rows(x)
@@ -178,13 +179,11 @@ def gated_scan_backward(grad_states: Optional[torch.Tensor], grad_last: Optional
     dx, df = (torch.empty(x.shape, dtype=x.dtype, device=dev) for _ in range(2))
     dg = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
     di = torch.empty((b, d), dtype=torch.float32, device=dev) if initial is not None else None
-    if tiles or offsets is not None:
-        workspace = _workspace(lib().mips_gated_scan_workspace_size, seq, d, "mips_gated_scan_workspace_size",
-                               workspace, dev)
+    workspace = _workspace("mips_gated_scan_workspace_size", seq, d, code, workspace=workspace, device=dev)
     _check(lib().mips_gated_scan_backward(
         C.byref(seq), d, code, C.byref(xr), C.byref(fr), None if gr is None else C.byref(gr), _ptr(initial),
-        None if sr is None else C.byref(sr), _ptr(grad_last), _ptr(carries) if tiles else None, _ptr(dx), _ptr(df),
-        _ptr(dg), _ptr(di), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev)),
+        None if sr is None else C.byref(sr), _ptr(grad_last), _ptr(carries), _ptr(dx), _ptr(df),
+        _ptr(dg), _ptr(di), _ptr(workspace), workspace.numel(), _stream(dev)),
         "mips_gated_scan_backward")
     return dx, df, dg, di
 
@@ -278,7 +277,7 @@ def pool_normalize(x: torch.Tensor, *, offsets: Optional[torch.Tensor] = None, l
     x, xr = _rows(x)
     out = Pooled(torch.empty((b, d), dtype=x.dtype, device=dev), torch.empty((b, d), dtype=torch.float32, device=dev),
                  torch.empty((b,), dtype=torch.float32, device=dev), bool(normalize))
-    workspace = _workspace(lib().mips_pool_workspace_size, seq, d, "mips_pool_workspace_size", workspace, dev)
+    workspace = _workspace("mips_pool_workspace_size", seq, d, workspace=workspace, device=dev)
     _check(lib().mips_pool_normalize(C.byref(seq), d, code, C.byref(xr), int(out.normalize), _ptr(out.vectors),
                                      _ptr(out.mean), _ptr(out.norm), _ptr(workspace), workspace.numel(), _stream(dev)),
            "mips_pool_normalize")

@@ -552,17 +552,16 @@ typedef struct mips_rows {
  *   states       device, contiguous rows of dtype in the layout of the input ([b, t, d] or [n, d]):
  *                every h, rounded once; or NULL.
  *   last         device float [b, d]: the state behind the last row; initial (or 0) without rows.
- *   carries      device float [mips_gated_scan_carries(seq, d), d]: states between tiles, for the
- *                gradient; may be NULL where that is 0. The number follows from the sizes alone.
+ *   carries      device float [mips_gated_scan_carries(seq, d, dtype), d]: states between short runs of
+ *                rows, for the gradient; or NULL. The number follows from the sizes and dtype.
  *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0 for unsupported
- *                sizes), may be NULL for dense and padded rows without carries. Calls that share one must
- *                be ordered.
+ *                sizes). Calls that share one must be ordered.
  * Rows whose elements lie in aligned groups of four (d, strides and pointers) move so, others one by one.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, index_bits, d, b or
  * rows above their limits), WORKSPACE, HIP.
  */
-MIPS_API int64_t mips_gated_scan_carries(const mips_sequences *seq, int32_t d);
-MIPS_API size_t mips_gated_scan_workspace_size(const mips_sequences *seq, int32_t d);
+MIPS_API int64_t mips_gated_scan_carries(const mips_sequences *seq, int32_t d, int32_t dtype);
+MIPS_API size_t mips_gated_scan_workspace_size(const mips_sequences *seq, int32_t d, int32_t dtype);
 MIPS_API int mips_gated_scan(const mips_sequences *seq, int32_t d, int32_t dtype, const mips_rows *x,
                              const mips_rows *forget, const mips_rows *gate, const float *initial,
                              void *states, float *last, float *carries, void *workspace,

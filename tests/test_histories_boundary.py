@@ -40,17 +40,18 @@ NO_SEQ = (dict(bits=16, lengths=0x100), dict(bits=0, offsets=0x100, n=5), dict(t
 
 
 def test_scan_sizes(L):
-    tiles = lambda q, d: L.mips_gated_scan_carries(C.byref(q), d)  # noqa: E731
-    size = lambda q, d: L.mips_gated_scan_workspace_size(C.byref(q), d)  # noqa: E731
-    assert tiles(seq(4096, t=127), 128) == 0          # whole sequences in a tile
-    assert tiles(seq(1, t=1), 16384) == 0
-    assert tiles(seq(2, t=1280), 128) > 1
-    assert tiles(seq(2, 32, 0, 10, 0x100), 128) == 0 and tiles(seq(2, 32, 0, 100000, 0x100), 128) > 1
+    tiles = lambda q, d, t=BF16: L.mips_gated_scan_carries(C.byref(q), d, t)  # noqa: E731
+    size = lambda q, d, t=BF16: L.mips_gated_scan_workspace_size(C.byref(q), d, t)  # noqa: E731
+    for q, n in ((seq(4096, t=127), 4096 * 127), (seq(1, t=1), 1), (seq(2, t=1280), 2560), (seq(2, 32, 0, 10, 0x100), 10),
+                 (seq(2, 32, 0, 100000, 0x100), 100000)):
+        for d in (1, 128, 16384):
+            assert n <= 8 * tiles(q, d) and n <= 4 * tiles(q, d, F32)   # a state for every 8 or 4 rows at least
     for bad in BAD_SEQ + NO_SEQ:
         assert tiles(seq(**bad), 64) == -1 and size(seq(**bad), 64) == 0, bad
     assert tiles(seq(), 0) == -1 and tiles(seq(), 16385) == -1 and size(seq(), 0) == 0
-    assert L.mips_gated_scan_carries(None, 4) == -1 and L.mips_gated_scan_workspace_size(None, 4) == 0
-    assert size(seq(2, t=1280), 128) >= 8 * 128 * tiles(seq(2, t=1280), 128)
+    assert tiles(seq(), 64, FP8) == -1 and size(seq(), 64, FP8) == 0 and tiles(seq(2, t=1280), 128, F32) > 1
+    assert L.mips_gated_scan_carries(None, 4, F32) == -1 and L.mips_gated_scan_workspace_size(None, 4, F32) == 0
+    assert size(seq(2, t=1280), 128) >= 8 * 128 * 2560 // 128 and size(seq(2, 32, 0, 100000, 0x100), 128) >= 400000
 
 
 def test_scan_refusals(L):
@@ -63,16 +64,17 @@ def test_scan_refusals(L):
     for bad in [dict(s=seq(**b)) for b in BAD_SEQ] + [dict(s=None), dict(d=0), dict(x=None), dict(f=None), dict(last=None),
                 dict(x=rows(None)), dict(x=rows(0x1001)), dict(f=rows(0x2000, 63)), dict(g=rows(0x3000, 64, 63)),
                 dict(init=0x4002), dict(states=0x5001), dict(last=0x6002), dict(ws=0x10010), dict(dt=F32, x=rows(0x1002)),
-                dict(s=seq(t=1280)), dict(s=seq(t=1280), carries=0x7000), dict(s=seq(t=1280), ws=0x10000, wsb=1 << 20)]:
+                dict(carries=0x7002), dict(s=seq(t=1280)), dict(s=seq(4, 32, 0, 200, 0x100))]:
         assert call(**bad) == INVALID, bad
     for bad in [dict(s=seq(**b)) for b in NO_SEQ] + [dict(dt=FP8), dict(d=16385, x=rows(row=1 << 20, step=1 << 30))]:
         assert call(**bad) == UNSUPPORTED, bad
-    assert call(s=seq(t=1280), carries=0x7000, ws=0x10000, wsb=1024) == WORKSPACE
+    assert call(s=seq(t=1280), ws=0x10000, wsb=1024) == WORKSPACE
+    assert call(s=seq(4, 32, 0, 200, 0x100), ws=0x10000, wsb=512) == WORKSPACE
 
 
 def test_scan_backward_refusals(L):
     def call(s=seq(), d=64, dt=BF16, x=rows(), f=rows(0x2000), g=rows(0x3000), init=0x4000, gs=rows(0x5000), gl=0x6000,
-             carries=None, dx=0x7000, df=0x8000, dg=0x9000, di=0xA000, ws=None, wsb=0):
+             carries=0xB000, dx=0x7000, df=0x8000, dg=0x9000, di=0xA000, ws=None, wsb=0):
         ref = lambda v: None if v is None else C.byref(v)  # noqa: E731
         return L.mips_gated_scan_backward(ref(s), d, dt, ref(x), ref(f), ref(g), vp(init), ref(gs), vp(gl), vp(carries), vp(dx),
                                           vp(df), vp(dg), vp(di), vp(ws), wsb, None)
@@ -80,11 +82,11 @@ def test_scan_backward_refusals(L):
     for bad in [dict(s=seq(**b)) for b in BAD_SEQ] + [dict(s=None), dict(d=0), dict(x=None), dict(f=None), dict(gs=None, gl=None),
                 dict(gs=rows(0x5001)), dict(gl=0x6002), dict(dx=None), dict(df=None), dict(dg=None), dict(dx=0x7001),
                 dict(df=0x8001), dict(dg=0x9001), dict(di=0xA002), dict(ws=0x10010), dict(s=seq(t=1280)),
-                dict(s=seq(t=1280), carries=0xB002, ws=0x10000, wsb=1 << 20)]:
+                dict(carries=None), dict(carries=0xB002)]:
         assert call(**bad) == INVALID, bad
     for bad in [dict(s=seq(**b)) for b in NO_SEQ] + [dict(dt=FP8)]:
         assert call(**bad) == UNSUPPORTED, bad
-    assert call(s=seq(t=1280), carries=0xB000, ws=0x10000, wsb=1024) == WORKSPACE
+    assert call(s=seq(t=1280), ws=0x10000, wsb=1024) == WORKSPACE
 
 
 def test_step_refusals(L):
