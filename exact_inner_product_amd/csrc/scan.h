@@ -118,11 +118,13 @@ __device__ __forceinline__ uint64_t chain_get(const uint64_t* w) {
 // there, or k; the same for all threads. The other threads fetch words with it: those of the
 // group's tiles and of the kGroup groups before it are asked for at once, so that a link costs one
 // trip to memory where nothing is late.
+// `words`: 2 kGroup rows of `width` words in LDS.
 template <int THREADS>
-__device__ __forceinline__ float chain_link(const Chain& C, uint32_t k, uint32_t source, int channels, float a, float b) {
-  __shared__ uint64_t tiles[kGroup][128], groups[kGroup][128];
+__device__ __forceinline__ float chain_link(int tid, const Chain& C, uint32_t k, uint32_t source, int channels, float a, float b,
+                                            uint64_t* words, int width) {
   constexpr int PARTS = THREADS / 128, EACH = kGroup / PARTS;
-  const int tid = threadIdx.x, i = tid & 127, part = tid >> 7;
+  const int i = tid & 127, part = tid >> 7;
+  uint64_t *tiles = words + i, *groups = words + kGroup * width + i;
   const uint32_t group = k / kGroup, begin = group * kGroup, before = k - begin;
   const bool closes = before == kGroup - 1;
   const bool owner = tid < channels, needs = source < k;
@@ -149,15 +151,15 @@ __device__ __forceinline__ float chain_link(const Chain& C, uint32_t k, uint32_t
         __builtin_amdgcn_s_sleep(1);
         tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
       }
-      tiles[t][i] = tw[j];
+      tiles[t * width] = tw[j];
     }
   }
   __syncthreads();
   float ga = 1.0f, gb = 0.0f, va = 0.0f, vb = 0.0f;  // of the group's tiles before this one, and with it
   if (owner) {
     for (uint32_t t = low; t < before; ++t) {
-      const uint32_t m = (uint32_t)(tiles[t][i] >> 32);
-      compose(ga, gb, m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)tiles[t][i]), &ga, &gb);
+      const uint32_t m = (uint32_t)(tiles[t * width] >> 32);
+      compose(ga, gb, m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)tiles[t * width]), &ga, &gb);
     }
     compose(ga, gb, a, b, &va, &vb);
     if (closes) chain_put(own, va, vb);
@@ -173,7 +175,7 @@ __device__ __forceinline__ float chain_link(const Chain& C, uint32_t k, uint32_t
         __builtin_amdgcn_s_sleep(1);
         gw[j] = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
       }
-      groups[t][i] = gw[j];
+      groups[t * width] = gw[j];
     }
   }
   __syncthreads();
@@ -181,7 +183,7 @@ __device__ __forceinline__ float chain_link(const Chain& C, uint32_t k, uint32_t
   // back to the nearest constant (the source's group is one), and forward again
   float v = 0.0f;
   uint32_t t = 0;
-  while (t < asked && (uint32_t)(groups[t][i] >> 32) != kConstant) ++t;
+  while (t < asked && (uint32_t)(groups[t * width] >> 32) != kConstant) ++t;
   if (t == asked && asked < depth) {  // further back than the words at hand
     uint32_t from = group - asked;
     uint64_t w;
@@ -197,8 +199,8 @@ __device__ __forceinline__ float chain_link(const Chain& C, uint32_t k, uint32_t
     }
   }
   for (t = t < asked ? t + 1 : asked; t > 0; --t) {
-    const uint32_t m = (uint32_t)(groups[t - 1][i] >> 32);
-    v = apply(m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)groups[t - 1][i]), v);
+    const uint32_t m = (uint32_t)(groups[(t - 1) * width] >> 32);
+    v = apply(m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)groups[(t - 1) * width]), v);
   }
   if (closes && !(va < 0.0f)) chain_put(own, kForgets, apply(va, vb, v));
   return apply(ga, gb, v);
@@ -233,7 +235,22 @@ inline ScanSpace scan_space(const Sequences& S, const Tiling& T, void* workspace
 int scan_begin(const Sequences& S, const Tiling& T, const ScanSpace& W, int32_t d, const float* as, float* of_none,
                hipStream_t s);
 
-// The tile of this workgroup, the block'th of a call, in its column; the same for all its threads.
+// What the threads of a workgroup share.
+struct Shared {
+  float2* maps;      // [halves][width]: maps of half waves
+  float* reach;      // [halves][width]: what reaches them
+  float4* inner;     // [threads][2], fewer than 32 lanes a row only
+  uint64_t* words;   // [2 kGroup][width], chained tiles only
+};
+__host__ __device__ inline size_t shared_bytes(int threads, int width, bool chained, Shared* s, uint8_t* p) {
+  const size_t halves = threads / 32, maps = halves * width * 8, reach = halves * width * 4;
+  const size_t inner = width < 128 ? (size_t)threads * 32 : 0, words = chained ? (size_t)2 * kGroup * width * 8 : 0;
+  if (s) *s = Shared{(float2*)p, (float*)(p + maps), (float4*)(p + maps + reach), (uint64_t*)(p + maps + reach + inner)};
+  return maps + reach + inner + words;
+}
+
+// The tile of a workgroup in its column. (Workgroups that stay and take one tile after another, with
+// the next one asked for ahead, make those behind it wait until they come to it: twice the time.)
 __device__ __forceinline__ uint32_t chain_ticket(uint32_t* counters, uint32_t column) {
   __shared__ uint32_t ticket;
   if (threadIdx.x == 0) ticket = atomicAdd(counters + column * kCounterPitch, 1u);
@@ -246,12 +263,12 @@ __device__ __forceinline__ uint32_t chain_ticket(uint32_t* counters, uint32_t co
 // one run. With fewer, the runs of a half are joined by shuffles first; what a run gets of what reaches its half
 // waits in LDS meanwhile (registers are short), as it is needed only again behind the chain.
 //
-// Writes the half's map of this lane's four channels into `maps`. BACK: the argument comes from the last run.
-template <int THREADS, bool BACK>
-__device__ __forceinline__ void half_maps(const float* ra, const float* rb, int lanes, float2 (*maps)[128], float4 (*inner)[2]) {
-  const int tid = threadIdx.x, in = tid & 31, ch = (tid & (lanes - 1)) * 4;
+// Writes the half's map of this lane's four channels. BACK: the argument comes from the last run.
+template <bool BACK>
+__device__ __forceinline__ void half_maps(int tid, const float* ra, const float* rb, int lanes, const Shared& M) {
+  const int in = tid & 31;
+  float4* p = (float4*)(M.maps + (tid >> 5) * lanes * 4 + (tid & (lanes - 1)) * 4);
   if (lanes == 32) {
-    float4* p = (float4*)&maps[tid >> 5][ch];
     p[0] = float4{ra[0], rb[0], ra[1], rb[1]};
     p[1] = float4{ra[2], rb[2], ra[3], rb[3]};
     return;
@@ -279,24 +296,22 @@ __device__ __forceinline__ void half_maps(const float* ra, const float* rb, int 
     ea[c] = edge ? 1.0f : pa;
     eb[c] = edge ? 0.0f : pb;
   }
-  inner[tid][0] = float4{ea[0], ea[1], ea[2], ea[3]};
-  inner[tid][1] = float4{eb[0], eb[1], eb[2], eb[3]};
+  M.inner[tid * 2] = float4{ea[0], ea[1], ea[2], ea[3]};
+  M.inner[tid * 2 + 1] = float4{eb[0], eb[1], eb[2], eb[3]};
   if (BACK ? in < lanes : in + lanes >= 32) {
-    float4* p = (float4*)&maps[tid >> 5][ch];
     p[0] = float4{xa[0], xb[0], xa[1], xb[1]};
     p[1] = float4{xa[2], xb[2], xa[3], xb[3]};
   }
 }
 // What reaches this lane's run, of what reaches its half.
-__device__ __forceinline__ void half_reach(const float (*reach)[128], const float4 (*inner)[2], int lanes, float* v) {
-  const int tid = threadIdx.x;
-  const float4 r = *(const float4*)&reach[tid >> 5][(tid & (lanes - 1)) * 4];
+__device__ __forceinline__ void half_reach(int tid, const Shared& M, int lanes, float* v) {
+  const float4 r = *(const float4*)(M.reach + (tid >> 5) * lanes * 4 + (tid & (lanes - 1)) * 4);
   v[0] = r.x;
   v[1] = r.y;
   v[2] = r.z;
   v[3] = r.w;
   if (lanes == 32) return;
-  const float4 a = inner[tid][0], b = inner[tid][1];
+  const float4 a = M.inner[tid * 2], b = M.inner[tid * 2 + 1];
   v[0] = apply(a.x, b.x, v[0]);
   v[1] = apply(a.y, b.y, v[1]);
   v[2] = apply(a.z, b.z, v[2]);

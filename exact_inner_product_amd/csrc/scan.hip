@@ -21,7 +21,6 @@ struct ScanArgs {
   int32_t lanes_log2;
   uint32_t rows, tiles, columns;
   uint32_t block0;       // of this launch
-  int32_t chained;
   int32_t flat;          // load_flat serves
 };
 
@@ -38,16 +37,15 @@ __device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t
 // STATES: every state is wanted, and held until the one before the run is known. Else a run keeps its map and, of
 // a sequence that goes on from the run before, the map up to its final row: registers for half as
 // many waves again, where this is bound by latency (4096 x 127 x 128 with lengths: 72 -> 45 us).
-template <typename T, bool GATE, bool VEC, bool STATES, int THREADS>
-__global__ __launch_bounds__(THREADS, STATES || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
+template <typename T, bool GATE, bool VEC, bool STATES, bool CHAINED, int THREADS>
+__global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
   constexpr int R = kRun<T>, HALVES = THREADS / 32;
-  __shared__ __attribute__((aligned(16))) float2 maps[HALVES][128];
-  __shared__ __attribute__((aligned(16))) float entry[HALVES][128];  // the state before each half wave's rows
-  __shared__ float4 inner[THREADS][2];
-
+  extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
+  Shared M;
+  shared_bytes(THREADS, 4 << A.lanes_log2, CHAINED, &M, shared);
   const int tid = threadIdx.x;
   const uint32_t job = A.block0 + blockIdx.x, column = job % A.columns;
-  const uint32_t tile = A.chained ? chain_ticket(A.counters, column) : job / A.columns;
+  const uint32_t tile = CHAINED ? chain_ticket(A.counters, column) : job / A.columns;
   const uint32_t r0 = tile * A.rows;
   const uint32_t rows = min(A.rows, A.S.n - r0);
   const int width = 4 << A.lanes_log2;
@@ -64,7 +62,7 @@ __global__ __launch_bounds__(THREADS, STATES || THREADS > 512 ? 4 : 6) void scan
   const bool special = __any(marks.any());
   const bool idle = special && __all((marks.bits & ((1u << R) - 1u)) == (1u << R) - 1u);  // a wave of padding
 
-  const uint32_t source = A.chained ? chain_source(A.S, A.info, r0, A.rows, tile) : 0;
+  const uint32_t source = CHAINED ? chain_source(A.S, A.info, r0, A.rows, tile) : 0;
 
   // the run from a state of 0: P the product of the gates so far, h the state
   constexpr int KEPT = STATES ? R : 1;
@@ -154,33 +152,34 @@ __global__ __launch_bounds__(THREADS, STATES || THREADS > 512 ? 4 : 6) void scan
   float ra[4];  // the run's map
 #pragma unroll
   for (int c = 0; c < 4; ++c) ra[c] = cut < R ? kForgets : P[KEPT - 1][c];
-  half_maps<THREADS, false>(ra, h[KEPT - 1], lanes, maps, inner);
+  half_maps<false>(tid, ra, h[KEPT - 1], lanes, M);
   __syncthreads();
   // one thread a channel takes the state through the half waves (all threads doing so for their own
   // would be a tenth of the kernel's instructions)
   const int channels = min(width, A.d - c0);
+  const float2* maps = M.maps + tid;
   float v = 0.0f;
-  if (A.chained) {
+  if (CHAINED) {
     float a = 1.0f, b = 0.0f;
     if (tid < channels) {
 #pragma unroll 4
-      for (int w = 0; w < HALVES; ++w) compose(a, b, maps[w][tid].x, maps[w][tid].y, &a, &b);
+      for (int w = 0; w < HALVES; ++w) compose(a, b, maps[w * width].x, maps[w * width].y, &a, &b);
     }
     const int64_t stride = (int64_t)A.columns * width;
     const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
-    v = chain_link<THREADS>(C, tile, source, channels, a, b);
+    v = chain_link<THREADS>(tid, C, tile, source, channels, a, b, M.words, width);
   }
   if (tid < channels) {
 #pragma unroll 4
     for (int w = 0; w < HALVES; ++w) {
-      entry[w][tid] = v;
-      v = apply(maps[w][tid].x, maps[w][tid].y, v);
+      M.reach[w * width + tid] = v;
+      v = apply(maps[w * width].x, maps[w * width].y, v);
     }
   }
   __syncthreads();
   if (live <= 0) return;
   float state[4];  // before the run
-  half_reach(entry, inner, lanes, state);
+  half_reach(tid, M, lanes, state);
 
   if (A.carries && at < rows)
     store4<VEC>(A.carries + ((int64_t)tile * (THREADS >> A.lanes_log2) + (tid >> A.lanes_log2)) * A.d + channel, live, state);
@@ -317,13 +316,17 @@ int check_rows(const mips_rows* r, const Sequences& S, int32_t d, int32_t dtype,
   return MIPS_OK;
 }
 
-template <typename T, int THREADS>
-static void (*scan_variant(bool gate, bool vec, bool states))(ScanArgs) {
-  if (states)
-    return gate ? (vec ? scan_kernel<T, true, true, true, THREADS> : scan_kernel<T, true, false, true, THREADS>)
-                : (vec ? scan_kernel<T, false, true, true, THREADS> : scan_kernel<T, false, false, true, THREADS>);
-  return gate ? (vec ? scan_kernel<T, true, true, false, THREADS> : scan_kernel<T, true, false, false, THREADS>)
-              : (vec ? scan_kernel<T, false, true, false, THREADS> : scan_kernel<T, false, false, false, THREADS>);
+template <typename T, bool STATES, bool CHAINED, int THREADS>
+static void (*scan_variant(bool gate, bool vec))(ScanArgs) {
+  return gate ? (vec ? scan_kernel<T, true, true, STATES, CHAINED, THREADS> : scan_kernel<T, true, false, STATES, CHAINED, THREADS>)
+              : (vec ? scan_kernel<T, false, true, STATES, CHAINED, THREADS> : scan_kernel<T, false, false, STATES, CHAINED, THREADS>);
+}
+template <bool STATES>
+static void (*scan_kernel_of(int32_t dtype, const Tiling& T, bool gate, bool vec))(ScanArgs) {
+  if (dtype == MIPS_BF16)
+    return T.chained ? scan_variant<__bf16, STATES, true, kTileThreads>(gate, vec) : scan_variant<__bf16, STATES, false, kTileThreads>(gate, vec);
+  if (T.threads > kTileThreads) return scan_variant<float, STATES, false, 2 * kTileThreads>(gate, vec);  // never chained
+  return T.chained ? scan_variant<float, STATES, true, kTileThreads>(gate, vec) : scan_variant<float, STATES, false, kTileThreads>(gate, vec);
 }
 
 }  // namespace mips
@@ -374,7 +377,6 @@ int mips_gated_scan(const mips_sequences* seq, int32_t d, int32_t dtype, const m
   A.rows = T.rows;
   A.tiles = T.tiles;
   A.columns = T.columns;
-  A.chained = T.chained;
   A.info = W.info;
   A.words = W.words;
   A.counters = W.counters;
@@ -382,15 +384,13 @@ int mips_gated_scan(const mips_sequences* seq, int32_t d, int32_t dtype, const m
   const bool vec = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
                    (!gate || rows_by_four(A.gate, d, dtype)) && aligned(states, 4 * elem_bytes(dtype)) && aligned(carries, 16);
   A.flat = rows_flat(A.x, T, dtype) && rows_flat(A.forget, T, dtype) && (!gate || rows_flat(A.gate, T, dtype));
-  void (*kernel)(ScanArgs) = nullptr;
-  if (dtype == MIPS_BF16) kernel = scan_variant<__bf16, kTileThreads>(gate != nullptr, vec, states != nullptr);
-  else if (T.threads == kTileThreads) kernel = scan_variant<float, kTileThreads>(gate != nullptr, vec, states != nullptr);
-  else kernel = scan_variant<float, 2 * kTileThreads>(gate != nullptr, vec, states != nullptr);
+  void (*kernel)(ScanArgs) = states ? scan_kernel_of<true>(dtype, T, gate != nullptr, vec) : scan_kernel_of<false>(dtype, T, gate != nullptr, vec);
   const uint64_t jobs = (uint64_t)T.tiles * T.columns, most = kMaxGridBlocks / 2;  // up to 1024 threads each
+  const size_t lds = shared_bytes(T.threads, 4 << T.lanes_log2, T.chained, nullptr, nullptr);
   for (uint64_t j = 0; j < jobs; j += most) {
     A.block0 = (uint32_t)j;
     const uint64_t left = jobs - j;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(left < most ? left : most)), dim3(T.threads), 0, s, A);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(left < most ? left : most)), dim3(T.threads), lds, s, A);
     if (const int rc = check_launch()) return rc;
   }
   return MIPS_OK;

@@ -33,19 +33,18 @@ struct ScanGradArgs {
   int32_t lanes_log2;
   uint32_t rows, tiles, columns;
   uint32_t block0;
-  int32_t chained, flat;
+  int32_t flat;
 };
 
-template <typename T, bool GATE, bool VEC, int THREADS>
+template <typename T, bool GATE, bool VEC, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   constexpr int R = kRun<T>, HALVES = THREADS / 32;
-  __shared__ __attribute__((aligned(16))) float2 flows[HALVES][128];  // maps of the gradient, backward
-  __shared__ __attribute__((aligned(16))) float leave[HALVES][128];   // what flows into each half wave's rows from behind
-  __shared__ float4 inner[THREADS][2];
-
+  extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
+  Shared M;
+  shared_bytes(THREADS, 4 << A.lanes_log2, CHAINED, &M, shared);
   const int tid = threadIdx.x;
   const uint32_t job = A.block0 + blockIdx.x, column = job % A.columns;
-  const uint32_t step = A.chained ? chain_ticket(A.counters, column) : job / A.columns;
+  const uint32_t step = CHAINED ? chain_ticket(A.counters, column) : job / A.columns;
   const uint32_t tile = A.tiles - 1 - step;
   const uint32_t r0 = tile * A.rows;
   const uint32_t rows = min(A.rows, A.S.n - r0);
@@ -58,7 +57,7 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   const int64_t channel = c0 + ch;
   const uint32_t from = live > 0 ? ch : 0;
   const int some = live > 0 ? live : 1;
-  const uint32_t source = A.chained ? chain_source_back(A.S, A.info, r0 + rows - 1, A.rows, A.tiles, step) : 0;
+  const uint32_t source = CHAINED ? chain_source_back(A.S, A.info, r0 + rows - 1, A.rows, A.tiles, step) : 0;
 
   const Marks marks = run_marks<R>(A.S, A.info, r0, rows, at);
   const bool special = __any(marks.any());
@@ -143,26 +142,27 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   };
   if (!special) forward(std::true_type{});
   else if (!idle) forward(std::false_type{});
-  half_maps<THREADS, true>(fa, fb, lanes, flows, inner);
+  half_maps<true>(tid, fa, fb, lanes, M);
   __syncthreads();
   // one thread a channel takes the gradient through the half waves
   const int channels = min(width, A.d - c0);
+  const float2* flows = M.maps + tid;
   float v = 0.0f;
-  if (A.chained) {
+  if (CHAINED) {
     float ta = 1.0f, tb = 0.0f;
     if (tid < channels) {
 #pragma unroll 4
-      for (int w = HALVES - 1; w >= 0; --w) compose(ta, tb, flows[w][tid].x, flows[w][tid].y, &ta, &tb);
+      for (int w = HALVES - 1; w >= 0; --w) compose(ta, tb, flows[w * width].x, flows[w * width].y, &ta, &tb);
     }
     const int64_t stride = (int64_t)A.columns * width;
     const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
-    v = chain_link<THREADS>(C, step, source, channels, ta, tb);
+    v = chain_link<THREADS>(tid, C, step, source, channels, ta, tb, M.words, width);
   }
   if (tid < channels) {
 #pragma unroll 4
     for (int w = HALVES - 1; w >= 0; --w) {
-      leave[w][tid] = v;
-      v = apply(flows[w][tid].x, flows[w][tid].y, v);
+      M.reach[w * width + tid] = v;
+      v = apply(flows[w * width].x, flows[w * width].y, v);
     }
   }
   __syncthreads();
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
     return;
   }
   float u[4];  // what flows into the run from behind, then into each row
-  half_reach(leave, inner, lanes, u);
+  half_reach(tid, M, lanes, u);
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     raw_again(&f[t]);
@@ -248,10 +248,16 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   else backward(std::true_type{});
 }
 
-template <typename T, int THREADS>
+template <typename T, bool CHAINED, int THREADS>
 static void (*grad_variant(bool gate, bool vec))(ScanGradArgs) {
-  return gate ? (vec ? scan_grad_kernel<T, true, true, THREADS> : scan_grad_kernel<T, true, false, THREADS>)
-              : (vec ? scan_grad_kernel<T, false, true, THREADS> : scan_grad_kernel<T, false, false, THREADS>);
+  return gate ? (vec ? scan_grad_kernel<T, true, true, CHAINED, THREADS> : scan_grad_kernel<T, true, false, CHAINED, THREADS>)
+              : (vec ? scan_grad_kernel<T, false, true, CHAINED, THREADS> : scan_grad_kernel<T, false, false, CHAINED, THREADS>);
+}
+static void (*grad_kernel_of(int32_t dtype, const Tiling& T, bool gate, bool vec))(ScanGradArgs) {
+  if (dtype == MIPS_BF16)
+    return T.chained ? grad_variant<__bf16, true, kTileThreads>(gate, vec) : grad_variant<__bf16, false, kTileThreads>(gate, vec);
+  if (T.threads > kTileThreads) return grad_variant<float, false, 2 * kTileThreads>(gate, vec);  // never chained
+  return T.chained ? grad_variant<float, true, kTileThreads>(gate, vec) : grad_variant<float, false, kTileThreads>(gate, vec);
 }
 
 }  // namespace mips
@@ -299,7 +305,6 @@ int mips_gated_scan_backward(const mips_sequences* seq, int32_t d, int32_t dtype
   A.rows = T.rows;
   A.tiles = T.tiles;
   A.columns = T.columns;
-  A.chained = T.chained;
   A.info = W.info;
   A.words = W.words;
   A.counters = W.counters;
@@ -310,15 +315,13 @@ int mips_gated_scan_backward(const mips_sequences* seq, int32_t d, int32_t dtype
                    aligned(carries, 16) && aligned(grad_x, V) && aligned(grad_forget, V) && aligned(grad_gate, V);
   A.flat = rows_flat(A.x, T, dtype) && rows_flat(A.forget, T, dtype) && (!gate || rows_flat(A.gate, T, dtype)) &&
            (!A.grad.p || rows_flat(A.grad, T, dtype));
-  void (*kernel)(ScanGradArgs) = nullptr;
-  if (dtype == MIPS_BF16) kernel = grad_variant<__bf16, kTileThreads>(gate != nullptr, vec);
-  else if (T.threads == kTileThreads) kernel = grad_variant<float, kTileThreads>(gate != nullptr, vec);
-  else kernel = grad_variant<float, 2 * kTileThreads>(gate != nullptr, vec);
+  void (*kernel)(ScanGradArgs) = grad_kernel_of(dtype, T, gate != nullptr, vec);
   const uint64_t jobs = (uint64_t)T.tiles * T.columns, most = kMaxGridBlocks / 2;
+  const size_t lds = shared_bytes(T.threads, 4 << T.lanes_log2, T.chained, nullptr, nullptr);
   for (uint64_t j = 0; j < jobs; j += most) {
     A.block0 = (uint32_t)j;
     const uint64_t left = jobs - j;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(left < most ? left : most)), dim3(T.threads), 0, s, A);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(left < most ? left : most)), dim3(T.threads), lds, s, A);
     if (const int rc = check_launch()) return rc;
   }
   return MIPS_OK;
