@@ -112,100 +112,6 @@ __device__ __forceinline__ uint64_t chain_get(const uint64_t* w) {
   return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// A link of the chain, all threads of a workgroup together. Thread `i` below `channels` has its channel's map
-// (a, b) of tile k; it gets the state before the tile, or 0 if the tile needs none (its map is then taken as
-// the constant b). `source`: the tile that the state comes from, one that is constant because the sequence begins
-// there, or k; the same for all threads. The other threads fetch words with it: those of the
-// group's tiles and of the kGroup groups before it are asked for at once, so that a link costs one
-// trip to memory where nothing is late.
-// `words`: 2 kGroup rows of `width` words in LDS.
-template <int THREADS>
-__device__ __forceinline__ float chain_link(int tid, const Chain& C, uint32_t k, uint32_t source, int channels, float a, float b,
-                                            uint64_t* words, int width) {
-  constexpr int PARTS = THREADS / 128, EACH = kGroup / PARTS;
-  const int i = tid & 127, part = tid >> 7;
-  uint64_t *tiles = words + i, *groups = words + kGroup * width + i;
-  const uint32_t group = k / kGroup, begin = group * kGroup, before = k - begin;
-  const bool closes = before == kGroup - 1;
-  const bool owner = tid < channels, needs = source < k;
-  if (!needs) a = kForgets;
-  if (owner) chain_put(C.tiles + k * C.stride + C.channel, a, b);
-  if (!needs && !closes) return 0.0f;
-  uint64_t* own = C.groups + group * C.stride + C.channel;
-  const uint32_t low = source > begin && !closes ? source - begin : 0u;  // tiles low .. before - 1 of the group
-  const uint32_t depth = group - min(source / kGroup, group);            // groups before it
-  const uint32_t asked = min(depth, kGroup);                             // at once, the nearest first
-  uint64_t tw[EACH], gw[EACH];
-  if (i < channels) {
-#pragma unroll
-    for (int j = 0; j < EACH; ++j) {
-      const uint32_t t = part + j * PARTS;
-      if (t >= low && t < before) tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
-      if (t < asked) gw[j] = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
-    }
-#pragma unroll
-    for (int j = 0; j < EACH; ++j) {
-      const uint32_t t = part + j * PARTS;
-      if (t < low || t >= before) continue;
-      while ((uint32_t)(tw[j] >> 32) == kEmpty) {
-        __builtin_amdgcn_s_sleep(1);
-        tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
-      }
-      tiles[t * width] = tw[j];
-    }
-  }
-  __syncthreads();
-  float ga = 1.0f, gb = 0.0f, va = 0.0f, vb = 0.0f;  // of the group's tiles before this one, and with it
-  if (owner) {
-    for (uint32_t t = low; t < before; ++t) {
-      const uint32_t m = (uint32_t)(tiles[t * width] >> 32);
-      compose(ga, gb, m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)tiles[t * width]), &ga, &gb);
-    }
-    compose(ga, gb, a, b, &va, &vb);
-    if (closes) chain_put(own, va, vb);
-  }
-  if (!needs) return 0.0f;
-  if (asked == 0) return apply(ga, gb, 0.0f);
-  if (i < channels) {
-#pragma unroll
-    for (int j = 0; j < EACH; ++j) {
-      const uint32_t t = part + j * PARTS;
-      if (t >= asked) continue;
-      while ((uint32_t)(gw[j] >> 32) == kEmpty) {
-        __builtin_amdgcn_s_sleep(1);
-        gw[j] = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
-      }
-      groups[t * width] = gw[j];
-    }
-  }
-  __syncthreads();
-  if (!owner) return 0.0f;
-  // back to the nearest constant (the source's group is one), and forward again
-  float v = 0.0f;
-  uint32_t t = 0;
-  while (t < asked && (uint32_t)(groups[t * width] >> 32) != kConstant) ++t;
-  if (t == asked && asked < depth) {  // further back than the words at hand
-    uint32_t from = group - asked;
-    uint64_t w;
-    do {
-      --from;
-      do w = chain_get(C.groups + from * C.stride + C.channel);
-      while ((uint32_t)(w >> 32) == kEmpty);
-    } while (from > group - depth && (uint32_t)(w >> 32) != kConstant);
-    for (; from < group - asked; ++from) {
-      w = chain_get(C.groups + from * C.stride + C.channel);
-      const uint32_t m = (uint32_t)(w >> 32);
-      v = apply(m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)w), v);
-    }
-  }
-  for (t = t < asked ? t + 1 : asked; t > 0; --t) {
-    const uint32_t m = (uint32_t)(groups[(t - 1) * width] >> 32);
-    v = apply(m == kConstant ? kForgets : __uint_as_float(m), __uint_as_float((uint32_t)groups[(t - 1) * width]), v);
-  }
-  if (closes && !(va < 0.0f)) chain_put(own, kForgets, apply(va, vb, v));
-  return apply(ga, gb, v);
-}
-
 // Workspace: the columns' counters (an atomic a tile on one address takes 12 ns, so they lie apart); of packed
 // rows, what is known of each (to the end of the last tile); of chained tiles the words of tiles and of
 // groups, [columns * width] each.
@@ -235,18 +141,25 @@ inline ScanSpace scan_space(const Sequences& S, const Tiling& T, void* workspace
 int scan_begin(const Sequences& S, const Tiling& T, const ScanSpace& W, int32_t d, const float* as, float* of_none,
                hipStream_t s);
 
-// What the threads of a workgroup share.
+// What the threads of a workgroup share, each row `width` long.
 struct Shared {
-  float2* maps;      // [halves][width]: maps of half waves
-  float* reach;      // [halves][width]: what reaches them
+  float2* maps;      // [halves]: maps of half waves
+  float* reach;      // [halves]: what reaches them
+  float2* parts;     // [parts]: maps of four halves in a row
   float4* inner;     // [threads][2], fewer than 32 lanes a row only
-  uint64_t* words;   // [2 kGroup][width], chained tiles only
+  float* state;      // chained tiles only: what reaches the tile
+  float2* before;    // [parts], chained tiles only: maps of some of the group's tiles
+  uint64_t* groups;  // [kGroup], chained tiles only: words of the groups before
 };
+constexpr int kPart = 4;  // halves of a part
 __host__ __device__ inline size_t shared_bytes(int threads, int width, bool chained, Shared* s, uint8_t* p) {
-  const size_t halves = threads / 32, maps = halves * width * 8, reach = halves * width * 4;
-  const size_t inner = width < 128 ? (size_t)threads * 32 : 0, words = chained ? (size_t)2 * kGroup * width * 8 : 0;
-  if (s) *s = Shared{(float2*)p, (float*)(p + maps), (float4*)(p + maps + reach), (uint64_t*)(p + maps + reach + inner)};
-  return maps + reach + inner + words;
+  const size_t halves = threads / 32, parts = halves / kPart, w = width;
+  const size_t o1 = halves * w * 8, o2 = o1 + halves * w * 4, o3 = o2 + parts * w * 8;
+  const size_t o4 = o3 + (width < 128 ? (size_t)threads * 32 : 0), o5 = o4 + (chained ? w * 8 : 0);
+  const size_t o6 = o5 + (chained ? parts * w * 8 : 0), o7 = o6 + (chained ? kGroup * w * 8 : 0);
+  if (s)
+    *s = Shared{(float2*)p, (float*)(p + o1), (float2*)(p + o2), (float4*)(p + o3), (float*)(p + o4), (float2*)(p + o5), (uint64_t*)(p + o6)};
+  return o7;
 }
 
 // The tile of a workgroup in its column. (Workgroups that stay and take one tile after another, with
@@ -316,6 +229,138 @@ __device__ __forceinline__ void half_reach(int tid, const Shared& M, int lanes, 
   v[1] = apply(a.y, b.y, v[1]);
   v[2] = apply(a.z, b.z, v[2]);
   v[3] = apply(a.w, b.w, v[3]);
+}
+
+__device__ __forceinline__ float word_a(uint64_t w) {
+  const uint32_t m = (uint32_t)(w >> 32);
+  return m == kConstant ? kForgets : __uint_as_float(m);
+}
+__device__ __forceinline__ float word_b(uint64_t w) { return __uint_as_float((uint32_t)w); }
+
+// From the maps of half waves to what reaches each, all threads of a workgroup together; begins and ends with
+// a barrier. Threads of a channel share it in parts: a part composes four halves, or four tiles.
+//
+// Chained: tile k's state is found from tile `source` on, one that is constant because the sequence begins
+// there; k itself if the tile needs no state, and its map is then taken as constant. Words of the
+// group's tiles and of the kGroup groups before it are asked for at once, so that a link costs one trip
+// to memory where nothing is late.
+template <int THREADS, bool BACK, bool CHAINED>
+__device__ __forceinline__ void join_halves(int tid, const Shared& M, const Chain& C, uint32_t k, uint32_t source,
+                                            int channels, int width) {
+  constexpr int HALVES = THREADS / 32, PARTS = HALVES / kPart, EACH = kGroup / PARTS;
+  const int i = tid & 127, part = tid >> 7;
+  const bool has = i < channels, owner = tid < channels;
+  const float2* maps = M.maps + (BACK ? HALVES - 1 - part * kPart : part * kPart) * width + i;
+  const int next = BACK ? -width : width;
+  __syncthreads();
+  float a = 1.0f, b = 0.0f;
+  if (has) {
+#pragma unroll
+    for (int w = 0; w < kPart; ++w) compose(a, b, maps[w * next].x, maps[w * next].y, &a, &b);
+    M.parts[part * width + i] = float2{a, b};
+  }
+  __syncthreads();
+  float v = 0.0f;  // what reaches the tile
+  if (CHAINED) {
+    const bool needs = source < k;
+    const uint32_t group = k / kGroup, begin = group * kGroup, before = k - begin;
+    const bool closes = before == kGroup - 1;
+    uint64_t* own = C.groups + group * C.stride + C.channel;
+    if (owner) {
+#pragma unroll
+      for (int p = 1; p < PARTS; ++p) compose(a, b, M.parts[p * width + i].x, M.parts[p * width + i].y, &a, &b);
+      if (!needs) a = kForgets;
+      chain_put(C.tiles + k * C.stride + C.channel, a, b);
+    }
+    if (needs || closes) {
+      const uint32_t low = source > begin && !closes ? source - begin : 0u;  // tiles low .. before - 1 of the group
+      const uint32_t depth = needs ? group - min(source / kGroup, group) : 0u;  // groups before it
+      const uint32_t asked = min(depth, kGroup);                                // at once, the nearest first
+      if (has) {
+        uint64_t tw[EACH], gw[EACH];
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          const uint32_t t = part * EACH + j;
+          if (t >= low && t < before) tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
+          if (t < asked) gw[j] = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
+        }
+        float ta = 1.0f, tb = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          const uint32_t t = part * EACH + j;
+          if (t < low || t >= before) continue;
+          while ((uint32_t)(tw[j] >> 32) == kEmpty) {
+            __builtin_amdgcn_s_sleep(1);
+            tw[j] = chain_get(C.tiles + (begin + t) * C.stride + C.channel);
+          }
+          compose(ta, tb, word_a(tw[j]), word_b(tw[j]), &ta, &tb);
+        }
+        M.before[part * width + i] = float2{ta, tb};
+#pragma unroll
+        for (int j = 0; j < EACH; ++j)
+          if (part * EACH + j < asked) M.groups[(part * EACH + j) * width + i] = gw[j];  // empty or not
+      }
+      __syncthreads();
+      if (owner) {
+        float ga = 1.0f, gb = 0.0f, va, vb;  // of the group's tiles before this one, and with it
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) compose(ga, gb, M.before[p * width + i].x, M.before[p * width + i].y, &ga, &gb);
+        compose(ga, gb, a, b, &va, &vb);
+        if (closes) chain_put(own, va, vb);
+        if (needs) {
+          // back to the nearest constant (the source's group is one), and forward again
+          uint32_t t = 0;
+          for (; t < asked; ++t) {
+            uint64_t w = M.groups[t * width + i];
+            if ((uint32_t)(w >> 32) == kEmpty) {
+              do {
+                __builtin_amdgcn_s_sleep(1);
+                w = chain_get(C.groups + (group - 1 - t) * C.stride + C.channel);
+              } while ((uint32_t)(w >> 32) == kEmpty);
+              M.groups[t * width + i] = w;
+            }
+            if ((uint32_t)(w >> 32) == kConstant) {
+              ++t;
+              break;
+            }
+          }
+          if (t == asked && asked < depth && (uint32_t)(M.groups[(t - 1) * width + i] >> 32) != kConstant) {
+            // further back than the words at hand
+            uint32_t from = group - asked;
+            uint64_t w;
+            do {
+              --from;
+              do w = chain_get(C.groups + from * C.stride + C.channel);
+              while ((uint32_t)(w >> 32) == kEmpty);
+            } while (from > group - depth && (uint32_t)(w >> 32) != kConstant);
+            for (; from < group - asked; ++from) {
+              w = chain_get(C.groups + from * C.stride + C.channel);
+              v = apply(word_a(w), word_b(w), v);
+            }
+          }
+          for (; t > 0; --t) {
+            const uint64_t w = M.groups[(t - 1) * width + i];
+            v = apply(word_a(w), word_b(w), v);
+          }
+          if (closes && !(va < 0.0f)) chain_put(own, kForgets, apply(va, vb, v));
+          v = apply(ga, gb, v);
+        }
+      }
+    }
+    if (owner) M.state[i] = v;
+    __syncthreads();
+    if (has) v = M.state[i];
+  }
+  if (has) {
+    for (int p = 0; p < part; ++p) v = apply(M.parts[p * width + i].x, M.parts[p * width + i].y, v);
+    float* reach = M.reach + (BACK ? HALVES - 1 - part * kPart : part * kPart) * width + i;
+#pragma unroll
+    for (int w = 0; w < kPart; ++w) {
+      reach[w * next] = v;
+      v = apply(maps[w * next].x, maps[w * next].y, v);
+    }
+  }
+  __syncthreads();
 }
 
 // -------------------------------------------------------------------- four channels

@@ -39,7 +39,7 @@ __device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t
 // many waves again, where this is bound by latency (4096 x 127 x 128 with lengths: 72 -> 45 us).
 template <typename T, bool GATE, bool VEC, bool STATES, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
-  constexpr int R = kRun<T>, HALVES = THREADS / 32;
+  constexpr int R = kRun<T>;
   extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
   Shared M;
   shared_bytes(THREADS, 4 << A.lanes_log2, CHAINED, &M, shared);
@@ -153,30 +153,9 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
 #pragma unroll
   for (int c = 0; c < 4; ++c) ra[c] = cut < R ? kForgets : P[KEPT - 1][c];
   half_maps<false>(tid, ra, h[KEPT - 1], lanes, M);
-  __syncthreads();
-  // one thread a channel takes the state through the half waves (all threads doing so for their own
-  // would be a tenth of the kernel's instructions)
-  const int channels = min(width, A.d - c0);
-  const float2* maps = M.maps + tid;
-  float v = 0.0f;
-  if (CHAINED) {
-    float a = 1.0f, b = 0.0f;
-    if (tid < channels) {
-#pragma unroll 4
-      for (int w = 0; w < HALVES; ++w) compose(a, b, maps[w * width].x, maps[w * width].y, &a, &b);
-    }
-    const int64_t stride = (int64_t)A.columns * width;
-    const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
-    v = chain_link<THREADS>(tid, C, tile, source, channels, a, b, M.words, width);
-  }
-  if (tid < channels) {
-#pragma unroll 4
-    for (int w = 0; w < HALVES; ++w) {
-      M.reach[w * width + tid] = v;
-      v = apply(maps[w * width].x, maps[w * width].y, v);
-    }
-  }
-  __syncthreads();
+  const int64_t stride = (int64_t)A.columns * width;
+  const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
+  join_halves<THREADS, false, CHAINED>(tid, M, C, tile, source, min(width, A.d - c0), width);
   if (live <= 0) return;
   float state[4];  // before the run
   half_reach(tid, M, lanes, state);

@@ -38,7 +38,7 @@ struct ScanGradArgs {
 
 template <typename T, bool GATE, bool VEC, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
-  constexpr int R = kRun<T>, HALVES = THREADS / 32;
+  constexpr int R = kRun<T>;
   extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
   Shared M;
   shared_bytes(THREADS, 4 << A.lanes_log2, CHAINED, &M, shared);
@@ -143,29 +143,9 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   if (!special) forward(std::true_type{});
   else if (!idle) forward(std::false_type{});
   half_maps<true>(tid, fa, fb, lanes, M);
-  __syncthreads();
-  // one thread a channel takes the gradient through the half waves
-  const int channels = min(width, A.d - c0);
-  const float2* flows = M.maps + tid;
-  float v = 0.0f;
-  if (CHAINED) {
-    float ta = 1.0f, tb = 0.0f;
-    if (tid < channels) {
-#pragma unroll 4
-      for (int w = HALVES - 1; w >= 0; --w) compose(ta, tb, flows[w * width].x, flows[w * width].y, &ta, &tb);
-    }
-    const int64_t stride = (int64_t)A.columns * width;
-    const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
-    v = chain_link<THREADS>(tid, C, step, source, channels, ta, tb, M.words, width);
-  }
-  if (tid < channels) {
-#pragma unroll 4
-    for (int w = HALVES - 1; w >= 0; --w) {
-      M.reach[w * width + tid] = v;
-      v = apply(flows[w * width].x, flows[w * width].y, v);
-    }
-  }
-  __syncthreads();
+  const int64_t stride = (int64_t)A.columns * width;
+  const Chain C{A.words, A.words + A.tiles * stride, stride, (uint32_t)(c0 + (tid & 127))};
+  join_halves<THREADS, true, CHAINED>(tid, M, C, step, source, min(width, A.d - c0), width);
   if (live <= 0) return;
   const int64_t tile0 = (int64_t)r0 * A.d + c0;
   const uint32_t pitch = (uint32_t)A.d * sizeof(T), out0 = at * pitch + ch * (uint32_t)sizeof(T);
