@@ -3,14 +3,14 @@
 // For events e in order: row = rows[e], h = a_e state[row] + b_e x_e, state[row] = h, out[e] = h.
 // A row that several events name gets them one after another: the first of them does the work
 // of all, so that no two workgroups touch one row. To find out, every workgroup looks through all
-// events' rows once (4 bytes each, from the caches) against a small table of hashes of its own.
+// events' rows once (4 or 8 bytes each, from the caches) against a small hash table of its own.
 #include "scan.h"
 
 namespace mips {
 
-constexpr int kEventThreads = 256;
-constexpr int kEventsMost = 64;        // events of a workgroup
-constexpr uint32_t kFilterBits = 2048;
+constexpr int kEventsMost = 128;       // events of a workgroup
+constexpr uint32_t kPlaces = 1024;     // of the workgroup's rows, by their hash
+constexpr int kLook = 16;              // events that a thread looks at together
 constexpr uint32_t kHitsMost = 1024;   // later events of a workgroup's rows that are kept in LDS
 
 struct EventArgs {
@@ -32,7 +32,7 @@ __device__ __forceinline__ int64_t event_row(const EventArgs& A, int64_t e) {
   return A.wide ? ((const int64_t*)A.ids)[e] : (int64_t)((const int32_t*)A.ids)[e];
 }
 __device__ __forceinline__ uint32_t row_hash(int64_t row) {
-  return ((uint32_t)row * 2654435761u + (uint32_t)(row >> 32) * 40503u) >> (32 - 11);
+  return ((uint32_t)row * 2654435761u + (uint32_t)(row >> 32) * 40503u) >> (32 - 10);
 }
 
 // The first event after e, below b, whose row is `row`, or b: all lanes of a group together. `hits` are the
@@ -58,16 +58,16 @@ __device__ __forceinline__ int32_t next_event(const EventArgs& A, const uint32_t
   return A.b;
 }
 
-template <typename T, bool GATE, bool VEC>
-__global__ __launch_bounds__(kEventThreads) void events_kernel(EventArgs A) {
+template <typename T, bool GATE, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
   __shared__ int64_t own[kEventsMost];
   __shared__ uint32_t earlier[kEventsMost], later[kEventsMost];
-  __shared__ uint32_t filter[kFilterBits / 32];
+  __shared__ uint32_t places[kPlaces];  // own event + 1, or 0
   __shared__ uint32_t hits[kHitsMost], nhits;
   const int tid = threadIdx.x;
   const int32_t e0 = (int32_t)blockIdx.x * A.own;
   const int count = min(A.own, A.b - e0);
-  for (int i = tid; i < (int)kFilterBits / 32; i += kEventThreads) filter[i] = 0;
+  for (int i = tid; i < (int)kPlaces; i += THREADS) places[i] = 0;
   if (tid == 0) nhits = 0;
   if (tid < count) {
     own[tid] = event_row(A, e0 + tid);
@@ -75,46 +75,64 @@ __global__ __launch_bounds__(kEventThreads) void events_kernel(EventArgs A) {
   }
   __syncthreads();
   if (tid < count) {
-    const uint32_t v = row_hash(own[tid]);
-    atomicOr(&filter[v >> 5], 1u << (v & 31));
+    // at most kEventsMost of kPlaces are taken: the search for a free one ends, and those below
+    uint32_t v = row_hash(own[tid]);
+    while (atomicCAS(&places[v], 0u, (uint32_t)tid + 1u) != 0u) v = (v + 1) & (kPlaces - 1);
   }
   __syncthreads();
-  for (int32_t e = tid; e < A.b; e += kEventThreads) {
-    const int64_t row = event_row(A, e);
-    const uint32_t v = row_hash(row);
-    if (!((filter[v >> 5] >> (v & 31)) & 1u)) continue;
-    for (int i = 0; i < count; ++i) {
-      if (own[i] != row) continue;
-      if (e < e0 + i) {
-        earlier[i] = 1;  // every writer writes the same
-      } else if (e > e0 + i) {
-        later[i] = 1;
-        const uint32_t k = atomicAdd(&nhits, 1u);
-        if (k < kHitsMost) hits[k] = (uint32_t)i << 16 | (uint32_t)e;
+  // what the group's first event reads is on its way while its row is looked for
+  const int lanes = 1 << A.lanes_log2, lane = tid & (lanes - 1), mine = tid >> A.lanes_log2;
+  float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  Raw<T> x{}, f{}, g{};
+  auto inputs = [&](int32_t e, int c0, int live) __attribute__((always_inline)) {
+    raw_load<VEC>((const T*)A.x + e * A.x_stride + c0, live, &x);
+    raw_load<VEC>((const T*)A.forget + e * A.forget_stride + c0, live, &f);
+    if (GATE) raw_load<VEC>((const T*)A.gate + e * A.gate_stride + c0, live, &g);
+  };
+  auto fetch = [&](int i, int c0, int live) __attribute__((always_inline)) {
+    load4<VEC>(A.state + own[i] * A.state_stride + c0, live, h);
+    inputs(e0 + i, c0, live);
+  };
+  if (mine < count && lane * 4 < A.d && own[mine] >= 0 && own[mine] < A.table) fetch(mine, lane * 4, min(4, A.d - lane * 4));
+
+  // many loads at once: one after another they would be most of the call
+  for (int32_t first = tid; first < A.b; first += THREADS * kLook) {
+    int64_t rows[kLook];
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) rows[u] = event_row(A, min(first + u * THREADS, A.b - 1));
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) {
+      const int32_t e = first + u * THREADS;
+      if (e >= A.b) break;
+      for (uint32_t v = row_hash(rows[u]), p; (p = places[v]) != 0u; v = (v + 1) & (kPlaces - 1)) {
+        const int i = (int)p - 1;
+        if (own[i] != rows[u]) continue;
+        if (e < e0 + i) {
+          earlier[i] = 1;  // every writer writes the same
+        } else if (e > e0 + i) {
+          later[i] = 1;
+          const uint32_t k = atomicAdd(&nhits, 1u);
+          if (k < kHitsMost) hits[k] = (uint32_t)i << 16 | (uint32_t)e;
+        }
       }
     }
   }
   __syncthreads();
 
-  const int lanes = 1 << A.lanes_log2, lane = tid & (lanes - 1);
-  for (int i = tid >> A.lanes_log2; i < count; i += kEventThreads >> A.lanes_log2) {
+  for (int i = tid >> A.lanes_log2; i < count; i += THREADS >> A.lanes_log2) {
     const int64_t row = own[i];
     const bool inside = row >= 0 && row < A.table;
     if (inside && earlier[i]) continue;
     for (int base = 0; base < A.d; base += lanes * 4) {
       const int c0 = base + lane * 4, live = min(4, A.d - c0);  // live <= 0: only looks for events
-      float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (!inside) {
-        if (live > 0) store4<VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, h);
+        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (live > 0) store4<VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, zero);
         continue;
       }
-      if (live > 0) load4<VEC>(A.state + row * A.state_stride + c0, live, h);
+      if ((i != mine || base) && live > 0) fetch(i, c0, live);
       for (int32_t e = e0 + i; e < A.b;) {
         if (live > 0) {
-          Raw<T> x, f, g;
-          raw_load<VEC>((const T*)A.x + e * A.x_stride + c0, live, &x);
-          raw_load<VEC>((const T*)A.forget + e * A.forget_stride + c0, live, &f);
-          if (GATE) raw_load<VEC>((const T*)A.gate + e * A.gate_stride + c0, live, &g);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float a, na, b, nb;
@@ -127,10 +145,17 @@ __global__ __launch_bounds__(kEventThreads) void events_kernel(EventArgs A) {
         }
         if (!later[i]) break;
         e = next_event(A, hits, nhits, i, row, e, lanes, lane);
+        if (e < A.b && live > 0) inputs(e, c0, live);
       }
       if (live > 0) store4<VEC>(A.out + row * A.out_stride + c0, live, h);
     }
   }
+}
+
+template <typename T, int THREADS>
+static void (*events_variant(bool gate, bool vec))(EventArgs) {
+  return gate ? (vec ? events_kernel<T, true, true, THREADS> : events_kernel<T, true, false, THREADS>)
+              : (vec ? events_kernel<T, false, true, THREADS> : events_kernel<T, false, false, THREADS>);
 }
 
 }  // namespace mips
@@ -156,10 +181,11 @@ extern "C" int mips_gated_step(const void* x, int64_t x_stride, const void* forg
   EventArgs A{x, forget, gate, x_stride, forget_stride, gate_stride, state, out_state, state_stride, out_stride,
               rows, ids, id_bits == 64, b, d, 0, 0, out};
   A.lanes_log2 = d > 128 ? 6 : d > 64 ? 5 : d > 32 ? 4 : d > 16 ? 3 : 2;
-  // a workgroup's events: one round of its threads, or as many as keep its look through all
-  // events below the cost of its own
-  const int round = kEventThreads >> A.lanes_log2;
-  int own = round;
+  // Large workgroups where there are many events: each looks through all of them. A workgroup's events
+  // are one round of its threads (more, one after another, are so many trips to memory) as long as that
+  // leaves no more workgroups than run at once.
+  const int threads = b > 1024 ? 1024 : 256;
+  int own = threads >> A.lanes_log2;
   while (own < kEventsMost && (int64_t)b / own > 512) own *= 2;
   A.own = own < kEventsMost ? own : kEventsMost;
   const int64_t strides = x_stride | forget_stride | (gate ? gate_stride : 0);
@@ -167,12 +193,8 @@ extern "C" int mips_gated_step(const void* x, int64_t x_stride, const void* forg
                    aligned(gate, 4 * E) && aligned(out, 4 * E) && aligned(state, 16) && out_stride % 4 == 0 &&
                    aligned(out_state, 16);
   void (*kernel)(EventArgs) = nullptr;
-  if (dtype == MIPS_F32)
-    kernel = gate ? (vec ? events_kernel<float, true, true> : events_kernel<float, true, false>)
-                  : (vec ? events_kernel<float, false, true> : events_kernel<float, false, false>);
-  else
-    kernel = gate ? (vec ? events_kernel<__bf16, true, true> : events_kernel<__bf16, true, false>)
-                  : (vec ? events_kernel<__bf16, false, true> : events_kernel<__bf16, false, false>);
-  hipLaunchKernelGGL(kernel, dim3((b + A.own - 1) / A.own), dim3(kEventThreads), 0, (hipStream_t)stream, A);
+  if (dtype == MIPS_F32) kernel = threads == 1024 ? events_variant<float, 1024>(gate != nullptr, vec) : events_variant<float, 256>(gate != nullptr, vec);
+  else kernel = threads == 1024 ? events_variant<__bf16, 1024>(gate != nullptr, vec) : events_variant<__bf16, 256>(gate != nullptr, vec);
+  hipLaunchKernelGGL(kernel, dim3((b + A.own - 1) / A.own), dim3(threads), 0, (hipStream_t)stream, A);
   return check_launch();
 }

@@ -325,7 +325,8 @@ size_t mips_gated_scan_workspace_size(const mips_sequences* seq, int32_t d, int3
   Sequences S;
   if (check_sequences(seq, &S) != MIPS_OK || d < 1 || d > MIPS_EMBEDDING_D_MAX || (dtype != MIPS_F32 && dtype != MIPS_BF16))
     return 0;
-  return scan_space(S, scan_tiling(S, d, dtype), nullptr).bytes;
+  const Tiling T = scan_tiling(S, d, dtype);
+  return T.chained || S.offsets ? scan_space(S, T, nullptr).bytes : 0;
 }
 
 int mips_gated_scan(const mips_sequences* seq, int32_t d, int32_t dtype, const mips_rows* x, const mips_rows* forget,

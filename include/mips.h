@@ -554,8 +554,8 @@ typedef struct mips_rows {
  *   last         device float [b, d]: the state behind the last row; initial (or 0) without rows.
  *   carries      device float [mips_gated_scan_carries(seq, d, dtype), d]: states between short runs of
  *                rows, for the gradient; or NULL. The number follows from the sizes and dtype.
- *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0 for unsupported
- *                sizes). Calls that share one must be ordered.
+ *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0: none is needed, or
+ *                sizes are unsupported). Calls that share one must be ordered.
  * Rows whose elements lie in aligned groups of four (d, strides and pointers) move so, others one by one.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, index_bits, d, b or
  * rows above their limits), WORKSPACE, HIP.
@@ -631,7 +631,8 @@ MIPS_API int mips_dropout(const void *x, int32_t dtype, int64_t n, double p, uin
  *   x            rows of dtype MIPS_F32 or MIPS_BF16.  d 1 .. 16384.
  *   vectors      device, [b, d] contiguous of dtype; mean device float [b, d]; norm device float
  *                [b]: the root (1 without normalize). The latter two are what the gradient needs.
- *   workspace    device, 256-byte aligned, mips_pool_workspace_size bytes (0 for unsupported sizes).
+ *   workspace    device, 256-byte aligned, mips_pool_workspace_size bytes (0: none is needed, or sizes
+ *                are unsupported). Calls that share one must be ordered.
  * mips_pool_normalize_backward -- its gradient: with g that of the vectors and u = m / norm,
  *   grad_x = (g - u (u . g)) / norm / rows of the sequence (g / norm / rows where the sum is below
  *   1e-12; g / rows without normalize), one row for all of a sequence's.

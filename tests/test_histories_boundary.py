@@ -46,6 +46,7 @@ def test_scan_sizes(L):
                  (seq(2, 32, 0, 100000, 0x100), 100000)):
         for d in (1, 128, 16384):
             assert n <= 8 * tiles(q, d) and n <= 4 * tiles(q, d, F32)   # a state for every 8 or 4 rows at least
+    assert size(seq(4096, t=127), 128) == 0 and size(seq(4096, t=127), 128, F32) == 0  # whole sequences in a tile
     for bad in BAD_SEQ + NO_SEQ:
         assert tiles(seq(**bad), 64) == -1 and size(seq(**bad), 64) == 0, bad
     assert tiles(seq(), 0) == -1 and tiles(seq(), 16385) == -1 and size(seq(), 0) == 0
@@ -135,7 +136,8 @@ def test_pool_refusals(L):
         assert call(**bad) == UNSUPPORTED and back(**bad) == UNSUPPORTED, bad
     assert call(s=seq(t=1280), wsb=256) == WORKSPACE
     size = L.mips_pool_workspace_size
-    assert size(None, 4) == 0 and size(C.byref(seq(b=0)), 4) == 0 and size(C.byref(seq()), 0) == 0 and size(C.byref(seq()), 64) > 0
+    assert size(None, 4) == 0 and size(C.byref(seq(b=0)), 4) == 0 and size(C.byref(seq()), 0) == 0 and size(C.byref(seq()), 64) == 0
+    assert size(C.byref(seq(t=1280)), 64) > 0 and size(C.byref(seq(4, 32, 0, 200, 0x100)), 64) > 0
 
 
 def test_python_refusals():
