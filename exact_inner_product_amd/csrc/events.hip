@@ -84,13 +84,14 @@ __global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
   const int lanes = 1 << A.lanes_log2, lane = tid & (lanes - 1), mine = tid >> A.lanes_log2;
   float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   Raw<T> x{}, f{}, g{};
+  const bool wide = A.d >= 4;
   auto inputs = [&](int32_t e, int c0, int live) __attribute__((always_inline)) {
-    raw_load<VEC>((const T*)A.x + e * A.x_stride + c0, live, &x);
-    raw_load<VEC>((const T*)A.forget + e * A.forget_stride + c0, live, &f);
-    if (GATE) raw_load<VEC>((const T*)A.gate + e * A.gate_stride + c0, live, &g);
+    raw_load<VEC>((const T*)A.x + e * A.x_stride + c0, live, wide, &x);
+    raw_load<VEC>((const T*)A.forget + e * A.forget_stride + c0, live, wide, &f);
+    if (GATE) raw_load<VEC>((const T*)A.gate + e * A.gate_stride + c0, live, wide, &g);
   };
   auto fetch = [&](int i, int c0, int live) __attribute__((always_inline)) {
-    load4<VEC>(A.state + own[i] * A.state_stride + c0, live, h);
+    load4<VEC>(A.state + own[i] * A.state_stride + c0, live, wide, h);
     inputs(e0 + i, c0, live);
   };
   if (mine < count && lane * 4 < A.d && own[mine] >= 0 && own[mine] < A.table) fetch(mine, lane * 4, min(4, A.d - lane * 4));
@@ -127,27 +128,29 @@ __global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
       const int c0 = base + lane * 4, live = min(4, A.d - c0);  // live <= 0: only looks for events
       if (!inside) {
         const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (live > 0) store4<VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, zero);
+        if (live > 0) store4<2 * VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, zero);
         continue;
       }
       if ((i != mine || base) && live > 0) fetch(i, c0, live);
       for (int32_t e = e0 + i; e < A.b;) {
+        // the next one's inputs are on their way while this one is applied
+        const int32_t then = later[i] ? next_event(A, hits, nhits, i, row, e, lanes, lane) : A.b;
+        const Raw<T> x0 = x, f0 = f, g0 = g;
+        if (then < A.b && live > 0) inputs(then, c0, live);
         if (live > 0) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float a, na, b, nb;
-            sigmoids(f.at(c), &a, &na);
+            sigmoids(f0.at(c), &a, &na);
             b = na;
-            if (GATE) sigmoids(g.at(c), &b, &nb);
-            h[c] = fmaf(a, h[c], b * x.at(c));
+            if (GATE) sigmoids(g0.at(c), &b, &nb);
+            h[c] = fmaf(a, h[c], b * x0.at(c));
           }
-          store4<VEC>((T*)A.h + (int64_t)e * A.d + c0, live, h);
+          store4<2 * VEC>((T*)A.h + (int64_t)e * A.d + c0, live, h);
         }
-        if (!later[i]) break;
-        e = next_event(A, hits, nhits, i, row, e, lanes, lane);
-        if (e < A.b && live > 0) inputs(e, c0, live);
+        e = then;
       }
-      if (live > 0) store4<VEC>(A.out + row * A.out_stride + c0, live, h);
+      if (live > 0) store4<2 * VEC>(A.out + row * A.out_stride + c0, live, h);
     }
   }
 }

@@ -147,10 +147,12 @@ __global__ __launch_bounds__(kPoolThreads) void pool_kernel(PoolArgs A) {
   });
 }
 
-// One workgroup a sequence: those that lie in several chunks, and packed ones without rows.
+// One workgroup a sequence: those that lie in several chunks, and packed ones without rows. A channel's
+// parts are added by kSlices threads, four in flight each, and joined in their order.
+constexpr int kJoinThreads = 1024;
 template <typename T>
-__global__ __launch_bounds__(kPoolThreads) void pool_join_kernel(PoolArgs A) {
-  __shared__ float red[kPoolWaves];
+__global__ __launch_bounds__(kJoinThreads) void pool_join_kernel(PoolArgs A) {
+  __shared__ float red[kJoinThreads / 64], part[kJoinThreads];
   const int tid = threadIdx.x;
   const int64_t s = blockIdx.x;
   uint32_t begin, end;
@@ -158,24 +160,42 @@ __global__ __launch_bounds__(kPoolThreads) void pool_join_kernel(PoolArgs A) {
   const uint32_t k0 = begin / A.chunk, k1 = end > begin ? (end - 1) / A.chunk : k0;
   if (k0 == k1 && (end > begin || A.S.t)) return;
   const float inv = end > begin ? 1.0f / (float)(end - begin) : 0.0f;
+  int span = 64;  // channels at a time
+  while (span < kJoinThreads && span < A.d) span *= 2;
+  const int slices = kJoinThreads / span, slice = tid / span;
+  const uint32_t parts = end > begin ? k1 - k0 + 1 : 0u, each = (parts + slices - 1) / slices;
   float square = 0.0f;
-  for (int c = tid; c < A.d; c += kPoolThreads) {
+  for (int c0 = 0; c0 < A.d; c0 += span) {
+    const int c = c0 + (tid & (span - 1));
     float sum = 0.0f;
-    if (end > begin) {
-      // the first chunk left it open, unless it starts there: then it was gone on with as in the others
-      sum = A.part[((int64_t)k0 * 2 + 1) * A.d + c];
-      for (uint32_t k = k0 + 1; k <= k1; ++k) sum += A.part[(int64_t)k * 2 * A.d + c];
+    if (c < A.d) {
+      const uint32_t lo = slice * each, hi = min(lo + each, parts);
+      // the first chunk left the sequence open, the others went on with it
+      auto at = [&](uint32_t j) { return A.part[((int64_t)(k0 + j) * 2 + (j == 0 ? 1 : 0)) * A.d + c]; };
+      uint32_t j = lo;
+      for (; j + 4 <= hi; j += 4) sum += (at(j) + at(j + 1)) + (at(j + 2) + at(j + 3));
+      for (; j < hi; ++j) sum += at(j);
     }
-    sum *= inv;
-    A.mean[s * A.d + c] = sum;
-    square = fmaf(sum, sum, square);
+    __syncthreads();
+    part[tid] = sum;
+    __syncthreads();
+    if (slice == 0 && c < A.d) {
+      for (int q = 1; q < slices; ++q) sum += part[q * span + tid];
+      sum *= inv;
+      A.mean[s * A.d + c] = sum;
+      square = fmaf(sum, sum, square);
+    }
   }
   square = wave_sum(square);
   if ((tid & 63) == 0) red[tid >> 6] = square;
   __syncthreads();
-  const float n = pool_norm(A, (red[0] + red[1]) + (red[2] + red[3]));
+  square = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 64; ++w) square += red[w];
+  const float n = pool_norm(A, square);
   if (tid == 0) A.norm[s] = n;
-  for (int c = tid; c < A.d; c += kPoolThreads)  // this thread wrote these
+  if (slice) return;
+  for (int c = tid; c < A.d; c += span)  // this thread wrote these
     ((T*)A.vectors)[s * A.d + c] = (T)(A.mean[s * A.d + c] / n);
 }
 
@@ -322,8 +342,8 @@ int mips_pool_normalize(const mips_sequences* seq, int32_t d, int32_t dtype, con
     if (const int rc = check_launch()) return rc;
   }
   if (joins) {
-    if (dtype == MIPS_F32) hipLaunchKernelGGL(pool_join_kernel<float>, dim3(A.S.b), dim3(kPoolThreads), 0, s, A);
-    else hipLaunchKernelGGL(pool_join_kernel<__bf16>, dim3(A.S.b), dim3(kPoolThreads), 0, s, A);
+    if (dtype == MIPS_F32) hipLaunchKernelGGL(pool_join_kernel<float>, dim3(A.S.b), dim3(kJoinThreads), 0, s, A);
+    else hipLaunchKernelGGL(pool_join_kernel<__bf16>, dim3(A.S.b), dim3(kJoinThreads), 0, s, A);
     return check_launch();
   }
   return MIPS_OK;

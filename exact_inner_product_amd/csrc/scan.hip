@@ -37,7 +37,7 @@ __device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t
 // STATES: every state is wanted, and held until the one before the run is known. Else a run keeps its map and, of
 // a sequence that goes on from the run before, the map up to its final row: registers for half as
 // many waves again, where this is bound by latency (4096 x 127 x 128 with lengths: 72 -> 45 us).
-template <typename T, bool GATE, bool VEC, bool STATES, bool CHAINED, int THREADS>
+template <typename T, bool GATE, int VEC, bool STATES, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
   constexpr int R = kRun<T>;
   extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
@@ -55,8 +55,9 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
   const int live = min(4, A.d - c0 - ch);               // <= 0: none
   const uint32_t at = (uint32_t)(tid >> A.lanes_log2) * R;  // its first row in the tile
   const int64_t channel = c0 + ch;
-  const uint32_t from = live > 0 ? ch : 0;              // lanes without channels load those of others
-  const int some = live > 0 ? live : 1;
+  const uint32_t from = live > 0 ? ch : 0;              // lanes without channels load those of the first
+  const int some = live > 0 ? live : min(4, A.d - c0);
+  const bool wide = A.d >= 4;
 
   const Marks marks = run_marks<R>(A.S, A.info, r0, rows, at);
   const bool special = __any(marks.any());
@@ -79,13 +80,13 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
   } else {
     Raw<T> x[R], f[R], g[R];
     if (A.flat) {
-      load_flat<VEC>(A.forget, r0, rows, at, c0, from, some, marks, f);
-      load_flat<VEC>(A.x, r0, rows, at, c0, from, some, marks, x);
-      if (GATE) load_flat<VEC>(A.gate, r0, rows, at, c0, from, some, marks, g);
+      load_flat<VEC>(A.forget, r0, rows, at, c0, from, some, wide, marks, f);
+      load_flat<VEC>(A.x, r0, rows, at, c0, from, some, wide, marks, x);
+      if (GATE) load_flat<VEC>(A.gate, r0, rows, at, c0, from, some, wide, marks, g);
     } else {
-      load_gaps<VEC>(A.S, A.forget, r0, rows, at, c0, from, some, marks, f);
-      load_gaps<VEC>(A.S, A.x, r0, rows, at, c0, from, some, marks, x);
-      if (GATE) load_gaps<VEC>(A.S, A.gate, r0, rows, at, c0, from, some, marks, g);
+      load_gaps<VEC>(A.S, A.forget, r0, rows, at, c0, from, some, wide, marks, f);
+      load_gaps<VEC>(A.S, A.x, r0, rows, at, c0, from, some, wide, marks, x);
+      if (GATE) load_gaps<VEC>(A.S, A.gate, r0, rows, at, c0, from, some, wide, marks, g);
     }
     auto run = [&](auto plain) __attribute__((always_inline)) {
       constexpr bool PLAIN = decltype(plain)::value;  // no row of the wave begins or ends a sequence, or is padding
@@ -234,15 +235,14 @@ static __global__ __launch_bounds__(256) void scan_begin_kernel(BeginArgs A) {
     });
   }
   if (!A.of_none) return;
-  for (int64_t s0 = wave * 64; s0 < A.S.b; s0 += waves * 64) {
-    uint32_t lo = 0, hi = 1;
-    if (s0 + lane < A.S.b) sequence_rows(A.S, s0 + lane, &lo, &hi);
-    uint64_t m = __ballot(lo == hi);
-    while (m) {
-      const int64_t s = s0 + __ffsll((unsigned long long)m) - 1;
-      m &= m - 1;
-      for (int c = lane; c < A.d; c += 64) A.of_none[s * A.d + c] = A.as ? A.as[s * A.d + c] : 0.0f;
-    }
+  const int64_t spans = (A.d + 255) / 256;
+  for (int64_t k = wave; k < A.S.b * spans; k += waves) {
+    const int64_t s = k / spans;
+    uint32_t lo, hi;
+    sequence_rows(A.S, s, &lo, &hi);
+    if (lo < hi) continue;
+    const int c0 = (int)(k - s * spans) * 256;
+    for (int c = c0 + lane; c < min(A.d, c0 + 256); c += 64) A.of_none[s * A.d + c] = A.as ? A.as[s * A.d + c] : 0.0f;
   }
 }
 
@@ -252,7 +252,7 @@ int scan_begin(const Sequences& S, const Tiling& T, const ScanSpace& W, int32_t 
   const BeginArgs A{S, W.info, T.tiles * T.rows, W.words, W.count, W.counters, T.columns, d, as, of_none};
   uint64_t blocks = (W.count + 1023) / 1024;
   if (W.info) {
-    const uint64_t rows = ((uint64_t)A.described + 4 * kDescribed - 1) / (4 * kDescribed), seqs = ((uint64_t)S.b + 255) / 256;
+    const uint64_t rows = ((uint64_t)A.described + 4 * kDescribed - 1) / (4 * kDescribed), seqs = of_none ? ((uint64_t)S.b * ((d + 255) / 256) + 3) / 4 : 0;
     blocks = blocks > rows ? blocks : rows;
     blocks = blocks > seqs ? blocks : seqs;
   }
@@ -296,12 +296,15 @@ int check_rows(const mips_rows* r, const Sequences& S, int32_t d, int32_t dtype,
 }
 
 template <typename T, bool STATES, bool CHAINED, int THREADS>
-static void (*scan_variant(bool gate, bool vec))(ScanArgs) {
-  return gate ? (vec ? scan_kernel<T, true, true, STATES, CHAINED, THREADS> : scan_kernel<T, true, false, STATES, CHAINED, THREADS>)
-              : (vec ? scan_kernel<T, false, true, STATES, CHAINED, THREADS> : scan_kernel<T, false, false, STATES, CHAINED, THREADS>);
+static void (*scan_variant(bool gate, int vec))(ScanArgs) {
+  if (vec == 2) return gate ? scan_kernel<T, true, 2, STATES, CHAINED, THREADS> : scan_kernel<T, false, 2, STATES, CHAINED, THREADS>;
+  if constexpr (std::is_same<T, __bf16>::value) {
+    if (vec == 1) return gate ? scan_kernel<T, true, 1, STATES, CHAINED, THREADS> : scan_kernel<T, false, 1, STATES, CHAINED, THREADS>;
+  }
+  return gate ? scan_kernel<T, true, 0, STATES, CHAINED, THREADS> : scan_kernel<T, false, 0, STATES, CHAINED, THREADS>;
 }
 template <bool STATES>
-static void (*scan_kernel_of(int32_t dtype, const Tiling& T, bool gate, bool vec))(ScanArgs) {
+static void (*scan_kernel_of(int32_t dtype, const Tiling& T, bool gate, int vec))(ScanArgs) {
   if (dtype == MIPS_BF16)
     return T.chained ? scan_variant<__bf16, STATES, true, kTileThreads>(gate, vec) : scan_variant<__bf16, STATES, false, kTileThreads>(gate, vec);
   if (T.threads > kTileThreads) return scan_variant<float, STATES, false, 2 * kTileThreads>(gate, vec);  // never chained
@@ -361,10 +364,11 @@ int mips_gated_scan(const mips_sequences* seq, int32_t d, int32_t dtype, const m
   A.words = W.words;
   A.counters = W.counters;
   if (const int rc = scan_begin(A.S, T, W, d, initial, last, s)) return rc;
-  const bool vec = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
+  const bool by_four = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
                    (!gate || rows_by_four(A.gate, d, dtype)) && aligned(states, 4 * elem_bytes(dtype)) && aligned(carries, 16);
   A.flat = rows_flat(A.x, T, dtype) && rows_flat(A.forget, T, dtype) && (!gate || rows_flat(A.gate, T, dtype));
-  void (*kernel)(ScanArgs) = states ? scan_kernel_of<true>(dtype, T, gate != nullptr, vec) : scan_kernel_of<false>(dtype, T, gate != nullptr, vec);
+  const int vec = rows_vec(by_four, d, dtype);
+  void (*kernel)(ScanArgs) = states ? scan_kernel_of<true>(dtype, T, gate, vec) : scan_kernel_of<false>(dtype, T, gate, vec);
   const uint64_t jobs = (uint64_t)T.tiles * T.columns, most = kMaxGridBlocks / 2;  // up to 1024 threads each
   const size_t lds = shared_bytes(T.threads, 4 << T.lanes_log2, T.chained, nullptr, nullptr);
   for (uint64_t j = 0; j < jobs; j += most) {

@@ -36,7 +36,7 @@ struct ScanGradArgs {
   int32_t flat;
 };
 
-template <typename T, bool GATE, bool VEC, bool CHAINED, int THREADS>
+template <typename T, bool GATE, int VEC, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   constexpr int R = kRun<T>;
   extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
@@ -55,8 +55,9 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   const int live = min(4, A.d - c0 - ch);
   const uint32_t at = (uint32_t)(tid >> A.lanes_log2) * R;
   const int64_t channel = c0 + ch;
-  const uint32_t from = live > 0 ? ch : 0;
-  const int some = live > 0 ? live : 1;
+  const uint32_t from = live > 0 ? ch : 0;              // lanes without channels load those of the first
+  const int some = live > 0 ? live : min(4, A.d - c0);
+  const bool wide = A.d >= 4;
   const uint32_t source = CHAINED ? chain_source_back(A.S, A.info, r0 + rows - 1, A.rows, A.tiles, step) : 0;
 
   const Marks marks = run_marks<R>(A.S, A.info, r0, rows, at);
@@ -68,18 +69,18 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   for (int t = 0; t < R; ++t) x[t] = f[t] = g[t] = G[t] = Raw<T>{};
   if (!idle) {
     if (A.flat) {
-      load_flat<VEC>(A.forget, r0, rows, at, c0, from, some, marks, f);
-      load_flat<VEC>(A.x, r0, rows, at, c0, from, some, marks, x);
-      if (GATE) load_flat<VEC>(A.gate, r0, rows, at, c0, from, some, marks, g);
-      if (A.grad.p) load_flat<VEC>(A.grad, r0, rows, at, c0, from, some, marks, G);
+      load_flat<VEC>(A.forget, r0, rows, at, c0, from, some, wide, marks, f);
+      load_flat<VEC>(A.x, r0, rows, at, c0, from, some, wide, marks, x);
+      if (GATE) load_flat<VEC>(A.gate, r0, rows, at, c0, from, some, wide, marks, g);
+      if (A.grad.p) load_flat<VEC>(A.grad, r0, rows, at, c0, from, some, wide, marks, G);
     } else {
-      load_gaps<VEC>(A.S, A.forget, r0, rows, at, c0, from, some, marks, f);
-      load_gaps<VEC>(A.S, A.x, r0, rows, at, c0, from, some, marks, x);
-      if (GATE) load_gaps<VEC>(A.S, A.gate, r0, rows, at, c0, from, some, marks, g);
-      if (A.grad.p) load_gaps<VEC>(A.S, A.grad, r0, rows, at, c0, from, some, marks, G);
+      load_gaps<VEC>(A.S, A.forget, r0, rows, at, c0, from, some, wide, marks, f);
+      load_gaps<VEC>(A.S, A.x, r0, rows, at, c0, from, some, wide, marks, x);
+      if (GATE) load_gaps<VEC>(A.S, A.gate, r0, rows, at, c0, from, some, wide, marks, g);
+      if (A.grad.p) load_gaps<VEC>(A.S, A.grad, r0, rows, at, c0, from, some, wide, marks, G);
     }
     if (at < rows)
-      load4<VEC>(A.carries + ((int64_t)tile * (THREADS >> A.lanes_log2) + (tid >> A.lanes_log2)) * A.d + c0 + from, some, h);
+      load4<VEC>(A.carries + ((int64_t)tile * (THREADS >> A.lanes_log2) + (tid >> A.lanes_log2)) * A.d + c0 + from, some, wide, h);
   }
 
   // [b, d] floats at a row's sequence, for the rows that have one
@@ -229,11 +230,14 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
 }
 
 template <typename T, bool CHAINED, int THREADS>
-static void (*grad_variant(bool gate, bool vec))(ScanGradArgs) {
-  return gate ? (vec ? scan_grad_kernel<T, true, true, CHAINED, THREADS> : scan_grad_kernel<T, true, false, CHAINED, THREADS>)
-              : (vec ? scan_grad_kernel<T, false, true, CHAINED, THREADS> : scan_grad_kernel<T, false, false, CHAINED, THREADS>);
+static void (*grad_variant(bool gate, int vec))(ScanGradArgs) {
+  if (vec == 2) return gate ? scan_grad_kernel<T, true, 2, CHAINED, THREADS> : scan_grad_kernel<T, false, 2, CHAINED, THREADS>;
+  if constexpr (std::is_same<T, __bf16>::value) {
+    if (vec == 1) return gate ? scan_grad_kernel<T, true, 1, CHAINED, THREADS> : scan_grad_kernel<T, false, 1, CHAINED, THREADS>;
+  }
+  return gate ? scan_grad_kernel<T, true, 0, CHAINED, THREADS> : scan_grad_kernel<T, false, 0, CHAINED, THREADS>;
 }
-static void (*grad_kernel_of(int32_t dtype, const Tiling& T, bool gate, bool vec))(ScanGradArgs) {
+static void (*grad_kernel_of(int32_t dtype, const Tiling& T, bool gate, int vec))(ScanGradArgs) {
   if (dtype == MIPS_BF16)
     return T.chained ? grad_variant<__bf16, true, kTileThreads>(gate, vec) : grad_variant<__bf16, false, kTileThreads>(gate, vec);
   if (T.threads > kTileThreads) return grad_variant<float, false, 2 * kTileThreads>(gate, vec);  // never chained
@@ -290,12 +294,12 @@ int mips_gated_scan_backward(const mips_sequences* seq, int32_t d, int32_t dtype
   A.counters = W.counters;
   if (const int rc = scan_begin(A.S, T, W, d, grad_last, grad_initial, s)) return rc;
   const uintptr_t V = 4 * E;
-  const bool vec = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
+  const bool by_four = rows_by_four(A.x, d, dtype) && rows_by_four(A.forget, d, dtype) &&
                    (!gate || rows_by_four(A.gate, d, dtype)) && (!A.grad.p || rows_by_four(A.grad, d, dtype)) &&
                    aligned(carries, 16) && aligned(grad_x, V) && aligned(grad_forget, V) && aligned(grad_gate, V);
   A.flat = rows_flat(A.x, T, dtype) && rows_flat(A.forget, T, dtype) && (!gate || rows_flat(A.gate, T, dtype)) &&
            (!A.grad.p || rows_flat(A.grad, T, dtype));
-  void (*kernel)(ScanGradArgs) = grad_kernel_of(dtype, T, gate != nullptr, vec);
+  void (*kernel)(ScanGradArgs) = grad_kernel_of(dtype, T, gate, rows_vec(by_four, d, dtype));
   const uint64_t jobs = (uint64_t)T.tiles * T.columns, most = kMaxGridBlocks / 2;
   const size_t lds = shared_bytes(T.threads, 4 << T.lanes_log2, T.chained, nullptr, nullptr);
   for (uint64_t j = 0; j < jobs; j += most) {
