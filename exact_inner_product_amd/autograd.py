@@ -1,8 +1,10 @@
 """The training operators as differentiable torch functions: the calls of
-exact_inner_product_amd.training with their gradients attached.
+exact_inner_product_amd.training and .histories with their gradients attached.
 
     from exact_inner_product_amd import autograd as mag
-    users = mag.embedding(table, history).mean(1)
+    events = mag.dropout(mag.embedding(table, history), 0.1, seed, step)
+    states, _ = mag.gated_scan(events, torch.nn.functional.linear(events, weight, bias), lengths=lengths)
+    users = mag.pool_normalize(states, lengths=lengths)
     logprobs, _ = mag.item_logprobs(users, items, targets, scale=1 / temperature, bias=-log_q)
     (-logprobs.mean()).backward()
 """
@@ -12,6 +14,8 @@ from typing import Optional, Tuple
 
 import torch
 
+from .histories import (GatedScan, Pooled, dropout as _dropout, gated_scan as _scan, gated_scan_backward,
+                        pool_normalize as _pool, pool_normalize_backward)
 from .training import (ItemLogprobs, embedding_grad, embedding_lookup, item_logprobs as _forward,
                        item_logprobs_backward as _backward)
 
@@ -61,3 +65,79 @@ class _Embedding(torch.autograd.Function):
 def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
     """training.embedding_lookup, differentiable in the table (a dense gradient)."""
     return _Embedding.apply(table, ids, float(scale))
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, forget, gate, initial, offsets, lengths, states, grad):
+        f = _scan(x, forget, gate, offsets=offsets, lengths=lengths, initial=initial, states=states, carries=grad)
+        ctx.save_for_backward(x, forget, gate, initial, offsets, lengths, f.carries)
+        ctx.set_materialize_grads(False)  # a result that nothing uses costs its gradient nothing
+        return f.states, f.last
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_states, grad_last):
+        if grad_states is None and grad_last is None:
+            return (None,) * 8
+        x, forget, gate, initial, offsets, lengths, carries = ctx.saved_tensors
+        dx, df, dg, di = gated_scan_backward(grad_states, grad_last, x, forget, gate, GatedScan(None, None, carries),
+                                             offsets=offsets, lengths=lengths, initial=initial)
+        return dx, df, dg, di, None, None, None, None
+
+
+def gated_scan(x: torch.Tensor, forget: torch.Tensor, gate: Optional[torch.Tensor] = None, *,
+               offsets: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+               initial: Optional[torch.Tensor] = None, states: bool = True
+               ) -> Tuple[Optional[torch.Tensor], torch.Tensor]:
+    """histories.gated_scan, differentiable in x, forget, gate and initial: (states, or None if they are
+    not wanted; the last ones, float32 [b, d])."""
+    grad = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, forget, gate, initial))
+    return _GatedScan.apply(x, forget, gate, initial, offsets, lengths, bool(states), grad)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset, counter):
+        ctx.args = (p, seed, offset)
+        # the caller advances the counter before the backward pass, which needs the value that was used
+        ctx.save_for_backward(None if counter is None else counter.clone())
+        ctx.set_materialize_grads(False)
+        return _dropout(x, p, seed, offset, residual=residual, counter=counter)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        if grad is None:
+            return (None,) * 6
+        (counter,) = ctx.saved_tensors
+        dx = _dropout(grad, *ctx.args, counter=counter) if ctx.needs_input_grad[0] else None
+        return dx, grad if ctx.needs_input_grad[1] else None, None, None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *, residual: Optional[torch.Tensor] = None,
+            counter: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """histories.dropout, differentiable in x and residual."""
+    return _Dropout.apply(x, residual, p, seed, offset, counter)
+
+
+class _Pool(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, offsets, lengths, normalize):
+        f = _pool(x, offsets=offsets, lengths=lengths, normalize=normalize)
+        ctx.save_for_backward(offsets, lengths, f.mean, f.norm)
+        ctx.shape, ctx.normalize = x.shape, normalize
+        return f.vectors
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        offsets, lengths, mean, norm = ctx.saved_tensors
+        f = Pooled(grad, mean, norm, ctx.normalize)  # (the vectors give their type and shape only)
+        return pool_normalize_backward(grad, ctx.shape, f, offsets=offsets, lengths=lengths), None, None, None
+
+
+def pool_normalize(x: torch.Tensor, *, offsets: Optional[torch.Tensor] = None,
+                   lengths: Optional[torch.Tensor] = None, normalize: bool = True) -> torch.Tensor:
+    """histories.pool_normalize's vectors, differentiable in x."""
+    return _Pool.apply(x, offsets, lengths, bool(normalize))

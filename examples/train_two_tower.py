@@ -12,7 +12,13 @@ Each step is
 Afterwards the table is packed into an index, users are searched, and the same softmax over the
 index gives the probability of their next item and its most likely alternatives.
 
-    python3 examples/train_two_tower.py [--steps 300] [--dtype f32|bf16]
+With --encoder recurrence the user is what a gated recurrence makes of the history instead,
+
+    embedding -> dropout -> gated_scan -> pool_normalize -> item_logprobs,
+
+trained through the differentiable functions, and followed event by event with gated_step.
+
+    python3 examples/train_two_tower.py [--steps 300] [--dtype f32|bf16] [--encoder mean|recurrence]
 """
 import argparse
 import math
@@ -23,6 +29,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import exact_inner_product_amd as mips  # noqa: E402
+from exact_inner_product_amd import autograd as mag  # noqa: E402
 
 GROUPS, PER, D, HISTORY, TAU = 8, 50, 16, 5, 0.1
 N = GROUPS * PER
@@ -85,11 +92,64 @@ def evaluate(table, users=256, seed=1, dtype="f32"):
             float(f.entropy.mean()))
 
 
+def encode(table, weight, bias, history, lengths, drop=0.0, seed=0, step=0):
+    """Unit vectors [b, D] of the users whose first `lengths` events are in history [b, HISTORY]."""
+    events = mag.dropout(mag.embedding(table, history), drop, seed, step)
+    states, _ = mag.gated_scan(events, torch.nn.functional.linear(events, weight, bias), lengths=lengths)
+    return mag.pool_normalize(states, lengths=lengths)
+
+
+def train_encoder(steps=300, b=128, dtype="f32", seed=0, device="cuda:0", log=print):
+    """((table, gates' weight and bias), losses) with a recurrence on the user side."""
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    params = [torch.randn(N, D, generator=gen, device=device) * 0.1, torch.randn(D, D, generator=gen, device=device) * 0.1,
+              torch.zeros(D, device=device)]
+    weight = (1.0 / torch.arange(1, PER + 1, device=device)).repeat_interleave(GROUPS)
+    log_q = torch.log(weight / weight.sum())
+    targets = torch.arange(b, device=device, dtype=torch.int32)[:, None]
+    losses = []
+    for step in range(steps):
+        history, clicked = sample(gen, b, device)
+        lengths = torch.randint(1, HISTORY + 1, (b,), generator=gen, device=device)
+        leaves = [p.to(dt).detach().requires_grad_() for p in params]
+        users = encode(*leaves, history, lengths, drop=0.1, seed=seed, step=step)
+        logprobs, _ = mag.item_logprobs(users, mag.embedding(leaves[0], clicked), targets, scale=1 / TAU,
+                                        bias=-log_q[clicked.long()])
+        loss = -logprobs.mean()
+        grads = [g.float() for g in torch.autograd.grad(loss, leaves)]
+        norm, _ = mips.clip_grad_norm(grads, 1.0)
+        for p, g in zip(params, grads):
+            p -= 0.5 * g
+        losses.append(loss.detach())
+        if log and (step + 1) % 100 == 0:
+            log(f"step {step + 1}: loss {float(losses[-1]):.3f}, gradient norm {float(norm):.3f}")
+    return params, [float(x) for x in losses]
+
+
+def follow(table, weight, bias, history, lengths):
+    """The users' states [b, D] after their events, taken one at a time as a server sees them."""
+    b = history.shape[0]
+    states = torch.zeros(b, D, device=table.device)
+    users = torch.arange(b, device=table.device)
+    for k in range(HISTORY):
+        events = mips.embedding_lookup(table, history[:, k].contiguous())
+        # a user without a k-th event is no row of the table: skipped
+        mips.gated_step(events, torch.nn.functional.linear(events, weight, bias), states, torch.where(k < lengths, users, -1))
+    return states
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=300)
     ap.add_argument("--dtype", choices=("f32", "bf16"), default="f32")
+    ap.add_argument("--encoder", choices=("mean", "recurrence"), default="mean")
     a = ap.parse_args()
+    if a.encoder == "recurrence":
+        _, losses = train_encoder(a.steps, dtype=a.dtype)
+        print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} (log of the batch: {math.log(128):.3f})")
+        sys.exit()
     table, losses = train(a.steps, dtype=a.dtype)
     hit, prob, entropy = evaluate(table, dtype=a.dtype)
     print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} (log of the batch: {math.log(128):.3f}); of the 10 best items "

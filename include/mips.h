@@ -520,7 +520,8 @@ MIPS_API int mips_logprobs_backward(const void *queries, int64_t query_stride, i
  *            or int64 [b + 1] on the device, not decreasing, in [0, n]. Rows before the first
  *            offset and behind the last one are padding. Offsets outside [0, n] are clamped;
  *            decreasing ones give meaningless results (no access leaves the buffers).
- * Padding is never read as data (it may hold anything, NaN included); in outputs it is 0.
+ * Padding is never read as data (it may hold anything, NaN included); in outputs it is 0. Outputs
+ * overlap neither inputs nor one another unless said otherwise.
  */
 typedef struct mips_sequences {
   int32_t b;           /* sequences, 1 .. MIPS_B_MAX */
@@ -556,7 +557,7 @@ typedef struct mips_rows {
  *                rows, for the gradient; or NULL. The number follows from the sizes and dtype.
  *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0: none is needed, or
  *                sizes are unsupported). Calls that share one must be ordered.
- * Rows whose elements lie in aligned groups of four (d, strides and pointers) move so, others one by one.
+ * Rows whose elements lie in aligned groups of four (d, strides and pointers) are the fastest.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, index_bits, d, b or
  * rows above their limits), WORKSPACE, HIP.
  */
