@@ -62,24 +62,35 @@ def _sequences(shape: Sequence[int], offsets: Optional[torch.Tensor], lengths: O
 
 
 def _rows(x: torch.Tensor) -> Tuple[torch.Tensor, _Rows]:
-    """x, or a copy where its rows are not runs of memory that do not overlap, and its description."""
-    if x.dim() == 2:
-        x = _rows_arg(x)
-        if _row_stride(x) > PACKED_STRIDE_MAX:
-            x = x.contiguous()
-        return x, _Rows(x.data_ptr(), _row_stride(x), 0)
-    b, t, d = x.shape
-    row, seq = x.stride(1) if t > 1 else d, x.stride(0) if b > 1 else t * d
-    if (x.stride(2) != 1 and d > 1) or row < d or seq < d:
+    """x, or a copy where its rows are not runs of memory that do not overlap, and its description.
+    (Strides are asked for once: a tenth of the smallest calls is the time that such questions take.)"""
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 2:
+        x, row = _packed(x, shape, stride)
+        if row > PACKED_STRIDE_MAX:
+            x, row = x.contiguous(), shape[1]
+        return x, _Rows(x.data_ptr(), row, 0)
+    b, t, d = shape
+    row, seq = stride[1] if t > 1 else d, stride[0] if b > 1 else t * d
+    if (stride[2] != 1 and d > 1) or row < d or seq < d:
         x = x.contiguous()
         row, seq = d, t * d
     return x, _Rows(x.data_ptr(), row, seq)
 
 
+def _packed(x: torch.Tensor, shape, stride) -> Tuple[torch.Tensor, int]:
+    """x [n, d], or a copy where its rows are not runs of memory that do not overlap, and its row stride."""
+    n, d = shape
+    if (stride[1] != 1 and d > 1) or (stride[0] < d and n > 1):
+        return x.contiguous(), d
+    return x, stride[0] if n > 1 else d
+
+
 def _like(x: torch.Tensor, **tensors) -> None:
     """The given tensors have x's shape and type."""
+    shape, dtype = x.shape, x.dtype
     for name, t in tensors.items():
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        if t is not None and (t.shape != shape or t.dtype != dtype):
             raise ValueError(f"{name} must be {x.dtype} {tuple(x.shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -195,6 +206,16 @@ def gated_scan_backward(grad_states: Optional[torch.Tensor], grad_last: Optional
     return dx, df, dg, di
 
 
+def _table(name: str, t: torch.Tensor, d: int):
+    """(shape, row stride) of a table of states."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != _F32 or len(shape) != 2 or shape[0] < 1 or shape[1] != d:
+        raise ValueError(f"{name} must be float32 [rows >= 1, {d}], got {t.dtype} {tuple(shape)}")
+    if (d > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] < d):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {stride}")
+    return shape, stride[0] if shape[0] > 1 else d
+
+
 def gated_step(x: torch.Tensor, forget: torch.Tensor, state: torch.Tensor, rows: torch.Tensor,
                gate: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """gated_scan for single events as they come: state[r] = a state[r] + b x for the events in order,
@@ -205,30 +226,32 @@ def gated_step(x: torch.Tensor, forget: torch.Tensor, state: torch.Tensor, rows:
     stride, updated in place; with `out` (the same shape, not overlapping) the changed rows are
     written there instead. rows: int32 or int64 [b]; one outside the table is padding (a state of 0).
     """
-    if x.dim() != 2 or x.shape[1] < 1:
-        raise ValueError(f"x must be [b, d >= 1], got {tuple(x.shape)}")
-    b, d = x.shape
+    shape = x.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"x must be [b, d >= 1], got {tuple(shape)}")
+    b, d = shape
     code = _code(x, "x")
     _like(x, forget=forget, gate=gate)
-    if rows.dim() != 1 or rows.shape[0] != b:
+    if rows.shape != shape[:1]:
         raise ValueError(f"rows must be [{b}], got {tuple(rows.shape)}")
-    into = state if out is None else out
-    for name, t in (("state", state), ("out", into)):
-        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] < 1 or t.shape[1] != d:
-            raise ValueError(f"{name} must be float32 [rows >= 1, {d}], got {t.dtype} {tuple(t.shape)}")
-        if (d > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < d):
-            raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {t.stride()}")
-    if into.shape != state.shape:
-        raise ValueError(f"out must be {list(state.shape)}, got {tuple(into.shape)}")
+    table, from_stride = _table("state", state, d)
+    into, to_stride = state, from_stride
+    if out is not None:
+        into, to_stride = out, _table("out", out, d)[1]
+        if out.shape != table:
+            raise ValueError(f"out must be {list(table)}, got {tuple(out.shape)}")
     dev = x.device
     _on_gpu(dev, forget=forget, gate=gate, state=state, rows=rows, out=out)
     ids, bits = _ids_arg(rows)
-    x, forget = _rows_arg(x), _rows_arg(forget)
-    gate = None if gate is None else _rows_arg(gate)
-    h = x.new_empty((b, d))
-    _check(lib().mips_gated_step(_ptr(x), _row_stride(x), _ptr(forget), _row_stride(forget), _ptr(gate),
-                                 0 if gate is None else _row_stride(gate), code, b, d, _ptr(state), _row_stride(state),
-                                 _ptr(into), _row_stride(into), state.shape[0], _ptr(ids), bits, _ptr(h), _stream(dev)),
+    x, xs = _packed(x, shape, x.stride())
+    forget, fs = _packed(forget, shape, forget.stride())
+    gp, gs = None, 0
+    if gate is not None:
+        gate, gs = _packed(gate, shape, gate.stride())
+        gp = gate.data_ptr()
+    h = x.new_empty(shape)
+    _check(lib().mips_gated_step(x.data_ptr(), xs, forget.data_ptr(), fs, gp, gs, code, b, d, state.data_ptr(), from_stride,
+                                 into.data_ptr(), to_stride, table[0], ids.data_ptr(), bits, h.data_ptr(), _stream(dev)),
            "mips_gated_step")
     torch.autograd.graph.increment_version(into)
     return h
