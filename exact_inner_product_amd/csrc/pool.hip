@@ -147,12 +147,14 @@ __global__ __launch_bounds__(kPoolThreads) void pool_kernel(PoolArgs A) {
   });
 }
 
-// One workgroup a sequence: those that lie in several chunks, and packed ones without rows. A channel's
-// parts are added by kSlices threads, four in flight each, and joined in their order.
-constexpr int kJoinThreads = 1024;
-template <typename T>
+// One workgroup a sequence: those that lie in several chunks, and packed ones without rows. W channels' parts
+// are added by several threads, eight in flight each, and joined in their order. (W = 4 where d allows it:
+// 8 sequences of 94 parts of 1024 channels take 19 us with 1, 12 with 4.)
+template <typename T, int kJoinThreads, int W>
 __global__ __launch_bounds__(kJoinThreads) void pool_join_kernel(PoolArgs A) {
-  __shared__ float red[kJoinThreads / 64], part[kJoinThreads];
+  typedef float v_t __attribute__((ext_vector_type(W)));
+  __shared__ float red[kJoinThreads / 64];
+  __shared__ v_t part[kJoinThreads];
   const int tid = threadIdx.x;
   const int64_t s = blockIdx.x;
   uint32_t begin, end;
@@ -160,20 +162,21 @@ __global__ __launch_bounds__(kJoinThreads) void pool_join_kernel(PoolArgs A) {
   const uint32_t k0 = begin / A.chunk, k1 = end > begin ? (end - 1) / A.chunk : k0;
   if (k0 == k1 && (end > begin || A.S.t)) return;
   const float inv = end > begin ? 1.0f / (float)(end - begin) : 0.0f;
-  int span = 64;  // channels at a time
-  while (span < kJoinThreads && span < A.d) span *= 2;
+  int span = 16;  // threads side by side
+  while (span < kJoinThreads && span * W < A.d) span *= 2;
   const int slices = kJoinThreads / span, slice = tid / span;
   const uint32_t parts = end > begin ? k1 - k0 + 1 : 0u, each = (parts + slices - 1) / slices;
   float square = 0.0f;
-  for (int c0 = 0; c0 < A.d; c0 += span) {
-    const int c = c0 + (tid & (span - 1));
-    float sum = 0.0f;
+  for (int c0 = 0; c0 < A.d; c0 += span * W) {
+    const int c = c0 + (tid & (span - 1)) * W;
+    v_t sum = 0.0f;
     if (c < A.d) {
       const uint32_t lo = slice * each, hi = min(lo + each, parts);
       // the first chunk left the sequence open, the others went on with it
-      auto at = [&](uint32_t j) { return A.part[((int64_t)(k0 + j) * 2 + (j == 0 ? 1 : 0)) * A.d + c]; };
+      auto at = [&](uint32_t j) { return *(const v_t*)(A.part + ((int64_t)(k0 + j) * 2 + (j == 0 ? 1 : 0)) * A.d + c); };
       uint32_t j = lo;
-      for (; j + 4 <= hi; j += 4) sum += (at(j) + at(j + 1)) + (at(j + 2) + at(j + 3));
+      for (; j + 8 <= hi; j += 8)
+        sum += ((at(j) + at(j + 1)) + (at(j + 2) + at(j + 3))) + ((at(j + 4) + at(j + 5)) + (at(j + 6) + at(j + 7)));
       for (; j < hi; ++j) sum += at(j);
     }
     __syncthreads();
@@ -181,9 +184,12 @@ __global__ __launch_bounds__(kJoinThreads) void pool_join_kernel(PoolArgs A) {
     __syncthreads();
     if (slice == 0 && c < A.d) {
       for (int q = 1; q < slices; ++q) sum += part[q * span + tid];
-      sum *= inv;
-      A.mean[s * A.d + c] = sum;
-      square = fmaf(sum, sum, square);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float m = sum[e] * inv;
+        A.mean[s * A.d + c + e] = m;
+        square = fmaf(m, m, square);
+      }
     }
   }
   square = wave_sum(square);
@@ -195,8 +201,9 @@ __global__ __launch_bounds__(kJoinThreads) void pool_join_kernel(PoolArgs A) {
   const float n = pool_norm(A, square);
   if (tid == 0) A.norm[s] = n;
   if (slice) return;
-  for (int c = tid; c < A.d; c += span)  // this thread wrote these
-    ((T*)A.vectors)[s * A.d + c] = (T)(A.mean[s * A.d + c] / n);
+  for (int c0 = tid * W; c0 < A.d; c0 += span * W)  // this thread wrote these
+#pragma unroll
+    for (int e = 0; e < W; ++e) ((T*)A.vectors)[s * A.d + c0 + e] = (T)(A.mean[s * A.d + c0 + e] / n);
 }
 
 // One wave a chunk of rows, each sequence's row of gradients computed again for every chunk.
@@ -251,22 +258,28 @@ __global__ __launch_bounds__(kPoolThreads) void pool_grad_kernel(PoolArgs A) {
       fill(lo, hi, at, live, v);
       return;
     }
-    float dot = 0.0f, square = 0.0f;
-    if (A.normalize) {
-      for (int c = lane; c < A.d; c += 64) {
-        dot = fmaf(m[c], (float)g[c], dot);
-        square = fmaf(m[c], m[c], square);
+    // several spans: their channels are read again for the results
+    auto read = [&](int c, int live, float* mv, float* gv) {
+      row8<float, VEC>(m + c, live, mv);
+      if (VEC && A.grad_aligned) row8<T, VEC>(g + c, live, gv);
+      else row8<T, false>(g + c, live, gv);
+    };
+    float mv[8], gv[8], dot = 0.0f, square = 0.0f;
+    for (int c = at; c < A.d && A.normalize; c += lanes * 8) {
+      read(c, min(8, A.d - c), mv, gv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dot = fmaf(mv[e], gv[e], dot);
+        square = fmaf(mv[e], mv[e], square);
       }
-      dot = wave_sum(dot);
-      square = wave_sum(square);
     }
-    const float t = along(dot, square);
-    for (int c0 = 0; c0 < A.d; c0 += lanes * 8) {
-      const int c = c0 + at, live = min(8, A.d - c);
-      if (live <= 0) continue;
+    const float t = along(wave_sum(dot), wave_sum(square));
+    for (int c = at; c < A.d; c += lanes * 8) {
+      const int live = min(8, A.d - c);
+      read(c, live, mv, gv);
       float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < live ? ((float)g[c + e] - m[c + e] * t) / n * inv : 0.0f;
+      for (int e = 0; e < 8; ++e) v[e] = (gv[e] - mv[e] * t) / n * inv;
       fill(lo, hi, c, live, v);
     }
   });
@@ -276,22 +289,38 @@ __global__ __launch_bounds__(kPoolThreads) void pool_grad_kernel(PoolArgs A) {
   }
 }
 
-// Rows of a wave: whole sequences where dense ones are short, else a length that leaves waves
-// enough to fill the card and few parts to join.
-static uint32_t pool_chunk(const Sequences& S) {
-  if (S.t && S.t <= 256) return S.t >= 32 ? S.t : 32 / S.t * S.t;
-  const uint32_t rows = S.n / 4096;
-  return rows < 64 ? 64 : (rows > 1024 ? 1024 : rows);
+// Whether every sequence is pooled whole by one wave: short dense ones, longer ones where there are waves
+// enough without cutting them.
+static bool pool_whole(const Sequences& S, int32_t d) {
+  return S.t && S.t <= 256 && (S.b >= 1024 || (int64_t)S.t * d <= 8192);
 }
-static bool pool_joins(const Sequences& S) { return !(S.t && S.t <= 256); }
+// Rows of a wave. Sequences are few microseconds of latency each, so few go to one wave where they are
+// short (2147 packed ones of up to two rows: 16 a wave take 20 us, 4 take 8). Cut ones: as many rows as leave
+// 4096 waves, but few parts to join, fewer where rows are wide.
+static uint32_t pool_chunk(const Sequences& S, int32_t d) {
+  if (pool_whole(S, d)) {
+    const uint32_t rows = S.n / 8192;
+    return rows < 32 ? (rows > S.t ? rows / S.t * S.t : S.t) : (S.t >= 32 ? S.t : 32 / S.t * S.t);
+  }
+  const uint32_t mean = S.n / S.b, wide = d > 512 ? 16 : 8192 / d;
+  uint32_t least = mean < 4 ? 4 : (mean > 64 ? 64 : mean);
+  if (wide < least) least = wide > 16 ? wide : (least < 16 ? least : 16);
+  const uint32_t rows = S.n / 4096;
+  return rows < least ? least : (rows > 1024 ? 1024 : rows);
+}
+template <typename T>
+static void (*join_kernel_of(bool few, int32_t d))(PoolArgs) {
+  if (d % 4) return few ? pool_join_kernel<T, 128, 1> : pool_join_kernel<T, 1024, 1>;
+  return few ? pool_join_kernel<T, 128, 4> : pool_join_kernel<T, 1024, 4>;
+}
 static int pool_lanes(int32_t d) {
   int lanes = 1;
   while (lanes < 64 && lanes * 8 < d) lanes *= 2;
   return lanes;
 }
 static size_t pool_bytes(const Sequences& S, int32_t d) {
-  if (!pool_joins(S)) return 0;
-  const uint32_t chunk = pool_chunk(S);
+  if (pool_whole(S, d)) return 0;
+  const uint32_t chunk = pool_chunk(S, d);
   return 256 + ((size_t)S.n + chunk - 1) / chunk * 2 * d * sizeof(float);
 }
 
@@ -316,7 +345,7 @@ int mips_pool_normalize(const mips_sequences* seq, int32_t d, int32_t dtype, con
   if (d > MIPS_EMBEDDING_D_MAX || (dtype != MIPS_F32 && dtype != MIPS_BF16)) return MIPS_ERR_UNSUPPORTED;
   if (const int rc = check_rows(x, A.S, d, dtype, &A.x)) return rc;
   const int E = elem_bytes(dtype);
-  const bool joins = pool_joins(A.S);
+  const bool joins = !pool_whole(A.S, d);
   if (!vectors || !mean || !norm || !aligned(vectors, E) || !aligned(mean, 4) || !aligned(norm, 4) ||
       !aligned(workspace, 256) || (joins && !workspace))
     return MIPS_ERR_INVALID_ARG;
@@ -325,7 +354,7 @@ int mips_pool_normalize(const mips_sequences* seq, int32_t d, int32_t dtype, con
   A.d = d;
   A.lanes = pool_lanes(d);
   A.normalize = normalize != 0;
-  A.chunk = pool_chunk(A.S);
+  A.chunk = pool_chunk(A.S, d);
   A.chunks = (uint32_t)(((uint64_t)A.S.n + A.chunk - 1) / A.chunk);
   A.part = (float*)workspace;
   A.vectors = vectors;
@@ -342,8 +371,10 @@ int mips_pool_normalize(const mips_sequences* seq, int32_t d, int32_t dtype, con
     if (const int rc = check_launch()) return rc;
   }
   if (joins) {
-    if (dtype == MIPS_F32) hipLaunchKernelGGL(pool_join_kernel<float>, dim3(A.S.b), dim3(kJoinThreads), 0, s, A);
-    else hipLaunchKernelGGL(pool_join_kernel<__bf16>, dim3(A.S.b), dim3(kJoinThreads), 0, s, A);
+    // (sequences of few parts leave most of 1024 threads idle: 4000 of 15 rows: 21 us, with 128 5)
+    const bool few = A.chunks < 32u * (uint32_t)A.S.b;
+    void (*join)(PoolArgs) = dtype == MIPS_F32 ? join_kernel_of<float>(few, d) : join_kernel_of<__bf16>(few, d);
+    hipLaunchKernelGGL(join, dim3(A.S.b), dim3(few ? 128 : 1024), 0, s, A);
     return check_launch();
   }
   return MIPS_OK;
@@ -369,7 +400,8 @@ int mips_pool_normalize_backward(const mips_sequences* seq, int32_t d, int32_t d
   A.grad = grad;
   A.grad_stride = grad_stride;
   A.dx = grad_x;
-  A.chunk = 64;  // rows that share one row's gradient (4096 x 127 x 128 bf16: 34 us with 32)
+  // rows that share one row's gradient: 64 where that leaves 8192 waves (4096 x 127 x 128 bf16: 34 us with 32)
+  A.chunk = A.S.n / 8192 < 4 ? 4 : (A.S.n / 8192 > 64 ? 64 : A.S.n / 8192);
   A.grad_aligned = grad_stride * E % 16 == 0 && aligned(grad, 16);
   while (A.chunk < 1024 && A.S.n / A.chunk > 65536) A.chunk *= 2;
   A.chunks = (uint32_t)(((uint64_t)A.S.n + A.chunk - 1) / A.chunk);

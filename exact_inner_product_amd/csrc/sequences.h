@@ -63,6 +63,13 @@ __device__ __forceinline__ void sequence_rows(const Sequences& S, int64_t s, uin
   }
 }
 
+// One wave's LDS accesses stay in order; this keeps the compiler from moving them.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Calls f(s, begin, end) for the sequences with rows in [r0, r1), those of a wave together. Dense ones
 // come with rows of padding or none too, packed ones only with rows.
 template <typename F>
