@@ -143,3 +143,30 @@ def test_agrees_with_l2_normalize():
     x = torch.randn(1000, 128, device=dev)
     got = mips.pool_normalize(x[:, None]).vectors
     assert torch.allclose(got, mips.l2_normalize(x), rtol=136 * 2.0 ** -24, atol=0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [2, 7, 8, 9, 12, 15, 17, 63, 65, 513, 1031])
+def test_widths(d, dtype):
+    """Widths beside those that move by eight, whole sequences and ones that are joined."""
+    dev = _dev()
+    rng = np.random.default_rng(d)
+    for b, t in ((3, 5), (2, 400)):
+        x = torch.from_numpy(rng.standard_normal((b, t, d)).astype(np.float32)).to(DT[dtype])
+        g = torch.from_numpy(rng.standard_normal((b, d)).astype(np.float32)).to(DT[dtype])
+        n = torch.tensor([t] + [t // 3] * (b - 1))
+        f = mips.pool_normalize(x.to(dev), lengths=n.to(dev))
+        dx = mips.pool_normalize_backward(g.to(dev), x.shape, f, lengths=n.to(dev))
+        for s in range(b):
+            k = int(n[s])
+            rows = x[s, :k].double()
+            m = rows.mean(0)
+            norm = float(m.norm())
+            u = m / norm
+            # the mean is off by (k + 3) u of the rows' mean size at most, the norm's sum by d u more
+            room = (k + 3 + d + 8) * 2.0 ** -24 * rows.abs().mean(0).norm() / norm
+            half = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+            assert (f.vectors[s].cpu().double() - u).abs().max() <= room + half
+            want = (g[s].double() - u * float(u @ g[s].double())) / norm / k
+            err = (dx[s].cpu().double() - torch.cat([want.expand(k, d), torch.zeros(t - k, d, dtype=torch.float64)])).abs().max()
+            assert err <= (4 * room + half) * g[s].double().norm() / norm / k
