@@ -4,6 +4,10 @@
 // A row that several events name gets them one after another: the first of them does the work
 // of all, so that no two workgroups touch one row. To find out, every workgroup looks through all
 // events' rows once (4 or 8 bytes each, from the caches) against a small hash table of its own.
+//
+// Bound by latency: ids, the look through them while the first events' rows arrive, one round of
+// arithmetic. 4096 events x 128 bf16 of a million rows with gates take 6.5 us in a graph (8 MB), 16 of
+// any 4.4; 65,536 take 90, mostly looking. Events of one row are a trip to memory each: 13,236 of 1265 rows 46.
 #include "scan.h"
 
 namespace mips {

@@ -3,9 +3,10 @@
 //   h_r = a_r h_{r-1} + b_r x_r,   a = sigmoid(forget),  b = sigmoid(-forget) or sigmoid(gate)
 //
 // is the composition of affine maps of the state, (A, B): h -> A h + B, which is associative. A
-// workgroup takes a tile: kTileRows(lanes) rows by up to 128 channels, 4 channels a thread and
-// a few rows in a run, all in registers. Runs are joined across the lanes of a wave by shuffles,
-// across the waves in LDS, and tiles by a chain through memory (below).
+// workgroup takes a tile: 512 threads, 4 channels and a run of rows each, all in registers, so
+// 128 rows by 128 channels in bf16. Runs are joined across the halves of a wave and its waves in LDS, tiles
+// by a chain through memory (below). Each tensor moves once; a thread alone down a channel would move
+// them as often, but 4096 x 128 channels are too few threads to fill the memory's queues.
 #pragma once
 
 #include "sequences.h"
@@ -464,7 +465,6 @@ __device__ __forceinline__ Marks run_marks(const Sequences& S, const int32_t* pa
       const i32x4_t v = *(const i32x4_t*)(packed + r + t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // (a row that broken offsets leave out has whatever lay there)
         pad |= (uint32_t)((uint32_t)v[e] >= (uint32_t)S.b << 2) << (t + e);
         cut |= (uint32_t)(v[e] & kFirst) << (t + e);
         final |= (uint32_t)(v[e] & kFinal) >> 1 << (t + e);
@@ -479,6 +479,21 @@ __device__ __forceinline__ Marks run_marks(const Sequences& S, const int32_t* pa
         cut |= (uint32_t)(pos == 0) << t;
         pos = pos + 1 == S.t ? 0 : pos + 1;
         final |= (uint32_t)(pos == 0) << t;
+      }
+    } else if (S.t >= (uint32_t)R) {  // rows of at most two sequences
+      auto below = [](uint32_t n) { return (1u << min(n, (uint32_t)R)) - 1u; };
+      if (here) {
+        const uint32_t split = S.t - pos, len = index_at(S.lengths, S.wide, s, S.t);
+        const uint32_t some = len > pos ? len - pos : 0u;  // rows of the first one, at most split
+        cut = pos == 0;
+        pad = below(split) & ~below(some);
+        final = some && some <= (uint32_t)R ? 1u << (some - 1) : 0u;
+        if (split < here) {
+          const uint32_t more = split + index_at(S.lengths, S.wide, s + 1, S.t);
+          cut |= 1u << split;
+          pad |= below(R) & ~below(more);
+          if (more > split && more <= (uint32_t)R) final |= 1u << (more - 1);
+        }
       }
     } else {
       uint32_t len = 0;
@@ -497,6 +512,15 @@ __device__ __forceinline__ Marks run_marks(const Sequences& S, const int32_t* pa
   pad |= beyond;
   final &= ~pad;
   return Marks{pad | beyond << 8 | (cut | pad) << 16 | final << 24};
+}
+
+// Padded sequences: a run's rows, from row r on, where sequences without rows would begin. A bit each.
+template <int R>
+__device__ __forceinline__ uint32_t run_nones(const Sequences& S, uint32_t r, const Marks& marks) {
+  uint32_t first = 0;
+  const uint32_t pos = r % S.t;
+  for (uint32_t t = pos ? S.t - pos : 0u; t < (uint32_t)R; t += S.t) first |= 1u << t;
+  return first & marks.bits & ~(marks.bits >> 8);
 }
 
 // The tile where the sequence of row r0 begins, the first of tile k, in whose chain k's state is then found;

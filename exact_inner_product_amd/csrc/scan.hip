@@ -1,6 +1,10 @@
 // scan.hip -- the gated linear recurrence over sequences, forward (gfx950). scan.h has the method.
 //
-// One pass: forget logits, inputs (and gate logits) are read once and the states written once.
+// One pass: forget logits, inputs (and gate logits) are read once and the states written once. Bound by
+// memory where sequences lie whole in tiles: 4096 x 127 x 128 bf16 take 84 us (5.1 TB/s, the carries
+// among them; vector units busy half of the time), and 42 where half of the rows are padding and only last
+// states are wanted (vector units and latency). Chained tiles add what they wait for one another: 65,536 x
+// 1024 bf16 take 109 (4.0 TB/s), 600,000 x 100 packed f32 with gates 226 (4.5 TB/s).
 #include <type_traits>
 
 #include "scan.h"
@@ -24,11 +28,9 @@ struct ScanArgs {
   int32_t flat;          // load_flat serves
 };
 
-// Row r is padding: if a padded sequence without rows would begin there, its last state is its initial one.
+// A padded sequence without rows would begin at row r: its last state is its initial one.
 __device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t channel, int live) {
-  const uint32_t s = r / A.S.t;
-  if (r != s * A.S.t) return;
-  const int64_t i = (int64_t)s * A.d + channel;
+  const int64_t i = (int64_t)(r / A.S.t) * A.d + channel;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     if (c < live) A.last[i + c] = A.initial ? A.initial[i + c] : 0.0f;
@@ -161,8 +163,13 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
   float state[4];  // before the run
   half_reach(tid, M, lanes, state);
 
-  if (A.carries && at < rows)
+  if (A.carries && at < rows && !idle)
     store4<VEC>(A.carries + ((int64_t)tile * (THREADS >> A.lanes_log2) + (tid >> A.lanes_log2)) * A.d + channel, live, state);
+  // sequences without rows that would begin in this run
+  auto none_lasts = [&]() __attribute__((always_inline)) {
+    if (!A.S.lengths) return;
+    for (uint32_t m = run_nones<R>(A.S, r0 + at, marks); m; m &= m - 1) none_last(A, r0 + at + (__ffs(m) - 1), channel, live);
+  };
   if (!STATES) {
     if (!special) return;
     if (ends < R) {
@@ -171,10 +178,7 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
       for (int c = 0; c < 4; ++c)
         if (c < live) p[c] = fmaf(fP[c], state[c], fh[c]);
     }
-    if (!A.S.lengths) return;
-#pragma unroll 1
-    for (int t = 0; t < R; ++t)
-      if (marks.pad(t) && !marks.beyond(t)) none_last(A, r0 + at + t, channel, live);
+    none_lasts();
     return;
   }
   uint8_t* base = (uint8_t*)((T*)A.states + (int64_t)r0 * A.d + c0);
@@ -191,7 +195,6 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
       if (has && marks.beyond(t)) continue;
       store4<VEC>((T*)(base + out), live, v);
       if (!has) continue;
-      if (A.S.lengths && marks.pad(t)) none_last(A, r0 + at + t, channel, live);
       if (!marks.final(t)) continue;
       float* p = A.last + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel;
 #pragma unroll
@@ -199,8 +202,9 @@ __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) v
         if (c < live) p[c] = v[c];
     }
   };
-  if (special) write(std::false_type{});
-  else write(std::true_type{});
+  if (!special) return write(std::true_type{});
+  write(std::false_type{});
+  none_lasts();
 }
 
 struct BeginArgs {

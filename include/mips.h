@@ -554,7 +554,8 @@ typedef struct mips_rows {
  *                every h, rounded once; or NULL.
  *   last         device float [b, d]: the state behind the last row; initial (or 0) without rows.
  *   carries      device float [mips_gated_scan_carries(seq, d, dtype), d]: states between short runs of
- *                rows, for the gradient; or NULL. The number follows from the sizes and dtype.
+ *                rows, for the gradient (left as they were for runs of padding alone); or NULL. The
+ *                number follows from the sizes and dtype.
  *   workspace    device, 256-byte aligned, mips_gated_scan_workspace_size bytes (0: none is needed, or
  *                sizes are unsupported). Calls that share one must be ordered.
  * Rows whose elements lie in aligned groups of four (d, strides and pointers) are the fastest.

@@ -124,6 +124,16 @@ def test_sequences_without_rows(layout, b, t, d, lens):
     check(c, *run(c, dev))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [2, 3, 4, 5, 7, 8, 9, 12, 15, 16, 17])
+def test_sequences_about_as_long_as_a_run(t, dtype):
+    """Padded sequences that begin and end at every place of a thread's rows, many of them empty."""
+    dev = _dev()
+    for lens in ("ends", "holes"):
+        c = make("padded", 70, t, 20, dtype, t % 2 == 0, True, lens=lens)
+        check(c, *run(c, dev))
+
+
 @pytest.mark.parametrize("layout,b,t,d", [("dense", 3, 40, 64), ("dense", 2, 600, 128), ("padded", 8, 200, 100), ("packed", 8, 200, 64)])
 def test_parts_of_the_gradient(layout, b, t, d):
     """Only the last state's gradient, only the states'; without states the last ones stay the same."""
