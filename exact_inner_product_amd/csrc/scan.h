@@ -375,14 +375,13 @@ __device__ __forceinline__ void load4(const float* p, int live, bool wide, float
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = q[c];
   } else if (wide) {
+    typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
     const int back = 4 - live;
-    float q[4];
-    __builtin_memcpy(q, p - back, 16);
-#pragma unroll
-    for (int c = 0; c < 3; ++c) q[c] = back & 1 ? q[c + 1] : q[c];
-    v[0] = back & 2 ? q[2] : q[0];
-    v[1] = back & 2 ? q[3] : q[1];
-    v[2] = q[2];
+    const f32x4u_t q = *(const f32x4u_t*)(p - back);
+    const float r0 = back & 1 ? q[1] : q[0], r1 = back & 1 ? q[2] : q[1], r2 = back & 1 ? q[3] : q[2];
+    v[0] = back & 2 ? r2 : r0;
+    v[1] = back & 2 ? q[3] : r1;
+    v[2] = r2;
     v[3] = q[3];
   } else {
 #pragma unroll
