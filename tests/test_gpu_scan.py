@@ -134,6 +134,18 @@ def test_sequences_about_as_long_as_a_run(t, dtype):
         check(c, *run(c, dev))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout,b,t,d,gate", [("dense", 1, 6000, 128, False), ("dense", 2, 3500, 70, True), ("padded", 2, 4500, 130, False),
+                                               ("packed", 3, 3000, 128, True), ("dense", 1, 30000, 3, False)])
+def test_states_that_reach_far(layout, b, t, d, gate, dtype):
+    """Gates near 1: what a row sees comes from thousands of rows before, over many tiles and groups of
+    them, as do the gradients from behind."""
+    dev = _dev()
+    c = make(layout, b, t, d, dtype, gate, True)
+    c["forget"] = (c["forget"].float() * 0.5 + 8.0).to(DT[dtype])
+    check(c, *run(c, dev))
+
+
 @pytest.mark.parametrize("layout,b,t,d", [("dense", 3, 40, 64), ("dense", 2, 600, 128), ("padded", 8, 200, 100), ("packed", 8, 200, 64)])
 def test_parts_of_the_gradient(layout, b, t, d):
     """Only the last state's gradient, only the states'; without states the last ones stay the same."""
