@@ -7,6 +7,9 @@ exact_inner_product_amd.training and .histories with their gradients attached.
     users = mag.pool_normalize(states, lengths=lengths)
     logprobs, _ = mag.item_logprobs(users, items, targets, scale=1 / temperature, bias=-log_q)
     (-logprobs.mean()).backward()
+
+Forward and backward passes can be captured into a graph together, as torch's own: on leaves whose gradients no
+eager pass that is still alive accumulates (torch.autograd.grad on leaves of the graph's own does).
 """
 from __future__ import annotations
 

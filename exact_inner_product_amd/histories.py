@@ -38,6 +38,12 @@ def _index(x: torch.Tensor, what: str) -> Tuple[torch.Tensor, int]:
     return x.contiguous(), 32 if x.dtype == torch.int32 else 64
 
 
+def _int32(what: str, *sizes: int) -> None:
+    """Sizes that the C interface takes as 32 bits fit (ctypes would cut them short)."""
+    if max(sizes) >= 1 << 31:
+        raise MipsError(2, what)
+
+
 def _sequences(shape: Sequence[int], offsets: Optional[torch.Tensor], lengths: Optional[torch.Tensor]):
     """(structure, b, d, tensors that it points into) of rows laid out as `shape`."""
     if offsets is not None:
@@ -47,12 +53,14 @@ def _sequences(shape: Sequence[int], offsets: Optional[torch.Tensor], lengths: O
             raise ValueError(f"packed rows must be [n, d >= 1], got {tuple(shape)}")
         if offsets.dim() != 1 or offsets.shape[0] < 2:
             raise ValueError(f"offsets must be [b + 1], b >= 1, got {tuple(offsets.shape)}")
-        offsets, bits = _index(offsets, "offsets")
         b = offsets.shape[0] - 1
+        _int32("sequences", b, shape[1])
+        offsets, bits = _index(offsets, "offsets")
         return _Sequences(b, bits, 0, shape[0], offsets.data_ptr(), None), b, shape[1], offsets
     if len(shape) != 3 or shape[0] < 1 or shape[1] < 1 or shape[2] < 1:
         raise ValueError(f"rows must be [b >= 1, t >= 1, d >= 1], or [n, d] with offsets, got {tuple(shape)}")
     b, t, d = shape
+    _int32("sequences", b, d)
     bits = 0
     if lengths is not None:
         if tuple(lengths.shape) != (b,):
@@ -103,6 +111,8 @@ def _floats(shape: Tuple[int, int], **tensors) -> None:
 def _workspace(what: str, seq, *sizes, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
     """The given workspace, or one of the size that the call needs, None if it needs none."""
     if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
         return workspace
     nbytes = getattr(lib(), what)(C.byref(seq), *sizes)
     return empty_workspace(nbytes, device) if nbytes else None
@@ -230,6 +240,7 @@ def gated_step(x: torch.Tensor, forget: torch.Tensor, state: torch.Tensor, rows:
     if len(shape) != 2 or shape[1] < 1:
         raise ValueError(f"x must be [b, d >= 1], got {tuple(shape)}")
     b, d = shape
+    _int32("mips_gated_step", b, d)
     code = _code(x, "x")
     _like(x, forget=forget, gate=gate)
     if rows.shape != shape[:1]:

@@ -321,7 +321,7 @@ def test_workspaces_of_the_caller():
         p = mips.pool_normalize(c["x"], offsets=c["offsets"], workspace=ws)
         assert torch.equal(f.states, want.states) and all(torch.equal(a, b) for a, b in zip(g, wg))
         assert torch.equal(p.vectors, mips.pool_normalize(c["x"], offsets=c["offsets"]).vectors)
-    for bad, error in ((ws.cpu(), ValueError), (ws[:256], mips.MipsError)):
+    for bad, error in ((ws.cpu(), ValueError), (ws[:256], mips.MipsError), (ws[:1].expand(1 << 23), ValueError)):
         with pytest.raises(error):
             mips.gated_scan(c["x"], c["forget"], c["gate"], workspace=bad, **args)
         with pytest.raises(error):

@@ -171,6 +171,23 @@ def test_python_refusals():
             call()
 
 
+def test_sizes_past_32_bits_are_refused():
+    """Before anything of such a size is looked at: the C interface would see them cut short."""
+    wide, far = 1 << 32, (1 << 32) + 1
+    one = torch.zeros(1, 1, 1)
+    for x in (one.expand(far, 1, 1), one.expand(1, 1, far)):
+        for call in (lambda: mips.gated_scan(x, x), lambda: mips.pool_normalize(x),
+                     lambda: mips.pool_normalize_backward(one[0], x.shape, None)):
+            with pytest.raises(mips.MipsError):
+                call()
+    row = torch.zeros(1, 1)
+    for x in (row.expand(far, 1), row.expand(1, wide + 4)):
+        with pytest.raises(mips.MipsError):
+            mips.gated_step(x, x, row, torch.zeros(1, dtype=torch.int32).expand(x.shape[0]))
+    with pytest.raises(mips.MipsError):
+        mips.gated_scan(row, row, offsets=torch.zeros(1, dtype=torch.int32).expand(far + 1))
+
+
 def test_limits_match_the_binding():
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mips.h")).read()
     assert int(re.search(r"#define MIPS_EVENTS_MAX (\d+)", text)[1]) == mips.EVENTS_MAX
