@@ -165,6 +165,23 @@ static void (*events_variant(bool gate, bool vec))(EventArgs) {
               : (vec ? events_kernel<T, false, true, THREADS> : events_kernel<T, false, false, THREADS>);
 }
 
+// Whether rows of two tables share elements.
+static bool tables_overlap(const float* p, int64_t p_stride, const float* q, int64_t q_stride, int64_t rows, int32_t d) {
+  if (p > q) {
+    const float* r = p;
+    p = q;
+    q = r;
+    const int64_t s = p_stride;
+    p_stride = q_stride;
+    q_stride = s;
+  }
+  const uint64_t apart = ((uint64_t)q - (uint64_t)p) / 4;
+  if (apart >= (uint64_t)(rows - 1) * p_stride + d) return false;
+  if (p_stride != q_stride) return true;  // one inside the other
+  const uint64_t in = apart % p_stride;   // columns of one tensor are apart
+  return in < (uint64_t)d || in + d > (uint64_t)p_stride;
+}
+
 }  // namespace mips
 
 using namespace mips;
@@ -183,7 +200,7 @@ extern "C" int mips_gated_step(const void* x, int64_t x_stride, const void* forg
   const int E = elem_bytes(dtype);
   if (!x || !forget || !state || !out_state || !ids || !out || !aligned(x, E) || !aligned(forget, E) || !aligned(gate, E) ||
       !aligned(out, E) || !aligned(state, 4) || !aligned(out_state, 4) || !aligned(ids, id_bits / 8) ||
-      (out_state == state && out_stride != state_stride))
+      (out_state == state ? out_stride != state_stride : tables_overlap(state, state_stride, out_state, out_stride, rows, d)))
     return MIPS_ERR_INVALID_ARG;
   EventArgs A{x, forget, gate, x_stride, forget_stride, gate_stride, state, out_state, state_stride, out_stride,
               rows, ids, id_bits == 64, b, d, 0, 0, out};

@@ -133,3 +133,22 @@ def test_autograd_notices_the_table():
     mips.gated_step(torch.ones(2, 8, device=dev), torch.ones(2, 8, device=dev), state.detach(), torch.tensor([0, 1], device=dev))
     with pytest.raises(RuntimeError, match="inplace operation"):
         y.backward()
+
+
+def test_tables_that_overlap():
+    """Tables beside each other in one tensor are taken, ones that share elements refused."""
+    dev = _dev()
+    x, f = torch.randn(5, 8, device=dev), torch.randn(5, 8, device=dev)
+    rows = torch.tensor([0, 3, 1, 3, 9], device=dev)
+    big = torch.randn(21, 20, device=dev)
+    state = big[:10, :8].clone()
+    want, out = mips.gated_step(x, f, state.clone(), rows), torch.zeros(10, 8, device=dev)
+    mips.gated_step(x, f, state, rows, out=out)
+    for into in (big[:10, 8:16], big[:10, 12:], big[10:20, :8], big[11:, 4:12]):
+        into.zero_()
+        assert torch.equal(mips.gated_step(x, f, big[:10, :8], rows, out=into), want) and torch.equal(into, out)
+    for into in (big[1:11, :8], big[:10, 4:12], big[9:19, 7:15], big[:20:2, :8]):
+        with pytest.raises(mips.MipsError):
+            mips.gated_step(x, f, big[:10, :8], rows, out=into)
+        with pytest.raises(mips.MipsError):
+            mips.gated_step(x, f, into, rows, out=big[:10, :8])

@@ -187,6 +187,23 @@ def test_functions_without_a_gradient():
         h.sum().backward()
 
 
+def test_broadcast_inputs():
+    """One row of gates for all rows and one history for all users: their gradients are sums."""
+    dev = _dev()
+    b, t, d = 6, 90, 24
+    x, g = torch.randn(1, t, d, device=dev), torch.randn(b, t, d, device=dev)
+    w = torch.randn(d, device=dev)
+    leaves = [v.clone().requires_grad_() for v in (x, w)]
+    h, _ = mag.gated_scan(leaves[0].expand(b, t, d), leaves[1].expand(b, t, d))
+    h.backward(g)
+    f = mips.gated_scan(x.expand(b, t, d), w.expand(b, t, d))
+    full = mips.gated_scan_backward(g, None, x.expand(b, t, d), w.expand(b, t, d), None, f)
+    for leaf, v, over in ((leaves[0], full[0], (0,)), (leaves[1], full[1], (0, 1))):
+        want = v.double().sum(over)
+        room = b * t * U * v.double().abs().sum(over)  # the order of the sum is torch's
+        assert bool(((leaf.grad.double().reshape(want.shape) - want).abs() <= room).all())
+
+
 def test_the_counter_may_advance_before_the_backward_pass():
     dev = _dev()
     x = torch.randn(1000, device=dev, requires_grad=True)

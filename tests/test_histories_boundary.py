@@ -100,7 +100,7 @@ def test_step_refusals(L):
     for bad in (dict(x=None), dict(f=None), dict(state=None), dict(out=None), dict(ids=None), dict(h=None), dict(b=-1), dict(d=0),
                 dict(n=0), dict(xs=63), dict(fs=63), dict(gs=63), dict(ss=63), dict(os_=63), dict(x=0x1001), dict(f=0x2001),
                 dict(g=0x3001), dict(state=0x4002), dict(out=0x7002), dict(ids=0x5002), dict(bits=64, ids=0x5004), dict(h=0x6001),
-                dict(os_=128)):
+                dict(os_=128), dict(out=0x4004), dict(state=0x4100), dict(ss=128, out=0x4100)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(dt=FP8), dict(bits=16), dict(b=65537), dict(d=16385, xs=1 << 15, fs=1 << 15, gs=1 << 15, ss=1 << 15, os_=1 << 15)):
         assert call(**bad) == UNSUPPORTED, bad
