@@ -38,7 +38,7 @@ __device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t
 
 // STATES: every state is wanted, and held until the one before the run is known. Else a run keeps its map and, of
 // a sequence that goes on from the run before, the map up to its final row: registers for half as
-// many waves again, where this is bound by latency (4096 x 127 x 128 with lengths: 72 -> 45 us).
+// many waves again, where this is bound by latency (4096 x 127 x 128 bf16 with lengths: 44 us for 72).
 template <typename T, bool GATE, int VEC, bool STATES, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
   constexpr int R = kRun<T>;
