@@ -290,3 +290,41 @@ def test_broken_offsets_stay_in_bounds():
     want = mips.gated_scan(x, x, lengths=torch.tensor([0, 300, 7], device=dev))
     got = mips.gated_scan(x, x, lengths=padded)
     assert torch.equal(got.states, want.states) and torch.equal(got.last, want.last)
+
+
+@pytest.mark.parametrize("layout,b,t,d,dtype", [("dense", 1, 60000, 128, "f32"), ("dense", 1, 120000, 100, "bf16"), ("dense", 2, 40000, 130, "bf16"),
+                                                ("padded", 3, 30000, 65, "f32"), ("packed", 4, 50000, 66, "f32"), ("packed", 300, 900, 128, "bf16"),
+                                                ("dense", 1, 300000, 16, "f32")])
+def test_exact_sums_over_long_chains(layout, b, t, d, dtype):
+    """Gates of infinity keep the state and take the input whole: states are sums of small whole numbers, exact
+    in binary32 in whatever order maps are joined (below 2^24), and gradients are sums from behind."""
+    dev = _dev()
+    gen = torch.Generator().manual_seed(t)
+    lengths = torch.randint(0, t + 1, (b,), generator=gen)
+    lengths[0] = t
+    if layout == "dense":
+        lengths[:] = t
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), lengths.cumsum(0)])
+    shape = (int(offsets[-1]), d) if layout == "packed" else (b, t, d)
+    x, gs = (torch.randint(-3, 4, shape, generator=gen) for _ in range(2))
+    initial, gl = (torch.randint(-9, 10, (b, d), generator=gen) for _ in range(2))
+    h, dx, last, di = torch.zeros_like(x), torch.zeros_like(x), initial.clone(), gl.clone()
+    for s in range(b):
+        n = int(lengths[s])
+        rows = (lambda v: v[offsets[s]:offsets[s] + n]) if layout == "packed" else (lambda v: v[s, :n])  # noqa: E731
+        if n:
+            rows(h)[:] = rows(x).cumsum(0) + initial[s]
+            rows(dx)[:] = rows(gs).flip(0).cumsum(0).flip(0) + gl[s]
+            last[s], di[s] = rows(h)[-1], rows(dx)[0]
+    at = {"padded": dict(lengths=lengths.to(dev)), "packed": dict(offsets=offsets.to(dev))}.get(layout, {})
+    at["initial"] = initial.float().to(dev)
+    dt, gates = DT[dtype], torch.full(shape, float("inf"), dtype=DT[dtype], device=dev)
+    xd, gd, gld = x.to(dev, dt), gs.to(dev, dt), gl.float().to(dev)
+    want_h, want_dx = h.to(dev).to(dt), dx.to(dev).to(dt)
+    for _ in range(5):
+        f = mips.gated_scan(xd, gates, gates, **at)
+        g = mips.gated_scan_backward(gd, gld, xd, gates, gates, f, **at)
+        assert torch.equal(f.states, want_h) and torch.equal(f.last, last.to(dev).float())
+        assert torch.equal(g[0], want_dx) and torch.equal(g[3], di.to(dev).float())
+        assert not g[1].any() and not g[2].any()
+        assert torch.equal(mips.gated_scan(xd, gates, gates, states=False, carries=False, **at).last, f.last)
