@@ -219,8 +219,8 @@ extern "C" int mips_gated_step(const void* x, int64_t x_stride, const void* forg
                    aligned(gate, 4 * E) && aligned(out, 4 * E) && aligned(state, 16) && out_stride % 4 == 0 &&
                    aligned(out_state, 16);
   void (*kernel)(EventArgs) = nullptr;
-  if (dtype == MIPS_F32) kernel = threads == 1024 ? events_variant<float, 1024>(gate != nullptr, vec) : events_variant<float, 256>(gate != nullptr, vec);
-  else kernel = threads == 1024 ? events_variant<__bf16, 1024>(gate != nullptr, vec) : events_variant<__bf16, 256>(gate != nullptr, vec);
+  if (dtype == MIPS_F32) kernel = threads == 1024 ? events_variant<float, 1024>(gate, vec) : events_variant<float, 256>(gate, vec);
+  else kernel = threads == 1024 ? events_variant<__bf16, 1024>(gate, vec) : events_variant<__bf16, 256>(gate, vec);
   hipLaunchKernelGGL(kernel, dim3((b + A.own - 1) / A.own), dim3(threads), 0, (hipStream_t)stream, A);
   return check_launch();
 }

@@ -4,8 +4,9 @@
 //   dm = (g - u (u . g)) / n, or g / n where the sum is below 1e-12;  each row's gradient dm / number
 //
 // Bound by reading the rows, and by writing their gradients: 4096 x 127 x 128 bf16 with lengths take 16 us
-// (67 MB, 4.2 TB/s) and 27 us (133 MB, 4.9 TB/s); short calls by latency, 16 x 50 x 64 5 us. (Normalisation as the index's: sum
-// over all channels, 1e-12 under the root: recsys_two_tower_model.py:69, 73-76, 1287-1306.)
+// (67 MB, 4.2 TB/s) and 27 us (133 MB, 4.9 TB/s); short calls by latency, 16 x 50 x 64 5 us.
+// (Normalisation as the index's: sum over all channels, 1e-12 under the root:
+// recsys_two_tower_model.py:69, 73-76, 1287-1306.)
 #include "sequences.h"
 
 namespace mips {

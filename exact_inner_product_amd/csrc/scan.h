@@ -402,10 +402,10 @@ template <> struct Raw<__bf16> {
   }
 };
 
-// Makes the compiler forget what it has computed from r, so that it does so again where it is needed
-// rather than keep it in registers.
 // Has v computed here, not where it is used, with all it comes from in registers until then.
 __device__ __forceinline__ void here(float* v) { asm volatile("" : "+v"(*v)); }
+// Makes the compiler forget what it has computed from r, so that it does so again where it is needed
+// rather than keep it in registers.
 template <typename T>
 __device__ __forceinline__ void raw_again(Raw<T>* r) {
 #pragma unroll

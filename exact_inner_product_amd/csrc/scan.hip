@@ -292,7 +292,8 @@ int scan_begin(const Sequences& S, const Tiling& T, const ScanSpace& W, int32_t 
   const BeginArgs A{S, W.info, T.tiles * T.rows, W.words, W.count, W.counters, T.columns, d, as, of_none};
   uint64_t blocks = (W.count + 1023) / 1024;
   if (W.info) {
-    const uint64_t rows = ((uint64_t)A.described + 4 * kDescribed - 1) / (4 * kDescribed), seqs = of_none ? ((uint64_t)S.b * ((d + 255) / 256) + 3) / 4 : 0;
+    const uint64_t rows = ((uint64_t)A.described + 4 * kDescribed - 1) / (4 * kDescribed);
+    const uint64_t seqs = of_none ? ((uint64_t)S.b * ((d + 255) / 256) + 3) / 4 : 0;
     blocks = blocks > rows ? blocks : rows;
     blocks = blocks > seqs ? blocks : seqs;
   }
@@ -346,9 +347,11 @@ static void (*scan_variant(bool gate, int vec))(ScanArgs) {
 template <bool STATES>
 static void (*scan_kernel_of(int32_t dtype, const Tiling& T, bool gate, int vec))(ScanArgs) {
   if (dtype == MIPS_BF16)
-    return T.chained ? scan_variant<__bf16, STATES, true, kTileThreads>(gate, vec) : scan_variant<__bf16, STATES, false, kTileThreads>(gate, vec);
+    return T.chained ? scan_variant<__bf16, STATES, true, kTileThreads>(gate, vec)
+                     : scan_variant<__bf16, STATES, false, kTileThreads>(gate, vec);
   if (T.threads > kTileThreads) return scan_variant<float, STATES, false, 2 * kTileThreads>(gate, vec);  // never chained
-  return T.chained ? scan_variant<float, STATES, true, kTileThreads>(gate, vec) : scan_variant<float, STATES, false, kTileThreads>(gate, vec);
+  return T.chained ? scan_variant<float, STATES, true, kTileThreads>(gate, vec)
+                   : scan_variant<float, STATES, false, kTileThreads>(gate, vec);
 }
 
 }  // namespace mips
