@@ -57,14 +57,16 @@ inline Tiling scan_tiling(const Sequences& S, int32_t d, int32_t dtype) {
 inline int64_t scan_runs(const Tiling& T) { return (int64_t)T.tiles * (T.threads >> T.lanes_log2); }
 
 // ------------------------------------------------------------------------------ gates
-// sigmoid(v) and sigmoid(-v), each exact to a few units in the last place (1 - sigmoid(v) would
-// not be): with e = exp(-v) they are 1 / (1 + e) and e / (1 + e). e is at most 2^126, so that the second is
-// not inf 0 (values of the first below 2^-126 are held there); a NaN stays one.
+// sigmoid(v) and sigmoid(-v) (1 - sigmoid(v) would lose the small one): with e = exp(-v) they are 1 / (1 + e) and
+// e / (1 + e), which is 1 to binary32 for e above 2^24, also where e is infinite and its product with 0 no
+// number. The product with log2 e is rounded, which is |v| units in the last place of e at most: the
+// smaller of the two is off by up to (2 |v| + 8) 2^-24 of its value. Values below 2^-126 may be 0, and
+// sigmoid(-inf) is: an input that it gates leaves nothing, whatever finite value it holds. A NaN stays one.
 __device__ __forceinline__ void sigmoids(float v, float* up, float* down) {
-  const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-1.44269504f * v, 126.0f));
+  const float e = __builtin_amdgcn_exp2f(-1.44269504f * v);
   const float r = __builtin_amdgcn_rcpf(1.0f + e);
   *up = r;
-  *down = e * r;
+  *down = e > 0x1p24f ? 1.0f : e * r;
 }
 
 // --------------------------------------------------------------------- affine maps

@@ -547,7 +547,8 @@ typedef struct mips_rows {
  *   h_r = a_r h_{r-1} + b_r x_r,  a = sigmoid(forget),  b = sigmoid(gate), or 1 - a without a gate,
  * from initial (or 0) before the first row. Rows are cut into tiles whose states are joined in an
  * order that follows from the sizes alone: the same call gives the same bits. A state that is not
- * finite makes those behind it in its sequence and channel not finite.
+ * finite makes those behind it in its sequence and channel not finite. Gates are off by up to
+ * (2 |logit| + 8) 2^-24 of their value; those below 2^-126 may be 0, and sigmoid(-inf) is.
  *   x, forget, gate   rows of dtype MIPS_F32 or MIPS_BF16; gate may be NULL.  d 1 .. 16384.
  *   initial      device float [b, d] or NULL.
  *   states       device, contiguous rows of dtype in the layout of the input ([b, t, d] or [n, d]):

@@ -152,3 +152,16 @@ def test_tables_that_overlap():
             mips.gated_step(x, f, big[:10, :8], rows, out=into)
         with pytest.raises(mips.MipsError):
             mips.gated_step(x, f, into, rows, out=big[:10, :8])
+
+
+def test_gates_of_minus_infinity_are_zero():
+    """An event of the type's lowest value behind a gate of -inf leaves the state as it is, and a forget logit
+    of -inf leaves nothing of a state that large."""
+    dev = _dev()
+    for dtype in (torch.float32, torch.bfloat16):
+        inf, low = float("inf"), torch.finfo(dtype).min
+        state = torch.tensor([2.0, torch.finfo(torch.float32).min], device=dev)[:, None].repeat(1, 20)
+        x, forget, gate = (torch.tensor(v, device=dev)[:, None].expand(3, 20).to(dtype) for v in ([low, 5.0, low], [inf, -inf, inf], [-inf, inf, -inf]))
+        h = mips.gated_step(x, forget, state, torch.tensor([0, 1, 1], device=dev), gate)
+        assert h[:, 0].tolist() == [2.0, 5.0, 5.0] and state[:, 19].tolist() == [2.0, 5.0]
+        assert (h == h[:, :1]).all() and (state == state[:, :1]).all()

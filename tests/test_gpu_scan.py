@@ -328,3 +328,37 @@ def test_exact_sums_over_long_chains(layout, b, t, d, dtype):
         assert torch.equal(g[0], want_dx) and torch.equal(g[3], di.to(dev).float())
         assert not g[1].any() and not g[2].any()
         assert torch.equal(mips.gated_scan(xd, gates, gates, states=False, carries=False, **at).last, f.last)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout,b,t,d", [("dense", 3, 9, 4), ("padded", 5, 60, 33), ("dense", 2, 1500, 64), ("packed", 4, 900, 128)])
+def test_gates_of_minus_infinity_are_zero(layout, b, t, d, dtype):
+    """Inputs of the type's lowest value behind gates of -inf leave nothing in the state, and a forget logit
+    of -inf nothing of a state that large: what is left are sums of small whole numbers, exact in binary32.
+    Likewise for the gradients of what such gates keep out."""
+    dev = _dev()
+    c = make(layout, b, t, d, dtype, True, True)
+    rng = np.random.default_rng(t)
+    shape, low = c["x"].shape, torch.finfo(DT[dtype]).min
+    whole = lambda *s: torch.from_numpy(rng.integers(-3, 4, s)).float()  # noqa: E731
+    masked, first = torch.from_numpy(rng.random(shape) < 0.4), torch.zeros(shape, dtype=torch.bool)
+    for lo, hi in c["seqs"]:
+        if hi > lo:
+            first.view(-1, d)[lo] = True
+    x, c["initial"] = whole(*shape), torch.full((b, d), torch.finfo(torch.float32).min)
+    inf = torch.full(shape, float("inf"))
+    c["x"] = torch.where(masked, low, x).to(DT[dtype])
+    c["gate"] = torch.where(masked, -inf, inf).to(DT[dtype])
+    c["forget"] = torch.where(first, -inf, inf).to(DT[dtype])  # nothing is left of the initial state
+    h, last = torch.zeros(shape).view(-1, d), c["initial"].clone()
+    kept, want_dx = torch.where(masked, 0.0, x).view(-1, d), torch.zeros(shape).view(-1, d)
+    c["gs"] = whole(*shape).to(DT[dtype])
+    f, (dx, df, dg, di) = run(c, dev, grads=("gs",))
+    for s, (lo, hi) in enumerate(c["seqs"]):
+        if hi > lo:
+            h[lo:hi] = kept[lo:hi].cumsum(0)
+            last[s] = h[hi - 1]
+            want_dx[lo:hi] = c["gs"].float().view(-1, d)[lo:hi].flip(0).cumsum(0).flip(0)
+    assert torch.equal(f.states.cpu().view(-1, d), h.to(DT[dtype])) and torch.equal(f.last.cpu(), last)
+    assert torch.equal(dx.cpu().view(-1, d), torch.where(masked.view(-1, d), 0.0, want_dx).to(DT[dtype]))
+    assert not di.any() and not df.any()
