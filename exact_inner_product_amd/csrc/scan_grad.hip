@@ -209,7 +209,7 @@ __global__ __launch_bounds__(THREADS, 4) void scan_grad_kernel(ScanGradArgs A) {
         b = down;
         if (GATE) {
           sigmoids(g[t].at(c), &b, &nb);
-          dg[c] = D * x[t].at(c) * b * nb;
+          dg[c] = D * (x[t].at(c) * (b * nb));  // (D x may be past the type's largest value where the product is not)
         }
         dx[c] = D * b;
         df[c] = D * q[t][c];

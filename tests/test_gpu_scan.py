@@ -362,3 +362,20 @@ def test_gates_of_minus_infinity_are_zero(layout, b, t, d, dtype):
     assert torch.equal(f.states.cpu().view(-1, d), h.to(DT[dtype])) and torch.equal(f.last.cpu(), last)
     assert torch.equal(dx.cpu().view(-1, d), torch.where(masked.view(-1, d), 0.0, want_dx).to(DT[dtype]))
     assert not di.any() and not df.any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout,b,t,d", [("dense", 2, 7, 5), ("padded", 3, 90, 64), ("dense", 1, 900, 128)])
+def test_gate_gradients_of_large_inputs(layout, b, t, d, dtype):
+    """grad_gate = D x b (1 - b) where D x alone is past the largest value: small with a gate far below 0,
+    0 with one of -inf."""
+    dev = _dev()
+    c = make(layout, b, t, d, dtype, True, False)
+    c["x"] = torch.sign(c["x"].float()).mul(3e38).to(DT[dtype])
+    c["gate"] = c["gate"].float().sub(24.0).to(DT[dtype])
+    c["forget"][..., 1, :] = 0.0
+    c["gs"], c["gl"] = (torch.where(v < 0, -8.0, 8.0).to(v.dtype) for v in (c["gs"], c["gl"]))
+    check(c, *run(c, dev))
+    c["gate"].fill_(-float("inf"))
+    f, g = run(c, dev)
+    assert not f.states.any() and not g[0].any() and not g[1].any() and not g[2].any()
