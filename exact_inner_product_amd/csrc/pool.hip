@@ -269,7 +269,12 @@ __global__ __launch_bounds__(kPoolThreads) void pool_grad_kernel(PoolArgs A) {
     auto along = [&](float dot, float square) { return A.normalize && !(square < kPoolEps) ? dot / n / n : 0.0f; };
     const uint32_t lo = max(begin, r0), hi = min(end, r1);
     auto read = [&](int c, int live, float* mv, float* gv) {
-      row8<float, VEC>(m + c, live, mv);
+      if (A.normalize) {
+        row8<float, VEC>(m + c, live, mv);
+      } else {  // the gradient does not depend on the mean, which need not be finite
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mv[e] = 0.0f;
+      }
       if (VEC && A.grad_aligned) row8<T, VEC>(g + c, live, gv);
       else row8<T, false>(g + c, live, gv);
     };

@@ -168,3 +168,23 @@ def test_widths(d, dtype):
             want = (g[s].double() - u * float(u @ g[s].double())) / norm / k
             err = (dx[s].cpu().double() - torch.cat([want.expand(k, d), torch.zeros(t - k, d, dtype=torch.float64)])).abs().max()
             assert err <= (4 * room + half) * g[s].double().norm() / norm / k
+
+
+@pytest.mark.parametrize("d", [5, 64, 100, 700])
+@pytest.mark.parametrize("layout", ["padded", "packed"])
+def test_gradient_of_a_mean_that_is_not_finite(layout, d):
+    """Without normalisation the gradient is g / rows whatever the rows hold."""
+    dev = _dev()
+    for dtype in ("f32", "bf16"):
+        c = make(layout, 5, 300, d, dtype, False, False)
+        at = {k: None if c[k] is None else c[k].to(dev) for k in ("lengths", "offsets")}
+        g = c["gl"].to(DT[dtype]).to(dev)
+        want = mips.pool_normalize_backward(g, c["x"].shape, mips.pool_normalize(c["x"].to(dev), normalize=False, **at), **at)
+        assert torch.isfinite(want).all() and want.any()
+        x = c["x"].view(-1, d)
+        for k, (lo, hi) in enumerate(c["seqs"]):
+            if hi > lo:
+                x[hi - 1, k % d] = (float("inf"), float("nan"), -float("inf"))[k % 3]
+        f = mips.pool_normalize(c["x"].to(dev), normalize=False, **at)
+        assert not torch.isfinite(f.mean).all()
+        assert torch.equal(mips.pool_normalize_backward(g, c["x"].shape, f, **at), want)
