@@ -74,8 +74,9 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropArgs A) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t bits = (e & 1) ? r[e >> 1] >> 16 : r[e >> 1] & 0xFFFFu;
-      v[e] = bits >= A.cut ? v[e] * A.scale : 0.0f;
-      if (A.residual) v[e] += res[e];
+      // one rounding, of the sum: the product's own would show where the two cancel
+      if (A.residual) v[e] = bits >= A.cut ? fmaf(v[e], A.scale, res[e]) : res[e];
+      else v[e] = bits >= A.cut ? v[e] * A.scale : 0.0f;
       q[e] = (T)v[e];
     }
     if (whole) {

@@ -276,8 +276,8 @@ def gated_step(x: torch.Tensor, forget: torch.Tensor, state: torch.Tensor, rows:
 # ------------------------------------------------------------------------ dropout
 def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *, residual: Optional[torch.Tensor] = None,
             counter: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """residual + x with each element dropped with probability p and the others scaled by 1 / (1 - p), rounded
-    once to x's type. The mask follows from seed, offset (two calls with one seed need different
+    """residual + x with each element dropped with probability p and the others scaled by 1 / (1 - p) (as a float32):
+    product and sum with one rounding in float32, then x's type. The mask follows from seed, offset (two calls with one seed need different
     ones) and the element's place in x alone; the same call on the gradient is the gradient for x.
 
     x: float32 or bfloat16 of any shape (copied first unless contiguous); p: taken in steps of

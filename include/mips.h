@@ -614,7 +614,8 @@ MIPS_API int mips_gated_step(const void *x, int64_t x_stride, const void *forget
 
 /*
  * mips_dropout -- out = residual + (kept ? x * 65536 / (65536 - c) : 0), c = p * 65536 rounded to
- * the nearest integer (p is taken in steps of 2^-16). Element i is kept if its 16 random bits are at
+ * the nearest integer (p is taken in steps of 2^-16). The ratio is rounded to binary32, product and sum
+ * together once more, and then to dtype. Element i is kept if its 16 random bits are at
  * least c: half-word i % 8, low halves first, of the four words of Philox4x32-10 with the counter
  * (i / 8 mod 2^32, i / 8 / 2^32, offset mod 2^32, offset / 2^32) and the key (seed mod 2^32, seed / 2^32).
  * The same call on the gradient is the gradient for x. Dropped elements count as 0 whatever they hold.

@@ -110,3 +110,22 @@ def test_places_past_32_bits():
     check(y[n - tail:], x[n - tail:].cpu(), 0.25, 11, 2, start=n - tail)
     del x, y
     torch.cuda.empty_cache()
+
+
+def test_one_rounding_with_a_residual():
+    """Sums that cancel: within half a unit in the last place of x scale + residual itself (64 bits hold the
+    product, and the sum to 2^-53, which is below a millionth of the room where the sum is above 2^-20 of its terms)."""
+    dev = _dev()
+    gen = torch.Generator().manual_seed(8)
+    n, p, seed = 1 << 17, 0.1, 21
+    c = int(p * 65536 + 0.5)
+    scale = float(np.float32(65536 / (65536 - c)))
+    x = torch.randn(n, generator=gen)
+    r = -(x.double() * scale * (1 + torch.randn(n, generator=gen).double() * 1e-3)).float()
+    keep = torch.from_numpy(hc.kept(n, p, seed, 0))
+    want = torch.where(keep, x.double() * scale, 0.0) + r.double()
+    sure = want.abs() > r.double().abs() * 2.0 ** -20
+    assert sure.double().mean() > 0.99
+    got = mips.dropout(x.to(dev), p, seed, residual=r.to(dev)).cpu().double()
+    assert ((got - want).abs() <= hc.U * want.abs() * (1 + 1e-6))[sure].all()
+    assert torch.equal(got[~keep], r.double()[~keep])
