@@ -599,8 +599,9 @@ MIPS_API int mips_gated_scan_backward(const mips_sequences *seq, int32_t d, int3
  *   b            0 .. MIPS_EVENTS_MAX (0 enqueues nothing).
  *   state        device float [rows, d], state_stride >= d.
  *   out_state    device float [rows, d]: the rows that events name are written, others are left as
- *                they are; either `state` itself with the same stride, or no overlap (INVALID_ARG;
- *                columns of one tensor do not).
+ *                they are; either `state` itself with the same stride, or no overlap (INVALID_ARG, also
+ *                for tables that lie within one another otherwise than as columns of one tensor,
+ *                all its rows or some at a stride).
  *   ids          device, int32 or int64 [b].
  *   out          device, [b, d] contiguous of dtype.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED (dtype, id_bits, d > 16384,

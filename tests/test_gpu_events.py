@@ -165,3 +165,23 @@ def test_gates_of_minus_infinity_are_zero():
         h = mips.gated_step(x, forget, state, torch.tensor([0, 1, 1], device=dev), gate)
         assert h[:, 0].tolist() == [2.0, 5.0, 5.0] and state[:, 19].tolist() == [2.0, 5.0]
         assert (h == h[:, :1]).all() and (state == state[:, :1]).all()
+
+
+def test_columns_of_one_tensor_with_other_rows():
+    """A table beside every second (third) row's other columns shares nothing with it; of the same columns it does."""
+    dev = _dev()
+    x, f = torch.randn(5, 8, device=dev), torch.randn(5, 8, device=dev)
+    rows = torch.tensor([0, 3, 1, 3, 9], device=dev)
+    big = torch.randn(60, 20, device=dev)
+    state = big[:10, :8].clone()
+    out = torch.zeros(10, 8, device=dev)
+    want = mips.gated_step(x, f, state, rows, out=out)
+    for table, into in ((big[:10, :8], big[:20:2, 8:16]), (big[:10, :8], big[1:31:3, 12:]), (big[:30:3, :8], big[:20:2, 9:17])):
+        table.copy_(state)
+        into.zero_()
+        assert torch.equal(mips.gated_step(x, f, table, rows, out=into), want) and torch.equal(into, out)
+        assert torch.equal(table, state)
+    for table, into in ((big[:10, :8], big[1:21:2, 4:12]), (big[:30:3, 8:16], big[:20:2, 9:17]), (big[:10, :8], big[1:21:2, 15:].as_strided((10, 8), (40, 1)))):
+        for a, b in ((table, into), (into, table)):
+            with pytest.raises(mips.MipsError):
+                mips.gated_step(x, f, a, rows, out=b)
