@@ -6,8 +6,9 @@
 // events' rows once (4 or 8 bytes each, from the caches) against a small hash table of its own.
 //
 // Bound by latency: ids, the look through them while the first events' rows arrive, one round of
-// arithmetic. 4096 events x 128 bf16 of a million rows with gates take 6.5 us in a graph (8 MB), 16 of
-// any 4.4; 65,536 take 90, mostly looking. Events of one row are a trip to memory each: 13,236 of 1265 rows 46.
+// arithmetic. In graphs 16 events of any size take 4.4 us, 4096 x 128 bf16 of a million rows with gates 7.2 (8
+// MB), 65,536 without 77, mostly looking, and 58 if half of them are padding. Events of one row are a trip to
+// memory each: 13,236 of 1265 rows take 31 us, 65,536 of which 30% name one row 6.8 ms.
 #include <numeric>
 #include <utility>
 
@@ -18,7 +19,8 @@ namespace mips {
 constexpr int kEventsMost = 128;       // events of a workgroup
 constexpr uint32_t kPlaces = 1024;     // of the workgroup's rows, by their hash
 constexpr int kLook = 16;              // events that a thread looks at together
-constexpr uint32_t kHitsMost = 1024;   // later events of a workgroup's rows that are kept in LDS
+constexpr uint32_t kHitsMost = 1024;   // later events of a workgroup's rows that it takes at once
+static_assert(kHitsMost >= (uint32_t)kEventsMost, "a workgroup's events lie in its first window");
 
 struct EventArgs {
   const void *x, *forget, *gate;
@@ -42,35 +44,20 @@ __device__ __forceinline__ uint32_t row_hash(int64_t row) {
   return ((uint32_t)row * 2654435761u + (uint32_t)(row >> 32) * 40503u) >> (32 - 10);
 }
 
-// The first event after e, below b, whose row is `row`, or b: all lanes of a group together. `hits` are the
-// workgroup's later events (their own event << 16 | event), in any order, if they are all there.
-__device__ __forceinline__ int32_t next_event(const EventArgs& A, const uint32_t* hits, uint32_t nhits, int i,
-                                              int64_t row, int32_t e, int lanes, int lane) {
-  if (nhits <= kHitsMost) {
-    uint32_t best = 0xFFFFFFFFu;
-    for (uint32_t k = lane; k < nhits; k += lanes) {
-      const uint32_t v = hits[k];
-      if ((int)(v >> 16) == i && (int32_t)(v & 0xFFFFu) > e) best = min(best, v & 0xFFFFu);
-    }
-    for (int o = lanes >> 1; o >= 1; o >>= 1) best = min(best, (uint32_t)__shfl_xor((int)best, o));
-    return best == 0xFFFFFFFFu ? A.b : (int32_t)best;
-  }
-  const int shift = (threadIdx.x & 63) & ~(lanes - 1);
-  const uint64_t group = (lanes == 64 ? ~uint64_t(0) : (uint64_t(1) << lanes) - 1) << shift;
-  for (int32_t at = e + 1; at < A.b; at += lanes) {
-    const bool same = at + lane < A.b && event_row(A, at + lane) == row;
-    const uint64_t m = __ballot(same) & group;  // this group's lanes are here together
-    if (m) return at + (__ffsll((unsigned long long)m) - 1 - shift);
-  }
-  return A.b;
-}
-
+// Rows outside the table are not entered in the hash table: nothing is found for them. All events are looked through
+// once: those before the workgroup's own say which of its rows another one has, those behind are sorted by row and
+// event. Where these are too many, as they are with a row of a thousand events, they are taken in windows of as
+// many events as there is room for, those of rows that another workgroup has left out.
 template <typename T, bool GATE, bool VEC, int THREADS>
 __global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
   __shared__ int64_t own[kEventsMost];
-  __shared__ uint32_t earlier[kEventsMost], later[kEventsMost];
-  __shared__ uint32_t places[kPlaces];  // own event + 1, or 0
-  __shared__ uint32_t hits[kHitsMost], nhits;
+  __shared__ uint32_t taken[kEventsMost];  // its row is another event's: of this workgroup or of one before
+  __shared__ uint32_t later[kEventsMost];  // events of its row behind it, of those found
+  __shared__ uint32_t start[kEventsMost];  // of them in `order`
+  __shared__ uint32_t places[kPlaces];     // own event + 1, the first of its row here, or 0
+  __shared__ __attribute__((aligned(16))) uint32_t hits[kHitsMost + 4];  // own event << 16 | event, as found
+  __shared__ uint32_t nhits;
+  __shared__ uint16_t order[kHitsMost];    // events by row, then as they come
   const int tid = threadIdx.x;
   const int32_t e0 = (int32_t)blockIdx.x * A.own;
   const int count = min(A.own, A.b - e0);
@@ -78,15 +65,21 @@ __global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
   if (tid == 0) nhits = 0;
   if (tid < count) {
     own[tid] = event_row(A, e0 + tid);
-    earlier[tid] = later[tid] = 0;
+    taken[tid] = later[tid] = 0;
   }
   __syncthreads();
-  if (tid < count) {
+  auto inside = [&](int64_t row) __attribute__((always_inline)) { return (uint64_t)row < (uint64_t)A.table; };
+  if (tid < count && inside(own[tid])) {
     // at most kEventsMost of kPlaces are taken: the search for a free one ends, and those below
-    uint32_t v = row_hash(own[tid]);
-    while (atomicCAS(&places[v], 0u, (uint32_t)tid + 1u) != 0u) v = (v + 1) & (kPlaces - 1);
+    for (uint32_t v = row_hash(own[tid]);; v = (v + 1) & (kPlaces - 1)) {
+      const uint32_t p = atomicCAS(&places[v], 0u, (uint32_t)tid + 1u);
+      if (p == 0u) break;
+      if (own[p - 1] != own[tid]) continue;
+      const uint32_t was = atomicMin(&places[v], (uint32_t)tid + 1u);  // (a place stays its row's)
+      taken[max(was, (uint32_t)tid + 1u) - 1] = 1;
+      break;
+    }
   }
-  __syncthreads();
   // what the group's first event reads is on its way while its row is looked for
   const int lanes = 1 << A.lanes_log2, lane = tid & (lanes - 1), mine = tid >> A.lanes_log2;
   float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -101,50 +94,94 @@ __global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
     load4<VEC>(A.state + own[i] * A.state_stride + c0, live, wide, h);
     inputs(e0 + i, c0, live);
   };
-  if (mine < count && lane * 4 < A.d && own[mine] >= 0 && own[mine] < A.table) fetch(mine, lane * 4, min(4, A.d - lane * 4));
+  if (mine < count && lane * 4 < A.d && inside(own[mine])) fetch(mine, lane * 4, min(4, A.d - lane * 4));
+  __syncthreads();
 
-  // many loads at once: one after another they would be most of the call
-  for (int32_t first = tid; first < A.b; first += THREADS * kLook) {
-    int64_t rows[kLook];
+  // calls found(i, e) for events e of [from, to) with the row of own event i, its first here; many loads at
+  // once: one after another they would be most of the call
+  auto look = [&](int32_t from, int32_t to, auto found) __attribute__((always_inline)) {
+    for (int32_t first = from + tid; first < to; first += THREADS * kLook) {
+      int64_t rows[kLook];
 #pragma unroll
-    for (int u = 0; u < kLook; ++u) rows[u] = event_row(A, min(first + u * THREADS, A.b - 1));
+      for (int u = 0; u < kLook; ++u) rows[u] = event_row(A, min(first + u * THREADS, to - 1));
 #pragma unroll
-    for (int u = 0; u < kLook; ++u) {
-      const int32_t e = first + u * THREADS;
-      if (e >= A.b) break;
-      for (uint32_t v = row_hash(rows[u]), p; (p = places[v]) != 0u; v = (v + 1) & (kPlaces - 1)) {
-        const int i = (int)p - 1;
-        if (own[i] != rows[u]) continue;
-        if (e < e0 + i) {
-          earlier[i] = 1;  // every writer writes the same
-        } else if (e > e0 + i) {
-          later[i] = 1;
-          const uint32_t k = atomicAdd(&nhits, 1u);
-          if (k < kHitsMost) hits[k] = (uint32_t)i << 16 | (uint32_t)e;
+      for (int u = 0; u < kLook; ++u) {
+        const int32_t e = first + u * THREADS;
+        if (e >= to) break;
+        for (uint32_t v = row_hash(rows[u]), p; (p = places[v]) != 0u; v = (v + 1) & (kPlaces - 1)) {
+          const int i = (int)p - 1;
+          if (own[i] == rows[u]) found(i, e);  // (and on to a free place: leaving here took 90 us for 77, 65,536 events)
         }
       }
     }
-  }
+  };
+  auto hit = [&](int i, int32_t e) __attribute__((always_inline)) {
+    atomicAdd(&later[i], 1u);
+    const uint32_t k = atomicAdd(&nhits, 1u);
+    if (k < kHitsMost) hits[k] = (uint32_t)i << 16 | (uint32_t)e;
+  };
+  look(0, A.b, [&](int i, int32_t e) __attribute__((always_inline)) {
+    if (e < e0) taken[i] = 1;  // every writer writes the same
+    else if (e > e0 + i) hit(i, e);
+  });
   __syncthreads();
-
-  for (int i = tid >> A.lanes_log2; i < count; i += THREADS >> A.lanes_log2) {
-    const int64_t row = own[i];
-    const bool inside = row >= 0 && row < A.table;
-    if (inside && earlier[i]) continue;
-    for (int base = 0; base < A.d; base += lanes * 4) {
-      const int c0 = base + lane * 4, live = min(4, A.d - c0);  // live <= 0: only looks for events
-      if (!inside) {
-        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (live > 0) store4<2 * VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, zero);
-        continue;
+  const bool whole = nhits <= kHitsMost;
+  for (int32_t w0 = e0;; w0 += kHitsMost) {
+    if (!whole) {
+      __syncthreads();  // nothing of the window before is read any more
+      if (tid < count) later[tid] = 0;
+      if (tid == 0) nhits = 0;
+      __syncthreads();
+      look(w0, min(w0 + (int32_t)kHitsMost, A.b), [&](int i, int32_t e) __attribute__((always_inline)) {
+        if (e > e0 + i && !taken[i]) hit(i, e);
+      });
+      __syncthreads();
+    }
+    const uint32_t n = nhits;
+    if (n) {
+      if (tid < 4) hits[n + tid] = 0xFFFFFFFFu;
+      __syncthreads();
+      for (uint32_t k = tid; k < n; k += THREADS) {
+        const uint32_t v = hits[k], row = v & 0xFFFF0000u;
+        uint32_t at = 0, begin = 0;
+        for (uint32_t j = 0; j < n; j += 4) {
+          const uint4 q = *(const uint4*)(hits + j);
+          at += (q.x < v) + (q.y < v) + (q.z < v) + (q.w < v);
+          begin += (q.x < row) + (q.y < row) + (q.z < row) + (q.w < row);
+        }
+        order[at] = (uint16_t)v;
+        start[v >> 16] = begin;  // the same from each of the row's
       }
-      if ((i != mine || base) && live > 0) fetch(i, c0, live);
-      for (int32_t e = e0 + i; e < A.b;) {
-        // the next one's inputs are on their way while this one is applied
-        const int32_t then = later[i] ? next_event(A, hits, nhits, i, row, e, lanes, lane) : A.b;
-        const Raw<T> x0 = x, f0 = f, g0 = g;
-        if (then < A.b && live > 0) inputs(then, c0, live);
-        if (live > 0) {
+      __syncthreads();
+    }
+
+    const bool first = w0 == e0;
+    for (int i = mine; i < count; i += THREADS >> A.lanes_log2) {
+      const bool none = !inside(own[i]);
+      if (none ? !first : taken[i] || !(first || later[i])) continue;
+      for (int c0 = lane * 4; c0 < A.d; c0 += lanes * 4) {
+        const int live = min(4, A.d - c0);
+        if (none) {
+          const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          store4<2 * VEC>((T*)A.h + (int64_t)(e0 + i) * A.d + c0, live, zero);
+          continue;
+        }
+        uint32_t left = later[i];
+        const uint16_t* next = order + (left ? start[i] : 0);
+        int32_t e = e0 + i;
+        if (!first) {  // goes on from the window before, whose state this lane wrote
+          e = *next++;
+          --left;
+          load4<VEC>(A.out + own[i] * A.out_stride + c0, live, wide, h);
+          inputs(e, c0, live);
+        } else if (i != mine || c0 != lane * 4) {
+          fetch(i, c0, live);
+        }
+        for (;;) {
+          // the next one's inputs are on their way while this one is applied
+          const Raw<T> x0 = x, f0 = f, g0 = g;
+          const int32_t then = left ? *next++ : 0;
+          if (left) inputs(then, c0, live);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float a, na, b, nb;
@@ -154,11 +191,14 @@ __global__ __launch_bounds__(THREADS) void events_kernel(EventArgs A) {
             h[c] = fmaf(a, h[c], b * x0.at(c));
           }
           store4<2 * VEC>((T*)A.h + (int64_t)e * A.d + c0, live, h);
+          if (!left) break;
+          --left;
+          e = then;
         }
-        e = then;
+        store4<2 * VEC>(A.out + own[i] * A.out_stride + c0, live, h);
       }
-      if (live > 0) store4<2 * VEC>(A.out + row * A.out_stride + c0, live, h);
     }
+    if (whole || w0 + (int32_t)kHitsMost >= A.b) break;
   }
 }
 
