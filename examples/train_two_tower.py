@@ -16,7 +16,8 @@ With --encoder recurrence the user is what a gated recurrence makes of the histo
 
     embedding -> dropout -> gated_scan -> pool_normalize -> item_logprobs,
 
-trained through the differentiable functions, and followed event by event with gated_step.
+trained through the differentiable functions. Afterwards new users are encoded and searched, and their states
+followed event by event with gated_step, as a server has them.
 
     python3 examples/train_two_tower.py [--steps 300] [--dtype f32|bf16] [--encoder mean|recurrence]
 """
@@ -140,6 +141,24 @@ def follow(table, weight, bias, history, lengths):
     return states
 
 
+def serve(table, weight, bias, users=256, seed=1):
+    """(share of the 10 best items that lie in the user's group, largest difference between a state from single
+    events and that of the whole history) of new users with histories of 1 to HISTORY events."""
+    device = table.device
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    history, _ = sample(gen, users, device)
+    lengths = torch.randint(1, HISTORY + 1, (users,), generator=gen, device=device)
+    with torch.no_grad():
+        q = encode(table, weight, bias, history, lengths)
+        _, best = mips.topk(q, mips.prepare_corpus(table.float(), "f32" if table.dtype == torch.float32 else "bf16"), 10)
+        events = mips.embedding_lookup(table, history)
+        gates = torch.nn.functional.linear(events, weight, bias)
+        whole = mips.gated_scan(events, gates, lengths=lengths, states=False, carries=False).last
+        apart = (follow(table, weight, bias, history, lengths) - whole).abs().max()
+    return float((best % GROUPS == history[:, :1] % GROUPS).float().mean()), float(apart)
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=300)
@@ -147,8 +166,10 @@ if __name__ == "__main__":
     ap.add_argument("--encoder", choices=("mean", "recurrence"), default="mean")
     a = ap.parse_args()
     if a.encoder == "recurrence":
-        _, losses = train_encoder(a.steps, dtype=a.dtype)
-        print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} (log of the batch: {math.log(128):.3f})")
+        params, losses = train_encoder(a.steps, dtype=a.dtype)
+        hit, apart = serve(*(p.to(torch.float32 if a.dtype == "f32" else torch.bfloat16) for p in params))
+        print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} (log of the batch: {math.log(128):.3f}); of the 10 best items "
+              f"{100 * hit:.1f}% lie in the user's group; states followed event by event are within {apart:.1e} of the histories'")
         sys.exit()
     table, losses = train(a.steps, dtype=a.dtype)
     hit, prob, entropy = evaluate(table, dtype=a.dtype)

@@ -3,6 +3,8 @@ streams, in captured graphs, with workspaces of the caller, and at sizes past 32
 import importlib.util
 import math
 import os
+import re
+import runpy
 
 import numpy as np
 import pytest
@@ -455,3 +457,19 @@ def test_example_with_an_encoder():
     with torch.no_grad():
         states = ex.follow(*leaves, history, lengths)
     assert (states.double().cpu() - last2.detach()).abs().max() <= 1e-4 * last2.abs().max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_example_serves_what_it_trained(dtype, monkeypatch, capsys):
+    """The program itself: it trains, searches for new users and follows them event by event. States are sums
+    of b x over at most five events, within (2 * 16 + 12 + 32) u of five of the largest input on either side."""
+    _dev()
+    path = os.path.join(ROOT, "examples", "train_two_tower.py")
+    monkeypatch.setattr("sys.argv", [path, "--encoder", "recurrence", "--steps", "2", "--dtype", dtype])
+    with pytest.raises(SystemExit) as end:
+        runpy.run_path(path, run_name="__main__")
+    assert not end.value.code
+    text = capsys.readouterr().out
+    found = re.search(r"([\d.]+)% lie in the user's group; states followed event by event are within (\S+) of", text)
+    assert found, text
+    assert 0 <= float(found[1]) <= 100 and float(found[2]) <= 2 * 76 * U * 5 * 1.0
