@@ -1,10 +1,11 @@
 // scan.hip -- the gated linear recurrence over sequences, forward (gfx950). scan.h has the method.
 //
 // One pass: forget logits, inputs (and gate logits) are read once and the states written once. Bound by
-// memory where sequences lie whole in tiles: 4096 x 127 x 128 bf16 take 84 us (5.1 TB/s, the carries
-// among them; vector units busy half of the time), and 42 where half of the rows are padding and only last
+// memory where sequences lie whole in tiles: 4096 x 127 x 128 bf16 take 82 us (5.3 TB/s, the carries
+// among them; vector units busy half of the time), and 43 where half of the rows are padding and only last
 // states are wanted (vector units and latency). Chained tiles add what they wait for one another: 65,536 x
-// 1024 bf16 take 109 (4.0 TB/s), 600,000 x 100 packed f32 with gates 226 (4.5 TB/s).
+// 1024 bf16 take 109 (4.0 TB/s), 600,000 x 100 packed f32 with gates 227 (4.5 TB/s). Dense sequences
+// just above half a tile leave half of its threads idle: 65 x 128 bf16 take 1.6 times what 127 x 128 do, row for row.
 #include <type_traits>
 
 #include "scan.h"
@@ -38,7 +39,7 @@ __device__ __forceinline__ void none_last(const ScanArgs& A, uint32_t r, int64_t
 
 // STATES: every state is wanted, and held until the one before the run is known. Else a run keeps its map and, of
 // a sequence that goes on from the run before, the map up to its final row: registers for half as
-// many waves again, where this is bound by latency (4096 x 127 x 128 bf16 with lengths: 44 us for 72).
+// many waves again, where this is bound by latency (4096 x 127 x 128 bf16 with lengths: 72 us when states were held, 43).
 template <typename T, bool GATE, int VEC, bool STATES, bool CHAINED, int THREADS>
 __global__ __launch_bounds__(THREADS, STATES || GATE || THREADS > 512 ? 4 : 6) void scan_kernel(ScanArgs A) {
   constexpr int R = kRun<T>;

@@ -7,15 +7,16 @@
 // What flows backward is u_r = a_r (G_r + u_{r+1}), again a composition of affine maps, from the
 // last tile to the first. The states h_{r-1} are not read: they follow from the inputs, which are
 // needed anyway, and the state before the run, which the forward call left in binary32 (an eighth of a
-// bf16 tensor's rows, and a quarter of its bytes; taking the states from tile to tile here as well, by maps
+// bf16 tensor's rows, and a quarter of its bytes, in full tiles; taking the states from tile to tile here as well, by maps
 // as the gradient, was a third more instructions, and they are what bounds this kernel).
 //
 // A run's rows are gone through twice: forward, for the factor of D in dforget and the run's map of u, and,
 // when it is known what flows in from behind, backward for D.
 //
-// 4096 x 127 x 128 bf16 take 132 us (5.3 TB/s; vector units busy 56% of the time, four waves a SIMD held by
-// 128 registers), 103 where half of the rows are padding; chained: 65,536 x 1024 bf16 145 (4.8 TB/s), 600,000
-// x 100 packed f32 with gates 366 (4.7 TB/s).
+// 4096 x 127 x 128 bf16 take 132 us (5.3 TB/s; vector units busy 59% of the time, four waves a SIMD held by
+// 128 registers), 105 where half of the rows are padding; chained: 65,536 x 1024 bf16 145 (4.8 TB/s), 600,000
+// x 100 packed f32 with gates 367 (4.7 TB/s). With gates bf16 spills 5 to 10 registers a thread in whole tiles, 30
+// to 42 chained, f32 36 where rows do not lie by four and tiles are chained: 188 us (5.2 TB/s) for 4096 x 127 x 128 bf16.
 #include <type_traits>
 
 #include "scan.h"

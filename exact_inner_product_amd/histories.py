@@ -158,7 +158,8 @@ def gated_scan(x: torch.Tensor, forget: torch.Tensor, gate: Optional[torch.Tenso
     `offsets` [b + 1], [n, d]; any strides (rows without unit stride along d, or that overlap, are
     copied first). initial: float32 [b, d], the state before each sequence (0 by default). With
     states false only the last states are written; with carries false the result has no gradient (they
-    are a quarter of x's bytes). Padding is not read and has states of 0; a sequence without rows has
+    are a quarter of x's bytes where sequences fill their tiles of up to 128 rows or, of few channels, more,
+    half where they leave almost half of them empty, and those of one tile at least). Padding is not read and has states of 0; a sequence without rows has
     its initial state as its last one.
     """
     seq, b, d, held = _sequences(x.shape, offsets, lengths)
